@@ -34,9 +34,13 @@ CM_OPT_DEBUG_FLAG_OFFSET = 15
 CM_OPT_RS_COL_SLABS = 16
 CM_OPT_RS_BUCKET_HINT = 17
 CM_MAX_RANKS, CM_MAX_CHUNKS = 16, 8
+CM_ACT_NONE, CM_ACT_RELU, CM_ACT_GELU, CM_ACT_GELU_TANH, CM_ACT_SILU = 0, 1, 2, 3, 4
+CM_ADAMW_BLOCK = 256
 
 DIRECTIONS = {"uni": CM_RING_UNI, "bidi": CM_RING_BIDI, "none": CM_RING_NONE}
 LAYOUTS = {"kn": CM_W_KN, "nk": CM_W_NK}
+ACTS = {"none": CM_ACT_NONE, "relu": CM_ACT_RELU, "gelu": CM_ACT_GELU, "gelu_tanh": CM_ACT_GELU_TANH,
+        "silu": CM_ACT_SILU}
 
 # Every symbol include/cm.h declares.
 EXPORTS = ["cm_plan", "cm_plan_destroy", "cm_plan_steps", "cm_plan_step", "cm_plan_tasks",
@@ -45,7 +49,10 @@ EXPORTS = ["cm_plan", "cm_plan_destroy", "cm_plan_steps", "cm_plan_step", "cm_pl
            "cm_ag_gemm_noalloc", "cm_ag_gemm_noalloc_check_status", "cm_cost_estimate", "cm_plan_choose",
            "cm_gemm_rs_pipelined_workspace_size", "cm_gemm_rs_pipelined",
            "cm_backward_pair_workspace_size", "cm_backward_pair",
-           "cm_cannon_workspace_size", "cm_cannon_gemm", "cm_einsum_cost", "cm_plan_choose_einsum"]
+           "cm_cannon_workspace_size", "cm_cannon_gemm", "cm_einsum_cost", "cm_plan_choose_einsum",
+           "cm_linear", "cm_linear_dgrad", "cm_linear_wgrad", "cm_linear_wgrad_workspace_size",
+           "cm_linear_check_status", "cm_layer_norm", "cm_layer_norm_backward",
+           "cm_layer_norm_backward_workspace_size", "cm_adamw"]
 CM_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -62,6 +69,13 @@ class cm_task(ctypes.Structure):
                 ("wait_in", ctypes.c_int16 * 2), ("wait_free", ctypes.c_int16 * 2),
                 ("sig_fwd", ctypes.c_int16 * 2), ("sig_done", ctypes.c_int16),
                 ("step", ctypes.c_int16), ("stream", ctypes.c_int16), ("tile_group", ctypes.c_int16)]
+
+
+class cm_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
 
 
 class CMError(RuntimeError):
@@ -137,6 +151,26 @@ def load():
     lib.cm_plan_choose_einsum.argtypes = [i32, i64, i64, i64, rp, i32, ctypes.POINTER(i32), ctypes.POINTER(i32),
                                           ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_double)]
     lib.cm_plan_choose_einsum.restype = i32
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    lib.cm_linear.argtypes = [p, i64, p, i64, i32, p, i32, i32, p, i64, p, i64, p, i32, i64, i64, i64, i64, p]
+    lib.cm_linear.restype = i32
+    lib.cm_linear_dgrad.argtypes = [p, i64, p, i64, i32, p, i64, i32, p, i64, p, i32, i64, i64, i64, i64, p]
+    lib.cm_linear_dgrad.restype = i32
+    lib.cm_linear_wgrad.argtypes = [p, i64, p, i64, p, i32, i64, i32, p, i32, i32, i64, i64, i64, p, sz, p]
+    lib.cm_linear_wgrad.restype = i32
+    lib.cm_linear_wgrad_workspace_size.argtypes = [i64, i64, i64]
+    lib.cm_linear_wgrad_workspace_size.restype = sz
+    lib.cm_linear_check_status.argtypes = [p, ctypes.POINTER(i32)]
+    lib.cm_linear_check_status.restype = i32
+    lib.cm_layer_norm.argtypes = [p, i32, i64, p, p, i32, f32, p, i32, i64, p, p, i64, i64, p]
+    lib.cm_layer_norm.restype = i32
+    lib.cm_layer_norm_backward.argtypes = [p, i32, i64, p, i32, i64, p, i32, p, p, p, i64, p, i64, p, p, i32, i32, i64,
+                                           i64, p, sz, p]
+    lib.cm_layer_norm_backward.restype = i32
+    lib.cm_layer_norm_backward_workspace_size.argtypes = [i64, i64]
+    lib.cm_layer_norm_backward_workspace_size.restype = sz
+    lib.cm_adamw.argtypes = [p, i32, f64, f64, f64, f64, i64, p, ctypes.c_uint64, p]
+    lib.cm_adamw.restype = i32
     _lib = lib
     return lib
 
@@ -349,6 +383,220 @@ def plan_choose_einsum(n_ranks, m, K, n, rates, max_chunks=CM_MAX_CHUNKS):
                                         ctypes.byref(c), ctypes.byref(d), ctypes.byref(us)), "cm_plan_choose_einsum")
     name = {CM_OP_AG_GEMM: "ag", CM_OP_GEMM_RS: "rs", -1: "none"}[w.value]
     return name, c.value, {v: k for k, v in DIRECTIONS.items()}[d.value], us.value
+
+
+def _matrix(name, t, rows=None, cols=None, dtype=None):
+    """A 2-D CUDA tensor with contiguous rows: (pointer, row stride)."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    ld, inner = t.stride()
+    if c > 1 and inner != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    # a single row has no stride of its own: the smallest multiple of 8 that holds it
+    return t.data_ptr(), ld if r > 1 else -(-c // 8) * 8
+
+
+def _vector(name, t, n, dtype=None):
+    if t is None:
+        return None
+    if t.dim() != 1 or not t.is_cuda or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous CUDA vector of {n} elements")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _dtype_of(name, t):
+    import torch
+    if t is None or t.dtype == torch.bfloat16:
+        return CM_BF16
+    if t.dtype == torch.float32:
+        return CM_F32
+    raise TypeError(f"{name} must be bf16 or fp32, not {t.dtype}")
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def cm_linear(x, w, y, bias=None, act: str = "none", residual=None, preact=None, w_layout: str = "nk", stream=None):
+    """y [M][n] = act(x @ W^T + bias) + residual; preact receives x @ W^T + bias (bf16)."""
+    import torch
+    b16 = torch.bfloat16
+    M, K = x.shape
+    n = y.shape[1]
+    _same_device(x, w, y, bias, residual, preact)
+    wr, wc = (n, K) if w_layout == "nk" else (K, n)
+    xp, ldx = _matrix("x", x, M, K, b16)
+    wp, ldw = _matrix("w", w, wr, wc, b16)
+    yp, ldy = _matrix("y", y, M, n)
+    rp, ldr = _matrix("residual", residual, M, n, b16) if residual is not None else (None, 0)
+    zp, ldz = _matrix("preact", preact, M, n, b16) if preact is not None else (None, 0)
+    st = load().cm_linear(xp, ldx, wp, ldw, LAYOUTS[w_layout], _vector("bias", bias, n), _dtype_of("bias", bias),
+                          ACTS[act], rp, ldr, zp, ldz, yp, _dtype_of("y", y), ldy, M, K, n, _stream_ptr(stream))
+    _check(st, "cm_linear")
+
+
+def cm_linear_dgrad(dy, w, dx, preact=None, act: str = "none", residual=None, w_layout: str = "nk", stream=None):
+    """dx [M][K] = (dy @ W) * act'(preact) + residual; act and preact are those of the layer in front."""
+    import torch
+    b16 = torch.bfloat16
+    M, n = dy.shape
+    K = dx.shape[1]
+    _same_device(dy, w, dx, preact, residual)
+    wr, wc = (n, K) if w_layout == "nk" else (K, n)
+    dyp, lddy = _matrix("dy", dy, M, n, b16)
+    wp, ldw = _matrix("w", w, wr, wc, b16)
+    dxp, lddx = _matrix("dx", dx, M, K)
+    rp, ldr = _matrix("residual", residual, M, K, b16) if residual is not None else (None, 0)
+    zp, ldz = _matrix("preact", preact, M, K, b16) if preact is not None else (None, 0)
+    st = load().cm_linear_dgrad(dyp, lddy, wp, ldw, LAYOUTS[w_layout], zp, ldz, ACTS[act], rp, ldr, dxp,
+                                _dtype_of("dx", dx), lddx, M, K, n, _stream_ptr(stream))
+    _check(st, "cm_linear_dgrad")
+
+
+def linear_wgrad_workspace_size(M: int, K: int, n: int) -> int:
+    return load().cm_linear_wgrad_workspace_size(M, K, n)
+
+
+def cm_linear_wgrad(x, dy, dw, ws=None, db=None, accumulate: bool = False, w_layout: str = "nk", stream=None):
+    """dw (+)= dy^T @ x ("nk": [n][K], "kn": [K][n]) and db [n] (+)= the sum of dy's rows.
+    ws (linear_wgrad_workspace_size bytes) is needed with db only."""
+    import torch
+    b16 = torch.bfloat16
+    M, K = x.shape
+    n = dy.shape[1]
+    _same_device(x, dy, dw, ws, db)
+    wr, wc = (n, K) if w_layout == "nk" else (K, n)
+    xp, ldx = _matrix("x", x, M, K, b16)
+    dyp, lddy = _matrix("dy", dy, M, n, b16)
+    dwp, lddw = _matrix("dw", dw, wr, wc)
+    st = load().cm_linear_wgrad(xp, ldx, dyp, lddy, dwp, _dtype_of("dw", dw), lddw, LAYOUTS[w_layout],
+                                _vector("db", db, n), _dtype_of("db", db), int(bool(accumulate)), M, K, n,
+                                None if ws is None else ws.data_ptr(),
+                                0 if ws is None else ws.numel() * ws.element_size(), _stream_ptr(stream))
+    _check(st, "cm_linear_wgrad")
+
+
+def cm_linear_check_status(stream=None):
+    """Synchronise and return (status, info[4]) of the linear kernels since the last read."""
+    info = (ctypes.c_int * 4)()
+    st = load().cm_linear_check_status(_stream_ptr(stream), info)
+    return st, list(info)
+
+
+def cm_layer_norm(x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * gamma + beta by rows; mean and rstd (fp32 [rows]) are written if given."""
+    import torch
+    rows, h = x.shape
+    _same_device(x, y, gamma, beta, mean, rstd)
+    xp, ldx = _matrix("x", x, rows, h)
+    yp, ldy = _matrix("y", y, rows, h)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have one dtype")
+    st = load().cm_layer_norm(xp, _dtype_of("x", x), ldx, _vector("gamma", gamma, h), _vector("beta", beta, h),
+                              _dtype_of("gamma", gamma if gamma is not None else beta), eps, yp, _dtype_of("y", y), ldy,
+                              _vector("mean", mean, rows, torch.float32), _vector("rstd", rstd, rows, torch.float32),
+                              rows, h, _stream_ptr(stream))
+    _check(st, "cm_layer_norm")
+
+
+def layer_norm_backward_workspace_size(rows: int, h: int) -> int:
+    return load().cm_layer_norm_backward_workspace_size(rows, h)
+
+
+def cm_layer_norm_backward(x, dy, gamma, mean, rstd, dx, ws=None, dgamma=None, dbeta=None, residual=None,
+                           accumulate: bool = False, stream=None):
+    """dx of cm_layer_norm (+ residual), dgamma and dbeta [h] (both optional; ws is needed for them:
+    layer_norm_backward_workspace_size bytes)."""
+    import torch
+    rows, h = x.shape
+    _same_device(x, dy, gamma, mean, rstd, dx, ws, dgamma, dbeta, residual)
+    xp, ldx = _matrix("x", x, rows, h)
+    dyp, lddy = _matrix("dy", dy, rows, h)
+    dxp, lddx = _matrix("dx", dx, rows, h, x.dtype)
+    rp, ldr = _matrix("residual", residual, rows, h, x.dtype) if residual is not None else (None, 0)
+    if dgamma is not None and dbeta is not None and dgamma.dtype != dbeta.dtype:
+        raise TypeError("dgamma and dbeta must have one dtype")
+    st = load().cm_layer_norm_backward(xp, _dtype_of("x", x), ldx, dyp, _dtype_of("dy", dy), lddy,
+                                       _vector("gamma", gamma, h), _dtype_of("gamma", gamma),
+                                       _vector("mean", mean, rows, torch.float32),
+                                       _vector("rstd", rstd, rows, torch.float32), rp, ldr, dxp, lddx,
+                                       _vector("dgamma", dgamma, h), _vector("dbeta", dbeta, h),
+                                       _dtype_of("dgamma", dgamma if dgamma is not None else dbeta),
+                                       int(bool(accumulate)), rows, h, None if ws is None else ws.data_ptr(),
+                                       0 if ws is None else ws.numel() * ws.element_size(), _stream_ptr(stream))
+    _check(st, "cm_layer_norm_backward")
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step (cm_adamw), listed once; holds references to them."""
+
+    def __init__(self):
+        self._rows, self._keep, self._array, self.device = [], [], None, None
+
+    def __len__(self):
+        return len(self._rows)
+
+    def add(self, param, grad, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, master=None,
+            weight_decay: float = 0.0):
+        """fp32 exp_avg and exp_avg_sq are 32-bit states; float8_e4m3fn (or uint8) ones, with their scales
+        (fp32, one per CM_ADAMW_BLOCK elements), the 8-bit states, exp_avg_sq then holding the root."""
+        import torch
+        n = param.numel()
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        bits = 32 if exp_avg.dtype == torch.float32 else 8
+        if exp_avg_sq.dtype != exp_avg.dtype or (bits == 8 and exp_avg.dtype not in codes):
+            raise TypeError("exp_avg and exp_avg_sq must both be fp32 or both float8_e4m3fn (or uint8)")
+        blocks = -(-n // CM_ADAMW_BLOCK)
+        if bits == 8 and (exp_avg_scale is None or exp_avg_sq_scale is None):
+            raise ValueError("8-bit states need exp_avg_scale and exp_avg_sq_scale")
+        if bits == 32 and (exp_avg_scale is not None or exp_avg_sq_scale is not None):
+            raise ValueError("32-bit states have no scales")
+        each = [("param", param, n, None), ("grad", grad, n, None), ("master", master, n, torch.float32),
+                ("exp_avg", exp_avg, n, None), ("exp_avg_sq", exp_avg_sq, n, None),
+                ("exp_avg_scale", exp_avg_scale, blocks, torch.float32),
+                ("exp_avg_sq_scale", exp_avg_sq_scale, blocks, torch.float32)]
+        ptrs = []
+        for name, t, count, dtype in each:
+            if t is None:
+                ptrs.append(None)
+                continue
+            if not t.is_cuda or not t.is_contiguous() or t.numel() != count or (self.device or t.device) != t.device:
+                raise ValueError(f"{name} must be a contiguous tensor of {count} elements on one CUDA device")
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+            self.device = t.device
+            ptrs.append(t.data_ptr())
+        self._rows.append(cm_adamw_tensor(*ptrs, n, float(weight_decay), _dtype_of("param", param),
+                                          _dtype_of("grad", grad), bits))
+        self._keep.append((param, grad, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale))
+        self._array = None
+
+    def array(self):
+        if self._array is None:
+            self._array = (cm_adamw_tensor * max(1, len(self._rows)))(*self._rows)
+        return self._array
+
+
+def cm_adamw(tensors: AdamWTensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             step: int = 1, grad_scale=None, seed: int = 0, stream=None):
+    """One AdamW step over the listed tensors.  grad_scale: a one-element fp32 CUDA tensor that multiplies every
+    gradient; seed: not 0 rounds 8-bit states up or down at random, keeping their mean (a new seed each step)."""
+    import torch
+    if grad_scale is not None and (grad_scale.numel() != 1 or grad_scale.dtype != torch.float32
+                                   or not grad_scale.is_cuda):
+        raise ValueError("grad_scale must be one fp32 CUDA element")
+    st = load().cm_adamw(tensors.array(), len(tensors), lr, beta1, beta2, eps, int(step),
+                         None if grad_scale is None else grad_scale.data_ptr(), seed, _stream_ptr(stream))
+    _check(st, "cm_adamw")
 
 
 def version() -> str:

@@ -1,0 +1,272 @@
+// cm_linear_api.cu -- the C ABI of the linear layer: argument checks, tensor
+// maps, the choice of kernel and tile, and the launches.
+#include <cudaTypedefs.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "cm_internal.h"
+#include "cm_kernel.cuh"
+#include "cm_linear.cuh"
+
+namespace cm {
+namespace {
+
+__device__ LinearStatus g_linear_status;
+
+constexpr uint64_t kLinearTimeoutNs = 1000000000ull;
+constexpr int64_t kMaxExtent = int64_t(1) << 30;
+
+struct NvtxRange {
+    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+};
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// Row-major bf16 [rows][cols] with row stride ld, in 64 x box_rows boxes,
+// 128-byte swizzle; elements outside are read as zeros.
+bool map_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), 1};
+    cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(ld) * 2 * cuuint64_t(rows)};
+    cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool bad_dtype(cm_dtype t) { return t != CM_BF16 && t != CM_F32; }
+
+// A matrix the kernels read with TMA or write in 16-byte pieces.
+cm_status check_matrix(const void *p, int64_t ld, int64_t cols) {
+    if (!p) return CM_ERR_INVALID_ARG;
+    if (ld < cols || ld > kMaxExtent) return CM_ERR_SHAPE;
+    if (ld % 8 != 0 || !aligned16(p)) return CM_ERR_ALIGNMENT;
+    return CM_OK;
+}
+
+cm_status check_extents(int64_t M, int64_t K, int64_t n) {
+    return M < 0 || K <= 0 || n <= 0 || M > kMaxExtent || K > kMaxExtent || n > kMaxExtent ? CM_ERR_SHAPE : CM_OK;
+}
+
+struct Device {
+    int id = 0, sms = 0;
+    LinearStatus *status = nullptr;
+};
+
+cm_status device(Device *d) {
+    if (cudaGetDevice(&d->id) != cudaSuccess) return CM_ERR_CUDA;
+    static std::mutex mu;
+    static Device cached[64];
+    if (d->id < 0 || d->id >= 64) return CM_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lock(mu);
+    Device &c = cached[d->id];
+    if (!c.status) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d->id) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d->id) != cudaSuccess ||
+            cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess)
+            return CM_ERR_CUDA;
+        if (major != 10 || minor != 3) return CM_ERR_UNSUPPORTED;
+        if (prepare_linear_strip(d->id) != cudaSuccess) return CM_ERR_CUDA;
+        void *sp = nullptr;
+        if (cudaGetSymbolAddress(&sp, g_linear_status) != cudaSuccess) return CM_ERR_CUDA;
+        c.status = static_cast<LinearStatus *>(sp);
+        c.id = d->id;
+    }
+    *d = c;
+    return CM_OK;
+}
+
+// One operand: `rows` x `k` where k is the contracted extent; K-major when
+// the contracted extent is contiguous.
+struct Operand {
+    const void *p;
+    int64_t ld;
+    bool mn_major;
+};
+
+bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t k, int tile_rows) {
+    return o.mn_major ? map_rows(m, o.p, k, rows, o.ld, 64) : map_rows(m, o.p, rows, k, o.ld, tile_rows);
+}
+
+// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.
+cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
+                  const LinearEpilogue &e, cudaStream_t stream) {
+    LinearStripParams p;
+    p.e = e;
+    p.rows = rows;
+    p.cols = cols;
+    p.kblocks = int((k + kBK - 1) / kBK);
+    int tok = b.mn_major ? 64 : 16;
+    while (tok < 128 && tok < rows) tok *= 2;
+    const int64_t row_tiles = (rows + tok - 1) / tok, tiles = row_tiles * ((cols + 127) / 128);
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * d.sms && splits * 2 <= p.kblocks) splits *= 2;
+    p.tok = tok;
+    p.row_tiles = int(row_tiles);
+    p.splits = splits;
+    p.stages = linear_strip_stages(tok, splits);
+    p.status = d.status;
+    p.timeout_ns = kLinearTimeoutNs;
+    if (!map_operand(&p.tmA, a, cols, k, 128) || !map_operand(&p.tmB, b, rows, k, tok)) return CM_ERR_CUDA;
+    const int layout = (b.mn_major ? 1 : 0) | (a.mn_major ? 2 : 0);
+    return launch_linear_strip(p, layout, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+}
+
+size_t wgrad_workspace(int64_t M, int64_t n) {
+    return std::max<size_t>(256, size_t(colsum_chunks(M, n)) * size_t(n) * sizeof(float));
+}
+
+}  // namespace
+}  // namespace cm
+
+using namespace cm;
+
+#define CM_TRY(x)                        \
+    do {                                 \
+        const cm_status st_ = (x);       \
+        if (st_ != CM_OK) return st_;    \
+    } while (0)
+
+extern "C" {
+
+cm_status cm_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout, const void *bias,
+                    cm_dtype bias_dtype, cm_act act, const void *residual, int64_t ldr, void *preact, int64_t ldz,
+                    void *y, cm_dtype y_dtype, int64_t ldy, int64_t M, int64_t K, int64_t n, cm_stream_t stream) {
+    NvtxRange range("cm_linear");
+    if (bad_dtype(y_dtype) || (bias && bad_dtype(bias_dtype)) || (wlayout != CM_W_KN && wlayout != CM_W_NK) ||
+        act < CM_ACT_NONE || act > CM_ACT_SILU)
+        return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    if (M == 0) return CM_OK;
+    CM_TRY(check_matrix(x, ldx, K));
+    CM_TRY(check_matrix(w, ldw, wlayout == CM_W_NK ? K : n));
+    CM_TRY(check_matrix(y, ldy, n));
+    if (residual) CM_TRY(check_matrix(residual, ldr, n));
+    if (preact) CM_TRY(check_matrix(preact, ldz, n));
+    Device d;
+    CM_TRY(device(&d));
+    LinearEpilogue e = {};
+    e.y = y;
+    e.ldy = ldy;
+    e.y_f32 = y_dtype == CM_F32;
+    e.bias = bias;
+    e.bias_f32 = bias_dtype == CM_F32;
+    e.act = act;
+    e.res = residual;
+    e.ldr = ldr;
+    e.z = preact;
+    e.ldz = ldz;
+    return product(d, {w, ldw, wlayout == CM_W_KN}, {x, ldx, false}, M, n, K, e, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cm_status cm_linear_dgrad(const void *dy, int64_t lddy, const void *w, int64_t ldw, cm_wlayout wlayout,
+                          const void *preact, int64_t ldz, cm_act act, const void *residual, int64_t ldr, void *dx,
+                          cm_dtype dx_dtype, int64_t lddx, int64_t M, int64_t K, int64_t n, cm_stream_t stream) {
+    NvtxRange range("cm_linear_dgrad");
+    if (bad_dtype(dx_dtype) || (wlayout != CM_W_KN && wlayout != CM_W_NK) || act < CM_ACT_NONE || act > CM_ACT_SILU ||
+        (act != CM_ACT_NONE && !preact))
+        return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    if (M == 0) return CM_OK;
+    CM_TRY(check_matrix(dy, lddy, n));
+    CM_TRY(check_matrix(w, ldw, wlayout == CM_W_NK ? K : n));
+    CM_TRY(check_matrix(dx, lddx, K));
+    if (residual) CM_TRY(check_matrix(residual, ldr, K));
+    if (act != CM_ACT_NONE) CM_TRY(check_matrix(preact, ldz, K));
+    Device d;
+    CM_TRY(device(&d));
+    LinearEpilogue e = {};
+    e.y = dx;
+    e.ldy = lddx;
+    e.y_f32 = dx_dtype == CM_F32;
+    e.act = act;
+    e.dact = act != CM_ACT_NONE;
+    e.zin = preact;
+    e.ldzin = ldz;
+    e.res = residual;
+    e.ldr = ldr;
+    // W stored [n][K]: its K columns are contiguous, the contracted n is not
+    return product(d, {w, ldw, wlayout == CM_W_NK}, {dy, lddy, false}, M, K, n, e, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t cm_linear_wgrad_workspace_size(int64_t M, int64_t K, int64_t n) {
+    if (check_extents(M, K, n) != CM_OK) return 0;
+    return wgrad_workspace(M, n);
+}
+
+cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t lddy, void *dw, cm_dtype dw_dtype,
+                          int64_t lddw, cm_wlayout wlayout, void *db, cm_dtype db_dtype, int accumulate, int64_t M,
+                          int64_t K, int64_t n, void *ws, size_t ws_bytes, cm_stream_t stream_) {
+    NvtxRange range("cm_linear_wgrad");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (bad_dtype(dw_dtype) || (db && bad_dtype(db_dtype)) || (wlayout != CM_W_KN && wlayout != CM_W_NK))
+        return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    const bool nk = wlayout == CM_W_NK;
+    CM_TRY(check_matrix(dw, lddw, nk ? K : n));
+    if (M > 0) {
+        CM_TRY(check_matrix(x, ldx, K));
+        CM_TRY(check_matrix(dy, lddy, n));
+    }
+    if (db && (!ws || ws_bytes < wgrad_workspace(M, n))) return CM_ERR_WORKSPACE;
+    if (db && !aligned16(ws)) return CM_ERR_ALIGNMENT;
+    Device d;
+    CM_TRY(device(&d));
+    if (M == 0) {   // the sum over no rows
+        if (accumulate) return CM_OK;
+        const size_t es = dw_dtype == CM_F32 ? 4 : 2;
+        if (cudaMemset2DAsync(dw, size_t(lddw) * es, 0, size_t(nk ? K : n) * es, size_t(nk ? n : K), stream) !=
+            cudaSuccess)
+            return CM_ERR_CUDA;
+        if (db && cudaMemsetAsync(db, 0, size_t(n) * (db_dtype == CM_F32 ? 4 : 2), stream) != cudaSuccess)
+            return CM_ERR_CUDA;
+        return CM_OK;
+    }
+    if (db && launch_colsum(dy, lddy, M, n, static_cast<float *>(ws), db, db_dtype == CM_F32, accumulate != 0,
+                            stream) != cudaSuccess)
+        return CM_ERR_CUDA;
+    LinearEpilogue e = {};
+    e.y = dw;
+    e.ldy = lddw;
+    e.y_f32 = dw_dtype == CM_F32;
+    e.accumulate = accumulate != 0;
+    const Operand ox = {x, ldx, true}, ody = {dy, lddy, true};
+    return nk ? product(d, ox, ody, n, K, M, e, stream) : product(d, ody, ox, K, n, M, e, stream);
+}
+
+cm_status cm_linear_check_status(cm_stream_t stream_, int32_t info[4]) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    Device d;
+    CM_TRY(device(&d));
+    LinearStatus s = {};
+    if (cudaMemcpyAsync(&s, d.status, sizeof(s), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return CM_ERR_CUDA;
+    if (s.w[0] != 0 && (cudaMemsetAsync(d.status, 0, sizeof(s), stream) != cudaSuccess ||
+                        cudaStreamSynchronize(stream) != cudaSuccess))
+        return CM_ERR_CUDA;
+    if (info)
+        for (int i = 0; i < 4; ++i) info[i] = int32_t(s.w[i]);
+    return static_cast<cm_status>(s.w[0]);
+}
+
+}  // extern "C"

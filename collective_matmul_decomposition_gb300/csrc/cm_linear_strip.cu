@@ -1,0 +1,314 @@
+// cm_linear_strip.cu -- the linear layer's kernel for few rows (tokens).
+//
+// D[row][col] = sum_k B[row][k] A[col][k], with the weights' columns on the
+// tensor core's 128-row side and 16 to 256 tokens on its column side: a call
+// with one token wastes 15 of 16 accumulator columns but none of the weights'
+// bandwidth, which bounds it (K*n*2 bytes are read for 2*K*n flops a token).
+// One CTA computes one tile.  Where there are fewer tiles than SMs, the K
+// slices of a tile are split over a cluster of up to eight CTAs: each leaves
+// its fp32 partial tile in its own shared memory, and the cluster's CTAs add
+// them in rank order, each for its share of the tokens, so one launch does it,
+// nothing passes through global memory, and the result does not depend on timing.
+//
+// Roles (128 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the
+// MMAs; then all four warps run the epilogue (a thread owns one column, so a
+// warp's loads and stores are 32 neighbouring elements of one row).  Two CTAs
+// fit on an SM: one's epilogue runs under the other's loads.
+//
+// Every wait is bounded by p.timeout_ns; on expiry the first failing thread
+// records {code, tile, CTA, site}, and the CTA drains its loads, frees its
+// tensor memory and returns.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "cm_device.cuh"
+#include "cm_kernel.cuh"
+#include "cm_linear.cuh"
+#include "cm_linear_epilogue.cuh"
+
+namespace cm {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreadsL = 128;
+constexpr int kTileCols = 128;
+constexpr int kStripA = kTileCols * kBK * 2;   // 16 KB of the column operand per slice
+constexpr int kStripRing = 108 * 1024;         // two CTAs per SM
+constexpr int kStripMaxStages = 8;
+constexpr int kStripSmem = kStripRing + 1024 /*align*/ + 256 /*barriers*/;
+
+struct StripSmem {
+    uint8_t *ring;
+    uint64_t *full, *empty, *acc, *drain;
+    uint32_t *tmem_slot;
+    volatile int *abort;
+};
+
+__device__ __noinline__ void report_linear(LinearStatus *s, uint32_t site, uint32_t tile) {
+    if (atomicCAS(&s->w[0], 0u, uint32_t(CM_ERR_TIMEOUT)) == 0u) {
+        s->w[1] = tile;
+        s->w[2] = blockIdx.x;
+        s->w[3] = site;
+        __threadfence();
+    }
+}
+
+__device__ bool wait_l(const LinearStripParams &p, const StripSmem &s, uint64_t *bar, uint32_t parity, uint32_t site) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*s.abort) return false;
+            if (globaltimer() - t0 > p.timeout_ns) {
+                report_linear(p.status, site, blockIdx.x);
+                *s.abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ void drain_l(const LinearStripParams &p, uint64_t *bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > p.timeout_ns) break;
+}
+
+// Sum over the cluster's partial tiles of one element, in rank order.
+__device__ __forceinline__ float cluster_sum(uint32_t addr, int splits) {
+    float f[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        f[r] = 0.0f;
+        if (r < splits)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[r]) : "r"(mapa_shared(addr, uint32_t(r))) : "memory");
+    }
+    float v = f[0];
+#pragma unroll
+    for (int r = 1; r < 8; ++r)
+        if (r < splits) v += f[r];
+    return v;
+}
+
+__device__ __forceinline__ void finish(const LinearEpilogue &e, float v, float bias, int64_t row, int64_t col) {
+    v += bias;
+    if (e.z) static_cast<__nv_bfloat16 *>(e.z)[row * e.ldz + col] = __float2bfloat16_rn(v);
+    if (e.dact)
+        v *= lin::dact1(__bfloat162float(static_cast<const __nv_bfloat16 *>(e.zin)[row * e.ldzin + col]), e.act);
+    else
+        v = lin::act1(v, e.act);
+    if (e.res) v += __bfloat162float(static_cast<const __nv_bfloat16 *>(e.res)[row * e.ldr + col]);
+    if (e.y_f32) {
+        float *y = static_cast<float *>(e.y) + row * e.ldy + col;
+        *y = e.accumulate ? *y + v : v;
+    } else {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(e.y) + row * e.ldy + col;
+        *y = __float2bfloat16_rn(e.accumulate ? __bfloat162float(*y) + v : v);
+    }
+}
+
+template <int LAYOUT>
+__global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid_constant__ LinearStripParams p) {
+    constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
+    extern __shared__ uint8_t smem_raw[];
+    StripSmem s;
+    s.ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    s.full = reinterpret_cast<uint64_t *>(s.ring + kStripRing);
+    s.empty = s.full + kStripMaxStages;
+    s.acc = s.empty + kStripMaxStages;
+    s.drain = s.acc + 1;
+    s.tmem_slot = reinterpret_cast<uint32_t *>(s.drain + 1);
+    s.abort = reinterpret_cast<volatile int *>(s.tmem_slot + 1);
+
+    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const uint32_t tmem_cols = uint32_t(p.tok < 32 ? 32 : p.tok);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        mbar_init(s.acc, 1);
+        mbar_init(s.drain, 1);
+        *s.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.tmA);
+        prefetch_tmap(&p.tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(s.tmem_slot, tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s.tmem_slot;
+
+    const int split = p.splits > 1 ? int(cluster_ctarank()) : 0;
+    const int tile = int(blockIdx.x) / p.splits;
+    const int ct = tile / p.row_tiles, rt = tile - ct * p.row_tiles;
+    const int col0 = ct * kTileCols, row0 = rt * p.tok;
+    const int kb0 = int(int64_t(p.kblocks) * split / p.splits), kb1 = int(int64_t(p.kblocks) * (split + 1) / p.splits);
+    const uint32_t stage_bytes = uint32_t(kStripA + p.tok * kBK * 2);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_l(p, s, &s.empty[stage], phase ^ 1u, kLinSiteEmpty)) break;
+                uint8_t *sa = s.ring + uint32_t(stage) * stage_bytes, *sb = sa + kStripA;
+                mbar_expect_tx(&s.full[stage], stage_bytes);
+                if (A_MN) {
+                    for (int j = 0; j < kTileCols / 64; ++j)
+                        tma_load_3d(sa + j * (64 * kBK * 2), &p.tmA, &s.full[stage], col0 + 64 * j, kb * kBK, 0);
+                } else {
+                    tma_load_3d(sa, &p.tmA, &s.full[stage], kb * kBK, col0, 0);
+                }
+                if (B_MN) {
+                    for (int j = 0; j < p.tok / 64; ++j)
+                        tma_load_3d(sb + j * (64 * kBK * 2), &p.tmB, &s.full[stage], row0 + 64 * j, kb * kBK, 0);
+                } else {
+                    tma_load_3d(sb, &p.tmB, &s.full[stage], kb * kBK, row0, 0);
+                }
+                ++issued;
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            // only an aborting CTA can get here with a load whose slice nobody
+            // waits for: no load may still write this shared memory at exit
+            if (*s.abort)
+                for (int i = 0; i < p.stages && i < issued; ++i)
+                    drain_l(p, &s.full[i], i < stage ? phase : phase ^ 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(kTileCols, p.tok, B_MN, A_MN);
+            constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kBLbo = B_MN ? 64 * kBK * 2 : 16;
+            constexpr uint32_t kAStep = A_MN ? (16 * 128) >> 4 : 32 >> 4, kBStep = B_MN ? (16 * 128) >> 4 : 32 >> 4;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_l(p, s, &s.full[stage], phase, kLinSiteFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_u32(s.ring) + uint32_t(stage) * stage_bytes;
+                const uint64_t ad = desc_sw128(sa, kALbo, 1024), bd = desc_sw128(sa + kStripA, kBLbo, 1024);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_bf16(tmem, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc, kb > kb0 || k ? 1u : 0u);
+                mma_commit(&s.empty[stage]);
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok) mma_commit(s.acc);
+            mma_commit(s.drain);
+            drain_l(p, s.drain, 0);   // every MMA is done before the tensor memory is freed
+        }
+        __syncwarp();
+    }
+    const bool good = wait_l(p, s, s.acc, 0, kLinSiteAcc);
+    __syncwarp();
+    tc_fence_after();
+    const int nrows = int(min(int64_t(p.tok), p.rows - row0));
+    const int64_t col = int64_t(col0) + threadIdx.x;
+    const uint32_t taddr = tmem + (uint32_t(warp * 32) << 16);
+    const float bias = col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
+    if (p.splits == 1) {
+        for (int t0 = 0; t0 < nrows; t0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(taddr + uint32_t(t0), v);
+            tmem_wait_ld();
+            if (good && col < p.cols) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (t0 + i < nrows) finish(p.e, __uint_as_float(v[i]), bias, int64_t(row0) + t0 + i, col);
+            }
+        }
+    } else {
+        // all loads of the ring have landed and been multiplied: it now holds
+        // the partial tile, [token][128]
+        float *part = reinterpret_cast<float *>(s.ring);
+        for (int t0 = 0; t0 < nrows; t0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(taddr + uint32_t(t0), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (t0 + i < nrows) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
+        }
+        if (!good) *s.abort = 1;
+        cluster_sync();
+        if (col < p.cols && good)
+            for (int t = split; t < nrows; t += p.splits)
+                finish(p.e, cluster_sum(smem_u32(part + t * kTileCols + int(threadIdx.x)), p.splits), bias,
+                       int64_t(row0) + t, col);
+        cluster_sync();   // the peers have read this CTA's partial tile
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, tmem_cols);
+    }
+}
+
+}  // namespace
+
+int linear_strip_stages(int tok, int splits) {
+    const int stage = kStripA + tok * kBK * 2;
+    (void)splits;
+    return std::min(kStripMaxStages, kStripRing / stage);
+}
+
+cudaError_t prepare_linear_strip(int device) {
+    static bool done[64] = {false};
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    if (!done[device]) {
+        void (*fns[3])(LinearStripParams) = {cm_linear_strip_kernel<0>, cm_linear_strip_kernel<2>,
+                                             cm_linear_strip_kernel<3>};
+        for (auto fn : fns) {
+            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripSmem);
+            if (e != cudaSuccess) return e;
+        }
+        done[device] = true;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream) {
+    const int64_t col_tiles = (p.cols + kTileCols - 1) / kTileCols;
+    const int64_t grid = col_tiles * p.row_tiles * p.splits;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(kThreadsL, 1, 1);
+    cfg.dynamicSmemBytes = kStripSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(p.splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (layout) {
+        case 0: return cudaLaunchKernelEx(&cfg, cm_linear_strip_kernel<0>, p);
+        case 2: return cudaLaunchKernelEx(&cfg, cm_linear_strip_kernel<2>, p);
+        case 3: return cudaLaunchKernelEx(&cfg, cm_linear_strip_kernel<3>, p);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace cm

@@ -575,6 +575,156 @@ cm_status cm_ag_gemm_noalloc(cm_plan_t plan, const void *x, const void *w, cm_wl
  */
 cm_status cm_ag_gemm_noalloc_check_status(cm_stream_t stream, int32_t info[4]);
 
+/*
+ * The linear layer on one rank: what stands around the collective products in
+ * a transformer's MLP and projections.  One matrix product whose epilogue adds
+ * the bias, applies the activation and adds the residual, and its gradients.
+ *
+ * Matrices are row-major with a row stride (ld*) in elements; operands are
+ * bf16, products and sums fp32, and each output element is rounded once.  A
+ * weight is stored [n][K] (CM_W_NK) or [K][n] (CM_W_KN).  Row strides must be
+ * multiples of 8 elements and matrices 16-byte aligned (the tensor-map rule);
+ * extents may be any positive number, and M may be 0 (nothing to do).
+ * Outputs must not alias inputs.
+ *
+ *  CM_ACT_RELU max(v, 0);  CM_ACT_GELU v (1 + erf(v / sqrt 2)) / 2;
+ *  CM_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2;
+ *  CM_ACT_SILU v / (1 + exp(-v)).
+ */
+typedef enum cm_act {
+    CM_ACT_NONE = 0,
+    CM_ACT_RELU = 1,
+    CM_ACT_GELU = 2,
+    CM_ACT_GELU_TANH = 3,
+    CM_ACT_SILU = 4
+} cm_act;
+
+/*
+ * cm_linear -- z = x W^T + bias;  y = act(z) + residual.
+ *  x [M][K] bf16; w as `wlayout` says; y [M][n] (y_dtype).
+ *  bias [n] (bias_dtype), residual [M][n] bf16 and preact [M][n] bf16 may be
+ *  NULL; preact receives z (rounded to bf16), which cm_linear_dgrad wants.
+ *  Asynchronous on `stream`; no workspace and no allocation.
+ *  Errors (synchronous, nothing enqueued): CM_ERR_INVALID_ARG for a null
+ *  pointer or a bad enum; CM_ERR_SHAPE if M < 0, K or n is not positive, one
+ *  exceeds 2^30, or a row stride is smaller than the row; CM_ERR_ALIGNMENT
+ *  if a row stride or pointer is misaligned; CM_ERR_UNSUPPORTED on another
+ *  device; CM_ERR_CUDA if a launch or tensor-map encoding fails.  Device-side
+ *  waits that expire come from cm_linear_check_status.
+ */
+cm_status cm_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout,
+                    const void *bias, cm_dtype bias_dtype, cm_act act, const void *residual, int64_t ldr,
+                    void *preact, int64_t ldz, void *y, cm_dtype y_dtype, int64_t ldy,
+                    int64_t M, int64_t K, int64_t n, cm_stream_t stream);
+
+/*
+ * cm_linear_dgrad -- dx = (dy W) * act'(preact) + residual.
+ *  dy [M][n] bf16, w as in the forward call, dx [M][K] (dx_dtype).  `act` and
+ *  preact [M][K] bf16 are those of the layer in front, whose output was this
+ *  layer's x: the result is then the gradient of that layer's product.
+ *  preact may be NULL for CM_ACT_NONE.  residual [M][K] bf16 (or NULL) is a
+ *  gradient that reaches x by another way.  Errors as cm_linear.
+ */
+cm_status cm_linear_dgrad(const void *dy, int64_t lddy, const void *w, int64_t ldw, cm_wlayout wlayout,
+                          const void *preact, int64_t ldz, cm_act act, const void *residual, int64_t ldr,
+                          void *dx, cm_dtype dx_dtype, int64_t lddx, int64_t M, int64_t K, int64_t n,
+                          cm_stream_t stream);
+
+/*
+ * cm_linear_wgrad -- dw = dy^T x (laid out as the weight is, `wlayout`) and,
+ * if db is not NULL, db = the sum of dy's rows; with `accumulate` both are
+ * added to what is there.  x [M][K], dy [M][n] bf16; dw (dw_dtype); db [n]
+ * (db_dtype).  ws: cm_linear_wgrad_workspace_size(M, K, n) bytes, 16-byte
+ * aligned, needed with db only; its contents need no initialisation, and
+ * calls that share it must be ordered on the GPU.  M = 0 gives zeros.
+ * Results do not depend on timing.  Errors as cm_linear, and CM_ERR_WORKSPACE.
+ */
+size_t cm_linear_wgrad_workspace_size(int64_t M, int64_t K, int64_t n);
+cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t lddy, void *dw, cm_dtype dw_dtype,
+                          int64_t lddw, cm_wlayout wlayout, void *db, cm_dtype db_dtype, int accumulate,
+                          int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes, cm_stream_t stream);
+
+/*
+ * cm_linear_check_status -- synchronise `stream` and read the status word of
+ * the linear kernels on the current device: CM_OK, or CM_ERR_TIMEOUT if a
+ * bounded device-side wait has expired in some call since the word was last
+ * read (that call's outputs are undefined); reading it clears it.  info, if
+ * not NULL, receives {code, tile, CTA, site}.
+ */
+cm_status cm_linear_check_status(cm_stream_t stream, int32_t info[4]);
+
+/*
+ * cm_layer_norm -- y = (x - mean) rstd gamma + beta for each of `rows` rows of
+ * h elements; mean and variance of the row in fp32, rstd = 1/sqrt(var + eps).
+ *  x (x_dtype), y (y_dtype) with row strides; gamma, beta [h] (param_dtype),
+ *  NULL for 1 and 0; mean, rstd [rows] fp32, NULL or written for the backward
+ *  pass.  Any extent, stride and element-aligned address; rows of at most
+ *  32768 elements with 16-byte aligned starts are read once.  y may be x.
+ *  Errors: as cm_linear (eps must not be negative or NaN; rows may be 0).
+ */
+cm_status cm_layer_norm(const void *x, cm_dtype x_dtype, int64_t ldx, const void *gamma, const void *beta,
+                        cm_dtype param_dtype, float eps, void *y, cm_dtype y_dtype, int64_t ldy, float *mean,
+                        float *rstd, int64_t rows, int64_t h, cm_stream_t stream);
+
+/*
+ * cm_layer_norm_backward -- with xh = (x - mean) rstd and t = dy gamma:
+ *   dx = rstd (t - mean_row(t) - xh mean_row(t xh)) + residual
+ *   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+ *  x, residual (NULL or a gradient that reaches x by another way) and dx have
+ *  x_dtype; dy dy_dtype; mean, rstd as the forward call wrote them.  dgamma
+ *  and dbeta [h] (grad_dtype) may be NULL; with `accumulate` they are added
+ *  to.  ws: cm_layer_norm_backward_workspace_size(rows, h) bytes, 16-byte
+ *  aligned, needed with dgamma or dbeta.  Results do not depend on timing.
+ *  dx must not alias x, dy or residual.
+ */
+size_t cm_layer_norm_backward_workspace_size(int64_t rows, int64_t h);
+cm_status cm_layer_norm_backward(const void *x, cm_dtype x_dtype, int64_t ldx, const void *dy, cm_dtype dy_dtype,
+                                 int64_t lddy, const void *gamma, cm_dtype param_dtype, const float *mean,
+                                 const float *rstd, const void *residual, int64_t ldr, void *dx, int64_t lddx,
+                                 void *dgamma, void *dbeta, cm_dtype grad_dtype, int accumulate, int64_t rows,
+                                 int64_t h, void *ws, size_t ws_bytes, cm_stream_t stream);
+
+/*
+ * cm_adamw -- one AdamW step over `count` tensors:
+ *   g = grad_scale * grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr weight_decay) - lr/(1 - b1^step) m / (sqrt(v/(1 - b2^step)) + eps)
+ * in fp32.  p is `master` where it is not NULL (param then receives its
+ * rounding), else `param`.  state_bits 32: exp_avg and exp_avg_sq are fp32 m
+ * and v.  state_bits 8: exp_avg holds e4m3 codes of m and exp_avg_sq of
+ * sqrt(v), one byte an element, with one fp32 scale per CM_ADAMW_BLOCK
+ * elements of the tensor (ceil(numel / CM_ADAMW_BLOCK) of each): value = code
+ * times scale, scale = largest finite magnitude of the block / 448.  All-zero
+ * codes and scales are the zero state.
+ *  tensors: host array, read during the call.  grad_scale: device pointer or
+ *  NULL (1).  step counts from 1.  Any element-aligned address; 16-byte
+ *  aligned ones (8-byte for codes) go in whole vectors.  Tensors must not
+ *  overlap.  One launch per 360 tensors, no workspace.
+ *  seed: 0 rounds the 8-bit states to the nearest code, which leaves a slow
+ *  average (beta2 near 1) where it was unless a step moves it by half a code;
+ *  another value (a new one each step) rounds each up or down at random so
+ *  that its mean is kept, the same way for the same seed, list and element.
+ *  Errors: CM_ERR_INVALID_ARG (null or out-of-range argument, bad enum),
+ *  CM_ERR_SHAPE (numel < 0 or beyond 2^42), CM_ERR_ALIGNMENT, CM_ERR_CUDA.
+ *  Tensors are all checked before anything is enqueued.
+ */
+#define CM_ADAMW_BLOCK 256
+typedef struct cm_adamw_tensor {
+    void *param;
+    const void *grad;
+    float *master;
+    void *exp_avg;
+    void *exp_avg_sq;
+    float *exp_avg_scale;
+    float *exp_avg_sq_scale;
+    int64_t numel;
+    float weight_decay;
+    int32_t param_dtype;   /* cm_dtype */
+    int32_t grad_dtype;    /* cm_dtype */
+    int32_t state_bits;    /* 32 or 8 */
+} cm_adamw_tensor;
+cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double lr, double beta1, double beta2, double eps,
+                   int64_t step, const float *grad_scale, uint64_t seed, cm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
