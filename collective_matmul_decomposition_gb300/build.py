@@ -19,7 +19,7 @@ LIB_DEBUG = os.path.join(BUILD_DEBUG, "libcm_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["cm_kernel.cu", "cm_kernel_pair.cu", "cm_api.cu", "cm_plan.cpp", "cm_noalloc.cu", "cm_cost.cpp", "cm_reduce.cu",
-           "cm_linear_strip.cu", "cm_linear_api.cu", "cm_norm.cu", "cm_norm_api.cu", "cm_adamw.cu"]
+           "cm_linear_strip.cu", "cm_linear_pair.cu", "cm_linear_api.cu", "cm_norm.cu", "cm_norm_api.cu", "cm_adamw.cu"]
 HEADERS = ["cm_internal.h", "cm_kernel.cuh", "cm_device.cuh", "cm_kernel_common.cuh",
            "cm_linear.cuh", "cm_linear_epilogue.cuh", "cm_norm.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

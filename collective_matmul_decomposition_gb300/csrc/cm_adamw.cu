@@ -189,7 +189,7 @@ __device__ __forceinline__ void put_codes(uint8_t *p, float *scale, const Span &
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const bool live = amax >= kTiny;
-    const float inv = live ? kE4m3Max / amax : 0.0f;
+    const float inv = live ? __fmul_rn(1.0f / amax, kE4m3Max) : 0.0f;
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -207,7 +207,7 @@ __device__ __forceinline__ void put_codes(uint8_t *p, float *scale, const Span &
         for (int i = 0; i < 8; ++i)
             if (i < s.n) p[s.i0 + i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
     }
-    if ((threadIdx.x & 31) == 0 && s.n > 0) *scale = live ? amax / kE4m3Max : 0.0f;
+    if ((threadIdx.x & 31) == 0 && s.n > 0) *scale = live ? amax * (1.0f / kE4m3Max) : 0.0f;
 }
 
 template <int CAP>
@@ -250,8 +250,10 @@ __global__ void __launch_bounds__(kAdamThreads) cm_adamw_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float gi = g[i] * scale;
-        m[i] = t.b1 * m[i] + t.c1 * gi;
-        v[i] = t.b2 * v[i] + t.c2 * gi * gi;
+        // rounded one by one, not contracted: a code must not depend on how
+        // the compiler groups a sum that lies on the border between two
+        m[i] = __fadd_rn(__fmul_rn(t.b1, m[i]), __fmul_rn(t.c1, gi));
+        v[i] = __fadd_rn(__fmul_rn(t.b2, v[i]), __fmul_rn(__fmul_rn(t.c2, gi), gi));
         root[i] = sqrtf(v[i]);
         p[i] = p[i] * e.keep - t.step * m[i] / (root[i] * t.root_scale + t.eps);
     }

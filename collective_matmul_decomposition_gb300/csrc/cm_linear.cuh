@@ -63,6 +63,25 @@ cudaError_t prepare_linear_strip(int device);
 cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream);
 int linear_strip_stages(int tok, int splits);
 
+// Tiles of 256 x 256 on CTA pairs, for calls with many of them.  A is the row
+// operand here, B the column operand.
+struct LinearPairParams {
+    CUtensorMap tmA, tmB;
+    CUtensorMap tmY;          // bf16: 64 x 32 boxes, fp32: 32 x 32
+    CUtensorMap tmZ;          // pre-activation kept (bf16 y only), 64 x 32
+    CUtensorMap tmIn0, tmIn1; // residual (or y, to be added to) and pre-activation read; bf16 y only
+    LinearEpilogue e;
+    int64_t rows, cols;
+    int kblocks, mtiles, ntiles, tiles;
+    int band;                 // row tiles that run through all columns together
+    LinearStatus *status;
+    uint64_t timeout_ns;
+};
+
+// layout: bit 0 = B MN-major, bit 1 = A MN-major.
+cudaError_t prepare_linear_pair(int device, int sms, int *max_clusters);
+cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int clusters, cudaStream_t stream);
+
 // Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu): partial
 // sums per row chunk in `partial`, then their sum in chunk order.
 int64_t colsum_chunks(int64_t rows, int64_t cols);

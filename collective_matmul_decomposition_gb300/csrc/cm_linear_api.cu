@@ -37,16 +37,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Row-major bf16 [rows][cols] with row stride ld, in 64 x box_rows boxes,
-// 128-byte swizzle; elements outside are read as zeros.
-bool map_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+// Row-major bf16 (or fp32) [rows][cols] with row stride ld, in boxes of 128
+// bytes x box_rows, 128-byte swizzle; elements outside are read as zeros and
+// not written.
+bool map_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f32 = false) {
     auto enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), 1};
-    cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(ld) * 2 * cuuint64_t(rows)};
-    cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
+    const cuuint64_t row_bytes = cuuint64_t(ld) * (f32 ? 4 : 2);
+    // the third extent is 1: its stride is never used and only has to be valid
+    cuuint64_t strides[2] = {row_bytes, row_bytes};
+    cuuint32_t box[3] = {f32 ? 32u : 64u, cuuint32_t(box_rows), 1};
     cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -67,7 +70,7 @@ cm_status check_extents(int64_t M, int64_t K, int64_t n) {
 }
 
 struct Device {
-    int id = 0, sms = 0;
+    int id = 0, sms = 0, clusters = 0;
     LinearStatus *status = nullptr;
 };
 
@@ -86,6 +89,8 @@ cm_status device(Device *d) {
             return CM_ERR_CUDA;
         if (major != 10 || minor != 3) return CM_ERR_UNSUPPORTED;
         if (prepare_linear_strip(d->id) != cudaSuccess) return CM_ERR_CUDA;
+        if (prepare_linear_pair(d->id, c.sms, &c.clusters) != cudaSuccess) return CM_ERR_CUDA;
+        if (c.clusters < 1) return CM_ERR_UNSUPPORTED;
         void *sp = nullptr;
         if (cudaGetSymbolAddress(&sp, g_linear_status) != cudaSuccess) return CM_ERR_CUDA;
         c.status = static_cast<LinearStatus *>(sp);
@@ -107,9 +112,39 @@ bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t k, int 
     return o.mn_major ? map_rows(m, o.p, k, rows, o.ld, 64) : map_rows(m, o.p, rows, k, o.ld, tile_rows);
 }
 
+constexpr int64_t kBandBytes = int64_t(32) << 20;   // of the row operand, kept in L2 while a band runs
+
+cm_status product_pair(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
+                       const LinearEpilogue &e, cudaStream_t stream) {
+    LinearPairParams p;
+    p.e = e;
+    p.rows = rows;
+    p.cols = cols;
+    p.kblocks = int((k + kBK - 1) / kBK);
+    p.mtiles = int((rows + 255) / 256);
+    p.ntiles = int((cols + 255) / 256);
+    if (int64_t(p.mtiles) * p.ntiles > 0x7fffffff) return CM_ERR_SHAPE;
+    p.tiles = p.mtiles * p.ntiles;
+    p.band = int(std::max<int64_t>(1, std::min<int64_t>(p.mtiles, kBandBytes / (int64_t(p.kblocks) * 256 * kBK * 2))));
+    p.status = d.status;
+    p.timeout_ns = kLinearTimeoutNs;
+    if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, 128) ||
+        !map_rows(&p.tmY, e.y, rows, cols, e.ldy, 32, e.y_f32 != 0))
+        return CM_ERR_CUDA;
+    if (!e.y_f32) {
+        if (e.z && !map_rows(&p.tmZ, e.z, rows, cols, e.ldz, 32)) return CM_ERR_CUDA;
+        if (e.accumulate) p.tmIn0 = p.tmY;
+        if (e.res && !map_rows(&p.tmIn0, e.res, rows, cols, e.ldr, 32)) return CM_ERR_CUDA;
+        if (e.dact && !map_rows(&p.tmIn1, e.zin, rows, cols, e.ldzin, 32)) return CM_ERR_CUDA;
+    }
+    const int layout = (a.mn_major ? 1 : 0) | (b.mn_major ? 2 : 0);
+    return launch_linear_pair(p, layout, d.clusters, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+}
+
 // D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
                   const LinearEpilogue &e, cudaStream_t stream) {
+    if (((rows + 255) / 256) * ((cols + 255) / 256) >= d.clusters) return product_pair(d, a, b, rows, cols, k, e, stream);
     LinearStripParams p;
     p.e = e;
     p.rows = rows;

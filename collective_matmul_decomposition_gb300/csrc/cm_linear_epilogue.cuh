@@ -51,6 +51,50 @@ __device__ __forceinline__ float dact1(float z, int act) {
     }
 }
 
+// The same over a slice, the choice outside the loop.
+__device__ __forceinline__ void apply_act(float (&f)[32], int act) {
+    switch (act) {
+        case CM_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_RELU);
+            break;
+        case CM_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_GELU);
+            break;
+        case CM_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_GELU_TANH);
+            break;
+        case CM_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_SILU);
+            break;
+        default: break;
+    }
+}
+__device__ __forceinline__ void mul_dact(float (&f)[32], const float (&z)[32], int act) {
+    switch (act) {
+        case CM_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_RELU);
+            break;
+        case CM_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_GELU);
+            break;
+        case CM_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_GELU_TANH);
+            break;
+        case CM_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_SILU);
+            break;
+        default: break;
+    }
+}
+
 __device__ __forceinline__ float load_bias(const LinearEpilogue &e, int64_t c) {
     if (!e.bias) return 0.0f;
     return e.bias_f32 ? static_cast<const float *>(e.bias)[c]
