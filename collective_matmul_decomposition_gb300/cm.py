@@ -385,81 +385,109 @@ def plan_choose_einsum(n_ranks, m, K, n, rates, max_chunks=CM_MAX_CHUNKS):
     return name, c.value, {v: k for k, v in DIRECTIONS.items()}[d.value], us.value
 
 
-def _matrix(name, t, rows=None, cols=None, dtype=None):
-    """A 2-D CUDA tensor with contiguous rows: (pointer, row stride)."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    r, c = t.shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    if dtype is not None and t.dtype != dtype:
+# torch's names that the calls below use, bound by _bind_torch at the first of them
+_torch = _b16 = _f32 = _raw_stream = None
+
+
+def _bind_torch():
+    global _torch, _b16, _f32, _raw_stream
+    import torch
+    _b16, _f32, _raw_stream = torch.bfloat16, torch.float32, torch._C._cuda_getCurrentRawStream
+    _torch = torch
+
+
+def _library():
+    if _torch is None:
+        _bind_torch()
+    return _lib or load()
+
+
+def _stream_of(stream, device: int) -> int:
+    return stream.cuda_stream if stream is not None else _raw_stream(device)
+
+
+def _matrix(name, t, shape, device, dtype=None):
+    """A 2-D tensor of that shape on that device, its rows contiguous: (pointer, row stride)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected CUDA device {device}")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     ld, inner = t.stride()
-    if c > 1 and inner != 1:
+    r, c = shape
+    if inner != 1 and c > 1:
         raise ValueError(f"{name}: rows must be contiguous")
     # a single row has no stride of its own: the smallest multiple of 8 that holds it
     return t.data_ptr(), ld if r > 1 else -(-c // 8) * 8
 
 
-def _vector(name, t, n, dtype=None):
+def _vector(name, t, n, device, dtype=None):
     if t is None:
         return None
-    if t.dim() != 1 or not t.is_cuda or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous CUDA vector of {n} elements")
-    if dtype is not None and t.dtype != dtype:
+    if t.dim() != 1 or t.shape[0] != n or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements on CUDA device {device}")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     return t.data_ptr()
 
 
 def _dtype_of(name, t):
-    import torch
-    if t is None or t.dtype == torch.bfloat16:
+    if t is None or t.dtype is _b16:
         return CM_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is _f32:
         return CM_F32
     raise TypeError(f"{name} must be bf16 or fp32, not {t.dtype}")
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+def _extents(name, t):
+    """(rows, columns, device) of the 2-D CUDA tensor that a call's other shapes follow from."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    r, c = t.shape
+    return r, c, t.get_device()
+
+
+def _workspace(ws, device):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on CUDA device {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def cm_linear(x, w, y, bias=None, act: str = "none", residual=None, preact=None, w_layout: str = "nk", stream=None):
     """y [M][n] = act(x @ W^T + bias) + residual; preact receives x @ W^T + bias (bf16)."""
-    import torch
-    b16 = torch.bfloat16
-    M, K = x.shape
-    n = y.shape[1]
-    _same_device(x, w, y, bias, residual, preact)
-    wr, wc = (n, K) if w_layout == "nk" else (K, n)
-    xp, ldx = _matrix("x", x, M, K, b16)
-    wp, ldw = _matrix("w", w, wr, wc, b16)
-    yp, ldy = _matrix("y", y, M, n)
-    rp, ldr = _matrix("residual", residual, M, n, b16) if residual is not None else (None, 0)
-    zp, ldz = _matrix("preact", preact, M, n, b16) if preact is not None else (None, 0)
-    st = load().cm_linear(xp, ldx, wp, ldw, LAYOUTS[w_layout], _vector("bias", bias, n), _dtype_of("bias", bias),
-                          ACTS[act], rp, ldr, zp, ldz, yp, _dtype_of("y", y), ldy, M, K, n, _stream_ptr(stream))
-    _check(st, "cm_linear")
+    lib = _library()
+    M, K, dev = _extents("x", x)
+    n = _extents("y", y)[1]
+    layout = LAYOUTS[w_layout]
+    xp, ldx = _matrix("x", x, (M, K), dev, _b16)
+    wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
+    yp, ldy = _matrix("y", y, (M, n), dev)
+    rp, ldr = _matrix("residual", residual, (M, n), dev, _b16) if residual is not None else (None, 0)
+    zp, ldz = _matrix("preact", preact, (M, n), dev, _b16) if preact is not None else (None, 0)
+    st = lib.cm_linear(xp, ldx, wp, ldw, layout, _vector("bias", bias, n, dev), _dtype_of("bias", bias), ACTS[act],
+                       rp, ldr, zp, ldz, yp, _dtype_of("y", y), ldy, M, K, n, _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear")
 
 
 def cm_linear_dgrad(dy, w, dx, preact=None, act: str = "none", residual=None, w_layout: str = "nk", stream=None):
     """dx [M][K] = (dy @ W) * act'(preact) + residual; act and preact are those of the layer in front."""
-    import torch
-    b16 = torch.bfloat16
-    M, n = dy.shape
-    K = dx.shape[1]
-    _same_device(dy, w, dx, preact, residual)
-    wr, wc = (n, K) if w_layout == "nk" else (K, n)
-    dyp, lddy = _matrix("dy", dy, M, n, b16)
-    wp, ldw = _matrix("w", w, wr, wc, b16)
-    dxp, lddx = _matrix("dx", dx, M, K)
-    rp, ldr = _matrix("residual", residual, M, K, b16) if residual is not None else (None, 0)
-    zp, ldz = _matrix("preact", preact, M, K, b16) if preact is not None else (None, 0)
-    st = load().cm_linear_dgrad(dyp, lddy, wp, ldw, LAYOUTS[w_layout], zp, ldz, ACTS[act], rp, ldr, dxp,
-                                _dtype_of("dx", dx), lddx, M, K, n, _stream_ptr(stream))
-    _check(st, "cm_linear_dgrad")
+    lib = _library()
+    M, n, dev = _extents("dy", dy)
+    K = _extents("dx", dx)[1]
+    layout = LAYOUTS[w_layout]
+    dyp, lddy = _matrix("dy", dy, (M, n), dev, _b16)
+    wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
+    dxp, lddx = _matrix("dx", dx, (M, K), dev)
+    rp, ldr = _matrix("residual", residual, (M, K), dev, _b16) if residual is not None else (None, 0)
+    zp, ldz = _matrix("preact", preact, (M, K), dev, _b16) if preact is not None else (None, 0)
+    st = lib.cm_linear_dgrad(dyp, lddy, wp, ldw, layout, zp, ldz, ACTS[act], rp, ldr, dxp, _dtype_of("dx", dx), lddx,
+                             M, K, n, _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear_dgrad")
 
 
 def linear_wgrad_workspace_size(M: int, K: int, n: int) -> int:
@@ -469,20 +497,19 @@ def linear_wgrad_workspace_size(M: int, K: int, n: int) -> int:
 def cm_linear_wgrad(x, dy, dw, ws=None, db=None, accumulate: bool = False, w_layout: str = "nk", stream=None):
     """dw (+)= dy^T @ x ("nk": [n][K], "kn": [K][n]) and db [n] (+)= the sum of dy's rows.
     ws (linear_wgrad_workspace_size bytes) is needed with db only."""
-    import torch
-    b16 = torch.bfloat16
-    M, K = x.shape
-    n = dy.shape[1]
-    _same_device(x, dy, dw, ws, db)
-    wr, wc = (n, K) if w_layout == "nk" else (K, n)
-    xp, ldx = _matrix("x", x, M, K, b16)
-    dyp, lddy = _matrix("dy", dy, M, n, b16)
-    dwp, lddw = _matrix("dw", dw, wr, wc)
-    st = load().cm_linear_wgrad(xp, ldx, dyp, lddy, dwp, _dtype_of("dw", dw), lddw, LAYOUTS[w_layout],
-                                _vector("db", db, n), _dtype_of("db", db), int(bool(accumulate)), M, K, n,
-                                None if ws is None else ws.data_ptr(),
-                                0 if ws is None else ws.numel() * ws.element_size(), _stream_ptr(stream))
-    _check(st, "cm_linear_wgrad")
+    lib = _library()
+    M, K, dev = _extents("x", x)
+    n = _extents("dy", dy)[1]
+    layout = LAYOUTS[w_layout]
+    xp, ldx = _matrix("x", x, (M, K), dev, _b16)
+    dyp, lddy = _matrix("dy", dy, (M, n), dev, _b16)
+    dwp, lddw = _matrix("dw", dw, (n, K) if layout == CM_W_NK else (K, n), dev)
+    wsp, ws_bytes = _workspace(ws, dev)
+    st = lib.cm_linear_wgrad(xp, ldx, dyp, lddy, dwp, _dtype_of("dw", dw), lddw, layout, _vector("db", db, n, dev),
+                             _dtype_of("db", db), 1 if accumulate else 0, M, K, n, wsp, ws_bytes,
+                             _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear_wgrad")
 
 
 def cm_linear_check_status(stream=None):
@@ -494,18 +521,18 @@ def cm_linear_check_status(stream=None):
 
 def cm_layer_norm(x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * gamma + beta by rows; mean and rstd (fp32 [rows]) are written if given."""
-    import torch
-    rows, h = x.shape
-    _same_device(x, y, gamma, beta, mean, rstd)
-    xp, ldx = _matrix("x", x, rows, h)
-    yp, ldy = _matrix("y", y, rows, h)
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+    lib = _library()
+    rows, h, dev = _extents("x", x)
+    xp, ldx = _matrix("x", x, (rows, h), dev)
+    yp, ldy = _matrix("y", y, (rows, h), dev)
+    if gamma is not None and beta is not None and gamma.dtype is not beta.dtype:
         raise TypeError("gamma and beta must have one dtype")
-    st = load().cm_layer_norm(xp, _dtype_of("x", x), ldx, _vector("gamma", gamma, h), _vector("beta", beta, h),
-                              _dtype_of("gamma", gamma if gamma is not None else beta), eps, yp, _dtype_of("y", y), ldy,
-                              _vector("mean", mean, rows, torch.float32), _vector("rstd", rstd, rows, torch.float32),
-                              rows, h, _stream_ptr(stream))
-    _check(st, "cm_layer_norm")
+    st = lib.cm_layer_norm(xp, _dtype_of("x", x), ldx, _vector("gamma", gamma, h, dev), _vector("beta", beta, h, dev),
+                           _dtype_of("gamma", gamma if gamma is not None else beta), eps, yp, _dtype_of("y", y), ldy,
+                           _vector("mean", mean, rows, dev, _f32), _vector("rstd", rstd, rows, dev, _f32), rows, h,
+                           _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_layer_norm")
 
 
 def layer_norm_backward_workspace_size(rows: int, h: int) -> int:
@@ -516,24 +543,24 @@ def cm_layer_norm_backward(x, dy, gamma, mean, rstd, dx, ws=None, dgamma=None, d
                            accumulate: bool = False, stream=None):
     """dx of cm_layer_norm (+ residual), dgamma and dbeta [h] (both optional; ws is needed for them:
     layer_norm_backward_workspace_size bytes)."""
-    import torch
-    rows, h = x.shape
-    _same_device(x, dy, gamma, mean, rstd, dx, ws, dgamma, dbeta, residual)
-    xp, ldx = _matrix("x", x, rows, h)
-    dyp, lddy = _matrix("dy", dy, rows, h)
-    dxp, lddx = _matrix("dx", dx, rows, h, x.dtype)
-    rp, ldr = _matrix("residual", residual, rows, h, x.dtype) if residual is not None else (None, 0)
-    if dgamma is not None and dbeta is not None and dgamma.dtype != dbeta.dtype:
+    lib = _library()
+    rows, h, dev = _extents("x", x)
+    xp, ldx = _matrix("x", x, (rows, h), dev)
+    dyp, lddy = _matrix("dy", dy, (rows, h), dev)
+    dxp, lddx = _matrix("dx", dx, (rows, h), dev, x.dtype)
+    rp, ldr = _matrix("residual", residual, (rows, h), dev, x.dtype) if residual is not None else (None, 0)
+    if dgamma is not None and dbeta is not None and dgamma.dtype is not dbeta.dtype:
         raise TypeError("dgamma and dbeta must have one dtype")
-    st = load().cm_layer_norm_backward(xp, _dtype_of("x", x), ldx, dyp, _dtype_of("dy", dy), lddy,
-                                       _vector("gamma", gamma, h), _dtype_of("gamma", gamma),
-                                       _vector("mean", mean, rows, torch.float32),
-                                       _vector("rstd", rstd, rows, torch.float32), rp, ldr, dxp, lddx,
-                                       _vector("dgamma", dgamma, h), _vector("dbeta", dbeta, h),
-                                       _dtype_of("dgamma", dgamma if dgamma is not None else dbeta),
-                                       int(bool(accumulate)), rows, h, None if ws is None else ws.data_ptr(),
-                                       0 if ws is None else ws.numel() * ws.element_size(), _stream_ptr(stream))
-    _check(st, "cm_layer_norm_backward")
+    wsp, ws_bytes = _workspace(ws, dev)
+    st = lib.cm_layer_norm_backward(xp, _dtype_of("x", x), ldx, dyp, _dtype_of("dy", dy), lddy,
+                                    _vector("gamma", gamma, h, dev), _dtype_of("gamma", gamma),
+                                    _vector("mean", mean, rows, dev, _f32), _vector("rstd", rstd, rows, dev, _f32),
+                                    rp, ldr, dxp, lddx, _vector("dgamma", dgamma, h, dev),
+                                    _vector("dbeta", dbeta, h, dev),
+                                    _dtype_of("dgamma", dgamma if dgamma is not None else dbeta),
+                                    1 if accumulate else 0, rows, h, wsp, ws_bytes, _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_layer_norm_backward")
 
 
 class AdamWTensors:
@@ -549,7 +576,8 @@ class AdamWTensors:
             weight_decay: float = 0.0):
         """fp32 exp_avg and exp_avg_sq are 32-bit states; float8_e4m3fn (or uint8) ones, with their scales
         (fp32, one per CM_ADAMW_BLOCK elements), the 8-bit states, exp_avg_sq then holding the root."""
-        import torch
+        _library()
+        torch = _torch
         n = param.numel()
         codes = (torch.float8_e4m3fn, torch.uint8)
         bits = 32 if exp_avg.dtype == torch.float32 else 8
@@ -590,13 +618,17 @@ def cm_adamw(tensors: AdamWTensors, lr: float, beta1: float = 0.9, beta2: float 
              step: int = 1, grad_scale=None, seed: int = 0, stream=None):
     """One AdamW step over the listed tensors.  grad_scale: a one-element fp32 CUDA tensor that multiplies every
     gradient; seed: not 0 rounds 8-bit states up or down at random, keeping their mean (a new seed each step)."""
-    import torch
-    if grad_scale is not None and (grad_scale.numel() != 1 or grad_scale.dtype != torch.float32
-                                   or not grad_scale.is_cuda):
-        raise ValueError("grad_scale must be one fp32 CUDA element")
-    st = load().cm_adamw(tensors.array(), len(tensors), lr, beta1, beta2, eps, int(step),
-                         None if grad_scale is None else grad_scale.data_ptr(), seed, _stream_ptr(stream))
-    _check(st, "cm_adamw")
+    lib = _library()
+    scale = None
+    if grad_scale is not None:
+        if grad_scale.numel() != 1 or grad_scale.dtype is not _f32 or not grad_scale.is_cuda:
+            raise ValueError("grad_scale must be one fp32 CUDA element")
+        scale = grad_scale.data_ptr()
+    dev = tensors.device.index if tensors.device is not None else _torch.cuda.current_device()
+    st = lib.cm_adamw(tensors.array(), len(tensors), lr, beta1, beta2, eps, int(step), scale, seed,
+                      _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_adamw")
 
 
 def version() -> str:

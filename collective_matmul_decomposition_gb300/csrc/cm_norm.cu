@@ -15,74 +15,16 @@
 #include <algorithm>
 
 #include "cm_linear.cuh"
+#include "cm_vec.cuh"
 
 namespace cm {
 namespace {
 
-using bf16 = __nv_bfloat16;
+using namespace vec;
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float *p, float v) { *p = v; }
-__device__ __forceinline__ void from_f(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
-// 8 neighbouring elements, 16-byte aligned
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const bf16 *p, float (&f)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(bf16 *p, const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-// The vector at column c of a row of h elements; past the end: zeros.  The
-// last vector of a ragged row goes element by element.
-template <typename T>
-__device__ __forceinline__ void load_row8(const T *row, int64_t c, int64_t h, float (&f)[8]) {
-    if (c + 8 <= h) {
-        load8(row + c, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = c + i < h ? to_f(row[c + i]) : 0.0f;
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store_row8(T *row, int64_t c, int64_t h, const float (&f)[8]) {
-    if (c + 8 <= h) {
-        store8(row + c, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < h) from_f(row + c + i, f[i]);
-    }
-}
-__device__ __forceinline__ void load_param8(const void *p, int f32, float null_value, int64_t c, int64_t h, float (&f)[8]) {
-    if (!p) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = null_value;
-    } else if (f32) {
-        load_row8(static_cast<const float *>(p), c, h, f);
-    } else {
-        load_row8(static_cast<const bf16 *>(p), c, h, f);
-    }
+__device__ __forceinline__ V8 load_param8(const void *p, int f32, float null_value, int c, int h) {
+    if (!p) return fill(null_value);
+    return f32 ? load_row8(static_cast<const float *>(p), c, h) : load_row8(static_cast<const bf16 *>(p), c, h);
 }
 __device__ __forceinline__ float param1(const void *p, int f32, float null_value, int64_t c) {
     return !p ? null_value : f32 ? static_cast<const float *>(p)[c] : to_f(static_cast<const bf16 *>(p)[c]);
@@ -106,41 +48,183 @@ __device__ __forceinline__ float row_sum(float v, int width, float *buf) {
     return warp_sum(lane < nw ? buf[first + lane] : 0.0f);
 }
 
+__device__ __forceinline__ void copy_param8(uint8_t *dst, const void *p, int f32, int c, int h) {
+    if (!p) return;
+    if (f32)
+        copy_row8(reinterpret_cast<float *>(dst), static_cast<const float *>(p), c, h);
+    else
+        copy_row8(reinterpret_cast<bf16 *>(dst), static_cast<const bf16 *>(p), c, h);
+}
+// The same vector back from shared memory.
+__device__ __forceinline__ V8 get_param8(const uint8_t *src, const void *p, int f32, float null_value, int c) {
+    if (!p) return fill(null_value);
+    return f32 ? load8(reinterpret_cast<const float *>(src) + c) : load8(reinterpret_cast<const bf16 *>(src) + c);
+}
+
+// Two row_sum()s at once.  `buf` holds a pair a warp; the caller alternates
+// between two of them, so that one barrier a call suffices.
+__device__ __forceinline__ float2 row_sum2(float a, float b, int width, float2 *buf) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if (width == 32) return make_float2(a, b);
+    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    if (lane == 0) buf[warp] = make_float2(a, b);
+    __syncthreads();
+    const int nw = width >> 5, first = warp / nw * nw;
+    const float2 v = lane < nw ? buf[first + lane] : make_float2(0.0f, 0.0f);
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
 // ---- forward ------------------------------------------------------------------
 
-// `width` threads hold a row in registers, R vectors of 8 each.
+constexpr int kRingThreads = 512;   // of a persistent CTA, as whole rows
+
+// A thread's share of a row: R vectors, vector r at column (r width + t) 8.
+template <int R>
+struct Share {
+    V8 x[R];
+};
+
+// sum of the elements; those past the row's end are zeros
+template <int R>
+__device__ __forceinline__ float total(const Share<R> &s) {
+    F2 q[2] = {both(0.0f), both(0.0f)};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i & 1] = add(q[i & 1], s.x[r].p[i]);
+    return sum(add(q[0], q[1]));
+}
+// sum of the squares of the elements less `mean`
+template <int R>
+__device__ __forceinline__ float squares(const Share<R> &s, float mean, int width, int t, int h) {
+    F2 q[2] = {both(0.0f), both(0.0f)};
+    const F2 m = both(-mean);
+    float tail = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * width + t) * 8;
+        if (c + 8 <= h) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 d = add(s.x[r].p[i], m);
+                q[i & 1] = fma(d, d, q[i & 1]);
+            }
+        } else if (c < h) {   // a ragged end
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 d = parts(add(s.x[r].p[i], m));
+                if (c + 2 * i < h) tail += d.x * d.x;
+                if (c + 2 * i + 1 < h) tail += d.y * d.y;
+            }
+        }
+    }
+    return sum(add(q[0], q[1])) + tail;
+}
+// (x - mean) rstd g + b; the difference first, so that a constant row gives b
+__device__ __forceinline__ V8 scaled(const V8 &x, float mean, float rstd, const V8 &g, const V8 &b) {
+    V8 y;
+    const F2 rs = both(rstd), m = both(-mean);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.p[i] = fma(mul(add(x.p[i], m), rs), g.p[i], b.p[i]);
+    return y;
+}
+
+// Many rows: persistent CTAs stream their rows through a ring of S row buffers
+// in shared memory, filled by asynchronous copies S - 1 rows ahead, so that
+// DRAM stays busy through the two reductions of a row.  A thread copies just
+// the vectors that it reads itself: the ring needs no barrier.  gamma and beta
+// stay in shared memory.
+template <typename X, typename Y, int R, int S>
+__global__ void __launch_bounds__(kRingThreads, 2) cm_layer_norm_ring_kernel(NormParams p, int width) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float buf[2][2][32];
+    const int per = int(blockDim.x) / width, group = int(threadIdx.x) / width, t = int(threadIdx.x) - group * width;
+    const int h = int(p.h), h8 = (h + 7) / 8 * 8, ps = p.p_f32 ? 4 : 2;
+    uint8_t *const sg = smem, *const sb = sg + (p.gamma ? h8 * ps : 0);
+    X *const ring = reinterpret_cast<X *>(sb + (p.beta ? h8 * ps : 0)) + group * h8;
+    const int stage = per * h8;
+    const int64_t first = int64_t(blockIdx.x) * per, step = int64_t(gridDim.x) * per;
+    auto ask = [&](int64_t base, int st) {
+        const int64_t row = base + group;
+        if (row < p.rows) {
+            const X *x = static_cast<const X *>(p.x) + row * p.ldx;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * width + t) * 8;
+                if (c < h) copy_row8(ring + st * stage, x, c, h);
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * width + t) * 8;
+        if (group == 0 && c < h) {
+            copy_param8(sg, p.gamma, p.p_f32, c, h);
+            copy_param8(sb, p.beta, p.p_f32, c, h);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) ask(first + k * step, k);
+    if (per > 1) {   // the other groups read what group 0 has copied
+        copy_wait<0>();
+        __syncthreads();
+    }
+    const float inv_h = 1.0f / float(h);
+    int st = 0, flip = 0;
+    for (int64_t base = first; base < p.rows; base += step) {
+        ask(base + (S - 1) * step, (st + S - 1) % S);
+        copy_wait<S - 1>();
+        const int64_t row = base + group;
+        const bool live = row < p.rows;
+        Share<R> f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+            f.x[r] = live && c < h ? load8(ring + st * stage + c) : fill(0.0f);
+        }
+        const float mean = row_sum(total(f), width, buf[flip][0]) * inv_h;
+        const float rstd =
+            1.0f / sqrtf(row_sum(squares(f, mean, width, t, h), width, buf[flip][1]) * inv_h + p.eps);
+        if (live) {
+            if (t == 0) {
+                if (p.mean) p.mean[row] = mean;
+                if (p.rstd) p.rstd[row] = rstd;
+            }
+            Y *y = static_cast<Y *>(p.out) + row * p.ldo;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * width + t) * 8;
+                if (c >= h) break;
+                store_row8(y, c, h, scaled(f.x[r], mean, rstd, get_param8(sg, p.gamma, p.p_f32, 1.0f, c),
+                                           get_param8(sb, p.beta, p.p_f32, 0.0f, c)));
+            }
+        }
+        st = st + 1 == S ? 0 : st + 1;
+        flip ^= 1;
+    }
+    copy_wait<0>();
+}
+
+// Few rows: `width` threads hold a row in registers.
 template <typename X, typename Y, int R>
 __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int width) {
     __shared__ float buf[2][32];
     const int per = int(blockDim.x) / width, group = int(threadIdx.x) / width, t = int(threadIdx.x) - group * width;
     const int64_t row = int64_t(blockIdx.x) * per + group;
+    const int h = int(p.h);
     const bool live = row < p.rows;
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
-    float f[R][8];
-    float s = 0.0f;
+    Share<R> f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int64_t c = (int64_t(r) * width + t) * 8;
-        if (live && c < p.h) {
-            load_row8(x, c, p.h, f[r]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[r][i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += f[r][i];
+        const int c = (r * width + t) * 8;
+        f.x[r] = live && c < h ? load_row8(x, c, h) : fill(0.0f);
     }
-    const float inv_h = 1.0f / float(p.h);
-    const float mean = row_sum(s, width, buf[0]) * inv_h;
-    float q = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t c = (int64_t(r) * width + t) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < p.h) q += (f[r][i] - mean) * (f[r][i] - mean);
-    }
-    const float rstd = 1.0f / sqrtf(row_sum(q, width, buf[1]) * inv_h + p.eps);
+    const float inv_h = 1.0f / float(h);
+    const float mean = row_sum(total(f), width, buf[0]) * inv_h;
+    const float rstd = 1.0f / sqrtf(row_sum(squares(f, mean, width, t, h), width, buf[1]) * inv_h + p.eps);
     if (!live) return;
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
@@ -149,14 +233,10 @@ __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int w
     Y *y = static_cast<Y *>(p.out) + row * p.ldo;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int64_t c = (int64_t(r) * width + t) * 8;
-        if (c >= p.h) break;
-        float g[8], b[8];
-        load_param8(p.gamma, p.p_f32, 1.0f, c, p.h, g);
-        load_param8(p.beta, p.p_f32, 0.0f, c, p.h, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[r][i] = (f[r][i] - mean) * rstd * g[i] + b[i];
-        store_row8(y, c, p.h, f[r]);
+        const int c = (r * width + t) * 8;
+        if (c >= h) break;
+        store_row8(y, c, h, scaled(f.x[r], mean, rstd, load_param8(p.gamma, p.p_f32, 1.0f, c, h),
+                                   load_param8(p.beta, p.p_f32, 0.0f, c, h)));
     }
 }
 
@@ -182,31 +262,235 @@ __global__ void __launch_bounds__(512) cm_layer_norm_any_kernel(NormParams p) {
         from_f(y + c, (to_f(x[c]) - mean) * rstd * param1(p.gamma, p.p_f32, 1.0f, c) + param1(p.beta, p.p_f32, 0.0f, c));
 }
 
-// ---- backward: input gradient -----------------------------------------------------
+// ---- backward -------------------------------------------------------------------
 
 // X: type of x, res and dx; Y: type of dy.
-template <typename X, typename Y>
+//
+// One pass over x, dy and res gives dx and the sums over rows: persistent CTAs
+// stream rows through a ring of S row buffers as the forward kernel does.  A
+// thread owns the same R vectors of columns in every row, so dgamma and dbeta
+// collect in its registers; after the rows' sums the row is read again from the
+// ring, not held in registers, which leaves those to the sums.  At the end the
+// groups of a CTA are added in order and written as its part.
+template <typename X, typename Y, int R, int S>
+__global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_kernel(NormParams p, int width) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 buf[2][32];
+    const int per = int(blockDim.x) / width, group = int(threadIdx.x) / width, t = int(threadIdx.x) - group * width;
+    const int h = int(p.h), h8 = (h + 7) / 8 * 8;
+    uint8_t *const sg = smem;
+    uint8_t *const ring = sg + (p.gamma ? h8 * (p.p_f32 ? 4 : 2) : 0);
+    const int xs = h8 * int(sizeof(X)), ys = h8 * int(sizeof(Y));
+    const int row_bytes = xs + ys + (p.res ? xs : 0);
+    const int64_t first = int64_t(blockIdx.x) * per, step = int64_t(gridDim.x) * per;
+    auto slot = [&](int st) { return ring + (st * per + group) * row_bytes; };
+    auto ask = [&](int64_t base, int st) {
+        const int64_t row = base + group;
+        if (row < p.rows) {
+            uint8_t *d = slot(st);
+            const X *x = static_cast<const X *>(p.x) + row * p.ldx, *res = static_cast<const X *>(p.res) + row * p.ldr;
+            const Y *dy = static_cast<const Y *>(p.dy) + row * p.lddy;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * width + t) * 8;
+                if (c >= h) break;
+                copy_row8(reinterpret_cast<X *>(d), x, c, h);
+                copy_row8(reinterpret_cast<Y *>(d + xs), dy, c, h);
+                if (p.res) copy_row8(reinterpret_cast<X *>(d + xs + ys), res, c, h);
+            }
+        }
+        copy_commit();
+    };
+    V8 a[R], b[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * width + t) * 8;
+        if (group == 0 && c < h) copy_param8(sg, p.gamma, p.p_f32, c, h);
+        a[r] = b[r] = fill(0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) ask(first + k * step, k);
+    if (per > 1) {
+        copy_wait<0>();
+        __syncthreads();
+    }
+    const float inv_h = 1.0f / float(h);
+    float mean = 0.0f, rstd = 0.0f;
+    if (first + group < p.rows) {
+        mean = p.mean[first + group];
+        rstd = p.rstd[first + group];
+    }
+    int st = 0, flip = 0;
+    for (int64_t base = first; base < p.rows; base += step) {
+        ask(base + (S - 1) * step, (st + S - 1) % S);
+        const int64_t row = base + group;
+        const bool live = row < p.rows;
+        float next_mean = 0.0f, next_rstd = 0.0f;
+        if (row + step < p.rows) {
+            next_mean = p.mean[row + step];
+            next_rstd = p.rstd[row + step];
+        }
+        copy_wait<S - 1>();
+        const uint8_t *d = slot(st);
+        float s1 = 0.0f, s2 = 0.0f;
+        if (live) {
+            const F2 rs = both(rstd), m = both(-mean);
+            F2 q1 = both(0.0f), q2 = both(0.0f);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * width + t) * 8;
+                if (c >= h) break;
+                const V8 x = load8(reinterpret_cast<const X *>(d) + c), y = load8(reinterpret_cast<const Y *>(d + xs) + c);
+                const V8 g = get_param8(sg, p.gamma, p.p_f32, 1.0f, c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // past a ragged end dy is zero: nothing is added
+                    const F2 xh = mul(add(x.p[i], m), rs), u = mul(y.p[i], g.p[i]);
+                    q1 = add(q1, u);
+                    q2 = fma(u, xh, q2);
+                    a[r].p[i] = fma(y.p[i], xh, a[r].p[i]);
+                    b[r].p[i] = add(b[r].p[i], y.p[i]);
+                }
+            }
+            s1 = sum(q1);
+            s2 = sum(q2);
+        }
+        const float2 rowsum = row_sum2(s1, s2, width, buf[flip]);
+        if (live) {
+            // dx = rstd u - (x - mean) k - rstd s1 + res, k = rstd^2 s2
+            s1 = rowsum.x * inv_h;
+            s2 = rowsum.y * inv_h;
+            const F2 rs = both(rstd), m = both(-mean), k = both(-rstd * rstd * s2), off = both(-rstd * s1);
+            X *dx = static_cast<X *>(p.out) + row * p.ldo;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * width + t) * 8;
+                if (c >= h) break;
+                const V8 x = load8(reinterpret_cast<const X *>(d) + c), y = load8(reinterpret_cast<const Y *>(d + xs) + c);
+                const V8 g = get_param8(sg, p.gamma, p.p_f32, 1.0f, c);
+                V8 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o.p[i] = fma(mul(y.p[i], g.p[i]), rs, fma(add(x.p[i], m), k, off));
+                if (p.res) {
+                    const V8 z = load8(reinterpret_cast<const X *>(d + xs + ys) + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o.p[i] = add(o.p[i], z.p[i]);
+                }
+                store_row8(dx, c, h, o);
+            }
+        }
+        mean = next_mean;
+        rstd = next_rstd;
+        flip ^= 1;
+        st = st + 1 == S ? 0 : st + 1;
+    }
+    copy_wait<0>();
+    if (!p.partial) return;
+    float *const mine = p.partial + int64_t(blockIdx.x) * 2 * h;
+    if (per == 1) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = parts(a[r].p[i]), v = parts(b[r].p[i]);
+                if (c + 2 * i < h) mine[c + 2 * i] = u.x, mine[h + c + 2 * i] = v.x;
+                if (c + 2 * i + 1 < h) mine[c + 2 * i + 1] = u.y, mine[h + c + 2 * i + 1] = v.y;
+            }
+        }
+        return;
+    }
+    // [group][2][h8] over the ring, which nobody uses any more: 8 bytes a
+    // column and group, of the S (2 + 2) at least that the ring has
+    __syncthreads();
+    float *const sums = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * width + t) * 8;
+        if (c >= h) break;
+        store8(sums + group * 2 * h8 + c, a[r]);
+        store8(sums + (group * 2 + 1) * h8 + c, b[r]);
+    }
+    __syncthreads();
+    for (int c = int(threadIdx.x); c < 2 * h; c += int(blockDim.x)) {
+        const int o = c < h ? c : c - h + h8;
+        float v = 0.0f;
+        for (int g = 0; g < per; ++g) v += sums[g * 2 * h8 + o];
+        mine[c] = v;
+    }
+}
+
+__device__ __forceinline__ void spread(const V8 &v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = parts(v.p[i]);
+        f[2 * i] = a.x;
+        f[2 * i + 1] = a.y;
+    }
+}
+__device__ __forceinline__ V8 gather(const float (&f)[8]) {
+    return {{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+}
+
+// Any extent, stride and alignment (V = 1), or rows too long for the ring
+// (V = 8): one CTA a row, x and dy read a second time from L2.  The sums over
+// rows are then the column kernel's.
+template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(512) cm_layer_norm_dx_any_kernel(NormParams p) {
-    __shared__ float buf[2][32];
+    __shared__ float2 buf[32];
     const int64_t row = blockIdx.x;
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
     const Y *dy = static_cast<const Y *>(p.dy) + row * p.lddy;
     const float mean = p.mean[row], rstd = p.rstd[row];
+    auto fetch = [&](int64_t c, float (&xh)[V], float (&u)[V]) {
+        float g[V];
+        if constexpr (V == 8) {
+            spread(load_row8(x, int(c), int(p.h)), xh);
+            spread(load_row8(dy, int(c), int(p.h)), u);
+            spread(load_param8(p.gamma, p.p_f32, 1.0f, int(c), int(p.h)), g);
+        } else {
+            xh[0] = to_f(x[c]);
+            u[0] = to_f(dy[c]);
+            g[0] = param1(p.gamma, p.p_f32, 1.0f, c);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            xh[i] = (xh[i] - mean) * rstd;
+            u[i] *= g[i];
+        }
+    };
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.h; c += blockDim.x) {
-        const float t = to_f(dy[c]) * param1(p.gamma, p.p_f32, 1.0f, c);
-        s1 += t;
-        s2 += t * ((to_f(x[c]) - mean) * rstd);
+    for (int64_t c = int64_t(threadIdx.x) * V; c < p.h; c += int64_t(blockDim.x) * V) {
+        float xh[V], u[V];
+        fetch(c, xh, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s1 += u[i];
+            s2 += u[i] * xh[i];
+        }
     }
-    s1 = row_sum(s1, int(blockDim.x), buf[0]) / float(p.h);
-    s2 = row_sum(s2, int(blockDim.x), buf[1]) / float(p.h);
+    const float2 sum = row_sum2(s1, s2, int(blockDim.x), buf);
+    s1 = sum.x / float(p.h);
+    s2 = sum.y / float(p.h);
     X *dx = static_cast<X *>(p.out) + row * p.ldo;
     const X *res = static_cast<const X *>(p.res) + row * p.ldr;
-    for (int64_t c = threadIdx.x; c < p.h; c += blockDim.x) {
-        const float t = to_f(dy[c]) * param1(p.gamma, p.p_f32, 1.0f, c);
-        float v = (t - s1 - (to_f(x[c]) - mean) * rstd * s2) * rstd;
-        if (p.res) v += to_f(res[c]);
-        from_f(dx + c, v);
+    for (int64_t c = int64_t(threadIdx.x) * V; c < p.h; c += int64_t(blockDim.x) * V) {
+        float xh[V], u[V], f[V];
+        fetch(c, xh, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = 0.0f;
+        if (p.res) {
+            if constexpr (V == 8)
+                spread(load_row8(res, int(c), int(p.h)), f);
+            else
+                f[0] = to_f(res[c]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] += (u[i] - s1 - xh[i] * s2) * rstd;
+        if constexpr (V == 8)
+            store_row8(dx, int(c), int(p.h), gather(f));
+        else
+            from_f(dx + c, f[0]);
     }
 }
 
@@ -232,8 +516,8 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
             const Y *dy = static_cast<const Y *>(p.dy) + r * p.lddy;
             const X *x = static_cast<const X *>(p.x) + r * p.ldx;
             if constexpr (V == 8) {
-                load_row8(dy, c, p.h, d);
-                if constexpr (STATS) load_row8(x, c, p.h, f);
+                spread(load_row8(dy, int(c), int(p.h)), d);
+                if constexpr (STATS) spread(load_row8(x, int(c), int(p.h)), f);
             } else {
                 d[0] = to_f(dy[c]);
                 if constexpr (STATS) f[0] = to_f(x[c]);
@@ -270,13 +554,27 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
     }
 }
 
-// out[c] (+)= sum over parts, in their order, of partial[part * stride + c]
-__device__ __forceinline__ void sum_parts(const float *partial, int64_t parts, int64_t stride, void *out, int f32,
-                                          int accumulate, int64_t c) {
+// out[c] (+)= sum over parts of partial[part * stride + c]: eight lanes take
+// every eighth part, then their sums are added in order.
+__global__ void __launch_bounds__(256) cm_sum_parts_kernel(const float *partial, int64_t parts, int64_t h, int64_t stride,
+                                                           void *out0, void *out1, int f32, int accumulate) {
+    __shared__ float sm[8][32];
+    const int tx = int(threadIdx.x) & 31, ty = int(threadIdx.x) >> 5;
+    const int64_t c = int64_t(blockIdx.x) * 32 + tx;
+    void *out = blockIdx.y ? out1 : out0;
     if (!out) return;
+    const float *src = partial + (blockIdx.y ? h : 0);
     float s = 0.0f;
+    if (c < h) {
 #pragma unroll 8
-    for (int64_t k = 0; k < parts; ++k) s += partial[k * stride + c];
+        for (int64_t k = ty; k < parts; k += 8) s += src[k * stride + c];
+    }
+    sm[ty][tx] = s;
+    __syncthreads();
+    if (ty || c >= h) return;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += sm[k][tx];
     if (f32) {
         float *o = static_cast<float *>(out) + c;
         *o = accumulate ? *o + s : s;
@@ -286,24 +584,13 @@ __device__ __forceinline__ void sum_parts(const float *partial, int64_t parts, i
     }
 }
 
-__global__ void __launch_bounds__(128) cm_sum_parts_kernel(const float *partial, int64_t parts, int64_t h, void *out0,
-                                                           void *out1, int f32, int accumulate) {
-    const int64_t c = int64_t(blockIdx.x) * 128 + threadIdx.x;
-    if (c >= h) return;
-    const int64_t stride = out1 || gridDim.y > 1 ? 2 * h : h;
-    if (blockIdx.y == 0)
-        sum_parts(partial, parts, stride, out0, f32, accumulate, c);
-    else
-        sum_parts(partial + h, parts, stride, out1, f32, accumulate, c);
-}
-
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 152;
-    return n;
+    return std::min(n, 160);
 }
 
 // Chunks of rows for the column sums: enough CTAs for two rounds of the SMs,
@@ -313,46 +600,142 @@ int64_t chunks_for(int64_t rows, int64_t cols) {
     return std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, std::max<int64_t>(1, 608 / blocks)));
 }
 
+constexpr int64_t kSmemCta = 227 * 1024, kSmemSm = 228 * 1024;
+
+// CTAs of a persistent launch: at most `most` an SM, if shared memory has room.
+int64_t resident(int sms, int64_t smem, int most) {
+    return int64_t(sms) * std::max<int64_t>(1, std::min<int64_t>(most, kSmemSm / (smem + 1024 + 512)));
+}
+
+// The sums over rows of the partial sums of `parts` CTAs.
+void sum_parts(const float *partial, int64_t parts, int64_t h, int64_t stride, void *out0, void *out1, int f32,
+               int accumulate, cudaStream_t stream) {
+    cm_sum_parts_kernel<<<dim3(unsigned((h + 31) / 32), stride > h ? 2 : 1), 256, 0, stream>>>(
+        partial, parts, h, stride, out0, out1, f32, accumulate);
+}
+
+template <typename K>
+cudaError_t opt_in(K kernel, int64_t smem) {
+    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemCta - 1024))
+                            : cudaSuccess;
+}
+
+int rows_per_cta(int width) { return std::max(1, kRingThreads / width); }
+
+template <typename X, typename Y, int R>
+cudaError_t forward_ring(const NormParams &p, int width, int per, int64_t smem, int64_t ctas, cudaStream_t stream) {
+    cudaError_t e = opt_in(cm_layer_norm_ring_kernel<X, Y, R, 3>, smem);
+    if (e != cudaSuccess) return e;
+    cm_layer_norm_ring_kernel<X, Y, R, 3><<<unsigned(ctas), unsigned(width * per), size_t(smem), stream>>>(p, width);
+    return cudaGetLastError();
+}
+
+int row_width(int64_t vecs, int R) { return int((vecs + 32 * R - 1) / (32 * R)) * 32; }
+
 template <typename X, typename Y>
 cudaError_t forward(const NormParams &p, cudaStream_t stream) {
     const int64_t vecs = (p.h + 7) / 8;
     const bool vec = aligned16(p.x) && aligned16(p.out) && aligned16(p.gamma) && aligned16(p.beta) && p.ldx % 8 == 0 &&
                      p.ldo % 8 == 0 && vecs <= 4096;
+    if (p.rows > 0x7fffffff) return cudaErrorInvalidValue;
     if (!vec) {
-        if (p.rows > 0x7fffffff) return cudaErrorInvalidValue;
         cm_layer_norm_any_kernel<X, Y><<<unsigned(p.rows), 512, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    // few rows: all of a row's loads at once; many: fewer, busier threads
     const int sms = sm_count();
-    int R = p.rows < 4 * sms ? (vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4) : (vecs >= 128 ? 4 : vecs >= 64 ? 2 : 1);
-    const int width = int((vecs + 32 * R - 1) / (32 * R)) * 32;
-    const int per = std::max(1, 128 / width);
-    const int64_t grid = (p.rows + per - 1) / per;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 g(static_cast<unsigned>(grid)), b(static_cast<unsigned>(width * per));
+    {
+        const int R = vecs < 64 ? 1 : vecs <= 1024 ? 2 : 4;
+        const int width = row_width(vecs, R), per = rows_per_cta(width);
+        const int64_t ps = (p.p_f32 ? 4 : 2) * ((p.gamma ? 1 : 0) + (p.beta ? 1 : 0));
+        const int64_t smem = vecs * 8 * (ps + int64_t(sizeof(X)) * 3 * per);
+        const int64_t ctas = resident(sms, smem, 2);
+        // the ring pays once a CTA has a few rows to run ahead on
+        if (width <= kRingThreads && smem <= kSmemCta - 1024 && p.rows >= 4 * ctas * per)
+            return R == 1   ? forward_ring<X, Y, 1>(p, width, per, smem, ctas, stream)
+                   : R == 2 ? forward_ring<X, Y, 2>(p, width, per, smem, ctas, stream)
+                            : forward_ring<X, Y, 4>(p, width, per, smem, ctas, stream);
+    }
+    // all of a row's loads at once
+    const int R = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+    const int width = row_width(vecs, R), per = std::max(1, 128 / width);
+    const unsigned grid = unsigned((p.rows + per - 1) / per), threads = unsigned(width * per);
     if (R == 1)
-        cm_layer_norm_kernel<X, Y, 1><<<g, b, 0, stream>>>(p, width);
+        cm_layer_norm_kernel<X, Y, 1><<<grid, threads, 0, stream>>>(p, width);
     else if (R == 2)
-        cm_layer_norm_kernel<X, Y, 2><<<g, b, 0, stream>>>(p, width);
+        cm_layer_norm_kernel<X, Y, 2><<<grid, threads, 0, stream>>>(p, width);
     else
-        cm_layer_norm_kernel<X, Y, 4><<<g, b, 0, stream>>>(p, width);
+        cm_layer_norm_kernel<X, Y, 4><<<grid, threads, 0, stream>>>(p, width);
+    return cudaGetLastError();
+}
+
+// Launch geometry of the one-pass backward kernel; ctas = 0 where a row is
+// too long for it.  Alignment aside, it depends on extents and types only, so
+// that the workspace's size can follow it.
+struct RingPlan {
+    int R = 0, S = 0, width = 0, per = 1;
+    int64_t ctas = 0, smem = 0;
+};
+
+RingPlan ring_plan(int64_t rows, int64_t h, int64_t xs, int64_t ys, bool res, int64_t gamma_bytes, int sms) {
+    RingPlan r;
+    const int64_t vecs = (h + 7) / 8;
+    if (vecs > 2048) return r;
+    r.R = vecs < 64 ? 1 : vecs <= 1024 ? 2 : 4;
+    r.width = row_width(vecs, r.R);
+    r.per = rows_per_cta(r.width);
+    const int64_t row = vecs * 8 * (xs + ys + (res ? xs : 0)) * r.per, fixed = vecs * 8 * gamma_bytes;
+    for (r.S = 3; r.S >= 2; --r.S) {
+        r.smem = fixed + r.S * row;
+        if (r.smem <= kSmemCta - 1024) break;
+    }
+    if (r.S < 2) return r;
+    r.ctas = std::min<int64_t>(resident(sms, r.smem, 1), (rows + r.per - 1) / r.per);
+    return r;
+}
+
+template <typename X, typename Y, int R, int S>
+cudaError_t backward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
+    cudaError_t e = opt_in(cm_layer_norm_backward_ring_kernel<X, Y, R, S>, r.smem);
+    if (e != cudaSuccess) return e;
+    cm_layer_norm_backward_ring_kernel<X, Y, R, S>
+        <<<unsigned(r.ctas), unsigned(r.width * r.per), size_t(r.smem), stream>>>(p, r.width);
     return cudaGetLastError();
 }
 
 template <typename X, typename Y>
-cudaError_t backward(const NormParams &p, cudaStream_t stream) {
+cudaError_t backward(NormParams p, cudaStream_t stream) {
     if (p.rows > 0x7fffffff) return cudaErrorInvalidValue;
-    if (p.rows > 0) cm_layer_norm_dx_any_kernel<X, Y><<<unsigned(p.rows), 512, 0, stream>>>(p);
-    if (!p.dgamma && !p.dbeta) return cudaGetLastError();
-    const bool vec = aligned16(p.x) && aligned16(p.dy) && p.ldx % 8 == 0 && p.lddy % 8 == 0;
-    const int64_t chunks = chunks_for(p.rows, p.h);
+    const bool sums = p.dgamma || p.dbeta;
+    if (!sums) p.partial = nullptr;
+    const bool in_vec = aligned16(p.x) && aligned16(p.dy) && p.ldx % 8 == 0 && p.lddy % 8 == 0;
+    const bool vec = in_vec && aligned16(p.out) && aligned16(p.gamma) && p.ldo % 8 == 0 &&
+                     (!p.res || (aligned16(p.res) && p.ldr % 8 == 0));
+    if (vec) {
+        const RingPlan r = ring_plan(p.rows, p.h, sizeof(X), sizeof(Y), p.res != nullptr,
+                                     p.gamma ? (p.p_f32 ? 4 : 2) : 0, sm_count());
+        if (r.ctas > 0) {
+            const cudaError_t e = r.S == 3 ? (r.R == 1   ? backward_ring<X, Y, 1, 3>(p, r, stream)
+                                              : r.R == 2 ? backward_ring<X, Y, 2, 3>(p, r, stream)
+                                                         : backward_ring<X, Y, 4, 3>(p, r, stream))
+                                           : (r.R == 1   ? backward_ring<X, Y, 1, 2>(p, r, stream)
+                                              : r.R == 2 ? backward_ring<X, Y, 2, 2>(p, r, stream)
+                                                         : backward_ring<X, Y, 4, 2>(p, r, stream));
+            if (e != cudaSuccess || !sums) return e;
+            sum_parts(p.partial, r.ctas, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
+            return cudaGetLastError();
+        }
+    }
     if (vec)
+        cm_layer_norm_dx_any_kernel<X, Y, 8><<<unsigned(p.rows), 512, 0, stream>>>(p);
+    else
+        cm_layer_norm_dx_any_kernel<X, Y, 1><<<unsigned(p.rows), 512, 0, stream>>>(p);
+    if (!sums) return cudaGetLastError();
+    const int64_t chunks = chunks_for(p.rows, p.h);
+    if (in_vec)
         cm_colsum_kernel<X, Y, 8, true><<<dim3(unsigned((p.h + 255) / 256), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
     else
         cm_colsum_kernel<X, Y, 1, true><<<dim3(unsigned((p.h + 31) / 32), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    cm_sum_parts_kernel<<<dim3(unsigned((p.h + 127) / 128), 2), 128, 0, stream>>>(p.partial, chunks, p.h, p.dgamma,
-                                                                                 p.dbeta, p.g_f32, p.accumulate);
+    sum_parts(p.partial, chunks, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
     return cudaGetLastError();
 }
 
@@ -363,7 +746,14 @@ cudaError_t launch_layer_norm(const NormParams &p, cm_dtype x, cm_dtype y, cudaS
     return y == CM_BF16 ? forward<float, bf16>(p, stream) : forward<float, float>(p, stream);
 }
 
-int64_t norm_backward_parts(int64_t rows, int64_t h) { return chunks_for(rows, h); }
+// The most parts that any types of a call with these extents make: a
+// persistent launch has one CTA an SM, and no more than rows need.  The SM count is an upper bound, so that the size can be asked
+// for without a device.
+int64_t norm_backward_parts(int64_t rows, int64_t h) {
+    constexpr int kMostSms = 160;
+    const RingPlan r = ring_plan(rows, h, 2, 2, false, 0, kMostSms);
+    return std::max(chunks_for(rows, h), r.ctas);
+}
 
 cudaError_t launch_layer_norm_backward(const NormParams &p, cm_dtype x, cm_dtype y, cudaStream_t stream) {
     if (x == CM_BF16) return y == CM_BF16 ? backward<bf16, bf16>(p, stream) : backward<bf16, float>(p, stream);
@@ -383,8 +773,7 @@ cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols
     const int64_t chunks = chunks_for(rows, cols);
     cm_colsum_kernel<bf16, bf16, 8, false>
         <<<dim3(unsigned((cols + 255) / 256), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    cm_sum_parts_kernel<<<dim3(unsigned((cols + 127) / 128), 1), 128, 0, stream>>>(partial, chunks, cols, out, nullptr,
-                                                                                  out_f32 ? 1 : 0, accumulate ? 1 : 0);
+    sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
     return cudaGetLastError();
 }
 
