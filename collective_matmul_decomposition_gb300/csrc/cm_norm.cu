@@ -36,50 +36,86 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the `width` threads (a multiple of 32) that share a row.  `buf`
-// holds one value a warp and is used once.
-__device__ __forceinline__ float row_sum(float v, int width, float *buf) {
+// The `width` threads (a multiple of 32) that share a row, one group of several
+// in a CTA.  Groups meet at a barrier of their own, so that they drift apart
+// and one's arithmetic fills another's waits.
+struct Group {
+    int width, index, warps, lane, warp;   // warp: in the group
+    __device__ Group(int w) {
+        width = w;
+        index = int(threadIdx.x) / w;
+        warps = w >> 5;
+        lane = int(threadIdx.x) & 31;
+        warp = (int(threadIdx.x) >> 5) - index * warps;
+    }
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(width) : "memory");
+    }
+};
+
+// Sum over a group.  `buf` has a slot a warp of the group, rounded up to a
+// multiple of four; the caller alternates between buffers, so that one barrier
+// a call suffices.
+__device__ __forceinline__ float row_sum(float v, const Group &g, float *buf) {
     v = warp_sum(v);
-    if (width == 32) return v;
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    if (lane == 0) buf[warp] = v;
-    __syncthreads();
-    const int nw = width >> 5, first = warp / nw * nw;
-    return warp_sum(lane < nw ? buf[first + lane] : 0.0f);
+    if (g.warps == 1) return v;
+    if (g.lane == 0) buf[g.warp] = v;
+    g.sync();
+    v = 0.0f;
+    for (int k = 0; k < g.warps; k += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(buf + k);
+        v += q.x;
+        if (k + 1 < g.warps) v += q.y;
+        if (k + 2 < g.warps) v += q.z;
+        if (k + 3 < g.warps) v += q.w;
+    }
+    return v;
 }
-
-__device__ __forceinline__ void copy_param8(uint8_t *dst, const void *p, int f32, int c, int h) {
-    if (!p) return;
-    if (f32)
-        copy_row8(reinterpret_cast<float *>(dst), static_cast<const float *>(p), c, h);
-    else
-        copy_row8(reinterpret_cast<bf16 *>(dst), static_cast<const bf16 *>(p), c, h);
-}
-// The same vector back from shared memory.
-__device__ __forceinline__ V8 get_param8(const uint8_t *src, const void *p, int f32, float null_value, int c) {
-    if (!p) return fill(null_value);
-    return f32 ? load8(reinterpret_cast<const float *>(src) + c) : load8(reinterpret_cast<const bf16 *>(src) + c);
-}
-
-// Two row_sum()s at once.  `buf` holds a pair a warp; the caller alternates
-// between two of them, so that one barrier a call suffices.
-__device__ __forceinline__ float2 row_sum2(float a, float b, int width, float2 *buf) {
+// Two sums at once; `buf` holds two floats a warp.
+__device__ __forceinline__ float2 row_sum2(float a, float b, const Group &g, float *buf) {
     a = warp_sum(a);
     b = warp_sum(b);
-    if (width == 32) return make_float2(a, b);
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    if (lane == 0) buf[warp] = make_float2(a, b);
-    __syncthreads();
-    const int nw = width >> 5, first = warp / nw * nw;
-    const float2 v = lane < nw ? buf[first + lane] : make_float2(0.0f, 0.0f);
-    return make_float2(warp_sum(v.x), warp_sum(v.y));
+    if (g.warps == 1) return make_float2(a, b);
+    if (g.lane == 0) *reinterpret_cast<float2 *>(buf + 2 * g.warp) = make_float2(a, b);
+    g.sync();
+    a = b = 0.0f;
+    for (int k = 0; k < g.warps; k += 2) {
+        const float4 q = *reinterpret_cast<const float4 *>(buf + 2 * k);
+        a += q.x;
+        b += q.y;
+        if (k + 1 < g.warps) a += q.z, b += q.w;
+    }
+    return make_float2(a, b);
+}
+// Slots of a group in a shared buffer of kRowBuf floats (32 warps at most, 16 groups).
+constexpr int kRowBuf = 128;
+__device__ __forceinline__ float *row_buf(float *buf, const Group &g, int floats) {
+    return buf + g.index * ((g.warps * floats + 3) & ~3);
+}
+
+// A parameter vector to shared memory as fp32, 1 (or 0) where there is none.
+__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int h) {
+    for (int c = int(threadIdx.x) * 8; c < h; c += int(blockDim.x) * 8)
+        store8(dst + c, load_param8(p, f32, null_value, c, h));
+}
+// Asynchronous copy of the vector at column c of a row of h to its place in `dst`.
+template <typename T>
+__device__ __forceinline__ void copy_vec(T *dst, const T *row, int c, int h) {
+    constexpr int kPer = 16 / int(sizeof(T));
+    if (c + 8 <= h) {
+#pragma unroll
+        for (int k = 0; k < 8 / kPer; ++k) copy16(dst + c + k * kPer, row + c + k * kPer);
+    } else if (c < h) {
+        copy_row8(dst, row, c, h);
+    }
 }
 
 // ---- forward ------------------------------------------------------------------
 
 constexpr int kRingThreads = 512;   // of a persistent CTA, as whole rows
 
-// A thread's share of a row: R vectors, vector r at column (r width + t) 8.
+// A thread's share of a row: R vectors, vector r at column (r width + t) 8,
+// t = its place in the group.
 template <int R>
 struct Share {
     V8 x[R];
@@ -134,73 +170,62 @@ __device__ __forceinline__ V8 scaled(const V8 &x, float mean, float rstd, const 
 // in shared memory, filled by asynchronous copies S - 1 rows ahead, so that
 // DRAM stays busy through the two reductions of a row.  A thread copies just
 // the vectors that it reads itself: the ring needs no barrier.  gamma and beta
-// stay in shared memory.
+// stay in shared memory as fp32.  What is left bounds the kernel by instructions
+// as much as by memory: hence four vectors a thread, pairs of fp32, and no
+// test for missing parameters in the loop.
 template <typename X, typename Y, int R, int S>
-__global__ void __launch_bounds__(kRingThreads, 2) cm_layer_norm_ring_kernel(NormParams p, int width) {
+__global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(const __grid_constant__ NormParams p, int width) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float buf[2][2][32];
-    const int per = int(blockDim.x) / width, group = int(threadIdx.x) / width, t = int(threadIdx.x) - group * width;
-    const int h = int(p.h), h8 = (h + 7) / 8 * 8, ps = p.p_f32 ? 4 : 2;
-    uint8_t *const sg = smem, *const sb = sg + (p.gamma ? h8 * ps : 0);
-    X *const ring = reinterpret_cast<X *>(sb + (p.beta ? h8 * ps : 0)) + group * h8;
+    __shared__ __align__(16) float sums[2][2][kRowBuf];
+    const Group g(width);
+    const int t = int(threadIdx.x) - g.index * width, per = int(blockDim.x) / width;
+    const int h = int(p.h), h8 = (h + 7) / 8 * 8;
+    float *const gamma = reinterpret_cast<float *>(smem), *const beta = gamma + h8;
+    X *const ring = reinterpret_cast<X *>(beta + h8) + g.index * h8;
     const int stage = per * h8;
-    const int64_t first = int64_t(blockIdx.x) * per, step = int64_t(gridDim.x) * per;
-    auto ask = [&](int64_t base, int st) {
-        const int64_t row = base + group;
-        if (row < p.rows) {
-            const X *x = static_cast<const X *>(p.x) + row * p.ldx;
+    const int64_t step = int64_t(gridDim.x) * per;
+    int64_t ask_row = int64_t(blockIdx.x) * per + g.index;
+    const X *ask_x = static_cast<const X *>(p.x) + ask_row * p.ldx;
+    auto ask = [&](int st) {
+        if (ask_row < p.rows) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int c = (r * width + t) * 8;
-                if (c < h) copy_row8(ring + st * stage, x, c, h);
-            }
+            for (int r = 0; r < R; ++r) copy_vec(ring + st * stage, ask_x, (r * width + t) * 8, h);
         }
         copy_commit();
+        ask_row += step;
+        ask_x += step * p.ldx;
     };
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = (r * width + t) * 8;
-        if (group == 0 && c < h) {
-            copy_param8(sg, p.gamma, p.p_f32, c, h);
-            copy_param8(sb, p.beta, p.p_f32, c, h);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < S - 1; ++k) ask(first + k * step, k);
-    if (per > 1) {   // the other groups read what group 0 has copied
-        copy_wait<0>();
-        __syncthreads();
-    }
+    for (int k = 0; k < S - 1; ++k) ask(k);
+    stage_param(gamma, p.gamma, p.p_f32, 1.0f, h);
+    stage_param(beta, p.beta, p.p_f32, 0.0f, h);
+    __syncthreads();
     const float inv_h = 1.0f / float(h);
     int st = 0, flip = 0;
-    for (int64_t base = first; base < p.rows; base += step) {
-        ask(base + (S - 1) * step, (st + S - 1) % S);
+    Y *y = static_cast<Y *>(p.out) + (int64_t(blockIdx.x) * per + g.index) * p.ldo;
+    for (int64_t row = int64_t(blockIdx.x) * per + g.index; row < p.rows; row += step) {
+        ask(st == 0 ? S - 1 : st - 1);
         copy_wait<S - 1>();
-        const int64_t row = base + group;
-        const bool live = row < p.rows;
         Share<R> f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int c = (r * width + t) * 8;
-            f.x[r] = live && c < h ? load8(ring + st * stage + c) : fill(0.0f);
+            f.x[r] = c < h ? load8(ring + st * stage + c) : fill(0.0f);
         }
-        const float mean = row_sum(total(f), width, buf[flip][0]) * inv_h;
-        const float rstd =
-            1.0f / sqrtf(row_sum(squares(f, mean, width, t, h), width, buf[flip][1]) * inv_h + p.eps);
-        if (live) {
-            if (t == 0) {
-                if (p.mean) p.mean[row] = mean;
-                if (p.rstd) p.rstd[row] = rstd;
-            }
-            Y *y = static_cast<Y *>(p.out) + row * p.ldo;
+        const float mean = row_sum(total(f), g, row_buf(sums[flip][0], g, 1)) * inv_h;
+        const float var = row_sum(squares(f, mean, width, t, h), g, row_buf(sums[flip][1], g, 1)) * inv_h;
+        const float rstd = rsqrtf(var + p.eps);
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int c = (r * width + t) * 8;
-                if (c >= h) break;
-                store_row8(y, c, h, scaled(f.x[r], mean, rstd, get_param8(sg, p.gamma, p.p_f32, 1.0f, c),
-                                           get_param8(sb, p.beta, p.p_f32, 0.0f, c)));
-            }
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+            if (c >= h) break;
+            store_row8(y, c, h, scaled(f.x[r], mean, rstd, load8(gamma + c), load8(beta + c)));
         }
+        y += step * p.ldo;
         st = st + 1 == S ? 0 : st + 1;
         flip ^= 1;
     }
@@ -210,9 +235,10 @@ __global__ void __launch_bounds__(kRingThreads, 2) cm_layer_norm_ring_kernel(Nor
 // Few rows: `width` threads hold a row in registers.
 template <typename X, typename Y, int R>
 __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int width) {
-    __shared__ float buf[2][32];
-    const int per = int(blockDim.x) / width, group = int(threadIdx.x) / width, t = int(threadIdx.x) - group * width;
-    const int64_t row = int64_t(blockIdx.x) * per + group;
+    __shared__ __align__(16) float sums[2][kRowBuf];
+    const Group g(width);
+    const int per = int(blockDim.x) / width, t = int(threadIdx.x) - g.index * width;
+    const int64_t row = int64_t(blockIdx.x) * per + g.index;
     const int h = int(p.h);
     const bool live = row < p.rows;
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
@@ -223,8 +249,8 @@ __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int w
         f.x[r] = live && c < h ? load_row8(x, c, h) : fill(0.0f);
     }
     const float inv_h = 1.0f / float(h);
-    const float mean = row_sum(total(f), width, buf[0]) * inv_h;
-    const float rstd = 1.0f / sqrtf(row_sum(squares(f, mean, width, t, h), width, buf[1]) * inv_h + p.eps);
+    const float mean = row_sum(total(f), g, row_buf(sums[0], g, 1)) * inv_h;
+    const float rstd = rsqrtf(row_sum(squares(f, mean, width, t, h), g, row_buf(sums[1], g, 1)) * inv_h + p.eps);
     if (!live) return;
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
@@ -244,15 +270,16 @@ __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int w
 // row read three times (the second and third time from L2).
 template <typename X, typename Y>
 __global__ void __launch_bounds__(512) cm_layer_norm_any_kernel(NormParams p) {
-    __shared__ float buf[2][32];
+    __shared__ __align__(16) float sums[2][kRowBuf];
+    const Group g{int(blockDim.x)};
     const int64_t row = blockIdx.x;
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
     float s = 0.0f;
     for (int64_t c = threadIdx.x; c < p.h; c += blockDim.x) s += to_f(x[c]);
-    const float mean = row_sum(s, int(blockDim.x), buf[0]) / float(p.h);
+    const float mean = row_sum(s, g, sums[0]) / float(p.h);
     float q = 0.0f;
     for (int64_t c = threadIdx.x; c < p.h; c += blockDim.x) q += (to_f(x[c]) - mean) * (to_f(x[c]) - mean);
-    const float rstd = 1.0f / sqrtf(row_sum(q, int(blockDim.x), buf[1]) / float(p.h) + p.eps);
+    const float rstd = rsqrtf(row_sum(q, g, sums[1]) / float(p.h) + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -269,62 +296,60 @@ __global__ void __launch_bounds__(512) cm_layer_norm_any_kernel(NormParams p) {
 // One pass over x, dy and res gives dx and the sums over rows: persistent CTAs
 // stream rows through a ring of S row buffers as the forward kernel does.  A
 // thread owns the same R vectors of columns in every row, so dgamma and dbeta
-// collect in its registers; after the rows' sums the row is read again from the
+// collect in its registers; after the row's sums the row is read again from the
 // ring, not held in registers, which leaves those to the sums.  At the end the
 // groups of a CTA are added in order and written as its part.
 template <typename X, typename Y, int R, int S>
-__global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_kernel(NormParams p, int width) {
+__global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_kernel(const __grid_constant__ NormParams p,
+                                                                                      int width) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 buf[2][32];
-    const int per = int(blockDim.x) / width, group = int(threadIdx.x) / width, t = int(threadIdx.x) - group * width;
+    __shared__ __align__(16) float sums[2][kRowBuf];
+    const Group g(width);
+    const int t = int(threadIdx.x) - g.index * width, per = int(blockDim.x) / width;
     const int h = int(p.h), h8 = (h + 7) / 8 * 8;
-    uint8_t *const sg = smem;
-    uint8_t *const ring = sg + (p.gamma ? h8 * (p.p_f32 ? 4 : 2) : 0);
+    float *const gamma = reinterpret_cast<float *>(smem);
+    uint8_t *const ring = smem + h8 * 4;
     const int xs = h8 * int(sizeof(X)), ys = h8 * int(sizeof(Y));
     const int row_bytes = xs + ys + (p.res ? xs : 0);
-    const int64_t first = int64_t(blockIdx.x) * per, step = int64_t(gridDim.x) * per;
-    auto slot = [&](int st) { return ring + (st * per + group) * row_bytes; };
-    auto ask = [&](int64_t base, int st) {
-        const int64_t row = base + group;
-        if (row < p.rows) {
+    const int64_t step = int64_t(gridDim.x) * per, row0 = int64_t(blockIdx.x) * per + g.index;
+    auto slot = [&](int st) { return ring + (st * per + g.index) * row_bytes; };
+    int64_t ask_row = row0;
+    const X *ask_x = static_cast<const X *>(p.x) + row0 * p.ldx, *ask_r = static_cast<const X *>(p.res) + row0 * p.ldr;
+    const Y *ask_y = static_cast<const Y *>(p.dy) + row0 * p.lddy;
+    auto ask = [&](int st) {
+        if (ask_row < p.rows) {
             uint8_t *d = slot(st);
-            const X *x = static_cast<const X *>(p.x) + row * p.ldx, *res = static_cast<const X *>(p.res) + row * p.ldr;
-            const Y *dy = static_cast<const Y *>(p.dy) + row * p.lddy;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int c = (r * width + t) * 8;
-                if (c >= h) break;
-                copy_row8(reinterpret_cast<X *>(d), x, c, h);
-                copy_row8(reinterpret_cast<Y *>(d + xs), dy, c, h);
-                if (p.res) copy_row8(reinterpret_cast<X *>(d + xs + ys), res, c, h);
+                copy_vec(reinterpret_cast<X *>(d), ask_x, c, h);
+                copy_vec(reinterpret_cast<Y *>(d + xs), ask_y, c, h);
+                if (p.res) copy_vec(reinterpret_cast<X *>(d + xs + ys), ask_r, c, h);
             }
         }
         copy_commit();
+        ask_row += step;
+        ask_x += step * p.ldx;
+        ask_y += step * p.lddy;
+        ask_r += step * p.ldr;
     };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) ask(k);
+    stage_param(gamma, p.gamma, p.p_f32, 1.0f, h);
     V8 a[R], b[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = (r * width + t) * 8;
-        if (group == 0 && c < h) copy_param8(sg, p.gamma, p.p_f32, c, h);
-        a[r] = b[r] = fill(0.0f);
-    }
-#pragma unroll
-    for (int k = 0; k < S - 1; ++k) ask(first + k * step, k);
-    if (per > 1) {
-        copy_wait<0>();
-        __syncthreads();
-    }
+    for (int r = 0; r < R; ++r) a[r] = b[r] = fill(0.0f);
+    __syncthreads();
     const float inv_h = 1.0f / float(h);
     float mean = 0.0f, rstd = 0.0f;
-    if (first + group < p.rows) {
-        mean = p.mean[first + group];
-        rstd = p.rstd[first + group];
+    if (row0 < p.rows) {
+        mean = p.mean[row0];
+        rstd = p.rstd[row0];
     }
     int st = 0, flip = 0;
-    for (int64_t base = first; base < p.rows; base += step) {
-        ask(base + (S - 1) * step, (st + S - 1) % S);
-        const int64_t row = base + group;
-        const bool live = row < p.rows;
+    X *dx = static_cast<X *>(p.out) + row0 * p.ldo;
+    for (int64_t row = row0; row < p.rows; row += step) {
+        ask(st == 0 ? S - 1 : st - 1);
         float next_mean = 0.0f, next_rstd = 0.0f;
         if (row + step < p.rows) {
             next_mean = p.mean[row + step];
@@ -332,53 +357,45 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
         }
         copy_wait<S - 1>();
         const uint8_t *d = slot(st);
-        float s1 = 0.0f, s2 = 0.0f;
-        if (live) {
-            const F2 rs = both(rstd), m = both(-mean);
-            F2 q1 = both(0.0f), q2 = both(0.0f);
+        const F2 rs = both(rstd), m = both(-mean);
+        F2 q1 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int c = (r * width + t) * 8;
-                if (c >= h) break;
-                const V8 x = load8(reinterpret_cast<const X *>(d) + c), y = load8(reinterpret_cast<const Y *>(d + xs) + c);
-                const V8 g = get_param8(sg, p.gamma, p.p_f32, 1.0f, c);
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+            if (c >= h) break;
+            const V8 x = load8(reinterpret_cast<const X *>(d) + c), y = load8(reinterpret_cast<const Y *>(d + xs) + c);
+            const V8 w = load8(gamma + c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // past a ragged end dy is zero: nothing is added
-                    const F2 xh = mul(add(x.p[i], m), rs), u = mul(y.p[i], g.p[i]);
-                    q1 = add(q1, u);
-                    q2 = fma(u, xh, q2);
-                    a[r].p[i] = fma(y.p[i], xh, a[r].p[i]);
-                    b[r].p[i] = add(b[r].p[i], y.p[i]);
-                }
-            }
-            s1 = sum(q1);
-            s2 = sum(q2);
-        }
-        const float2 rowsum = row_sum2(s1, s2, width, buf[flip]);
-        if (live) {
-            // dx = rstd u - (x - mean) k - rstd s1 + res, k = rstd^2 s2
-            s1 = rowsum.x * inv_h;
-            s2 = rowsum.y * inv_h;
-            const F2 rs = both(rstd), m = both(-mean), k = both(-rstd * rstd * s2), off = both(-rstd * s1);
-            X *dx = static_cast<X *>(p.out) + row * p.ldo;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int c = (r * width + t) * 8;
-                if (c >= h) break;
-                const V8 x = load8(reinterpret_cast<const X *>(d) + c), y = load8(reinterpret_cast<const Y *>(d + xs) + c);
-                const V8 g = get_param8(sg, p.gamma, p.p_f32, 1.0f, c);
-                V8 o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o.p[i] = fma(mul(y.p[i], g.p[i]), rs, fma(add(x.p[i], m), k, off));
-                if (p.res) {
-                    const V8 z = load8(reinterpret_cast<const X *>(d + xs + ys) + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o.p[i] = add(o.p[i], z.p[i]);
-                }
-                store_row8(dx, c, h, o);
+            for (int i = 0; i < 4; ++i) {
+                // past a ragged end dy is zero: nothing is added
+                const F2 xh = mul(add(x.p[i], m), rs), u = mul(y.p[i], w.p[i]);
+                q1 = add(q1, u);
+                q2 = fma(u, xh, q2);
+                a[r].p[i] = fma(y.p[i], xh, a[r].p[i]);
+                b[r].p[i] = add(b[r].p[i], y.p[i]);
             }
         }
+        const float2 rowsum = row_sum2(sum(q1), sum(q2), g, row_buf(sums[flip], g, 2));
+        // dx = rstd u - (x - mean) k - rstd s1 + res, k = rstd^2 s2
+        const float s1 = rowsum.x * inv_h, s2 = rowsum.y * inv_h;
+        const F2 k = both(-rstd * rstd * s2), off = both(-rstd * s1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+            if (c >= h) break;
+            const V8 x = load8(reinterpret_cast<const X *>(d) + c), y = load8(reinterpret_cast<const Y *>(d + xs) + c);
+            const V8 w = load8(gamma + c);
+            V8 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o.p[i] = fma(mul(y.p[i], w.p[i]), rs, fma(add(x.p[i], m), k, off));
+            if (p.res) {
+                const V8 z = load8(reinterpret_cast<const X *>(d + xs + ys) + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o.p[i] = add(o.p[i], z.p[i]);
+            }
+            store_row8(dx, c, h, o);
+        }
+        dx += step * p.ldo;
         mean = next_mean;
         rstd = next_rstd;
         flip ^= 1;
@@ -403,19 +420,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
     // [group][2][h8] over the ring, which nobody uses any more: 8 bytes a
     // column and group, of the S (2 + 2) at least that the ring has
     __syncthreads();
-    float *const sums = reinterpret_cast<float *>(ring);
+    float *const parts_of = reinterpret_cast<float *>(ring);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int c = (r * width + t) * 8;
         if (c >= h) break;
-        store8(sums + group * 2 * h8 + c, a[r]);
-        store8(sums + (group * 2 + 1) * h8 + c, b[r]);
+        store8(parts_of + g.index * 2 * h8 + c, a[r]);
+        store8(parts_of + (g.index * 2 + 1) * h8 + c, b[r]);
     }
     __syncthreads();
     for (int c = int(threadIdx.x); c < 2 * h; c += int(blockDim.x)) {
         const int o = c < h ? c : c - h + h8;
         float v = 0.0f;
-        for (int g = 0; g < per; ++g) v += sums[g * 2 * h8 + o];
+        for (int i = 0; i < per; ++i) v += parts_of[i * 2 * h8 + o];
         mine[c] = v;
     }
 }
@@ -437,7 +454,8 @@ __device__ __forceinline__ V8 gather(const float (&f)[8]) {
 // rows are then the column kernel's.
 template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(512) cm_layer_norm_dx_any_kernel(NormParams p) {
-    __shared__ float2 buf[32];
+    __shared__ __align__(16) float sums[kRowBuf];
+    const Group gr{int(blockDim.x)};
     const int64_t row = blockIdx.x;
     const X *x = static_cast<const X *>(p.x) + row * p.ldx;
     const Y *dy = static_cast<const Y *>(p.dy) + row * p.lddy;
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(512) cm_layer_norm_dx_any_kernel(NormParams p)
             s2 += u[i] * xh[i];
         }
     }
-    const float2 sum = row_sum2(s1, s2, int(blockDim.x), buf);
+    const float2 sum = row_sum2(s1, s2, gr, sums);
     s1 = sum.x / float(p.h);
     s2 = sum.y / float(p.h);
     X *dx = static_cast<X *>(p.out) + row * p.ldo;
@@ -586,11 +604,13 @@ __global__ void __launch_bounds__(256) cm_sum_parts_kernel(const float *partial,
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+constexpr int kMostSms = 160;
+
 int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 152;
-    return std::min(n, 160);
+    return std::min(n, kMostSms);
 }
 
 // Chunks of rows for the column sums: enough CTAs for two rounds of the SMs,
@@ -600,12 +620,7 @@ int64_t chunks_for(int64_t rows, int64_t cols) {
     return std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, std::max<int64_t>(1, 608 / blocks)));
 }
 
-constexpr int64_t kSmemCta = 227 * 1024, kSmemSm = 228 * 1024;
-
-// CTAs of a persistent launch: at most `most` an SM, if shared memory has room.
-int64_t resident(int sms, int64_t smem, int most) {
-    return int64_t(sms) * std::max<int64_t>(1, std::min<int64_t>(most, kSmemSm / (smem + 1024 + 512)));
-}
+constexpr int64_t kSmemCta = 227 * 1024;
 
 // The sums over rows of the partial sums of `parts` CTAs.
 void sum_parts(const float *partial, int64_t parts, int64_t h, int64_t stride, void *out0, void *out1, int f32,
@@ -616,21 +631,45 @@ void sum_parts(const float *partial, int64_t parts, int64_t h, int64_t stride, v
 
 template <typename K>
 cudaError_t opt_in(K kernel, int64_t smem) {
-    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemCta - 1024))
+    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemCta - 3 * 1024))
                             : cudaSuccess;
 }
 
-int rows_per_cta(int width) { return std::max(1, kRingThreads / width); }
+int row_width(int64_t vecs, int R) { return int((vecs + 32 * R - 1) / (32 * R)) * 32; }
 
-template <typename X, typename Y, int R>
-cudaError_t forward_ring(const NormParams &p, int width, int per, int64_t smem, int64_t ctas, cudaStream_t stream) {
-    cudaError_t e = opt_in(cm_layer_norm_ring_kernel<X, Y, R, 3>, smem);
-    if (e != cudaSuccess) return e;
-    cm_layer_norm_ring_kernel<X, Y, R, 3><<<unsigned(ctas), unsigned(width * per), size_t(smem), stream>>>(p, width);
-    return cudaGetLastError();
+// Geometry of a persistent launch over rows of h elements: R vectors a thread,
+// `per` rows at a time of `width` threads each, S row buffers a group.  As many
+// rows as 512 threads and shared memory hold with two buffers each, then a third
+// buffer if it fits; one CTA an SM.  ctas = 0 where a row is too long.
+struct RingPlan {
+    int R = 0, S = 0, width = 0, per = 1;
+    int64_t ctas = 0, smem = 0;
+};
+
+RingPlan ring_plan(int64_t rows, int64_t h, int64_t row_bytes, int64_t fixed_bytes, int sms) {
+    RingPlan r;
+    const int64_t vecs = (h + 7) / 8, limit = kSmemCta - 3 * 1024 /* the kernels' own buffers */;
+    r.R = vecs < 64 ? 1 : vecs < 128 ? 2 : 4;
+    r.width = row_width(vecs, r.R);
+    if (r.width > kRingThreads) return r;
+    const int64_t row = vecs * 8 * row_bytes, fixed = vecs * 8 * fixed_bytes;
+    for (r.per = std::min(kRingThreads / r.width, kRingThreads / 32 - 1); r.per > 1 && fixed + 2 * r.per * row > limit;)
+        --r.per;
+    r.S = fixed + 3 * r.per * row <= limit ? 3 : 2;
+    r.smem = fixed + r.S * r.per * row;
+    if (r.smem > limit) return r;
+    r.ctas = std::min<int64_t>(sms, (rows + r.per - 1) / r.per);
+    return r;
 }
 
-int row_width(int64_t vecs, int R) { return int((vecs + 32 * R - 1) / (32 * R)) * 32; }
+template <typename X, typename Y, int R, int S>
+cudaError_t forward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
+    cudaError_t e = opt_in(cm_layer_norm_ring_kernel<X, Y, R, S>, r.smem);
+    if (e != cudaSuccess) return e;
+    cm_layer_norm_ring_kernel<X, Y, R, S>
+        <<<unsigned(r.ctas), unsigned(r.width * r.per), size_t(r.smem), stream>>>(p, r.width);
+    return cudaGetLastError();
+}
 
 template <typename X, typename Y>
 cudaError_t forward(const NormParams &p, cudaStream_t stream) {
@@ -642,18 +681,14 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
         cm_layer_norm_any_kernel<X, Y><<<unsigned(p.rows), 512, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    const int sms = sm_count();
-    {
-        const int R = vecs < 64 ? 1 : vecs <= 1024 ? 2 : 4;
-        const int width = row_width(vecs, R), per = rows_per_cta(width);
-        const int64_t ps = (p.p_f32 ? 4 : 2) * ((p.gamma ? 1 : 0) + (p.beta ? 1 : 0));
-        const int64_t smem = vecs * 8 * (ps + int64_t(sizeof(X)) * 3 * per);
-        const int64_t ctas = resident(sms, smem, 2);
-        // the ring pays once a CTA has a few rows to run ahead on
-        if (width <= kRingThreads && smem <= kSmemCta - 1024 && p.rows >= 4 * ctas * per)
-            return R == 1   ? forward_ring<X, Y, 1>(p, width, per, smem, ctas, stream)
-                   : R == 2 ? forward_ring<X, Y, 2>(p, width, per, smem, ctas, stream)
-                            : forward_ring<X, Y, 4>(p, width, per, smem, ctas, stream);
+    const RingPlan r = ring_plan(p.rows, p.h, sizeof(X), 8, sm_count());
+    // the ring pays once a group has a few rows to run ahead on
+    if (r.ctas > 0 && p.rows >= 4 * r.ctas * r.per) {
+        if (r.S == 3)
+            return r.R == 1   ? forward_ring<X, Y, 1, 3>(p, r, stream)
+                   : r.R == 2 ? forward_ring<X, Y, 2, 3>(p, r, stream)
+                              : forward_ring<X, Y, 4, 3>(p, r, stream);
+        if (r.R == 4) return forward_ring<X, Y, 4, 2>(p, r, stream);   // shorter rows leave room for three
     }
     // all of a row's loads at once
     const int R = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
@@ -666,31 +701,6 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
     else
         cm_layer_norm_kernel<X, Y, 4><<<grid, threads, 0, stream>>>(p, width);
     return cudaGetLastError();
-}
-
-// Launch geometry of the one-pass backward kernel; ctas = 0 where a row is
-// too long for it.  Alignment aside, it depends on extents and types only, so
-// that the workspace's size can follow it.
-struct RingPlan {
-    int R = 0, S = 0, width = 0, per = 1;
-    int64_t ctas = 0, smem = 0;
-};
-
-RingPlan ring_plan(int64_t rows, int64_t h, int64_t xs, int64_t ys, bool res, int64_t gamma_bytes, int sms) {
-    RingPlan r;
-    const int64_t vecs = (h + 7) / 8;
-    if (vecs > 2048) return r;
-    r.R = vecs < 64 ? 1 : vecs <= 1024 ? 2 : 4;
-    r.width = row_width(vecs, r.R);
-    r.per = rows_per_cta(r.width);
-    const int64_t row = vecs * 8 * (xs + ys + (res ? xs : 0)) * r.per, fixed = vecs * 8 * gamma_bytes;
-    for (r.S = 3; r.S >= 2; --r.S) {
-        r.smem = fixed + r.S * row;
-        if (r.smem <= kSmemCta - 1024) break;
-    }
-    if (r.S < 2) return r;
-    r.ctas = std::min<int64_t>(resident(sms, r.smem, 1), (rows + r.per - 1) / r.per);
-    return r;
 }
 
 template <typename X, typename Y, int R, int S>
@@ -711,8 +721,7 @@ cudaError_t backward(NormParams p, cudaStream_t stream) {
     const bool vec = in_vec && aligned16(p.out) && aligned16(p.gamma) && p.ldo % 8 == 0 &&
                      (!p.res || (aligned16(p.res) && p.ldr % 8 == 0));
     if (vec) {
-        const RingPlan r = ring_plan(p.rows, p.h, sizeof(X), sizeof(Y), p.res != nullptr,
-                                     p.gamma ? (p.p_f32 ? 4 : 2) : 0, sm_count());
+        const RingPlan r = ring_plan(p.rows, p.h, int64_t(sizeof(X)) * (p.res ? 2 : 1) + int64_t(sizeof(Y)), 4, sm_count());
         if (r.ctas > 0) {
             const cudaError_t e = r.S == 3 ? (r.R == 1   ? backward_ring<X, Y, 1, 3>(p, r, stream)
                                               : r.R == 2 ? backward_ring<X, Y, 2, 3>(p, r, stream)
@@ -746,13 +755,11 @@ cudaError_t launch_layer_norm(const NormParams &p, cm_dtype x, cm_dtype y, cudaS
     return y == CM_BF16 ? forward<float, bf16>(p, stream) : forward<float, float>(p, stream);
 }
 
-// The most parts that any types of a call with these extents make: a
-// persistent launch has one CTA an SM, and no more than rows need.  The SM count is an upper bound, so that the size can be asked
-// for without a device.
+// The most parts that a call with these extents makes, whatever its types: a
+// persistent launch has one CTA an SM, at most as many as there are rows.  The
+// SM count is an upper bound, so that the size can be asked for without a device.
 int64_t norm_backward_parts(int64_t rows, int64_t h) {
-    constexpr int kMostSms = 160;
-    const RingPlan r = ring_plan(rows, h, 2, 2, false, 0, kMostSms);
-    return std::max(chunks_for(rows, h), r.ctas);
+    return std::max(chunks_for(rows, h), std::min<int64_t>(kMostSms, std::max<int64_t>(1, rows)));
 }
 
 cudaError_t launch_layer_norm_backward(const NormParams &p, cm_dtype x, cm_dtype y, cudaStream_t stream) {
