@@ -14,6 +14,7 @@
 
 #include <algorithm>
 
+#include "cm_device.cuh"
 #include "cm_linear.cuh"
 #include "cm_vec.cuh"
 
@@ -92,11 +93,61 @@ constexpr int kRowBuf = 128;
 __device__ __forceinline__ float *row_buf(float *buf, const Group &g, int floats) {
     return buf + g.index * ((g.warps * floats + 3) & ~3);
 }
+// The sum of one row, or the sums of two.
+__device__ __forceinline__ void rows_sum(float a, float, const Group &g, float *buf, float (&v)[1]) {
+    v[0] = row_sum(a, g, row_buf(buf, g, 1));
+}
+__device__ __forceinline__ void rows_sum(float a, float b, const Group &g, float *buf, float (&v)[2]) {
+    const float2 q = row_sum2(a, b, g, row_buf(buf, g, 2));
+    v[0] = q.x;
+    v[1] = q.y;
+}
+
+// The columns of a CTA: all, or its half of them in a cluster of two.
+struct Columns {
+    int half, first, count, rank, cta, ctas;
+    __device__ Columns(int64_t h, bool split) {
+        half = split ? int((h + 15) / 16 * 8) : int(h);
+        rank = split ? int(blockIdx.x & 1) : 0;
+        first = rank * half;
+        count = split ? min(half, int(h) - first) : half;
+        cta = split ? int(blockIdx.x >> 1) : int(blockIdx.x);
+        ctas = split ? int(gridDim.x >> 1) : int(gridDim.x);
+    }
+};
+__device__ __forceinline__ float of_other(const float *slot, int rank) {
+    float o;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(o)
+                 : "r"(dev::mapa_shared(dev::smem_u32(slot), uint32_t(rank ^ 1)))
+                 : "memory");
+    return o;
+}
+// The sum of a row from the sums of its halves, in their order, so that both
+// CTAs have the same.  All threads of both call it; `slot` is one of two that
+// take turns, so that the next sum is not written before this one is read.
+__device__ __forceinline__ float with_other(float v, float *slot, int rank) {
+    if (threadIdx.x == 0) *slot = v;
+    dev::cluster_sync();
+    const float o = of_other(slot, rank);
+    return rank == 0 ? v + o : o + v;
+}
 
 // A parameter vector to shared memory as fp32, 1 (or 0) where there is none.
-__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int h) {
-    for (int c = int(threadIdx.x) * 8; c < h; c += int(blockDim.x) * 8)
-        store8(dst + c, load_param8(p, f32, null_value, c, h));
+// The first and second halves of the vectors lie in two planes of h8 / 2, so
+// that neighbouring threads read neighbouring 16 bytes.  Columns c0 .. c0 + h.
+__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int c0, int h, int h8) {
+    for (int c = int(threadIdx.x) * 8; c < h; c += int(blockDim.x) * 8) {
+        const V8 v = load_param8(p, f32, null_value, c0 + c, c0 + h);
+        const float2 a0 = parts(v.p[0]), a1 = parts(v.p[1]), b0 = parts(v.p[2]), b1 = parts(v.p[3]);
+        *reinterpret_cast<float4 *>(dst + c / 2) = make_float4(a0.x, a0.y, a1.x, a1.y);
+        *reinterpret_cast<float4 *>(dst + (h8 + c) / 2) = make_float4(b0.x, b0.y, b1.x, b1.y);
+    }
+}
+__device__ __forceinline__ V8 staged_param(const float *src, int c, int h8) {
+    const float4 a = *reinterpret_cast<const float4 *>(src + c / 2);
+    const float4 b = *reinterpret_cast<const float4 *>(src + (h8 + c) / 2);
+    return {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
 // Asynchronous copy of the vector at column c of a row of h to its place in `dst`.
 template <typename T>
@@ -112,7 +163,7 @@ __device__ __forceinline__ void copy_vec(T *dst, const T *row, int c, int h) {
 
 // ---- forward ------------------------------------------------------------------
 
-constexpr int kRingThreads = 512;   // of a persistent CTA, as whole rows
+constexpr int kRingThreads = 512;   // of a persistent CTA at most, as whole groups
 
 // A thread's share of a row: R vectors, vector r at column (r width + t) 8,
 // t = its place in the group.
@@ -166,70 +217,97 @@ __device__ __forceinline__ V8 scaled(const V8 &x, float mean, float rstd, const 
     return y;
 }
 
-// Many rows: persistent CTAs stream their rows through a ring of S row buffers
-// in shared memory, filled by asynchronous copies S - 1 rows ahead, so that
-// DRAM stays busy through the two reductions of a row.  A thread copies just
-// the vectors that it reads itself: the ring needs no barrier.  gamma and beta
-// stay in shared memory as fp32.  What is left bounds the kernel by instructions
-// as much as by memory: hence four vectors a thread, pairs of fp32, and no
-// test for missing parameters in the loop.
-template <typename X, typename Y, int R, int S>
+// Many rows: persistent CTAs stream their rows through a ring of S buffers in
+// shared memory, filled by asynchronous copies S - 1 steps ahead, so that DRAM
+// stays busy through the reductions.  A thread copies just the vectors that it
+// reads itself: the ring needs no barrier.  A group takes NR rows a step: what
+// bounds it is the latency of the two reductions, one after the other, and two
+// rows share that, and the reads of gamma and beta (8192 x 8192 in bf16: 50 us
+// with two, 68 with one).  Rows longer than 8192 go one by one, to keep the
+// registers.  gamma and beta stay in shared memory as fp32.
+//
+// SPLIT: rows longer than 16384 are shared by a cluster of two CTAs, the first
+// half of the columns in one and the second in the other; they exchange a
+// row's sums through shared memory.
+template <typename X, typename Y, int R, int NR, int S, bool SPLIT>
 __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(const __grid_constant__ NormParams p, int width) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float sums[2][2][kRowBuf];
+    __shared__ float other[SPLIT ? 4 : 1];
+    static_assert(!SPLIT || NR == 1, "a cluster exchanges one row's sums");
     const Group g(width);
     const int t = int(threadIdx.x) - g.index * width, per = int(blockDim.x) / width;
-    const int h = int(p.h), h8 = (h + 7) / 8 * 8;
+    const Columns cols(p.h, SPLIT);
+    const int h = cols.count, h8 = (cols.half + 7) / 8 * 8, c0 = cols.first;
     float *const gamma = reinterpret_cast<float *>(smem), *const beta = gamma + h8;
-    X *const ring = reinterpret_cast<X *>(beta + h8) + g.index * h8;
-    const int stage = per * h8;
-    const int64_t step = int64_t(gridDim.x) * per;
-    int64_t ask_row = int64_t(blockIdx.x) * per + g.index;
-    const X *ask_x = static_cast<const X *>(p.x) + ask_row * p.ldx;
+    X *const ring = reinterpret_cast<X *>(beta + h8) + g.index * NR * h8;
+    const int stage = per * NR * h8;
+    const int64_t step = int64_t(cols.ctas) * per * NR, row0 = (int64_t(cols.cta) * per + g.index) * NR;
+    int64_t ask_row = row0;
+    const X *ask_x = static_cast<const X *>(p.x) + row0 * p.ldx + c0;
     auto ask = [&](int st) {
-        if (ask_row < p.rows) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) copy_vec(ring + st * stage, ask_x, (r * width + t) * 8, h);
-        }
+        for (int k = 0; k < NR; ++k)
+            if (ask_row + k < p.rows) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    copy_vec(ring + st * stage + k * h8, ask_x + k * p.ldx, (r * width + t) * 8, h);
+            }
         copy_commit();
         ask_row += step;
         ask_x += step * p.ldx;
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) ask(k);
-    stage_param(gamma, p.gamma, p.p_f32, 1.0f, h);
-    stage_param(beta, p.beta, p.p_f32, 0.0f, h);
+    stage_param(gamma, p.gamma, p.p_f32, 1.0f, c0, h, h8);
+    stage_param(beta, p.beta, p.p_f32, 0.0f, c0, h, h8);
     __syncthreads();
-    const float inv_h = 1.0f / float(h);
+    const float inv_h = 1.0f / float(p.h);
     int st = 0, flip = 0;
-    Y *y = static_cast<Y *>(p.out) + (int64_t(blockIdx.x) * per + g.index) * p.ldo;
-    for (int64_t row = int64_t(blockIdx.x) * per + g.index; row < p.rows; row += step) {
+    Y *y = static_cast<Y *>(p.out) + row0 * p.ldo + c0;
+    for (int64_t row = row0; row < p.rows; row += step) {
         ask(st == 0 ? S - 1 : st - 1);
         copy_wait<S - 1>();
-        Share<R> f;
+        const bool second = NR > 1 && row + 1 < p.rows;   // its buffer holds an older row if not
+        Share<R> f[NR];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int c = (r * width + t) * 8;
-            f.x[r] = c < h ? load8(ring + st * stage + c) : fill(0.0f);
+#pragma unroll
+            for (int k = 0; k < NR; ++k) f[k].x[r] = c < h ? load8(ring + st * stage + k * h8 + c) : fill(0.0f);
         }
-        const float mean = row_sum(total(f), g, row_buf(sums[flip][0], g, 1)) * inv_h;
-        const float var = row_sum(squares(f, mean, width, t, h), g, row_buf(sums[flip][1], g, 1)) * inv_h;
-        const float rstd = rsqrtf(var + p.eps);
-        if (t == 0) {
-            if (p.mean) p.mean[row] = mean;
-            if (p.rstd) p.rstd[row] = rstd;
+        float mean[NR], rstd[NR];
+        rows_sum(total(f[0]), NR > 1 ? total(f[NR - 1]) : 0.0f, g, sums[flip][0], mean);
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+            if (SPLIT) mean[k] = with_other(mean[k], &other[flip], cols.rank);
+            mean[k] *= inv_h;
+        }
+        rows_sum(squares(f[0], mean[0], width, t, h), NR > 1 ? squares(f[NR - 1], mean[NR - 1], width, t, h) : 0.0f, g,
+                 sums[flip][1], rstd);
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+            if (SPLIT) rstd[k] = with_other(rstd[k], &other[2 + flip], cols.rank);
+            rstd[k] = rsqrtf(rstd[k] * inv_h + p.eps);
+            if (t == 0 && c0 == 0 && (k == 0 || second)) {
+                if (p.mean) p.mean[row + k] = mean[k];
+                if (p.rstd) p.rstd[row + k] = rstd[k];
+            }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int c = (r * width + t) * 8;
             if (c >= h) break;
-            store_row8(y, c, h, scaled(f.x[r], mean, rstd, load8(gamma + c), load8(beta + c)));
+            const V8 w = staged_param(gamma, c, h8), b = staged_param(beta, c, h8);
+            store_row8(y, c, h, scaled(f[0].x[r], mean[0], rstd[0], w, b));
+            if (second) store_row8(y + p.ldo, c, h, scaled(f[NR - 1].x[r], mean[NR - 1], rstd[NR - 1], w, b));
         }
         y += step * p.ldo;
         st = st + 1 == S ? 0 : st + 1;
         flip ^= 1;
     }
     copy_wait<0>();
+    if (SPLIT) dev::cluster_sync();   // the other CTA has read this one's last sum
 }
 
 // Few rows: `width` threads hold a row in registers.
@@ -299,23 +377,33 @@ __global__ void __launch_bounds__(512) cm_layer_norm_any_kernel(NormParams p) {
 // collect in its registers; after the row's sums the row is read again from the
 // ring, not held in registers, which leaves those to the sums.  At the end the
 // groups of a CTA are added in order and written as its part.
-template <typename X, typename Y, int R, int S>
+//
+// G: type of the staged gamma, fp32, or bf16 where that is what it came as and
+// the longer rows leave no room for more.
+//
+// SPLIT: rows too long for one CTA are shared by a cluster of two, the first
+// half of the columns in one and the second in the other; they exchange a
+// row's two sums through shared memory.
+template <typename X, typename Y, typename G, int R, int S, bool SPLIT>
 __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_kernel(const __grid_constant__ NormParams p,
                                                                                       int width) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float sums[2][kRowBuf];
+    __shared__ float other[SPLIT ? 4 : 1];
     const Group g(width);
     const int t = int(threadIdx.x) - g.index * width, per = int(blockDim.x) / width;
-    const int h = int(p.h), h8 = (h + 7) / 8 * 8;
-    float *const gamma = reinterpret_cast<float *>(smem);
-    uint8_t *const ring = smem + h8 * 4;
+    const Columns cols(p.h, SPLIT);
+    const int h = cols.count, h8 = (cols.half + 7) / 8 * 8, c0 = cols.first;
+    G *const gamma = reinterpret_cast<G *>(smem);
+    uint8_t *const ring = smem + h8 * int(sizeof(G));
     const int xs = h8 * int(sizeof(X)), ys = h8 * int(sizeof(Y));
     const int row_bytes = xs + ys + (p.res ? xs : 0);
-    const int64_t step = int64_t(gridDim.x) * per, row0 = int64_t(blockIdx.x) * per + g.index;
+    const int64_t step = int64_t(cols.ctas) * per, row0 = int64_t(cols.cta) * per + g.index;
     auto slot = [&](int st) { return ring + (st * per + g.index) * row_bytes; };
     int64_t ask_row = row0;
-    const X *ask_x = static_cast<const X *>(p.x) + row0 * p.ldx, *ask_r = static_cast<const X *>(p.res) + row0 * p.ldr;
-    const Y *ask_y = static_cast<const Y *>(p.dy) + row0 * p.lddy;
+    const X *ask_x = static_cast<const X *>(p.x) + row0 * p.ldx + c0;
+    const X *ask_r = static_cast<const X *>(p.res) + row0 * p.ldr + c0;
+    const Y *ask_y = static_cast<const Y *>(p.dy) + row0 * p.lddy + c0;
     auto ask = [&](int st) {
         if (ask_row < p.rows) {
             uint8_t *d = slot(st);
@@ -335,19 +423,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) ask(k);
-    stage_param(gamma, p.gamma, p.p_f32, 1.0f, h);
+    for (int c = int(threadIdx.x) * 8; c < h; c += int(blockDim.x) * 8)
+        store8(gamma + c, load_param8(p.gamma, p.p_f32, 1.0f, c0 + c, c0 + h));
     V8 a[R], b[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) a[r] = b[r] = fill(0.0f);
     __syncthreads();
-    const float inv_h = 1.0f / float(h);
+    const float inv_h = 1.0f / float(p.h);
     float mean = 0.0f, rstd = 0.0f;
     if (row0 < p.rows) {
         mean = p.mean[row0];
         rstd = p.rstd[row0];
     }
     int st = 0, flip = 0;
-    X *dx = static_cast<X *>(p.out) + row0 * p.ldo;
+    X *dx = static_cast<X *>(p.out) + row0 * p.ldo + c0;
     for (int64_t row = row0; row < p.rows; row += step) {
         ask(st == 0 ? S - 1 : st - 1);
         float next_mean = 0.0f, next_rstd = 0.0f;
@@ -375,7 +464,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
                 b[r].p[i] = add(b[r].p[i], y.p[i]);
             }
         }
-        const float2 rowsum = row_sum2(sum(q1), sum(q2), g, row_buf(sums[flip], g, 2));
+        float2 rowsum = row_sum2(sum(q1), sum(q2), g, row_buf(sums[flip], g, 2));
+        if constexpr (SPLIT) {   // one row a step (per = 1): both CTAs make the same steps
+            if (threadIdx.x == 0) other[2 * flip + 1] = rowsum.y;
+            const float x = with_other(rowsum.x, &other[2 * flip], cols.rank), o = of_other(&other[2 * flip + 1], cols.rank);
+            rowsum = make_float2(x, cols.rank == 0 ? rowsum.y + o : o + rowsum.y);
+        }
         // dx = rstd u - (x - mean) k - rstd s1 + res, k = rstd^2 s2
         const float s1 = rowsum.x * inv_h, s2 = rowsum.y * inv_h;
         const F2 k = both(-rstd * rstd * s2), off = both(-rstd * s1);
@@ -402,8 +496,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
         st = st + 1 == S ? 0 : st + 1;
     }
     copy_wait<0>();
+    if constexpr (SPLIT) dev::cluster_sync();   // the other CTA has read this one's last sums
     if (!p.partial) return;
-    float *const mine = p.partial + int64_t(blockIdx.x) * 2 * h;
+    float *const mine = p.partial + int64_t(cols.cta) * 2 * p.h + c0;
     if (per == 1) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -411,8 +506,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 u = parts(a[r].p[i]), v = parts(b[r].p[i]);
-                if (c + 2 * i < h) mine[c + 2 * i] = u.x, mine[h + c + 2 * i] = v.x;
-                if (c + 2 * i + 1 < h) mine[c + 2 * i + 1] = u.y, mine[h + c + 2 * i + 1] = v.y;
+                if (c + 2 * i < h) mine[c + 2 * i] = u.x, mine[p.h + c + 2 * i] = v.x;
+                if (c + 2 * i + 1 < h) mine[c + 2 * i + 1] = u.y, mine[p.h + c + 2 * i + 1] = v.y;
             }
         }
         return;
@@ -639,21 +734,24 @@ int row_width(int64_t vecs, int R) { return int((vecs + 32 * R - 1) / (32 * R)) 
 
 // Geometry of a persistent launch over rows of h elements: R vectors a thread,
 // `per` rows at a time of `width` threads each, S row buffers a group.  As many
-// rows as 512 threads and shared memory hold with two buffers each, then a third
+// rows as the threads and shared memory hold with two buffers each, then a third
 // buffer if it fits; one CTA an SM.  ctas = 0 where a row is too long.
 struct RingPlan {
     int R = 0, S = 0, width = 0, per = 1;
     int64_t ctas = 0, smem = 0;
 };
 
-RingPlan ring_plan(int64_t rows, int64_t h, int64_t row_bytes, int64_t fixed_bytes, int sms) {
+// rows: how many there are for the groups to share; row_bytes: ring bytes a
+// column and buffer; fixed_bytes: bytes a column outside the ring; most_per:
+// groups at most (15 have a barrier each).
+RingPlan ring_plan(int64_t rows, int64_t h, int64_t row_bytes, int64_t fixed_bytes, int most_r, int most_per, int sms) {
     RingPlan r;
     const int64_t vecs = (h + 7) / 8, limit = kSmemCta - 3 * 1024 /* the kernels' own buffers */;
-    r.R = vecs < 64 ? 1 : vecs < 128 ? 2 : 4;
+    r.R = vecs < 64 ? 1 : vecs < 128 ? 2 : most_r;
     r.width = row_width(vecs, r.R);
     if (r.width > kRingThreads) return r;
     const int64_t row = vecs * 8 * row_bytes, fixed = vecs * 8 * fixed_bytes;
-    for (r.per = std::min(kRingThreads / r.width, kRingThreads / 32 - 1); r.per > 1 && fixed + 2 * r.per * row > limit;)
+    for (r.per = std::min(kRingThreads / r.width, most_per); r.per > 1 && fixed + 2 * r.per * row > limit;)
         --r.per;
     r.S = fixed + 3 * r.per * row <= limit ? 3 : 2;
     r.smem = fixed + r.S * r.per * row;
@@ -662,13 +760,29 @@ RingPlan ring_plan(int64_t rows, int64_t h, int64_t row_bytes, int64_t fixed_byt
     return r;
 }
 
-template <typename X, typename Y, int R, int S>
-cudaError_t forward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
-    cudaError_t e = opt_in(cm_layer_norm_ring_kernel<X, Y, R, S>, r.smem);
+// Launches a persistent kernel, in clusters of two CTAs a row if `split`.
+template <typename K>
+cudaError_t launch_ring(K kernel, const NormParams &p, const RingPlan &r, bool split, cudaStream_t stream) {
+    cudaError_t e = opt_in(kernel, r.smem);
     if (e != cudaSuccess) return e;
-    cm_layer_norm_ring_kernel<X, Y, R, S>
-        <<<unsigned(r.ctas), unsigned(r.width * r.per), size_t(r.smem), stream>>>(p, r.width);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(split ? 2 * r.ctas : r.ctas));
+    cfg.blockDim = dim3(unsigned(r.width * r.per));
+    cfg.dynamicSmemBytes = size_t(r.smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, r.width);
+}
+
+template <typename X, typename Y, int R, int NR, int S, bool SPLIT = false>
+cudaError_t forward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
+    return launch_ring(cm_layer_norm_ring_kernel<X, Y, R, NR, S, SPLIT>, p, r, SPLIT, stream);
 }
 
 template <typename X, typename Y>
@@ -681,14 +795,20 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
         cm_layer_norm_any_kernel<X, Y><<<unsigned(p.rows), 512, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    const RingPlan r = ring_plan(p.rows, p.h, sizeof(X), 8, sm_count());
-    // the ring pays once a group has a few rows to run ahead on
-    if (r.ctas > 0 && p.rows >= 4 * r.ctas * r.per) {
-        if (r.S == 3)
-            return r.R == 1   ? forward_ring<X, Y, 1, 3>(p, r, stream)
-                   : r.R == 2 ? forward_ring<X, Y, 2, 3>(p, r, stream)
-                              : forward_ring<X, Y, 4, 3>(p, r, stream);
-        if (r.R == 4) return forward_ring<X, Y, 4, 2>(p, r, stream);   // shorter rows leave room for three
+    const int sms = sm_count();
+    // the rings pay once a group has a few steps to run ahead on
+    if (RingPlan r = ring_plan((p.rows + 1) / 2, p.h, 2 * sizeof(X), 8, 4, 15, sms); vecs <= 1024 && r.ctas > 0) {
+        if (p.rows >= 4 * r.ctas * r.per) {
+            if (r.R == 4) return r.S == 3 ? forward_ring<X, Y, 4, 2, 3>(p, r, stream) : forward_ring<X, Y, 4, 2, 2>(p, r, stream);
+            if (r.S == 3)   // rows this short leave room for three
+                return r.R == 1 ? forward_ring<X, Y, 1, 2, 3>(p, r, stream) : forward_ring<X, Y, 2, 2, 3>(p, r, stream);
+        }
+    } else if (r = ring_plan(p.rows, p.h, sizeof(X), 8, 4, 15, sms); r.ctas > 0) {
+        if (p.rows >= 2 * r.ctas * r.per)
+            return r.S == 3 ? forward_ring<X, Y, 4, 1, 3>(p, r, stream) : forward_ring<X, Y, 4, 1, 2>(p, r, stream);
+    } else if (r = ring_plan(p.rows, (p.h + 15) / 16 * 8, sizeof(X), 8, 4, 1, sms / 2); r.ctas > 0) {
+        if (p.rows >= 2 * r.ctas)
+            return r.S == 3 ? forward_ring<X, Y, 4, 1, 3, true>(p, r, stream) : forward_ring<X, Y, 4, 1, 2, true>(p, r, stream);
     }
     // all of a row's loads at once
     const int R = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
@@ -703,13 +823,9 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <typename X, typename Y, int R, int S>
+template <typename X, typename Y, int R, int S, bool SPLIT = false, typename G = float>
 cudaError_t backward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
-    cudaError_t e = opt_in(cm_layer_norm_backward_ring_kernel<X, Y, R, S>, r.smem);
-    if (e != cudaSuccess) return e;
-    cm_layer_norm_backward_ring_kernel<X, Y, R, S>
-        <<<unsigned(r.ctas), unsigned(r.width * r.per), size_t(r.smem), stream>>>(p, r.width);
-    return cudaGetLastError();
+    return launch_ring(cm_layer_norm_backward_ring_kernel<X, Y, G, R, S, SPLIT>, p, r, SPLIT, stream);
 }
 
 template <typename X, typename Y>
@@ -721,15 +837,25 @@ cudaError_t backward(NormParams p, cudaStream_t stream) {
     const bool vec = in_vec && aligned16(p.out) && aligned16(p.gamma) && p.ldo % 8 == 0 &&
                      (!p.res || (aligned16(p.res) && p.ldr % 8 == 0));
     if (vec) {
-        const RingPlan r = ring_plan(p.rows, p.h, int64_t(sizeof(X)) * (p.res ? 2 : 1) + int64_t(sizeof(Y)), 4, sm_count());
+        const int64_t bytes = int64_t(sizeof(X)) * (p.res ? 2 : 1) + int64_t(sizeof(Y));
+        const int sms = sm_count();
+        RingPlan r = ring_plan(p.rows, p.h, bytes, 4, 4, 15, sms);
+        cudaError_t e = cudaErrorInvalidValue;
         if (r.ctas > 0) {
-            const cudaError_t e = r.S == 3 ? (r.R == 1   ? backward_ring<X, Y, 1, 3>(p, r, stream)
-                                              : r.R == 2 ? backward_ring<X, Y, 2, 3>(p, r, stream)
-                                                         : backward_ring<X, Y, 4, 3>(p, r, stream))
-                                           : (r.R == 1   ? backward_ring<X, Y, 1, 2>(p, r, stream)
-                                              : r.R == 2 ? backward_ring<X, Y, 2, 2>(p, r, stream)
-                                                         : backward_ring<X, Y, 4, 2>(p, r, stream));
-            if (e != cudaSuccess || !sums) return e;
+            e = r.S == 3 ? (r.R == 1   ? backward_ring<X, Y, 1, 3>(p, r, stream)
+                            : r.R == 2 ? backward_ring<X, Y, 2, 3>(p, r, stream)
+                                       : backward_ring<X, Y, 4, 3>(p, r, stream))
+                         : (r.R == 1   ? backward_ring<X, Y, 1, 2>(p, r, stream)
+                            : r.R == 2 ? backward_ring<X, Y, 2, 2>(p, r, stream)
+                                       : backward_ring<X, Y, 4, 2>(p, r, stream));
+        } else if (r = ring_plan(p.rows, p.h, bytes, 2, 4, 1, sms); r.ctas > 0 && !(p.gamma && p.p_f32)) {
+            e = r.S == 3 ? backward_ring<X, Y, 4, 3, false, bf16>(p, r, stream)
+                         : backward_ring<X, Y, 4, 2, false, bf16>(p, r, stream);
+        } else if (r = ring_plan(p.rows, (p.h + 15) / 16 * 8, bytes, 4, 4, 1, sms / 2); r.ctas > 0) {
+            e = r.S == 3 ? backward_ring<X, Y, 4, 3, true>(p, r, stream) : backward_ring<X, Y, 4, 2, true>(p, r, stream);
+        }
+        if (r.ctas > 0 && (e != cudaSuccess || !sums)) return e;
+        if (r.ctas > 0) {
             sum_parts(p.partial, r.ctas, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
             return cudaGetLastError();
         }
