@@ -50,9 +50,10 @@ struct LinearStripParams {
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks;        // 64-wide K slices
-    int tok;            // rows of a tile: 16, 32, 64, 128 or 256
+    int tok;            // rows of a tile: a multiple of 16 up to 256 (of 64 if the row operand is MN-major)
     int row_tiles;
     int splits;         // CTAs of a cluster that share a tile's K slices
+    int ring_bytes;     // shared memory for `stages` slices, and for a split tile's partial sums
     int stages;
     LinearStatus *status;
     uint64_t timeout_ns;
@@ -61,7 +62,7 @@ struct LinearStripParams {
 // layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.
 cudaError_t prepare_linear_strip(int device);
 cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream);
-int linear_strip_stages(int tok, int splits);
+int linear_strip_stages(int tok, int ring_bytes);
 
 // Tiles of 256 x 256 on CTA pairs, for calls with many of them.  A is the row
 // operand here, B the column operand.
@@ -73,6 +74,7 @@ struct LinearPairParams {
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks, mtiles, ntiles, tiles;
+    int bn;                   // columns of a tile: 256 or 128
     int band;                 // row tiles that run through all columns together
     LinearStatus *status;
     uint64_t timeout_ns;

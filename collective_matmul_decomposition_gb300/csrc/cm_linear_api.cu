@@ -114,21 +114,46 @@ bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t k, int 
 
 constexpr int64_t kBandBytes = int64_t(32) << 20;   // of the row operand, kept in L2 while a band runs
 
-cm_status product_pair(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
-                       const LinearEpilogue &e, cudaStream_t stream) {
+// How a product is run: pair (256 x bn tiles on CTA pairs) or strip (128 columns
+// x tok rows, K split over `splits` CTAs).
+struct Choice {
+    bool pair;
+    int bn;
+    int tok, splits, ring_bytes;
+};
+
+Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn) {
+    Choice c = {};
+    if (((rows + 255) / 256) * ((cols + 255) / 256) >= d.clusters) {
+        c.pair = true;
+        c.bn = 256;
+        return c;
+    }
+    c.ring_bytes = 108 * 1024;
+    c.tok = row_mn ? 64 : 16;
+    while (c.tok < 128 && c.tok < rows) c.tok *= 2;
+    const int64_t tiles = ((rows + c.tok - 1) / c.tok) * ((cols + 127) / 128);
+    c.splits = 1;
+    while (c.splits < 8 && tiles * c.splits <= d.sms && c.splits * 2 * kBK <= k) c.splits *= 2;
+    return c;
+}
+
+cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const Operand &b, int64_t rows, int64_t cols,
+                       int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
     LinearPairParams p;
     p.e = e;
     p.rows = rows;
     p.cols = cols;
+    p.bn = c.bn;
     p.kblocks = int((k + kBK - 1) / kBK);
     p.mtiles = int((rows + 255) / 256);
-    p.ntiles = int((cols + 255) / 256);
+    p.ntiles = int((cols + c.bn - 1) / c.bn);
     if (int64_t(p.mtiles) * p.ntiles > 0x7fffffff) return CM_ERR_SHAPE;
     p.tiles = p.mtiles * p.ntiles;
     p.band = int(std::max<int64_t>(1, std::min<int64_t>(p.mtiles, kBandBytes / (int64_t(p.kblocks) * 256 * kBK * 2))));
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
-    if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, 128) ||
+    if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, c.bn / 2) ||
         !map_rows(&p.tmY, e.y, rows, cols, e.ldy, 32, e.y_f32 != 0))
         return CM_ERR_CUDA;
     if (!e.y_f32) {
@@ -144,24 +169,21 @@ cm_status product_pair(const Device &d, const Operand &a, const Operand &b, int6
 // D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
                   const LinearEpilogue &e, cudaStream_t stream) {
-    if (((rows + 255) / 256) * ((cols + 255) / 256) >= d.clusters) return product_pair(d, a, b, rows, cols, k, e, stream);
+    const Choice c = choose(d, rows, cols, k, b.mn_major);
+    if (c.pair) return product_pair(d, c, a, b, rows, cols, k, e, stream);
     LinearStripParams p;
     p.e = e;
     p.rows = rows;
     p.cols = cols;
     p.kblocks = int((k + kBK - 1) / kBK);
-    int tok = b.mn_major ? 64 : 16;
-    while (tok < 128 && tok < rows) tok *= 2;
-    const int64_t row_tiles = (rows + tok - 1) / tok, tiles = row_tiles * ((cols + 127) / 128);
-    int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= 2 * d.sms && splits * 2 <= p.kblocks) splits *= 2;
-    p.tok = tok;
-    p.row_tiles = int(row_tiles);
-    p.splits = splits;
-    p.stages = linear_strip_stages(tok, splits);
+    p.tok = c.tok;
+    p.row_tiles = int((rows + c.tok - 1) / c.tok);
+    p.splits = c.splits;
+    p.ring_bytes = c.ring_bytes;
+    p.stages = linear_strip_stages(c.tok, c.ring_bytes);
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
-    if (!map_operand(&p.tmA, a, cols, k, 128) || !map_operand(&p.tmB, b, rows, k, tok)) return CM_ERR_CUDA;
+    if (!map_operand(&p.tmA, a, cols, k, 128) || !map_operand(&p.tmB, b, rows, k, c.tok)) return CM_ERR_CUDA;
     const int layout = (b.mn_major ? 1 : 0) | (a.mn_major ? 2 : 0);
     return launch_linear_strip(p, layout, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }

@@ -10,7 +10,7 @@
 // run band by band of rows (32 MB of A, which then stay in L2) and column by
 // column inside a band.
 //
-// Epilogue: a warp owns 32 rows x 128 columns of the tile, as two chunks of
+// Epilogue: a warp owns 32 rows x half the columns of the tile, in chunks of
 // 128 bytes a row.  What the chunk needs besides the accumulator (residual,
 // pre-activation, the old value) is fetched by TMA into a swizzled buffer while
 // the products still run; a thread owns one row, replaces its part of the buffer
@@ -33,14 +33,21 @@ namespace {
 
 using namespace dev;
 
-constexpr int kTile = 256;              // rows and columns of a pair's tile
-constexpr int kHalf = 128;              // rows (columns) staged by one CTA
-constexpr int kLStages = 5;
+constexpr int kTile = 256;              // rows of a pair's tile; columns: BN = 256 or 128
+constexpr int kHalf = 128;              // rows staged by one CTA
 constexpr int kLThreads = 384;
 constexpr int kLEpiWarps = 8;
-constexpr int kHalfBytes = kHalf * kBK * 2;      // 16 KB of A or B per stage
+constexpr int kHalfBytes = kHalf * kBK * 2;      // 16 KB of A per stage
+constexpr int kRingBytes = 160 * 1024;
 constexpr int kEpiBuf = 32 * 128;                // 32 rows of 128 bytes
-constexpr int kLSmem = kLStages * 2 * kHalfBytes + kLEpiWarps * 2 * kEpiBuf + 1024 /*barriers*/ + 1024 /*align*/;
+constexpr int kLSmem = kRingBytes + kLEpiWarps * 2 * kEpiBuf + 1024 /*barriers*/ + 1024 /*align*/;
+
+template <int BN>
+struct Tile {
+    static constexpr int kB = BN / 2 * kBK * 2;                // bytes of B per stage and CTA
+    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static_assert(kStages * (kHalfBytes + kB) <= kRingBytes, "the ring fits");
+};
 
 struct LSmem {
     uint8_t *a0, *b0, *epi;
@@ -90,9 +97,10 @@ __device__ __forceinline__ void tile_at(const LinearPairParams &p, int t, int &m
     mt = b * p.band + (u - nt * rows);
 }
 
-template <int LAYOUT>
+template <int LAYOUT, int BN>
 __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, int rank) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
+    constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
     const uint32_t full_leader = mapa_shared(smem_u32(s.full), 0);
     const uint32_t a0 = smem_u32(s.a0), b0 = smem_u32(s.b0);
     const uint64_t tma = reinterpret_cast<uint64_t>(&p.tmA), tmb = reinterpret_cast<uint64_t>(&p.tmB);
@@ -102,7 +110,7 @@ __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, int rank) 
     for (int t = int(blockIdx.x) >> 1; t < p.tiles && ok; t += int(gridDim.x) >> 1) {
         int mt, nt;
         tile_at(p, t, mt, nt);
-        const int row0 = mt * kTile + rank * kHalf, col0 = nt * kTile + rank * kHalf;
+        const int row0 = mt * kTile + rank * kHalf, col0 = nt * BN + rank * (BN / 2);
         for (int kb = 0; kb < p.kblocks; ++kb) {
             if (!mbar_try_wait(s.empty + stage, phase ^ 1u) &&
                 !wait_p(p, s, s.empty + stage, phase ^ 1u, kLinSiteEmpty, t)) {
@@ -110,9 +118,9 @@ __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, int rank) 
                 break;
             }
             const uint32_t bar = full_leader + 8u * uint32_t(stage);
-            const uint32_t sa = a0 + uint32_t(stage) * kHalfBytes, sb = b0 + uint32_t(stage) * kHalfBytes;
+            const uint32_t sa = a0 + uint32_t(stage) * kHalfBytes, sb = b0 + uint32_t(stage) * kB;
             const int k0 = kb * kBK;
-            if (rank == 0) mbar_expect_tx(s.full + stage, 4u * kHalfBytes);
+            if (rank == 0) mbar_expect_tx(s.full + stage, 2u * (kHalfBytes + kB));
             if (A_MN) {
                 tma_load_3d_pair_a(sa, tma, bar, row0, k0, 0);
                 tma_load_3d_pair_a(sa + 64 * kBK * 2, tma, bar, row0 + 64, k0, 0);
@@ -120,13 +128,14 @@ __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, int rank) 
                 tma_load_3d_pair_a(sa, tma, bar, k0, row0, 0);
             }
             if (B_MN) {
-                tma_load_3d_pair_a(sb, tmb, bar, col0, k0, 0);
-                tma_load_3d_pair_a(sb + 64 * kBK * 2, tmb, bar, col0 + 64, k0, 0);
+#pragma unroll
+                for (int j = 0; j < BN / 128; ++j)
+                    tma_load_3d_pair_a(sb + uint32_t(j * 64 * kBK * 2), tmb, bar, col0 + 64 * j, k0, 0);
             } else {
                 tma_load_3d_pair_a(sb, tmb, bar, k0, col0, 0);
             }
             ++issued;
-            if (++stage == kLStages) {
+            if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -135,14 +144,15 @@ __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, int rank) 
     // the leader's barriers count both CTAs' loads: once they complete no load
     // is still writing this pair's shared memory
     if (rank == 0)
-        for (int i = 0; i < kLStages; ++i)
+        for (int i = 0; i < kStages; ++i)
             if (uint32_t(i) < issued) drain_p(p, &s.full[i], i < stage ? phase : phase ^ 1u);
 }
 
-template <int LAYOUT>
+template <int LAYOUT, int BN>
 __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, uint32_t tmem) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
-    constexpr uint32_t kIdesc = idesc_bf16(kTile, kTile, B_MN, A_MN);
+    constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
+    constexpr uint32_t kIdesc = idesc_bf16(kTile, BN, B_MN, A_MN);
     constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kBLbo = B_MN ? 64 * kBK * 2 : 16;
     constexpr uint32_t kAStep = A_MN ? (16 * 128) >> 4 : 32 >> 4, kBStep = B_MN ? (16 * 128) >> 4 : 32 >> 4;
     const uint64_t ad0 = desc_sw128(smem_u32(s.a0), kALbo, 1024), bd0 = desc_sw128(smem_u32(s.b0), kBLbo, 1024);
@@ -152,7 +162,7 @@ __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, uint32
     for (int t = int(blockIdx.x) >> 1; t < p.tiles && ok; t += int(gridDim.x) >> 1) {
         if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) break;
         tc_fence_after();
-        const uint32_t d = tmem + uint32_t(acc * kTile);
+        const uint32_t d = tmem + uint32_t(acc * BN);
         for (int kb = 0; kb < p.kblocks; ++kb) {
             if (!mbar_try_wait(s.full + stage, phase) && !wait_p(p, s, s.full + stage, phase, kLinSiteFull, t)) {
                 ok = false;
@@ -160,12 +170,12 @@ __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, uint32
             }
             tc_fence_after();
             const uint64_t ad = ad0 + uint64_t((uint32_t(stage) * kHalfBytes) >> 4);
-            const uint64_t bd = bd0 + uint64_t((uint32_t(stage) * kHalfBytes) >> 4);
+            const uint64_t bd = bd0 + uint64_t((uint32_t(stage) * kB) >> 4);
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
                 mma_bf16_pair(d, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), kIdesc, (kb | k) != 0 ? 1u : 0u);
             mma_commit_pair_mc(s.empty + stage, uint16_t(3));
-            if (++stage == kLStages) {
+            if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -204,9 +214,9 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
 }
 
 // F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).
-template <bool F32>
+template <bool F32, int BN>
 __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t tmem, int rank) {
-    constexpr int kChunk = F32 ? 32 : 64;
+    constexpr int kChunk = F32 ? 32 : 64, kCols = BN / 2;   // columns of a warp
     const LinearEpilogue &e = p.e;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
     const int quad = ew & 3, half = ew >> 2;
@@ -224,8 +234,8 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
     for (int t = int(blockIdx.x) >> 1; t < p.tiles && ok; t += int(gridDim.x) >> 1) {
         int mt, nt;
         tile_at(p, t, mt, nt);
-        const int row0 = mt * kTile + rank * kHalf + quad * 32, cbase = nt * kTile + half * 128;
-        const int nch = row0 < p.rows && cbase < p.cols ? min(128, int(p.cols) - cbase + kChunk - 1) / kChunk : 0;
+        const int row0 = mt * kTile + rank * kHalf + quad * 32, cbase = nt * BN + half * kCols;
+        const int nch = row0 < p.rows && cbase < p.cols ? min(kCols, int(min(p.cols - cbase, int64_t(kCols))) + kChunk - 1) / kChunk : 0;
         float bias[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -248,7 +258,7 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * kTile + half * 128);
+        const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
         for (int ch = 0; ch < nch; ++ch) {
             if (lane == 0 && !(ch == 0 && in_bytes)) ask(ch);
             __syncwarp();
@@ -262,7 +272,7 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
             }
 #pragma unroll
             for (int h = 0; h < kChunk / 32; ++h) {
-                const int sub = ch * (kChunk / 32) + h;   // 32-column slice of the warp's 128
+                const int sub = ch * (kChunk / 32) + h;   // 32-column slice of the warp's columns
                 uint32_t v[32];
                 tmem_ld32(taddr + uint32_t(sub * 32), v);
                 tmem_wait_ld();
@@ -358,16 +368,17 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
     __syncwarp();
 }
 
-template <int LAYOUT>
+template <int LAYOUT, int BN>
 __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __grid_constant__ LinearPairParams p) {
+    constexpr int kStages = Tile<BN>::kStages;
     extern __shared__ uint8_t smem_raw[];
     LSmem s;
     s.a0 = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    s.b0 = s.a0 + kLStages * kHalfBytes;
-    s.epi = s.b0 + kLStages * kHalfBytes;
+    s.b0 = s.a0 + kStages * kHalfBytes;
+    s.epi = s.a0 + kRingBytes;
     s.full = reinterpret_cast<uint64_t *>(s.epi + kLEpiWarps * 2 * kEpiBuf);
-    s.empty = s.full + kLStages;
-    s.tfull = s.empty + kLStages;
+    s.empty = s.full + kStages;
+    s.tfull = s.empty + kStages;
     s.tempty = s.tfull + 2;
     s.drain = s.tempty + 2;
     s.ibar = s.drain + 1;
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
     const int rank = int(cluster_ctarank());
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kLStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
@@ -403,16 +414,16 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = *s.tmem_slot;
     if (warp == 0) {
-        if (lane == 0) load_tiles<LAYOUT>(p, s, rank);
+        if (lane == 0) load_tiles<LAYOUT, BN>(p, s, rank);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) multiply_tiles<LAYOUT>(p, s, tmem);
+        if (lane == 0 && rank == 0) multiply_tiles<LAYOUT, BN>(p, s, tmem);
         __syncwarp();
     } else if (warp >= 4) {
         if (p.e.y_f32)
-            finish_tiles<true>(p, s, tmem, rank);
+            finish_tiles<true, BN>(p, s, tmem, rank);
         else
-            finish_tiles<false>(p, s, tmem, rank);
+            finish_tiles<false, BN>(p, s, tmem, rank);
     }
     tc_fence_before();
     __syncthreads();
@@ -443,7 +454,9 @@ cudaError_t pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, unsi
 
 cudaError_t prepare_linear_pair(int device, int sms, int *max_clusters) {
     (void)device;
-    void (*fns[3])(LinearPairParams) = {cm_linear_pair_kernel<0>, cm_linear_pair_kernel<1>, cm_linear_pair_kernel<3>};
+    void (*fns[6])(LinearPairParams) = {cm_linear_pair_kernel<0, 256>, cm_linear_pair_kernel<1, 256>,
+                                        cm_linear_pair_kernel<3, 256>, cm_linear_pair_kernel<0, 128>,
+                                        cm_linear_pair_kernel<1, 128>, cm_linear_pair_kernel<3, 128>};
     for (auto fn : fns) {
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
         if (e != cudaSuccess) return e;
@@ -451,17 +464,18 @@ cudaError_t prepare_linear_pair(int device, int sms, int *max_clusters) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     pair_config(cfg, attr, unsigned(sms / 2 * 2), nullptr);
-    return cudaOccupancyMaxActiveClusters(max_clusters, cm_linear_pair_kernel<0>, &cfg);
+    return cudaOccupancyMaxActiveClusters(max_clusters, cm_linear_pair_kernel<0, 256>, &cfg);
 }
 
 cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int clusters, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     pair_config(cfg, attr, unsigned(2 * std::max(1, std::min(clusters, p.tiles))), stream);
+    const bool wide = p.bn == 256;
     switch (layout) {
-        case 0: return cudaLaunchKernelEx(&cfg, cm_linear_pair_kernel<0>, p);
-        case 1: return cudaLaunchKernelEx(&cfg, cm_linear_pair_kernel<1>, p);
-        case 3: return cudaLaunchKernelEx(&cfg, cm_linear_pair_kernel<3>, p);
+        case 0: return cudaLaunchKernelEx(&cfg, wide ? cm_linear_pair_kernel<0, 256> : cm_linear_pair_kernel<0, 128>, p);
+        case 1: return cudaLaunchKernelEx(&cfg, wide ? cm_linear_pair_kernel<1, 256> : cm_linear_pair_kernel<1, 128>, p);
+        case 3: return cudaLaunchKernelEx(&cfg, wide ? cm_linear_pair_kernel<3, 256> : cm_linear_pair_kernel<3, 128>, p);
         default: return cudaErrorInvalidValue;
     }
 }

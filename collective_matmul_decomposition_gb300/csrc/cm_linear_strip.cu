@@ -35,9 +35,8 @@ using namespace dev;
 constexpr int kThreadsL = 128;
 constexpr int kTileCols = 128;
 constexpr int kStripA = kTileCols * kBK * 2;   // 16 KB of the column operand per slice
-constexpr int kStripRing = 108 * 1024;         // two CTAs per SM
-constexpr int kStripMaxStages = 8;
-constexpr int kStripSmem = kStripRing + 1024 /*align*/ + 256 /*barriers*/;
+constexpr int kStripMaxStages = 12;
+constexpr int kStripMost = 216 * 1024;         // ring bytes of a CTA that has an SM to itself
 
 struct StripSmem {
     uint8_t *ring;
@@ -116,15 +115,17 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     extern __shared__ uint8_t smem_raw[];
     StripSmem s;
     s.ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    s.full = reinterpret_cast<uint64_t *>(s.ring + kStripRing);
+    __shared__ uint64_t bars[2 * kStripMaxStages + 2];
+    __shared__ uint32_t slots[2];
+    s.full = bars;
     s.empty = s.full + kStripMaxStages;
     s.acc = s.empty + kStripMaxStages;
     s.drain = s.acc + 1;
-    s.tmem_slot = reinterpret_cast<uint32_t *>(s.drain + 1);
-    s.abort = reinterpret_cast<volatile int *>(s.tmem_slot + 1);
+    s.tmem_slot = slots;
+    s.abort = reinterpret_cast<volatile int *>(slots + 1);
 
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    const uint32_t tmem_cols = uint32_t(p.tok < 32 ? 32 : p.tok);
+    const uint32_t tmem_cols = p.tok <= 32 ? 32u : p.tok <= 64 ? 64u : p.tok <= 128 ? 128u : 256u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s.full[i], 1);
@@ -266,10 +267,8 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
 
 }  // namespace
 
-int linear_strip_stages(int tok, int splits) {
-    const int stage = kStripA + tok * kBK * 2;
-    (void)splits;
-    return std::min(kStripMaxStages, kStripRing / stage);
+int linear_strip_stages(int tok, int ring_bytes) {
+    return std::min(kStripMaxStages, ring_bytes / (kStripA + tok * kBK * 2));
 }
 
 cudaError_t prepare_linear_strip(int device) {
@@ -279,7 +278,7 @@ cudaError_t prepare_linear_strip(int device) {
         void (*fns[3])(LinearStripParams) = {cm_linear_strip_kernel<0>, cm_linear_strip_kernel<2>,
                                              cm_linear_strip_kernel<3>};
         for (auto fn : fns) {
-            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripSmem);
+            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripMost + 1024);
             if (e != cudaSuccess) return e;
         }
         done[device] = true;
@@ -294,7 +293,7 @@ cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStre
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid), 1, 1);
     cfg.blockDim = dim3(kThreadsL, 1, 1);
-    cfg.dynamicSmemBytes = kStripSmem;
+    cfg.dynamicSmemBytes = size_t(p.ring_bytes) + 1024;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

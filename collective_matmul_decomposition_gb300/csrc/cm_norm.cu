@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cm_device.cuh"
 #include "cm_linear.cuh"
@@ -701,11 +702,19 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 constexpr int kMostSms = 160;
 
-int sm_count() {
+constexpr int kDevices = 64;
+
+// SMs of the current device and its number (looked up once a device).
+int sm_count(int *device = nullptr) {
+    static std::atomic<int> cached[kDevices];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 152;
-    return std::min(n, kMostSms);
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
+    if (device) *device = dev;
+    if (const int c = cached[dev].load(std::memory_order_relaxed)) return c;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    n = std::min(n, kMostSms);
+    cached[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // Chunks of rows for the column sums: enough CTAs for two rounds of the SMs,
@@ -715,19 +724,13 @@ int64_t chunks_for(int64_t rows, int64_t cols) {
     return std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, std::max<int64_t>(1, 608 / blocks)));
 }
 
-constexpr int64_t kSmemCta = 227 * 1024;
+constexpr int64_t kRingSmem = 224 * 1024;   // of 227 KB; the kernels' own buffers take up to 2
 
 // The sums over rows of the partial sums of `parts` CTAs.
 void sum_parts(const float *partial, int64_t parts, int64_t h, int64_t stride, void *out0, void *out1, int f32,
                int accumulate, cudaStream_t stream) {
     cm_sum_parts_kernel<<<dim3(unsigned((h + 31) / 32), stride > h ? 2 : 1), 256, 0, stream>>>(
         partial, parts, h, stride, out0, out1, f32, accumulate);
-}
-
-template <typename K>
-cudaError_t opt_in(K kernel, int64_t smem) {
-    return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemCta - 3 * 1024))
-                            : cudaSuccess;
 }
 
 int row_width(int64_t vecs, int R) { return int((vecs + 32 * R - 1) / (32 * R)) * 32; }
@@ -746,7 +749,7 @@ struct RingPlan {
 // groups at most (15 have a barrier each).
 RingPlan ring_plan(int64_t rows, int64_t h, int64_t row_bytes, int64_t fixed_bytes, int most_r, int most_per, int sms) {
     RingPlan r;
-    const int64_t vecs = (h + 7) / 8, limit = kSmemCta - 3 * 1024 /* the kernels' own buffers */;
+    const int64_t vecs = (h + 7) / 8, limit = kRingSmem;
     r.R = vecs < 64 ? 1 : vecs < 128 ? 2 : most_r;
     r.width = row_width(vecs, r.R);
     if (r.width > kRingThreads) return r;
@@ -761,10 +764,16 @@ RingPlan ring_plan(int64_t rows, int64_t h, int64_t row_bytes, int64_t fixed_byt
 }
 
 // Launches a persistent kernel, in clusters of two CTAs a row if `split`.
-template <typename K>
-cudaError_t launch_ring(K kernel, const NormParams &p, const RingPlan &r, bool split, cudaStream_t stream) {
-    cudaError_t e = opt_in(kernel, r.smem);
-    if (e != cudaSuccess) return e;
+template <auto kernel>
+cudaError_t launch_ring(const NormParams &p, const RingPlan &r, bool split, cudaStream_t stream) {
+    static std::atomic<bool> prepared[kDevices];   // setting it twice does no harm
+    int dev = 0;
+    sm_count(&dev);
+    if (!prepared[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingSmem));
+        if (e != cudaSuccess) return e;
+        prepared[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(split ? 2 * r.ctas : r.ctas));
     cfg.blockDim = dim3(unsigned(r.width * r.per));
@@ -782,7 +791,7 @@ cudaError_t launch_ring(K kernel, const NormParams &p, const RingPlan &r, bool s
 
 template <typename X, typename Y, int R, int NR, int S, bool SPLIT = false>
 cudaError_t forward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
-    return launch_ring(cm_layer_norm_ring_kernel<X, Y, R, NR, S, SPLIT>, p, r, SPLIT, stream);
+    return launch_ring<cm_layer_norm_ring_kernel<X, Y, R, NR, S, SPLIT>>(p, r, SPLIT, stream);
 }
 
 template <typename X, typename Y>
@@ -825,7 +834,7 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
 
 template <typename X, typename Y, int R, int S, bool SPLIT = false, typename G = float>
 cudaError_t backward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
-    return launch_ring(cm_layer_norm_backward_ring_kernel<X, Y, G, R, S, SPLIT>, p, r, SPLIT, stream);
+    return launch_ring<cm_layer_norm_backward_ring_kernel<X, Y, G, R, S, SPLIT>>(p, r, SPLIT, stream);
 }
 
 template <typename X, typename Y>
