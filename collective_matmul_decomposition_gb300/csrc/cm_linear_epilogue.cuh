@@ -52,44 +52,46 @@ __device__ __forceinline__ float dact1(float z, int act) {
 }
 
 // The same over a slice, the choice outside the loop.
-__device__ __forceinline__ void apply_act(float (&f)[32], int act) {
+template <int N>
+__device__ __forceinline__ void apply_act(float (&f)[N], int act) {
     switch (act) {
         case CM_ACT_RELU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_RELU);
+            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_RELU);
             break;
         case CM_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_GELU);
+            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_GELU);
             break;
         case CM_ACT_GELU_TANH:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_GELU_TANH);
+            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_GELU_TANH);
             break;
         case CM_ACT_SILU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = act1(f[i], CM_ACT_SILU);
+            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_SILU);
             break;
         default: break;
     }
 }
-__device__ __forceinline__ void mul_dact(float (&f)[32], const float (&z)[32], int act) {
+template <int N>
+__device__ __forceinline__ void mul_dact(float (&f)[N], const float (&z)[N], int act) {
     switch (act) {
         case CM_ACT_RELU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_RELU);
+            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_RELU);
             break;
         case CM_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_GELU);
+            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_GELU);
             break;
         case CM_ACT_GELU_TANH:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_GELU_TANH);
+            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_GELU_TANH);
             break;
         case CM_ACT_SILU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= dact1(z[i], CM_ACT_SILU);
+            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_SILU);
             break;
         default: break;
     }

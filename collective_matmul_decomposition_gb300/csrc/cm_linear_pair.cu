@@ -163,8 +163,9 @@ __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, uint32
         if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * BN);
+        bool ready = mbar_test_wait(s.full + stage, phase);   // looked at ahead, so that its latency overlaps the issue
         for (int kb = 0; kb < p.kblocks; ++kb) {
-            if (!mbar_try_wait(s.full + stage, phase) && !wait_p(p, s, s.full + stage, phase, kLinSiteFull, t)) {
+            if (!ready && !mbar_try_wait(s.full + stage, phase) && !wait_p(p, s, s.full + stage, phase, kLinSiteFull, t)) {
                 ok = false;
                 break;
             }
@@ -179,6 +180,7 @@ __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, uint32
                 stage = 0;
                 phase ^= 1u;
             }
+            ready = mbar_test_wait(s.full + stage, phase);
         }
         if (!ok) break;
         mma_commit_pair_mc(&s.tfull[acc], uint16_t(3));
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     s.tmem_slot = reinterpret_cast<uint32_t *>(s.ibar + kLEpiWarps);
     s.abort = reinterpret_cast<volatile int *>(s.tmem_slot + 1);
 
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const int warp = int(threadIdx.x) >> 5;
     const int rank = int(cluster_ctarank());
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -414,10 +416,10 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = *s.tmem_slot;
     if (warp == 0) {
-        if (lane == 0) load_tiles<LAYOUT, BN>(p, s, rank);
+        if (elect_one()) load_tiles<LAYOUT, BN>(p, s, rank);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) multiply_tiles<LAYOUT, BN>(p, s, tmem);
+        if (rank == 0 && elect_one()) multiply_tiles<LAYOUT, BN>(p, s, tmem);
         __syncwarp();
     } else if (warp >= 4) {
         if (p.e.y_f32)

@@ -92,20 +92,58 @@ __device__ __forceinline__ float cluster_sum(uint32_t addr, int splits) {
     return v;
 }
 
-__device__ __forceinline__ void finish(const LinearEpilogue &e, float v, float bias, int64_t row, int64_t col) {
-    v += bias;
-    if (e.z) static_cast<__nv_bfloat16 *>(e.z)[row * e.ldz + col] = __float2bfloat16_rn(v);
-    if (e.dact)
-        v *= lin::dact1(__bfloat162float(static_cast<const __nv_bfloat16 *>(e.zin)[row * e.ldzin + col]), e.act);
-    else
-        v = lin::act1(v, e.act);
-    if (e.res) v += __bfloat162float(static_cast<const __nv_bfloat16 *>(e.res)[row * e.ldr + col]);
-    if (e.y_f32) {
-        float *y = static_cast<float *>(e.y) + row * e.ldy + col;
-        *y = e.accumulate ? *y + v : v;
+// The epilogue of kBatch rows (row0 + k * step, those below `end`) of one
+// column: every load of the batch before the first store, so that their
+// latencies overlap.
+constexpr int kBatch = 8;
+__device__ __forceinline__ void finish(const LinearEpilogue &e, float (&v)[kBatch], float bias, int64_t row0, int64_t step,
+                                       int64_t end, int64_t col) {
+    float in[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v[k] += bias;
+    if (e.z) {
+        __nv_bfloat16 *z = static_cast<__nv_bfloat16 *>(e.z) + row0 * e.ldz + col;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (row0 + k * step < end) z[k * step * e.ldz] = __float2bfloat16_rn(v[k]);
+    }
+    auto read = [&](const void *m, int64_t ld) {
+        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(m) + row0 * ld + col;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) in[k] = row0 + k * step < end ? __bfloat162float(p[k * step * ld]) : 0.0f;
+    };
+    if (e.dact) {
+        read(e.zin, e.ldzin);
+        lin::mul_dact(v, in, e.act);
     } else {
-        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(e.y) + row * e.ldy + col;
-        *y = __float2bfloat16_rn(e.accumulate ? __bfloat162float(*y) + v : v);
+        lin::apply_act(v, e.act);
+    }
+    if (e.res) {
+        read(e.res, e.ldr);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] += in[k];
+    }
+    if (e.y_f32) {
+        float *y = static_cast<float *>(e.y) + row0 * e.ldy + col;
+        if (e.accumulate) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) in[k] = row0 + k * step < end ? y[k * step * e.ldy] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) v[k] += in[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (row0 + k * step < end) y[k * step * e.ldy] = v[k];
+    } else {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(e.y) + row0 * e.ldy + col;
+        if (e.accumulate) {
+            read(e.y, e.ldy);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) v[k] += in[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (row0 + k * step < end) y[k * step * e.ldy] = __float2bfloat16_rn(v[k]);
     }
 }
 
@@ -124,7 +162,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     s.tmem_slot = slots;
     s.abort = reinterpret_cast<volatile int *>(slots + 1);
 
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const int warp = int(threadIdx.x) >> 5;
     const uint32_t tmem_cols = p.tok <= 32 ? 32u : p.tok <= 64 ? 64u : p.tok <= 128 ? 128u : 256u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -155,11 +193,12 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const uint32_t stage_bytes = uint32_t(kStripA + p.tok * kBK * 2);
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_l(p, s, &s.empty[stage], phase ^ 1u, kLinSiteEmpty)) break;
+                if (!mbar_try_wait(&s.empty[stage], phase ^ 1u) && !wait_l(p, s, &s.empty[stage], phase ^ 1u, kLinSiteEmpty))
+                    break;
                 uint8_t *sa = s.ring + uint32_t(stage) * stage_bytes, *sb = sa + kStripA;
                 mbar_expect_tx(&s.full[stage], stage_bytes);
                 if (A_MN) {
@@ -188,21 +227,24 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc = idesc_bf16(kTileCols, p.tok, B_MN, A_MN);
             constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kBLbo = B_MN ? 64 * kBK * 2 : 16;
             constexpr uint32_t kAStep = A_MN ? (16 * 128) >> 4 : 32 >> 4, kBStep = B_MN ? (16 * 128) >> 4 : 32 >> 4;
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
+            const uint64_t ad0 = desc_sw128(smem_u32(s.ring), kALbo, 1024);
+            const uint64_t bd0 = desc_sw128(smem_u32(s.ring) + kStripA, kBLbo, 1024);
+            bool ready = mbar_test_wait(&s.full[0], 0);   // looked at ahead, so that its latency overlaps the issue
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_l(p, s, &s.full[stage], phase, kLinSiteFull)) {
+                if (!ready && !mbar_try_wait(&s.full[stage], phase) && !wait_l(p, s, &s.full[stage], phase, kLinSiteFull)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sa = smem_u32(s.ring) + uint32_t(stage) * stage_bytes;
-                const uint64_t ad = desc_sw128(sa, kALbo, 1024), bd = desc_sw128(sa + kStripA, kBLbo, 1024);
+                const uint64_t off = (uint32_t(stage) * stage_bytes) >> 4;
+                const uint64_t ad = ad0 + off, bd = bd0 + off;
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
                     mma_bf16(tmem, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc, kb > kb0 || k ? 1u : 0u);
@@ -211,6 +253,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                     stage = 0;
                     phase ^= 1u;
                 }
+                ready = kb + 1 < kb1 && mbar_test_wait(&s.full[stage], phase);
             }
             if (ok) mma_commit(s.acc);
             mma_commit(s.drain);
@@ -232,8 +275,13 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             tmem_wait_ld();
             if (good && col < p.cols) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (t0 + i < nrows) finish(p.e, __uint_as_float(v[i]), bias, int64_t(row0) + t0 + i, col);
+                for (int b = 0; b < 32; b += kBatch)
+                    if (t0 + b < nrows) {
+                        float f[kBatch];
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k) f[k] = __uint_as_float(v[b + k]);
+                        finish(p.e, f, bias, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
+                    }
             }
         }
     } else {
@@ -251,9 +299,15 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         if (!good) *s.abort = 1;
         cluster_sync();
         if (col < p.cols && good)
-            for (int t = split; t < nrows; t += p.splits)
-                finish(p.e, cluster_sum(smem_u32(part + t * kTileCols + int(threadIdx.x)), p.splits), bias,
-                       int64_t(row0) + t, col);
+            for (int t = split; t < nrows; t += p.splits * kBatch) {
+                float f[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    f[k] = t + k * p.splits < nrows
+                               ? cluster_sum(smem_u32(part + (t + k * p.splits) * kTileCols + int(threadIdx.x)), p.splits)
+                               : 0.0f;
+                finish(p.e, f, bias, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
+            }
         cluster_sync();   // the peers have read this CTA's partial tile
     }
     tc_fence_before();
