@@ -80,9 +80,11 @@ struct LinearPairParams {
     uint64_t timeout_ns;
 };
 
-// layout: bit 0 = B MN-major, bit 1 = A MN-major.
-cudaError_t prepare_linear_pair(int device, int sms, int *max_clusters);
-cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int clusters, cudaStream_t stream);
+// layout: bit 0 = B MN-major, bit 1 = A MN-major.  splits: 1 (persistent, on
+// `clusters` pairs), or 2 or 4 pairs a cluster that share a tile's K slices,
+// one cluster a tile.  clusters[i]: clusters of 2^i pairs that run together.
+cudaError_t prepare_linear_pair(int sms, int *clusters);
+cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int splits, int clusters, cudaStream_t stream);
 
 // Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu): partial
 // sums per row chunk in `partial`, then their sum in chunk order.

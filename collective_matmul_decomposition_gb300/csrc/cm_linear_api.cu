@@ -70,7 +70,8 @@ cm_status check_extents(int64_t M, int64_t K, int64_t n) {
 }
 
 struct Device {
-    int id = 0, sms = 0, clusters = 0;
+    int id = 0, sms = 0;
+    int clusters[3] = {0, 0, 0};   // of 1, 2 and 4 pairs
     LinearStatus *status = nullptr;
 };
 
@@ -89,8 +90,8 @@ cm_status device(Device *d) {
             return CM_ERR_CUDA;
         if (major != 10 || minor != 3) return CM_ERR_UNSUPPORTED;
         if (prepare_linear_strip(d->id) != cudaSuccess) return CM_ERR_CUDA;
-        if (prepare_linear_pair(d->id, c.sms, &c.clusters) != cudaSuccess) return CM_ERR_CUDA;
-        if (c.clusters < 1) return CM_ERR_UNSUPPORTED;
+        if (prepare_linear_pair(c.sms, c.clusters) != cudaSuccess) return CM_ERR_CUDA;
+        if (c.clusters[0] < 1) return CM_ERR_UNSUPPORTED;
         void *sp = nullptr;
         if (cudaGetSymbolAddress(&sp, g_linear_status) != cudaSuccess) return CM_ERR_CUDA;
         c.status = static_cast<LinearStatus *>(sp);
@@ -114,28 +115,70 @@ bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t k, int 
 
 constexpr int64_t kBandBytes = int64_t(32) << 20;   // of the row operand, kept in L2 while a band runs
 
-// How a product is run: pair (256 x bn tiles on CTA pairs) or strip (128 columns
-// x tok rows, K split over `splits` CTAs).
+// How a product is run: pair (256 x bn tiles on CTA pairs, K split over 1, 2
+// or 4 pairs) or strip (128 columns x tok rows, K split over up to 8 CTAs).
 struct Choice {
-    bool pair;
-    int bn;
-    int tok, splits, ring_bytes;
+    bool pair = false;
+    int bn = 256;
+    int tok = 16, splits = 1, ring_bytes = 0;
 };
 
+// The choice with the least estimated time.  The estimates' constants were fitted to
+// calls on one GB300 with weights from HBM (us): a K slice of 64 takes a
+// wave of pair tiles 0.33 (256 columns) or 0.21 (128 columns), starting and
+// finishing 7.5 or 5.5, splitting 2 more; strips start and finish in 6.5 (8 if
+// split) and then run at what HBM (6.3 TB/s) or the SMs' reads of L2 (11
+// TB/s, each tile its own copy of the rows) allow, 0.2 a slice at least.  Measured
+// on both sides of where the choice changes (best strip against best pair):
+//   rows 45,  K 8190,  cols 3579:   16.0 / 18.5      rows 100, K 8192, cols 3584:  19.3 / 20.5
+//   rows 200, K 8192,  cols 3584:   24.9 / 20.8      rows 256, K 12288, cols 4608: 37.4 / 31.2
+//   rows 128, K 4096,  cols 16384:  30.8 / 30.5      rows 512, K 4096, cols 4096:  22.9 / 18.7
+// and between pair tiles (256 columns / 128 columns / split):
+//   rows 2048, K 12288, cols 4608:  128.7 / 161 / -  rows 512, K 4096, cols 4096:  24.8 / 18.7 / 19.0
+//   rows 1024, cols 1024, K 8192:   40.1 / 23.1 / 16.8 (128 columns, two pairs)
 Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn) {
-    Choice c = {};
-    if (((rows + 255) / 256) * ((cols + 255) / 256) >= d.clusters) {
-        c.pair = true;
-        c.bn = 256;
-        return c;
+    Choice best;
+    double least = 1e30;
+    const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t slices = up(k, kBK);
+    const double weights = double(cols) * double(k) * 2.0;   // bytes
+    // pair tiles waste what they have beyond `rows`: not worth a look below 33
+    for (int bn = 256; bn >= 128 && rows > 32; bn /= 2) {
+        const int64_t tiles = up(rows, 256) * up(cols, bn);
+        for (int i = 0; i < 3; ++i) {
+            const int splits = 1 << i;
+            if (i > 0 && (tiles > d.clusters[i] || slices < 2 * splits)) break;
+            const double t = (bn == 256 ? 7.5 : 5.5) + (i ? 2.0 : 0.0) +
+                             std::max(double(up(tiles, d.clusters[i])) * double(up(slices, splits)) * (bn == 256 ? 0.33 : 0.21),
+                                      weights / 6.3e6);
+            if (t < least) {
+                least = t;
+                best.pair = true;
+                best.bn = bn;
+                best.splits = splits;
+            }
+        }
     }
-    c.ring_bytes = 108 * 1024;
-    c.tok = row_mn ? 64 : 16;
-    while (c.tok < 128 && c.tok < rows) c.tok *= 2;
-    const int64_t tiles = ((rows + c.tok - 1) / c.tok) * ((cols + 127) / 128);
-    c.splits = 1;
-    while (c.splits < 8 && tiles * c.splits <= d.sms && c.splits * 2 * kBK <= k) c.splits *= 2;
-    return c;
+    for (int64_t parts = 1; parts <= 2 && rows <= 512; ++parts) {
+        const int64_t unit = row_mn ? 64 : 16, tok = up(up(rows, parts), unit) * unit;
+        if (tok > 256) continue;
+        const int64_t row_tiles = up(rows, tok), tiles = row_tiles * up(cols, 128);
+        // two CTAs an SM if there are tiles or K slices for them
+        int64_t splits = std::max<int64_t>(1, std::min({int64_t(8), 2 * d.sms / tiles, slices}));
+        if (tok > 128) splits = 1;   // partial tiles of more rows do not fit two to an SM
+        const double per_sm = double(up(tiles * splits, d.sms));
+        const double traffic = double(tiles) * double(128 + tok) * double(k) * 2.0;
+        const double t = (splits > 1 ? 8.0 : 6.5) +
+                         std::max({weights / 6.3e6, traffic / 11e6, 0.2 * double(up(slices, splits)) * per_sm});
+        if (t < least) {
+            least = t;
+            best.pair = false;
+            best.tok = int(tok);
+            best.splits = int(splits);
+            best.ring_bytes = (splits == 1 && tiles <= d.sms ? 216 : 108) * 1024;   // clusters pack worse at 216
+        }
+    }
+    return best;
 }
 
 cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const Operand &b, int64_t rows, int64_t cols,
@@ -163,7 +206,7 @@ cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const
         if (e.dact && !map_rows(&p.tmIn1, e.zin, rows, cols, e.ldzin, 32)) return CM_ERR_CUDA;
     }
     const int layout = (a.mn_major ? 1 : 0) | (b.mn_major ? 2 : 0);
-    return launch_linear_pair(p, layout, d.clusters, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+    return launch_linear_pair(p, layout, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
 // D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.
