@@ -35,17 +35,22 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "cm_internal.h"
+#include "cm_vec.cuh"
 
 namespace cm {
 namespace {
 
-using bf16 = __nv_bfloat16;
-
 constexpr int kBlock = CM_ADAMW_BLOCK;
 constexpr int kAdamThreads = 256;
-constexpr int64_t kAdamChunk = int64_t(kAdamThreads) * 8;   // elements a CTA updates
+constexpr int kAdamPass = kAdamThreads * 8;             // elements a CTA updates at a time
+// Passes of a CTA.  Four with codes, whose passes are long on arithmetic: finding
+// the tensor is paid once for them (50 M elements: 171 us, with one pass 183);
+// one without, where four would only put loads behind stores (59 M elements:
+// 242 us, with four 252).
+constexpr int kCodePasses = 4;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
 
@@ -74,87 +79,60 @@ struct Table {
     bool seeded;
 };
 
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void load8(const bf16 *p, float (&f)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void store8(bf16 *p, const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+using namespace vec;
 
-__device__ __forceinline__ float decode(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-// The code nearest to v (already divided by the scale), ties to even; |v| <= 448.
-__device__ __forceinline__ uint8_t encode(float v) {
-    return uint8_t(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
-}
-
-// Whether the thread's 8 elements can go in whole vectors.
+// A thread's 8 elements: the first one's index, how many belong to the tensor,
+// and whether they can go in whole vectors.
 struct Span {
     int64_t i0;
-    int n;      // 0..8 elements of the tensor
+    int n;
     bool vec;
 };
 
 template <typename T>
-__device__ __forceinline__ void get(const T *p, const Span &s, float (&f)[8]) {
-    if (s.vec) {
-        load8(p + s.i0, f);
-    } else {
+__device__ __forceinline__ V8 get(const T *p, const Span &s) {
+    if (s.vec) return load8(p + s.i0);
+    float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < s.n ? float(p[s.i0 + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) f[i] = i < s.n ? to_f(p[s.i0 + i]) : 0.0f;
+    return {{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+}
+template <typename T>
+__device__ __forceinline__ void put(T *p, const Span &s, const V8 &v) {
+    if (s.vec) {
+        store8(p + s.i0, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = parts(v.p[i]);
+        if (2 * i < s.n) from_f(p + s.i0 + 2 * i, q.x);
+        if (2 * i + 1 < s.n) from_f(p + s.i0 + 2 * i + 1, q.y);
     }
 }
-__device__ __forceinline__ void put(float *p, const Span &s, const float (&f)[8]) {
+
+// The values of 8 codes times their scale.
+__device__ __forceinline__ V8 get_codes(const uint8_t *p, const Span &s, float scale) {
+    uint2 w = make_uint2(0u, 0u);
     if (s.vec) {
-        store8(p + s.i0, f);
+        w = *reinterpret_cast<const uint2 *>(p + s.i0);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < s.n) p[s.i0 + i] = f[i];
+            if (i < s.n) (i < 4 ? w.x : w.y) |= uint32_t(p[s.i0 + i]) << (8 * (i & 3));
     }
+    V8 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t q = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(q & 0xffffu), __NV_E4M3)));
+        v.p[i] = mul(pair(f.x, f.y), both(scale));
+    }
+    return v;
 }
-__device__ __forceinline__ void put(bf16 *p, const Span &s, const float (&f)[8]) {
-    if (s.vec) {
-        store8(p + s.i0, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < s.n) p[s.i0 + i] = __float2bfloat16_rn(f[i]);
-    }
-}
-__device__ __forceinline__ void get_codes(const uint8_t *p, const Span &s, uint8_t (&c)[8]) {
-    if (s.vec) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p + s.i0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c[i] = uint8_t(w.x >> (8 * i));
-            c[4 + i] = uint8_t(w.y >> (8 * i));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = i < s.n ? p[s.i0 + i] : uint8_t(0);
-    }
+// The two nearest codes, ties to even; beyond 448 the largest, not a number the NaN code.
+__device__ __forceinline__ uint32_t encode2(float a, float b) {
+    return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
 
 // 32 mixed bits of a counter (the finalizer of MurmurHash3).
@@ -178,101 +156,129 @@ __device__ __forceinline__ float dither(float v, uint32_t u) {
 }
 
 // Quantise the warp's block: codes and scale of the 256 values its threads
-// hold.  `bits`: 16 random bits an element where the rounding is seeded.
+// hold (zeros behind the tensor's end).  ROOT: a positive value keeps a code
+// above zero.  `bits`: 16 random bits an element where the rounding is seeded.
 template <bool ROOT>
-__device__ __forceinline__ void put_codes(uint8_t *p, float *scale, const Span &s, const float (&f)[8], bool seeded,
+__device__ __forceinline__ void put_codes(uint8_t *p, float *scale, const Span &s, const V8 &v, bool seeded,
                                           const uint32_t (&bits)[8]) {
-    float amax = 0.0f;
+    float f[8];
+    // magnitudes order as their bits do, and what is not finite lies above them
+    uint32_t top = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < s.n && isfinite(f[i])) amax = fmaxf(amax, fabsf(f[i]));
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = parts(v.p[i]);
+        f[2 * i] = q.x;
+        f[2 * i + 1] = q.y;
+        top = max(top, max(__float_as_uint(q.x) & 0x7fffffffu, __float_as_uint(q.y) & 0x7fffffffu));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool odd = top >= 0x7f800000u;   // somewhere in the block
+    if (odd) {
+        top = 0u;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int i = 0; i < 8; ++i)
+            if (isfinite(f[i])) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    const float amax = __uint_as_float(top);
     const bool live = amax >= kTiny;
     const float inv = live ? __fmul_rn(1.0f / amax, kE4m3Max) : 0.0f;
-    uint32_t w[2] = {0u, 0u};
+    const float least = live ? 0x1p-9f : 0.0f;   // the smallest code's value
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // the block's largest value times inv may end one unit above 448; the codes end there
-        float x = fminf(fmaxf(f[i] * inv, -kE4m3Max), kE4m3Max);
-        if (seeded) x = dither(x, ROOT ? bits[i] >> 16 : bits[i] & 0xffffu);
-        uint8_t c = isfinite(f[i]) ? encode(x) : uint8_t(0x7f);
-        if (ROOT && live && c == 0 && f[i] > 0.0f) c = 1;
-        w[i >> 2] |= uint32_t(c) << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i) {
+        float x[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float a = f[2 * i + k];
+            x[k] = a * inv;
+            if (seeded) x[k] = dither(fminf(fmaxf(x[k], -kE4m3Max), kE4m3Max), ROOT ? bits[2 * i + k] >> 16 : bits[2 * i + k] & 0xffffu);
+            if (ROOT) x[k] = a > 0.0f ? fmaxf(x[k], least) : 0.0f;
+            if (odd && !isfinite(a)) x[k] = __uint_as_float(0x7fffffffu);
+        }
+        w[i] = encode2(x[0], x[1]);
     }
+    const uint2 c = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
     if (s.vec) {
-        *reinterpret_cast<uint2 *>(p + s.i0) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(p + s.i0) = c;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < s.n) p[s.i0 + i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+            if (i < s.n) p[s.i0 + i] = uint8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
     }
     if ((threadIdx.x & 31) == 0 && s.n > 0) *scale = live ? amax * (1.0f / kE4m3Max) : 0.0f;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kAdamThreads) cm_adamw_kernel(const __grid_constant__ Table<CAP> t) {
+// CODES: some tensor of the table has 8-bit states, each by its own flag.  A
+// table without any runs without that path's registers (59 M elements with fp32
+// states: 242 us, with the path 246).  Five CTAs an SM: with
+// four or six, 8-bit steps were 10 and 4 % slower.
+template <int CAP, bool CODES>
+__global__ void __launch_bounds__(kAdamThreads, 5) cm_adamw_kernel(const __grid_constant__ Table<CAP> t) {
     // the tensor of this chunk: the last one that starts at or before it
     int lo = 0, hi = t.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (t.e[mid].first_chunk <= int(blockIdx.x)) lo = mid; else hi = mid - 1;
     }
-    const Entry &e = t.e[lo];
+    const std::conditional_t<CODES, Entry, const Entry &> e = t.e[lo];
+    const F2 scale = both(t.grad_scale ? *t.grad_scale : 1.0f);
     Span s;
-    s.i0 = int64_t(int(blockIdx.x) - e.first_chunk) * kAdamChunk + int64_t(threadIdx.x) * 8;
-    s.n = int(max(int64_t(0), min(int64_t(8), e.numel - s.i0)));
-    s.vec = e.vec && s.n == 8;
-    const int64_t block = s.i0 / kBlock;
-    const float scale = t.grad_scale ? *t.grad_scale : 1.0f;
-
-    float g[8], p[8], m[8], v[8], root[8];
-    if (e.grad_f32) get(static_cast<const float *>(e.grad), s, g);
-    else get(static_cast<const bf16 *>(e.grad), s, g);
-    if (e.master) get(e.master, s, p);
-    else if (e.param_f32) get(static_cast<const float *>(e.param), s, p);
-    else get(static_cast<const bf16 *>(e.param), s, p);
-    if (e.bits8) {
-        uint8_t cm[8], cv[8];
-        get_codes(static_cast<const uint8_t *>(e.m), s, cm);
-        get_codes(static_cast<const uint8_t *>(e.v), s, cv);
-        const float sm = s.n ? e.ms[block] : 0.0f, sv = s.n ? e.vs[block] : 0.0f;
+    constexpr int kPasses = CODES ? kCodePasses : 1;
+    s.i0 = int64_t(int(blockIdx.x) - e.first_chunk) * (kPasses * kAdamPass) + int64_t(threadIdx.x) * 8;
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass, s.i0 += kAdamPass) {
+        if (s.i0 - int64_t(threadIdx.x & 31) * 8 >= e.numel) break;   // by warps: a block's threads stay together
+        s.n = int(max(int64_t(0), min(int64_t(8), e.numel - s.i0)));
+        s.vec = e.vec && s.n == 8;
+        const int64_t block = s.i0 / kBlock;
+        V8 g = e.grad_f32 ? get(static_cast<const float *>(e.grad), s) : get(static_cast<const bf16 *>(e.grad), s);
+        V8 p = e.master ? get(e.master, s)
+               : e.param_f32 ? get(static_cast<const float *>(e.param), s) : get(static_cast<const bf16 *>(e.param), s);
+        V8 m, v, root;
+        if (CODES && e.bits8) {
+            m = get_codes(static_cast<const uint8_t *>(e.m), s, s.n ? e.ms[block] : 0.0f);
+            v = get_codes(static_cast<const uint8_t *>(e.v), s, s.n ? e.vs[block] : 0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m[i] = decode(cm[i]) * sm;
-            const float r = decode(cv[i]) * sv;
-            v[i] = r * r;
+            for (int i = 0; i < 4; ++i) v.p[i] = mul(v.p[i], v.p[i]);
+        } else {
+            m = get(static_cast<const float *>(e.m), s);
+            v = get(static_cast<const float *>(e.v), s);
         }
-    } else {
-        get(static_cast<const float *>(e.m), s, m);
-        get(static_cast<const float *>(e.v), s, v);
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float gi = g[i] * scale;
-        // rounded one by one, not contracted: a code must not depend on how
-        // the compiler groups a sum that lies on the border between two
-        m[i] = __fadd_rn(__fmul_rn(t.b1, m[i]), __fmul_rn(t.c1, gi));
-        v[i] = __fadd_rn(__fmul_rn(t.b2, v[i]), __fmul_rn(__fmul_rn(t.c2, gi), gi));
-        root[i] = sqrtf(v[i]);
-        p[i] = p[i] * e.keep - t.step * m[i] / (root[i] * t.root_scale + t.eps);
-    }
-    if (e.master) put(e.master, s, p);
-    if (e.param_f32) put(static_cast<float *>(e.param), s, p);
-    else put(static_cast<bf16 *>(e.param), s, p);
-    if (e.bits8) {
-        __syncwarp();   // every lane has read the block's old scales
-        uint32_t bits[8];
-        if (t.seeded) {
-            const uint32_t key = mix(mix(uint32_t(s.i0 >> 32) + t.seed_hi) ^ (e.index + t.seed_lo));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) bits[i] = mix((uint32_t(s.i0) + uint32_t(i)) ^ key);
+        for (int i = 0; i < 4; ++i) {
+            const F2 gi = mul(g.p[i], scale);
+            // rounded one by one, not fused (which pairs would be): a code must not
+            // depend on how a sum that lies on the border between two is grouped
+            const float2 gs = parts(gi), ms = parts(m.p[i]), vs = parts(v.p[i]);
+            m.p[i] = pair(__fadd_rn(__fmul_rn(t.b1, ms.x), __fmul_rn(t.c1, gs.x)),
+                          __fadd_rn(__fmul_rn(t.b1, ms.y), __fmul_rn(t.c1, gs.y)));
+            v.p[i] = pair(__fadd_rn(__fmul_rn(t.b2, vs.x), __fmul_rn(__fmul_rn(t.c2, gs.x), gs.x)),
+                          __fadd_rn(__fmul_rn(t.b2, vs.y), __fmul_rn(__fmul_rn(t.c2, gs.y), gs.y)));
+            const float2 q = parts(v.p[i]), num = parts(mul(both(t.step), m.p[i]));
+            const float2 r = make_float2(sqrtf(q.x), sqrtf(q.y));
+            root.p[i] = pair(r.x, r.y);
+            // the fast division is off by two units of the update's last place
+            const float2 den = parts(fma(root.p[i], both(t.root_scale), both(t.eps)));
+            p.p[i] = fma(p.p[i], both(e.keep), pair(-__fdividef(num.x, den.x), -__fdividef(num.y, den.y)));
         }
-        put_codes<false>(static_cast<uint8_t *>(e.m), e.ms + block, s, m, t.seeded, bits);
-        put_codes<true>(static_cast<uint8_t *>(e.v), e.vs + block, s, root, t.seeded, bits);
-    } else {
-        put(static_cast<float *>(e.m), s, m);
-        put(static_cast<float *>(e.v), s, v);
+        if (e.master) put(e.master, s, p);
+        if (e.param_f32) put(static_cast<float *>(e.param), s, p);
+        else put(static_cast<bf16 *>(e.param), s, p);
+        if (CODES && e.bits8) {
+            __syncwarp();   // every lane has read the block's old scales
+            uint32_t bits[8] = {};
+            if (t.seeded) {
+                const uint32_t key = mix(mix(uint32_t(s.i0 >> 32) + t.seed_hi) ^ (e.index + t.seed_lo));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bits[i] = mix((uint32_t(s.i0) + uint32_t(i)) ^ key);
+            }
+            put_codes<false>(static_cast<uint8_t *>(e.m), e.ms + block, s, m, t.seeded, bits);
+            put_codes<true>(static_cast<uint8_t *>(e.v), e.vs + block, s, root, t.seeded, bits);
+        } else {
+            put(static_cast<float *>(e.m), s, m);
+            put(static_cast<float *>(e.v), s, v);
+        }
     }
 }
 
@@ -282,7 +288,7 @@ static_assert(sizeof(Table<kLargeTable>) <= 32764, "kernel parameters");
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <int CAP>
-cudaError_t launch(const Table<kLargeTable> &all, int64_t chunks, cudaStream_t stream) {
+cudaError_t launch(const Table<kLargeTable> &all, bool codes, int64_t chunks, cudaStream_t stream) {
     Table<CAP> t;
     std::copy(all.e, all.e + all.count, t.e);
     t.count = all.count;
@@ -290,7 +296,10 @@ cudaError_t launch(const Table<kLargeTable> &all, int64_t chunks, cudaStream_t s
     t.step = all.step, t.root_scale = all.root_scale, t.eps = all.eps;
     t.grad_scale = all.grad_scale;
     t.seed_lo = all.seed_lo, t.seed_hi = all.seed_hi, t.seeded = all.seeded;
-    cm_adamw_kernel<CAP><<<unsigned(chunks), kAdamThreads, 0, stream>>>(t);
+    if (codes)
+        cm_adamw_kernel<CAP, true><<<unsigned(chunks), kAdamThreads, 0, stream>>>(t);
+    else
+        cm_adamw_kernel<CAP, false><<<unsigned(chunks), kAdamThreads, 0, stream>>>(t);
     return cudaGetLastError();
 }
 
@@ -298,7 +307,7 @@ cm_status check_tensor(const cm_adamw_tensor &x) {
     if ((x.param_dtype != CM_BF16 && x.param_dtype != CM_F32) || (x.grad_dtype != CM_BF16 && x.grad_dtype != CM_F32) ||
         (x.state_bits != 32 && x.state_bits != 8))
         return CM_ERR_INVALID_ARG;
-    if (x.numel < 0 || x.numel > (int64_t(1) << 42)) return CM_ERR_SHAPE;
+    if (x.numel < 0 || x.numel > (int64_t(1) << 41)) return CM_ERR_SHAPE;
     if (x.numel == 0) return CM_OK;
     if (!x.param || !x.grad || !x.exp_avg || !x.exp_avg_sq) return CM_ERR_INVALID_ARG;
     if (x.state_bits == 8 && (!x.exp_avg_scale || !x.exp_avg_sq_scale)) return CM_ERR_INVALID_ARG;
@@ -325,10 +334,13 @@ extern "C" cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double 
     if (count < 0 || (count > 0 && !tensors) || step < 1 || !std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) ||
         !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) || !aligned(grad_scale, 4))
         return CM_ERR_INVALID_ARG;
+    bool codes = false;
     for (int i = 0; i < count; ++i) {
         const cm_status st = check_tensor(tensors[i]);
         if (st != CM_OK) return st;
+        codes = codes || (tensors[i].state_bits == 8 && tensors[i].numel > 0);
     }
+    const int64_t chunk = int64_t(codes ? kCodePasses : 1) * kAdamPass;
     Table<kLargeTable> t;
     t.b1 = float(beta1), t.b2 = float(beta2), t.c1 = float(1.0 - beta1), t.c2 = float(1.0 - beta2);
     t.step = float(lr / (1.0 - std::pow(beta1, double(step))));
@@ -343,7 +355,7 @@ extern "C" cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double 
         for (; i < count && t.count < kLargeTable; ++i) {
             const cm_adamw_tensor &x = tensors[i];
             if (x.numel == 0) continue;
-            const int64_t c = (x.numel + kAdamChunk - 1) / kAdamChunk;
+            const int64_t c = (x.numel + chunk - 1) / chunk;
             if (chunks + c > 0x7fffffff) break;
             Entry &e = t.e[t.count++];
             e = {x.param, x.grad, x.master, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.numel};
@@ -359,8 +371,8 @@ extern "C" cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double 
             chunks += c;
         }
         if (t.count == 0) continue;
-        const cudaError_t err = t.count <= kSmallTable ? launch<kSmallTable>(t, chunks, stream)
-                                                       : launch<kLargeTable>(t, chunks, stream);
+        const cudaError_t err = t.count <= kSmallTable ? launch<kSmallTable>(t, codes, chunks, stream)
+                                                       : launch<kLargeTable>(t, codes, chunks, stream);
         if (err != cudaSuccess) return CM_ERR_CUDA;
     }
     return CM_OK;

@@ -10,14 +10,24 @@ namespace cm {
 namespace lin {
 namespace {
 
-// 1 / (1 + exp(-t)): exp's overflow to infinity gives 0, its underflow 1.
-// __expf is off by at most 2 + 1.2 |t| units of the last place and the fast
-// division by 2: below 2^-20 where 1 / (1 + exp(-t)) is not itself below 2^-8,
-// which a bf16 output (2^-9) does not see.
-__device__ __forceinline__ float sigmoid(float t) {
-    const float d = 1.0f + __expf(-t);
-    return d > 1e38f ? 0.0f : __fdividef(1.0f, d);
+// 2^a and 1 / a by the special-function unit, within two units of the last
+// place of fp32; 2^a overflows to infinity, whose reciprocal is 0.
+__device__ __forceinline__ float exp2_fast(float a) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
 }
+__device__ __forceinline__ float rcp_fast(float a) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+// 1 / (1 + exp(-t)), given a = -t log2(e).  The rounding of a costs |a| 2^-24
+// of the result at most: below 2^-19 where the result is not itself below
+// 2^-24, which a bf16 output (2^-8) does not see.
+__device__ __forceinline__ float sigmoid_of(float a) { return rcp_fast(1.0f + exp2_fast(a)); }
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid(float t) { return sigmoid_of(-kLog2e * t); }
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
@@ -27,7 +37,8 @@ __device__ __forceinline__ float act1(float v, int act) {
         case CM_ACT_RELU: return v > 0.0f || v != v ? v : 0.0f;
         case CM_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.7071067811865476f));
         // (1 + tanh u) / 2 = sigmoid(2u)
-        case CM_ACT_GELU_TANH: return v * sigmoid(2.0f * kGeluC * (v + kGeluA * v * v * v));
+        case CM_ACT_GELU_TANH:
+            return v * sigmoid_of(v * (-2.0f * kLog2e * kGeluC + -2.0f * kLog2e * kGeluC * kGeluA * (v * v)));
         case CM_ACT_SILU: return v * sigmoid(v);
         default: return v;
     }
@@ -38,9 +49,9 @@ __device__ __forceinline__ float dact1(float z, int act) {
     switch (act) {
         case CM_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
         case CM_ACT_GELU:
-            return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
+            return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * exp2_fast(-0.5f * kLog2e * z * z) * 0.3989422804014327f;
         case CM_ACT_GELU_TANH: {
-            const float s = sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+            const float s = sigmoid_of(z * (-2.0f * kLog2e * kGeluC + -2.0f * kLog2e * kGeluC * kGeluA * (z * z)));
             return s + 2.0f * z * s * (1.0f - s) * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
         }
         case CM_ACT_SILU: {

@@ -69,11 +69,13 @@ __device__ __noinline__ void report_pair(LinearStatus *s, uint32_t site, int til
 }
 
 // Bounded wait; false once the bound has expired or the CTA is aborting.
+// Every barrier here hands over shared memory that TMA and the tensor cores
+// write and read, or tensor memory: no wait has to order memory of the peer CTA.
 __device__ bool wait_p(const LinearPairParams &p, const LSmem &s, uint64_t *bar, uint32_t parity, uint32_t site, int tile) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0u) {
             if (*s.abort) return false;
             if (globaltimer() - t0 > p.timeout_ns) {
@@ -87,7 +89,7 @@ __device__ bool wait_p(const LinearPairParams &p, const LSmem &s, uint64_t *bar,
 
 __device__ void drain_p(const LinearPairParams &p, uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_cluster(bar, parity))
+    while (!mbar_try_wait(bar, parity))
         if (globaltimer() - t0 > p.timeout_ns) break;
 }
 
@@ -301,6 +303,12 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        // the accumulator is in registers: the products of the next tile but one may start
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
+        };
         const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
         for (int ch = 0; ch < nch; ++ch) {
             if (lane == 0 && !(ch == 0 && in_bytes)) ask(ch);
@@ -320,7 +328,8 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
             for (int h = 0; h < kChunk / 32; ++h) {
                 const int sub = ch * (kChunk / 32) + h;   // 32-column slice of the warp's columns
                 uint32_t (&v)[32] = raw[h];
-                tmem_wait_ld_regs(v);
+                tmem_wait_ld_regs(v);   // the first wait is for all loads of the chunk
+                if (h == 0 && ch == nch - 1) release();
                 const float bsel = sub == 0 ? bias[0] : sub == 1 ? bias[1] : sub == 2 ? bias[2] : bias[3];
                 float f[32];
 #pragma unroll
@@ -408,9 +417,7 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
             if (two) buf0 = buf0 == bufs ? buf1 : bufs;
         }
         if (!ok) break;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty_leader + 8u * uint32_t(acc));
+        if (nch == 0) release();
         if (++acc == 2) {
             acc = 0;
             acc_phase ^= 1u;

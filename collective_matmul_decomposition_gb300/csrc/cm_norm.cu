@@ -612,6 +612,18 @@ __global__ void __launch_bounds__(512) cm_layer_norm_dx_any_kernel(NormParams p)
 
 constexpr int kColY = 8;   // row lanes of a CTA; its 32 column lanes hold V columns each
 
+// out[c] (+)= s, if there is an output
+__device__ __forceinline__ void put_sum(void *out, int f32, int accumulate, int64_t c, float s) {
+    if (!out) return;
+    if (f32) {
+        float *o = static_cast<float *>(out) + c;
+        *o = accumulate ? *o + s : s;
+    } else {
+        bf16 *o = static_cast<bf16 *>(out) + c;
+        from_f(o, accumulate ? to_f(*o) + s : s);
+    }
+}
+
 // Partial sums over the rows of chunk blockIdx.y.  STATS: [chunk][2][h] of
 // dy xh and dy; otherwise [chunk][h] of dy.
 template <typename X, typename Y, int V, bool STATS>
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = b[i] = 0.0f;
     if (c < p.h) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t r = r0 + ty; r < r1; r += kColY) {
             float d[V], f[V];
             const Y *dy = static_cast<const Y *>(p.dy) + r * p.lddy;
@@ -659,7 +671,10 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
             sb += sm[0][k][j];
             if constexpr (STATS) sa += sm[1][k][j];
         }
-        if constexpr (STATS) {
+        if (gridDim.y == 1) {   // a chunk that is all rows: the result itself
+            put_sum(p.dgamma, p.g_f32, p.accumulate, cc, sa);
+            put_sum(p.dbeta, p.g_f32, p.accumulate, cc, sb);
+        } else if constexpr (STATS) {
             p.partial[(int64_t(blockIdx.y) * 2) * p.h + cc] = sa;
             p.partial[(int64_t(blockIdx.y) * 2 + 1) * p.h + cc] = sb;
         } else {
@@ -689,13 +704,7 @@ __global__ void __launch_bounds__(256) cm_sum_parts_kernel(const float *partial,
     s = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s += sm[k][tx];
-    if (f32) {
-        float *o = static_cast<float *>(out) + c;
-        *o = accumulate ? *o + s : s;
-    } else {
-        bf16 *o = static_cast<bf16 *>(out) + c;
-        from_f(o, accumulate ? to_f(*o) + s : s);
-    }
+    put_sum(out, f32, accumulate, c, s);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -718,8 +727,9 @@ int sm_count(int *device = nullptr) {
 }
 
 // Chunks of rows for the column sums: enough CTAs for two rounds of the SMs,
-// at least 32 rows each.
+// at least 32 rows each; few rows are one chunk, whose sum is the result.
 int64_t chunks_for(int64_t rows, int64_t cols) {
+    if (rows <= 128) return 1;
     const int64_t blocks = (cols + 255) / 256;
     return std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, std::max<int64_t>(1, 608 / blocks)));
 }
@@ -879,7 +889,7 @@ cudaError_t backward(NormParams p, cudaStream_t stream) {
         cm_colsum_kernel<X, Y, 8, true><<<dim3(unsigned((p.h + 255) / 256), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
     else
         cm_colsum_kernel<X, Y, 1, true><<<dim3(unsigned((p.h + 31) / 32), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    sum_parts(p.partial, chunks, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
+    if (chunks > 1) sum_parts(p.partial, chunks, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
     return cudaGetLastError();
 }
 
@@ -912,10 +922,13 @@ cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols
     p.rows = rows;
     p.h = cols;
     p.partial = partial;
+    p.dbeta = out;
+    p.g_f32 = out_f32;
+    p.accumulate = accumulate;
     const int64_t chunks = chunks_for(rows, cols);
     cm_colsum_kernel<bf16, bf16, 8, false>
         <<<dim3(unsigned((cols + 255) / 256), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
+    if (chunks > 1) sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
     return cudaGetLastError();
 }
 

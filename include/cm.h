@@ -704,7 +704,7 @@ cm_status cm_layer_norm_backward(const void *x, cm_dtype x_dtype, int64_t ldx, c
  *  another value (a new one each step) rounds each up or down at random so
  *  that its mean is kept, the same way for the same seed, list and element.
  *  Errors: CM_ERR_INVALID_ARG (null or out-of-range argument, bad enum),
- *  CM_ERR_SHAPE (numel < 0 or beyond 2^42), CM_ERR_ALIGNMENT, CM_ERR_CUDA.
+ *  CM_ERR_SHAPE (numel < 0 or beyond 2^41), CM_ERR_ALIGNMENT, CM_ERR_CUDA.
  *  Tensors are all checked before anything is enqueued.
  */
 #define CM_ADAMW_BLOCK 256
