@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "cm_internal.h"
+#include "cm_launch.cuh"
 #include "cm_vec.cuh"
 
 namespace cm {
@@ -215,6 +216,8 @@ __device__ __forceinline__ void put_codes(uint8_t *p, float *scale, const Span &
 // four or six, 8-bit steps were 10 and 4 % slower.
 template <int CAP, bool CODES>
 __global__ void __launch_bounds__(kAdamThreads, 5) cm_adamw_kernel(const __grid_constant__ Table<CAP> t) {
+    let_next_start();
+    wait_for_previous();
     // the tensor of this chunk: the last one that starts at or before it
     int lo = 0, hi = t.count - 1;
     while (lo < hi) {
@@ -296,11 +299,8 @@ cudaError_t launch(const Table<kLargeTable> &all, bool codes, int64_t chunks, cu
     t.step = all.step, t.root_scale = all.root_scale, t.eps = all.eps;
     t.grad_scale = all.grad_scale;
     t.seed_lo = all.seed_lo, t.seed_hi = all.seed_hi, t.seeded = all.seeded;
-    if (codes)
-        cm_adamw_kernel<CAP, true><<<unsigned(chunks), kAdamThreads, 0, stream>>>(t);
-    else
-        cm_adamw_kernel<CAP, false><<<unsigned(chunks), kAdamThreads, 0, stream>>>(t);
-    return cudaGetLastError();
+    return launch_after(codes ? cm_adamw_kernel<CAP, true> : cm_adamw_kernel<CAP, false>, dim3(unsigned(chunks)),
+                        kAdamThreads, 0, 1, stream, t);
 }
 
 cm_status check_tensor(const cm_adamw_tensor &x) {

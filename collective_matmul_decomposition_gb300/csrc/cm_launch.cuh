@@ -1,0 +1,42 @@
+// cm_launch.cuh -- launches that overlap their predecessor's end.
+//
+// A kernel launched with launch_after() may start while the kernel before it
+// in the stream is still finishing (programmatic dependent launch): it sets up
+// its barriers and tensor memory, then wait_for_previous() holds it until that
+// kernel has completed and its writes are visible.  Every kernel launched so
+// calls it in every thread before its first access to global memory, and
+// says with let_next_start() that its own successor may be set up in turn.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace cm {
+namespace {
+
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                         cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+}  // namespace
+}  // namespace cm

@@ -28,6 +28,7 @@
 
 #include "cm_device.cuh"
 #include "cm_kernel.cuh"
+#include "cm_launch.cuh"
 #include "cm_linear.cuh"
 #include "cm_linear_epilogue.cuh"
 
@@ -469,6 +470,8 @@ __device__ uint32_t open_pair(const LinearPairParams &p, LSmem &s, uint8_t *smem
     __syncthreads();
     cluster_sync();   // the CTAs' barriers exist before any cross-CTA arrival or load
     tc_fence_after();
+    let_next_start();
+    wait_for_previous();
     return *s.tmem_slot;
 }
 
@@ -752,10 +755,7 @@ cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int splits
     if (!fn) return cudaErrorInvalidValue;
     // split: one cluster a tile; else persistent
     const int n = splits > 1 ? p.tiles : std::max(1, std::min(clusters, p.tiles));
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
-    pair_config(cfg, attr, unsigned(2 * splits), unsigned(2 * splits * n), stream);
-    return cudaLaunchKernelEx(&cfg, fn, p);
+    return launch_after(fn, dim3(unsigned(2 * splits * n)), kLThreads, size_t(kLSmem), unsigned(2 * splits), stream, p);
 }
 
 }  // namespace cm

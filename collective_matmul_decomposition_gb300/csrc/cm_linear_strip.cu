@@ -24,6 +24,7 @@
 
 #include "cm_device.cuh"
 #include "cm_kernel.cuh"
+#include "cm_launch.cuh"
 #include "cm_linear.cuh"
 #include "cm_linear_epilogue.cuh"
 
@@ -184,6 +185,8 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s.tmem_slot;
+    let_next_start();
+    wait_for_previous();
 
     const int split = p.splits > 1 ? int(cluster_ctarank()) : 0;
     const int tile = int(blockIdx.x) / p.splits;
@@ -344,24 +347,12 @@ cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStre
     const int64_t col_tiles = (p.cols + kTileCols - 1) / kTileCols;
     const int64_t grid = col_tiles * p.row_tiles * p.splits;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(grid), 1, 1);
-    cfg.blockDim = dim3(kThreadsL, 1, 1);
-    cfg.dynamicSmemBytes = size_t(p.ring_bytes) + 1024;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(p.splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    switch (layout) {
-        case 0: return cudaLaunchKernelEx(&cfg, cm_linear_strip_kernel<0>, p);
-        case 2: return cudaLaunchKernelEx(&cfg, cm_linear_strip_kernel<2>, p);
-        case 3: return cudaLaunchKernelEx(&cfg, cm_linear_strip_kernel<3>, p);
-        default: return cudaErrorInvalidValue;
-    }
+    void (*fn)(LinearStripParams) = layout == 0   ? cm_linear_strip_kernel<0>
+                                    : layout == 2 ? cm_linear_strip_kernel<2>
+                                    : layout == 3 ? cm_linear_strip_kernel<3>
+                                                  : nullptr;
+    if (!fn) return cudaErrorInvalidValue;
+    return launch_after(fn, dim3(unsigned(grid)), kThreadsL, size_t(p.ring_bytes) + 1024, unsigned(p.splits), stream, p);
 }
 
 }  // namespace cm

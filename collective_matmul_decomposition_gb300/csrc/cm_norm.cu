@@ -16,6 +16,7 @@
 #include <atomic>
 
 #include "cm_device.cuh"
+#include "cm_launch.cuh"
 #include "cm_linear.cuh"
 #include "cm_vec.cuh"
 
@@ -232,6 +233,8 @@ __device__ __forceinline__ V8 scaled(const V8 &x, float mean, float rstd, const 
 // row's sums through shared memory.
 template <typename X, typename Y, int R, int NR, int S, bool SPLIT>
 __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(const __grid_constant__ NormParams p, int width) {
+    let_next_start();
+    wait_for_previous();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float sums[2][2][kRowBuf];
     __shared__ float other[SPLIT ? 4 : 1];
@@ -314,6 +317,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(con
 // Few rows: `width` threads hold a row in registers.
 template <typename X, typename Y, int R>
 __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int width) {
+    let_next_start();
+    wait_for_previous();
     __shared__ __align__(16) float sums[2][kRowBuf];
     const Group g(width);
     const int per = int(blockDim.x) / width, t = int(threadIdx.x) - g.index * width;
@@ -349,6 +354,8 @@ __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int w
 // row read three times (the second and third time from L2).
 template <typename X, typename Y>
 __global__ void __launch_bounds__(512) cm_layer_norm_any_kernel(NormParams p) {
+    let_next_start();
+    wait_for_previous();
     __shared__ __align__(16) float sums[2][kRowBuf];
     const Group g{int(blockDim.x)};
     const int64_t row = blockIdx.x;
@@ -388,6 +395,8 @@ __global__ void __launch_bounds__(512) cm_layer_norm_any_kernel(NormParams p) {
 template <typename X, typename Y, typename G, int R, int S, bool SPLIT>
 __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_kernel(const __grid_constant__ NormParams p,
                                                                                       int width) {
+    let_next_start();
+    wait_for_previous();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float sums[2][kRowBuf];
     __shared__ float other[SPLIT ? 4 : 1];
@@ -550,6 +559,8 @@ __device__ __forceinline__ V8 gather(const float (&f)[8]) {
 // rows are then the column kernel's.
 template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(512) cm_layer_norm_dx_any_kernel(NormParams p) {
+    let_next_start();
+    wait_for_previous();
     __shared__ __align__(16) float sums[kRowBuf];
     const Group gr{int(blockDim.x)};
     const int64_t row = blockIdx.x;
@@ -628,6 +639,8 @@ __device__ __forceinline__ void put_sum(void *out, int f32, int accumulate, int6
 // dy xh and dy; otherwise [chunk][h] of dy.
 template <typename X, typename Y, int V, bool STATS>
 __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
+    let_next_start();
+    wait_for_previous();
     __shared__ float sm[STATS ? 2 : 1][kColY][32 * V];
     const int tx = int(threadIdx.x) & 31, ty = int(threadIdx.x) >> 5;
     const int64_t c = (int64_t(blockIdx.x) * 32 + tx) * V;
@@ -687,6 +700,8 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
 // every eighth part, then their sums are added in order.
 __global__ void __launch_bounds__(256) cm_sum_parts_kernel(const float *partial, int64_t parts, int64_t h, int64_t stride,
                                                            void *out0, void *out1, int f32, int accumulate) {
+    let_next_start();
+    wait_for_previous();
     __shared__ float sm[8][32];
     const int tx = int(threadIdx.x) & 31, ty = int(threadIdx.x) >> 5;
     const int64_t c = int64_t(blockIdx.x) * 32 + tx;
@@ -737,10 +752,10 @@ int64_t chunks_for(int64_t rows, int64_t cols) {
 constexpr int64_t kRingSmem = 224 * 1024;   // of 227 KB; the kernels' own buffers take up to 2
 
 // The sums over rows of the partial sums of `parts` CTAs.
-void sum_parts(const float *partial, int64_t parts, int64_t h, int64_t stride, void *out0, void *out1, int f32,
-               int accumulate, cudaStream_t stream) {
-    cm_sum_parts_kernel<<<dim3(unsigned((h + 31) / 32), stride > h ? 2 : 1), 256, 0, stream>>>(
-        partial, parts, h, stride, out0, out1, f32, accumulate);
+cudaError_t sum_parts(const float *partial, int64_t parts, int64_t h, int64_t stride, void *out0, void *out1, int f32,
+                      int accumulate, cudaStream_t stream) {
+    return launch_after(cm_sum_parts_kernel, dim3(unsigned((h + 31) / 32), stride > h ? 2 : 1), 256, 0, 1, stream, partial,
+                        parts, h, stride, out0, out1, f32, accumulate);
 }
 
 int row_width(int64_t vecs, int R) { return int((vecs + 32 * R - 1) / (32 * R)) * 32; }
@@ -784,19 +799,8 @@ cudaError_t launch_ring(const NormParams &p, const RingPlan &r, bool split, cuda
         if (e != cudaSuccess) return e;
         prepared[dev].store(true, std::memory_order_release);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(split ? 2 * r.ctas : r.ctas));
-    cfg.blockDim = dim3(unsigned(r.width * r.per));
-    cfg.dynamicSmemBytes = size_t(r.smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = split ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, r.width);
+    return launch_after(kernel, dim3(unsigned(split ? 2 * r.ctas : r.ctas)), unsigned(r.width * r.per), size_t(r.smem),
+                        split ? 2 : 1, stream, p, r.width);
 }
 
 template <typename X, typename Y, int R, int NR, int S, bool SPLIT = false>
@@ -811,8 +815,7 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
                      p.ldo % 8 == 0 && vecs <= 4096;
     if (p.rows > 0x7fffffff) return cudaErrorInvalidValue;
     if (!vec) {
-        cm_layer_norm_any_kernel<X, Y><<<unsigned(p.rows), 512, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_after(cm_layer_norm_any_kernel<X, Y>, dim3(unsigned(p.rows)), 512, 0, 1, stream, p);
     }
     const int sms = sm_count();
     // the rings pay once a group has a few steps to run ahead on
@@ -833,13 +836,10 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
     const int R = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
     const int width = row_width(vecs, R), per = std::max(1, 128 / width);
     const unsigned grid = unsigned((p.rows + per - 1) / per), threads = unsigned(width * per);
-    if (R == 1)
-        cm_layer_norm_kernel<X, Y, 1><<<grid, threads, 0, stream>>>(p, width);
-    else if (R == 2)
-        cm_layer_norm_kernel<X, Y, 2><<<grid, threads, 0, stream>>>(p, width);
-    else
-        cm_layer_norm_kernel<X, Y, 4><<<grid, threads, 0, stream>>>(p, width);
-    return cudaGetLastError();
+    return launch_after(R == 1   ? cm_layer_norm_kernel<X, Y, 1>
+                        : R == 2 ? cm_layer_norm_kernel<X, Y, 2>
+                                 : cm_layer_norm_kernel<X, Y, 4>,
+                        dim3(grid), threads, 0, 1, stream, p, width);
 }
 
 template <typename X, typename Y, int R, int S, bool SPLIT = false, typename G = float>
@@ -875,22 +875,18 @@ cudaError_t backward(NormParams p, cudaStream_t stream) {
         }
         if (r.ctas > 0 && (e != cudaSuccess || !sums)) return e;
         if (r.ctas > 0) {
-            sum_parts(p.partial, r.ctas, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
-            return cudaGetLastError();
+            return sum_parts(p.partial, r.ctas, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
         }
     }
-    if (vec)
-        cm_layer_norm_dx_any_kernel<X, Y, 8><<<unsigned(p.rows), 512, 0, stream>>>(p);
-    else
-        cm_layer_norm_dx_any_kernel<X, Y, 1><<<unsigned(p.rows), 512, 0, stream>>>(p);
-    if (!sums) return cudaGetLastError();
+    cudaError_t e = launch_after(vec ? cm_layer_norm_dx_any_kernel<X, Y, 8> : cm_layer_norm_dx_any_kernel<X, Y, 1>,
+                                 dim3(unsigned(p.rows)), 512, 0, 1, stream, p);
+    if (e != cudaSuccess || !sums) return e;
     const int64_t chunks = chunks_for(p.rows, p.h);
-    if (in_vec)
-        cm_colsum_kernel<X, Y, 8, true><<<dim3(unsigned((p.h + 255) / 256), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    else
-        cm_colsum_kernel<X, Y, 1, true><<<dim3(unsigned((p.h + 31) / 32), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    if (chunks > 1) sum_parts(p.partial, chunks, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
-    return cudaGetLastError();
+    const int per_cta = in_vec ? 256 : 32;   // columns
+    e = launch_after(in_vec ? cm_colsum_kernel<X, Y, 8, true> : cm_colsum_kernel<X, Y, 1, true>,
+                     dim3(unsigned((p.h + per_cta - 1) / per_cta), unsigned(chunks)), 32 * kColY, 0, 1, stream, p);
+    if (e != cudaSuccess || chunks == 1) return e;
+    return sum_parts(p.partial, chunks, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
 }
 
 }  // namespace
@@ -926,10 +922,10 @@ cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols
     p.g_f32 = out_f32;
     p.accumulate = accumulate;
     const int64_t chunks = chunks_for(rows, cols);
-    cm_colsum_kernel<bf16, bf16, 8, false>
-        <<<dim3(unsigned((cols + 255) / 256), unsigned(chunks)), 32 * kColY, 0, stream>>>(p);
-    if (chunks > 1) sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
-    return cudaGetLastError();
+    const cudaError_t e = launch_after(cm_colsum_kernel<bf16, bf16, 8, false>,
+                                       dim3(unsigned((cols + 255) / 256), unsigned(chunks)), 32 * kColY, 0, 1, stream, p);
+    if (e != cudaSuccess || chunks == 1) return e;
+    return sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
 }
 
 }  // namespace cm
