@@ -123,34 +123,37 @@ struct Choice {
     int tok = 16, splits = 1, ring_bytes = 0;
 };
 
-// The choice with the least estimated time.  The estimates' constants were fitted to
-// calls on one GB300 with weights from HBM (us): a K slice of 64 takes a
-// wave of pair tiles 0.33 (256 columns) or 0.21 (128 columns), starting and
-// finishing 7.5 or 5.5, splitting 2 more; strips start and finish in 6.5 (8 if
-// split) and then run at what HBM (6.3 TB/s) or the SMs' reads of L2 (11
-// TB/s, each tile its own copy of the rows) allow, 0.2 a slice at least.  Measured
-// on both sides of where the choice changes (best strip against best pair):
-//   rows 45,  K 8190,  cols 3579:   16.0 / 18.5      rows 100, K 8192, cols 3584:  19.3 / 20.5
-//   rows 200, K 8192,  cols 3584:   24.9 / 20.8      rows 256, K 12288, cols 4608: 37.4 / 31.2
-//   rows 128, K 4096,  cols 16384:  30.8 / 30.5      rows 512, K 4096, cols 4096:  22.9 / 18.7
-// and between pair tiles (256 columns / 128 columns / split):
-//   rows 2048, K 12288, cols 4608:  128.7 / 161 / -  rows 512, K 4096, cols 4096:  24.8 / 18.7 / 19.0
-//   rows 1024, cols 1024, K 8192:   40.1 / 23.1 / 16.8 (128 columns, two pairs)
+// The choice with the least estimated time.  The estimates' constants were
+// fitted to calls on one GB300 with weights from HBM, in us.
+//   pair: a K slice of 64 takes a wave of tiles 0.33 (256 columns) or 0.21
+//     (128), but no wave is shorter than its epilogue, 2.9 or 2.0; a launch
+//     takes 2.5 beyond that, summing over a cluster's pairs 6.5 or 4.
+//   strip: a launch takes 4, and 0.02 a row of the tile; split, 5.5 and 0.045.
+//   Between, HBM gives 6.3 TB/s, the SMs read L2 (every tile its own copy of the
+//   rows) at 11 TB/s, and a slice takes 0.2.
+// Measured on both sides of where the choice changes (best strip / best pair):
+//   rows 45,  K 8190, cols 3579:  15.0 / 18.5     rows 100, K 8192,  cols 3584: 19.3 / 20.5
+//   rows 200, K 8192, cols 3584:  24.9 / 20.8     rows 256, K 12288, cols 4608: 37.4 / 31.2
+//   rows 100, K 1024, cols 2048:   7.0 / 6.5      rows 512, K 4096,  cols 4096: 22.9 / 18.7
+// between pair tiles (256 columns / 128 / 128 on two pairs a tile):
+//   rows 2048, K 12288, cols 4608:  129 / 161 / -     rows 1024, K 8192, cols 1024:  40.1 / 23.1 / 16.8
+// and between strips (one tile of rows / more, shorter ones):
+//   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  24.4 / 29.0 (three)
 Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn) {
     Choice best;
     double least = 1e30;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t slices = up(k, kBK);
-    const double weights = double(cols) * double(k) * 2.0;   // bytes
+    const double from_hbm = double(cols) * double(k) * 2.0 / 6.3e6;
     // pair tiles waste what they have beyond `rows`: not worth a look below 33
     for (int bn = 256; bn >= 128 && rows > 32; bn /= 2) {
         const int64_t tiles = up(rows, 256) * up(cols, bn);
         for (int i = 0; i < 3; ++i) {
             const int splits = 1 << i;
             if (i > 0 && (tiles > d.clusters[i] || slices < 2 * splits)) break;
-            const double t = (bn == 256 ? 7.5 : 5.5) + (i ? 2.0 : 0.0) +
-                             std::max(double(up(tiles, d.clusters[i])) * double(up(slices, splits)) * (bn == 256 ? 0.33 : 0.21),
-                                      weights / 6.3e6);
+            const double wave = std::max(double(up(slices, splits)) * (bn == 256 ? 0.33 : 0.21), bn == 256 ? 2.9 : 2.0);
+            const double t = 2.5 + (i == 0 ? 0.0 : bn == 256 ? 6.5 : 4.0) +
+                             std::max(double(up(tiles, d.clusters[i])) * wave, from_hbm);
             if (t < least) {
                 least = t;
                 best.pair = true;
@@ -159,23 +162,26 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
             }
         }
     }
-    for (int64_t parts = 1; parts <= 2 && rows <= 512; ++parts) {
+    for (int64_t parts = 1; parts <= 4 && rows <= 512; ++parts) {
         const int64_t unit = row_mn ? 64 : 16, tok = up(up(rows, parts), unit) * unit;
         if (tok > 256) continue;
-        const int64_t row_tiles = up(rows, tok), tiles = row_tiles * up(cols, 128);
-        // two CTAs an SM if there are tiles or K slices for them
-        int64_t splits = std::max<int64_t>(1, std::min({int64_t(8), 2 * d.sms / tiles, slices}));
-        if (tok > 128) splits = 1;   // partial tiles of more rows do not fit two to an SM
-        const double per_sm = double(up(tiles * splits, d.sms));
-        const double traffic = double(tiles) * double(128 + tok) * double(k) * 2.0;
-        const double t = (splits > 1 ? 8.0 : 6.5) +
-                         std::max({weights / 6.3e6, traffic / 11e6, 0.2 * double(up(slices, splits)) * per_sm});
-        if (t < least) {
+        const int64_t tiles = up(rows, tok) * up(cols, 128);
+        const double from_l2 = double(tiles) * double(128 + tok) * double(k) * 2.0 / 11e6;
+        // unsplit, or split until there are two CTAs an SM; partial tiles of
+        // more than 128 rows do not fit two to an SM
+        const int64_t most = tok > 128 ? 1 : std::max<int64_t>(1, std::min({int64_t(8), 2 * d.sms / tiles, slices}));
+        for (int64_t splits = 1; splits <= most; splits += std::max<int64_t>(1, most - 1)) {
+            const double run = 0.2 * double(up(slices, splits)) * double(up(tiles * splits, d.sms));
+            const double t = (splits > 1 ? 5.5 + 0.045 * double(tok) : 4.0 + 0.02 * double(tok)) +
+                             std::max({from_hbm, from_l2, run});
+            if (t >= least) continue;
             least = t;
             best.pair = false;
             best.tok = int(tok);
             best.splits = int(splits);
-            best.ring_bytes = (splits == 1 && tiles <= d.sms ? 216 : 108) * 1024;   // clusters pack worse at 216
+            // a CTA has an SM to itself where there are SMs enough; clusters
+            // of such CTAs only pack where half of them are
+            best.ring_bytes = (tiles * splits <= (splits == 1 ? d.sms : d.sms / 2) ? 216 : 108) * 1024;
         }
     }
     return best;

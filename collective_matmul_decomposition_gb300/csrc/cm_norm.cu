@@ -138,10 +138,22 @@ __device__ __forceinline__ float with_other(float v, float *slot, int rank) {
 // A parameter vector to shared memory as fp32, 1 (or 0) where there is none.
 // The first and second halves of the vectors lie in two planes of h8 / 2, so
 // that neighbouring threads read neighbouring 16 bytes.  Columns c0 .. c0 + h.
-__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int c0, int h, int h8) {
-    for (int c = int(threadIdx.x) * 8; c < h; c += int(blockDim.x) * 8) {
-        const V8 v = load_param8(p, f32, null_value, c0 + c, c0 + h);
-        const float2 a0 = parts(v.p[0]), a1 = parts(v.p[1]), b0 = parts(v.p[2]), b1 = parts(v.p[3]);
+// A group of `width` threads, t its place in it, covers the row with R vectors
+// a thread; all loads before the first store.
+template <int R>
+__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int c0, int h, int h8,
+                                            int width, int t) {
+    V8 v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * width + t) * 8;
+        v[r] = c < h ? load_param8(p, f32, null_value, c0 + c, c0 + h) : fill(0.0f);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * width + t) * 8;
+        if (c >= h) break;
+        const float2 a0 = parts(v[r].p[0]), a1 = parts(v[r].p[1]), b0 = parts(v[r].p[2]), b1 = parts(v[r].p[3]);
         *reinterpret_cast<float4 *>(dst + c / 2) = make_float4(a0.x, a0.y, a1.x, a1.y);
         *reinterpret_cast<float4 *>(dst + (h8 + c) / 2) = make_float4(b0.x, b0.y, b1.x, b1.y);
     }
@@ -263,8 +275,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(con
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) ask(k);
-    stage_param(gamma, p.gamma, p.p_f32, 1.0f, c0, h, h8);
-    stage_param(beta, p.beta, p.p_f32, 0.0f, c0, h, h8);
+    if (g.index == 0) {
+        stage_param<R>(gamma, p.gamma, p.p_f32, 1.0f, c0, h, h8, width, t);
+        stage_param<R>(beta, p.beta, p.p_f32, 0.0f, c0, h, h8, width, t);
+    }
     __syncthreads();
     const float inv_h = 1.0f / float(p.h);
     int st = 0, flip = 0;
@@ -433,9 +447,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) ask(k);
-    for (int c = int(threadIdx.x) * 8; c < h; c += int(blockDim.x) * 8)
-        store8(gamma + c, load_param8(p.gamma, p.p_f32, 1.0f, c0 + c, c0 + h));
     V8 a[R], b[R];
+    if (g.index == 0) {   // all loads before the first store
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+            a[r] = c < h ? load_param8(p.gamma, p.p_f32, 1.0f, c0 + c, c0 + h) : fill(0.0f);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * width + t) * 8;
+            if (c < h) store8(gamma + c, a[r]);
+        }
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) a[r] = b[r] = fill(0.0f);
     __syncthreads();
@@ -510,9 +534,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_backward_ring_k
     if (!p.partial) return;
     float *const mine = p.partial + int64_t(cols.cta) * 2 * p.h + c0;
     if (per == 1) {
+        const bool whole = p.h % 8 == 0;   // every part's row starts on 16 bytes
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int c = (r * width + t) * 8;
+            if (whole && c < h) {
+                store8(mine + c, a[r]);
+                store8(mine + p.h + c, b[r]);
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 u = parts(a[r].p[i]), v = parts(b[r].p[i]);
@@ -621,7 +651,7 @@ __global__ void __launch_bounds__(512) cm_layer_norm_dx_any_kernel(NormParams p)
 
 // ---- column sums: dgamma and dbeta, or the plain sum of a matrix's rows ---------------
 
-constexpr int kColY = 8;   // row lanes of a CTA; its 32 column lanes hold V columns each
+constexpr int kColY = 8;   // row lanes of a CTA, or 32 for few rows; its 32 column lanes hold V columns each
 
 // out[c] (+)= s, if there is an output
 __device__ __forceinline__ void put_sum(void *out, int f32, int accumulate, int64_t c, float s) {
@@ -637,11 +667,11 @@ __device__ __forceinline__ void put_sum(void *out, int f32, int accumulate, int6
 
 // Partial sums over the rows of chunk blockIdx.y.  STATS: [chunk][2][h] of
 // dy xh and dy; otherwise [chunk][h] of dy.
-template <typename X, typename Y, int V, bool STATS>
-__global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
+template <typename X, typename Y, int V, bool STATS, int kY>
+__global__ void __launch_bounds__(32 * kY) cm_colsum_kernel(NormParams p) {
     let_next_start();
     wait_for_previous();
-    __shared__ float sm[STATS ? 2 : 1][kColY][32 * V];
+    __shared__ float sm[STATS ? 2 : 1][kY][32 * V];
     const int tx = int(threadIdx.x) & 31, ty = int(threadIdx.x) >> 5;
     const int64_t c = (int64_t(blockIdx.x) * 32 + tx) * V;
     const int64_t r0 = p.rows * blockIdx.y / gridDim.y, r1 = p.rows * (blockIdx.y + 1) / gridDim.y;
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
     for (int i = 0; i < V; ++i) a[i] = b[i] = 0.0f;
     if (c < p.h) {
 #pragma unroll 8
-        for (int64_t r = r0 + ty; r < r1; r += kColY) {
+        for (int64_t r = r0 + ty; r < r1; r += kY) {
             float d[V], f[V];
             const Y *dy = static_cast<const Y *>(p.dy) + r * p.lddy;
             const X *x = static_cast<const X *>(p.x) + r * p.ldx;
@@ -676,11 +706,11 @@ __global__ void __launch_bounds__(32 * kColY) cm_colsum_kernel(NormParams p) {
         sm[0][ty][tx * V + i] = b[i];
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < 32 * V; j += 32 * kColY) {
+    for (int j = threadIdx.x; j < 32 * V; j += 32 * kY) {
         const int64_t cc = int64_t(blockIdx.x) * 32 * V + j;
         if (cc >= p.h) continue;
         float sb = 0.0f, sa = 0.0f;
-        for (int k = 0; k < kColY; ++k) {
+        for (int k = 0; k < kY; ++k) {
             sb += sm[0][k][j];
             if constexpr (STATS) sa += sm[1][k][j];
         }
@@ -883,7 +913,7 @@ cudaError_t backward(NormParams p, cudaStream_t stream) {
     if (e != cudaSuccess || !sums) return e;
     const int64_t chunks = chunks_for(p.rows, p.h);
     const int per_cta = in_vec ? 256 : 32;   // columns
-    e = launch_after(in_vec ? cm_colsum_kernel<X, Y, 8, true> : cm_colsum_kernel<X, Y, 1, true>,
+    e = launch_after(in_vec ? cm_colsum_kernel<X, Y, 8, true, kColY> : cm_colsum_kernel<X, Y, 1, true, kColY>,
                      dim3(unsigned((p.h + per_cta - 1) / per_cta), unsigned(chunks)), 32 * kColY, 0, 1, stream, p);
     if (e != cudaSuccess || chunks == 1) return e;
     return sum_parts(p.partial, chunks, p.h, 2 * p.h, p.dgamma, p.dbeta, p.g_f32, p.accumulate, stream);
@@ -922,8 +952,10 @@ cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols
     p.g_f32 = out_f32;
     p.accumulate = accumulate;
     const int64_t chunks = chunks_for(rows, cols);
-    const cudaError_t e = launch_after(cm_colsum_kernel<bf16, bf16, 8, false>,
-                                       dim3(unsigned((cols + 255) / 256), unsigned(chunks)), 32 * kColY, 0, 1, stream, p);
+    const cudaError_t e = launch_after(chunks == 1 ? cm_colsum_kernel<bf16, bf16, 8, false, 32>
+                                                   : cm_colsum_kernel<bf16, bf16, 8, false, kColY>,
+                                       dim3(unsigned((cols + 255) / 256), unsigned(chunks)),
+                                       32 * (chunks == 1 ? 32 : kColY), 0, 1, stream, p);
     if (e != cudaSuccess || chunks == 1) return e;
     return sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
 }

@@ -104,7 +104,8 @@ cm_status cm_layer_norm_backward(const void *x, cm_dtype x_dtype, int64_t ldx, c
     CM_TRY(check_rows(dx, x_dtype, lddx, h));
     if (residual) CM_TRY(check_rows(residual, x_dtype, ldr, h));
     if (!mean || !rstd) return CM_ERR_INVALID_ARG;
-    if (misaligned(mean, CM_F32) || misaligned(rstd, CM_F32) || misaligned(ws, CM_F32)) return CM_ERR_ALIGNMENT;
+    if (misaligned(mean, CM_F32) || misaligned(rstd, CM_F32) || (reinterpret_cast<uintptr_t>(ws) & 15u) != 0)
+        return CM_ERR_ALIGNMENT;
     if ((dgamma || dbeta) && (!ws || ws_bytes < backward_workspace(rows, h))) return CM_ERR_WORKSPACE;
     NormParams p = {};
     p.x = x;
