@@ -186,7 +186,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     tc_fence_after();
     const uint32_t tmem = *s.tmem_slot;
     let_next_start();
-    wait_for_previous();
 
     const int split = p.splits > 1 ? int(cluster_ctarank()) : 0;
     const int tile = int(blockIdx.x) / p.splits;
@@ -194,6 +193,20 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const int col0 = ct * kTileCols, row0 = rt * p.tok;
     const int kb0 = int(int64_t(p.kblocks) * split / p.splits), kb1 = int(int64_t(p.kblocks) * (split + 1) / p.splits);
     const uint32_t stage_bytes = uint32_t(kStripA + p.tok * kBK * 2);
+
+    // The first slices of the column operand start on their way to L2 while the
+    // previous kernel finishes.  Should that kernel still write them, L2 gets its
+    // values all the same: the loads below, which come after it, read L2.
+    if (warp == 0 && elect_one())
+        for (int kb = kb0; kb < min(kb1, kb0 + p.stages); ++kb) {
+            if (A_MN) {
+                for (int j = 0; j < kTileCols / 64; ++j) tma_prefetch_3d(&p.tmA, col0 + 64 * j, kb * kBK, 0);
+            } else {
+                tma_prefetch_3d(&p.tmA, kb * kBK, col0, 0);
+            }
+        }
+    __syncwarp();
+    wait_for_previous();
 
     if (warp == 0) {
         if (elect_one()) {
