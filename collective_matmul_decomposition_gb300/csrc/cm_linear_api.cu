@@ -54,6 +54,14 @@ bool map_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A matrix that 32-row boxes are stored to: up to the last whole 16-byte piece
+// of its rows, because stores are clipped in such pieces (a map needs one at
+// least; where there is none nothing is stored through it).
+bool map_written(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, bool f32) {
+    const int64_t piece = f32 ? 4 : 8;
+    return map_rows(m, base, rows, std::max(piece, cols / piece * piece), ld, 32, f32);
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool bad_dtype(cm_dtype t) { return t != CM_BF16 && t != CM_F32; }
 
@@ -203,11 +211,11 @@ cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
     if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, c.bn / 2) ||
-        !map_rows(&p.tmY, e.y, rows, cols, e.ldy, 32, e.y_f32 != 0))
+        !map_written(&p.tmY, e.y, rows, cols, e.ldy, e.y_f32 != 0))
         return CM_ERR_CUDA;
     if (!e.y_f32) {
-        if (e.z && !map_rows(&p.tmZ, e.z, rows, cols, e.ldz, 32)) return CM_ERR_CUDA;
-        if (e.accumulate) p.tmIn0 = p.tmY;
+        if (e.z && !map_written(&p.tmZ, e.z, rows, cols, e.ldz, false)) return CM_ERR_CUDA;
+        if (e.accumulate && !map_rows(&p.tmIn0, e.y, rows, cols, e.ldy, 32)) return CM_ERR_CUDA;
         if (e.res && !map_rows(&p.tmIn0, e.res, rows, cols, e.ldr, 32)) return CM_ERR_CUDA;
         if (e.dact && !map_rows(&p.tmIn1, e.zin, rows, cols, e.ldzin, 32)) return CM_ERR_CUDA;
     }

@@ -229,24 +229,33 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// One row of a chunk's results from the buffers, element by element.
+// The results of one row's columns col .. col + n - 1 (fewer than a 16-byte
+// piece holds), the first of them at element `at` of the buffers' rows.
 template <bool F32>
-__device__ __noinline__ void store_tail(const LinearPairParams &p, uint8_t *buf0, uint8_t *buf1, int64_t row, int64_t col,
-                                        int ncols, int r) {
+__device__ __noinline__ void store_rest(const LinearPairParams &p, uint8_t *buf0, uint8_t *buf1, int64_t row, int64_t col,
+                                        int at, int n, int r) {
     if (row >= p.rows) return;
-    for (int i = 0; i < ncols; ++i) {
-        if (F32) {
-            const float v = reinterpret_cast<const float *>(piece(buf0, r, i >> 2))[i & 3];
-            float *y = static_cast<float *>(p.e.y) + row * p.e.ldy + col + i;
-            *y = p.e.accumulate ? *y + v : v;
-        } else {
-            static_cast<__nv_bfloat16 *>(p.e.y)[row * p.e.ldy + col + i] =
-                reinterpret_cast<const __nv_bfloat16 *>(piece(buf0, r, i >> 3))[i & 7];
-            if (p.e.z)
-                static_cast<__nv_bfloat16 *>(p.e.z)[row * p.e.ldz + col + i] =
-                    reinterpret_cast<const __nv_bfloat16 *>(piece(buf1, r, i >> 3))[i & 7];
-        }
+    if (F32) {
+        const uint4 w = *piece(buf0, r, at >> 2);
+        const float f[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+        float *y = static_cast<float *>(p.e.y) + row * p.e.ldy + col;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < n) y[i] = p.e.accumulate ? y[i] + f[i] : f[i];
+        return;
     }
+    float f[8];
+    unpack8(*piece(buf0, r, at >> 3), f);
+    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.e.y) + row * p.e.ldy + col;
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) y[i] = __float2bfloat16_rn(f[i]);
+    if (!p.e.z) return;
+    unpack8(*piece(buf1, r, at >> 3), f);
+    __nv_bfloat16 *z = static_cast<__nv_bfloat16 *>(p.e.z) + row * p.e.ldz + col;
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) z[i] = __float2bfloat16_rn(f[i]);
 }
 
 // F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).
@@ -267,9 +276,11 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
     // take turns with the two, so that one is filled while the other is written out
     const bool two = !(in1 || (!F32 && e.z));
     uint8_t *buf0 = bufs, *const buf1 = bufs + kEpiBuf;
-    // TMA writes whole 16-byte pieces: a row that ends inside one has its last
-    // chunk written by the threads
-    const bool ragged = p.cols % (F32 ? 4 : 8) != 0;
+    // TMA writes whole 16-byte pieces: the maps written through end at the last
+    // whole one of a row, and the threads write what is left of it
+    constexpr int kPiece = F32 ? 4 : 8;
+    const int rest = int(p.cols % kPiece);
+    const int64_t whole = p.cols - rest;
     int acc = 0;
     uint32_t acc_phase = 0, in_phase = 0;
     bool pending = false;   // inputs asked for and not yet waited for
@@ -396,23 +407,19 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
                                                            __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3]));
                 }
             }
-            const int ncols = int(min(int64_t(kChunk), p.cols - (cbase + ch * kChunk)));
-            if (ncols < kChunk && ragged) {
-                store_tail<F32>(p, buf0, buf1, int64_t(row0) + lane, cbase + ch * kChunk, ncols, lane);
-                fence_proxy_async_smem();   // the buffers' next filling comes after these reads
-                __syncwarp();
-                if (lane == 0) bulk_commit();   // one group a chunk, as the others have
-                if (two) buf0 = buf0 == bufs ? buf1 : bufs;
-                continue;
-            }
+            const int c0 = cbase + ch * kChunk;
+            if (rest && c0 + kChunk > whole)
+                store_rest<F32>(p, buf0, buf1, int64_t(row0) + lane, whole, int(whole - c0), rest, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (F32 && e.accumulate)
-                    tma_reduce_add_3d(&p.tmY, buf0, cbase + ch * kChunk, row0, 0);
-                else
-                    tma_store_3d(&p.tmY, buf0, cbase + ch * kChunk, row0, 0);
-                if (!F32 && e.z) tma_store_3d(&p.tmZ, buf1, cbase + ch * kChunk, row0, 0);
+                if (c0 < whole) {
+                    if (F32 && e.accumulate)
+                        tma_reduce_add_3d(&p.tmY, buf0, c0, row0, 0);
+                    else
+                        tma_store_3d(&p.tmY, buf0, c0, row0, 0);
+                    if (!F32 && e.z) tma_store_3d(&p.tmZ, buf1, c0, row0, 0);
+                }
                 bulk_commit();
             }
             if (two) buf0 = buf0 == bufs ? buf1 : bufs;
