@@ -5,10 +5,13 @@
 #include <cuda_bf16.h>
 
 #include "cm_linear.cuh"
+#include "cm_vec.cuh"
 
 namespace cm {
 namespace lin {
 namespace {
+
+using namespace vec;
 
 // 2^a and 1 / a by the special-function unit, within two units of the last
 // place of fp32; 2^a overflows to infinity, whose reciprocal is 0.
@@ -22,107 +25,125 @@ __device__ __forceinline__ float rcp_fast(float a) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
     return r;
 }
-// 1 / (1 + exp(-t)), given a = -t log2(e).  The rounding of a costs |a| 2^-24
-// of the result at most: below 2^-19 where the result is not itself below
-// 2^-24, which a bf16 output (2^-8) does not see.
-__device__ __forceinline__ float sigmoid_of(float a) { return rcp_fast(1.0f + exp2_fast(a)); }
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float sigmoid(float t) { return sigmoid_of(-kLog2e * t); }
-
-// The normal distribution's integral up to v, and exp(-v^2 / 2).  By formula
-// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions, whose
-// error is at most 1.5e-7: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with
-// t = 1 / (1 + p x), for x = |v| / sqrt 2.  A third of erff's instructions.
-__device__ __forceinline__ float normal_cdf(float v, float &e) {
-    const float x = fabsf(v) * 0.7071067811865476f;
-    e = exp2_fast(-0.5f * kLog2e * (v * v));
-    const float t = rcp_fast(fmaf(0.3275911f, x, 1.0f));
-    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-    const float half = 0.5f * q * e;   // of erfc
-    return v < 0.0f ? half : 1.0f - half;
+__device__ __forceinline__ F2 exp2_fast(F2 a) {
+    const float2 p = parts(a);
+    return pair(exp2_fast(p.x), exp2_fast(p.y));
+}
+__device__ __forceinline__ F2 rcp_fast(F2 a) {
+    const float2 p = parts(a);
+    return pair(rcp_fast(p.x), rcp_fast(p.y));
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float act1(float v, int act) {
-    switch (act) {
-        case CM_ACT_RELU: return v > 0.0f || v != v ? v : 0.0f;
-        case CM_ACT_GELU: {
-            float e;
-            return v * normal_cdf(v, e);
-        }
-        // (1 + tanh u) / 2 = sigmoid(2u)
-        case CM_ACT_GELU_TANH:
-            return v * sigmoid_of(v * (-2.0f * kLog2e * kGeluC + -2.0f * kLog2e * kGeluC * kGeluA * (v * v)));
-        case CM_ACT_SILU: return v * sigmoid(v);
-        default: return v;
+// 1 / (1 + exp(-t)), given a = -t log2(e).  The rounding of a costs |a| 2^-24
+// of the result at most: below 2^-19 where the result is not itself below
+// 2^-24, which a bf16 output (2^-8) does not see.
+__device__ __forceinline__ F2 sigmoid_of(F2 a) { return rcp_fast(add(both(1.0f), exp2_fast(a))); }
+// (1 + tanh u) / 2 = sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3); v2 = v^2
+__device__ __forceinline__ F2 gelu_tanh_gate(F2 v, F2 v2) {
+    constexpr float k = -2.0f * kLog2e * kGeluC;
+    return sigmoid_of(mul(v, fma(v2, both(k * kGeluA), both(k))));
+}
+// The normal distribution's integral up to v, and e = exp(-v^2 / 2).  By formula
+// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions, whose
+// error is at most 1.5e-7: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with
+// t = 1 / (1 + p x), for x = |v| / sqrt 2.  A third of erff's instructions.
+__device__ __forceinline__ F2 normal_cdf(F2 v, F2 &e) {
+    const float2 s = parts(v);
+    constexpr float px = 0.3275911f * 0.7071067811865476f;
+    const F2 t = rcp_fast(pair(fmaf(px, fabsf(s.x), 1.0f), fmaf(px, fabsf(s.y), 1.0f)));
+    e = exp2_fast(mul(mul(v, v), both(-0.5f * kLog2e)));
+    F2 q = fma(t, both(1.061405429f), both(-1.453152027f));
+    q = fma(t, q, both(1.421413741f));
+    q = fma(t, q, both(-0.284496736f));
+    q = fma(t, q, both(0.254829592f));
+    // q t e / 2 lies under the near tail; what is left to 1/2 goes by v's sign
+    const float2 d = parts(fma(mul(q, t), mul(e, both(-0.5f)), both(0.5f)));
+    const float2 h = parts(mul(mul(q, t), mul(e, both(0.5f))));
+    return pair(s.x < 0.0f ? h.x : 0.5f + d.x, s.y < 0.0f ? h.y : 0.5f + d.y);
+}
+
+// act(v) of a pair
+template <int ACT>
+__device__ __forceinline__ F2 act2(F2 v) {
+    if constexpr (ACT == CM_ACT_RELU) {
+        const float2 s = parts(v);
+        return pair(s.x > 0.0f || s.x != s.x ? s.x : 0.0f, s.y > 0.0f || s.y != s.y ? s.y : 0.0f);
+    } else if constexpr (ACT == CM_ACT_GELU) {
+        F2 e;
+        return mul(v, normal_cdf(v, e));
+    } else if constexpr (ACT == CM_ACT_GELU_TANH) {
+        return mul(v, gelu_tanh_gate(v, mul(v, v)));
+    } else if constexpr (ACT == CM_ACT_SILU) {
+        return mul(v, sigmoid_of(mul(v, both(-kLog2e))));
+    } else {
+        return v;
     }
 }
 
-// the activation's derivative at z
-__device__ __forceinline__ float dact1(float z, int act) {
-    switch (act) {
-        case CM_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-        case CM_ACT_GELU: {
-            float e;
-            const float cdf = normal_cdf(z, e);
-            return cdf + z * e * 0.3989422804014327f;
-        }
-        case CM_ACT_GELU_TANH: {
-            const float s = sigmoid_of(z * (-2.0f * kLog2e * kGeluC + -2.0f * kLog2e * kGeluC * kGeluA * (z * z)));
-            return s + 2.0f * z * s * (1.0f - s) * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
-        }
-        case CM_ACT_SILU: {
-            const float s = sigmoid(z);
-            return s * (1.0f + z * (1.0f - s));
-        }
-        default: return 1.0f;
+// act'(z) of a pair
+template <int ACT>
+__device__ __forceinline__ F2 dact2(F2 z) {
+    if constexpr (ACT == CM_ACT_RELU) {
+        const float2 s = parts(z);
+        return pair(s.x > 0.0f ? 1.0f : 0.0f, s.y > 0.0f ? 1.0f : 0.0f);
+    } else if constexpr (ACT == CM_ACT_GELU) {
+        F2 e;
+        const F2 cdf = normal_cdf(z, e);
+        return fma(mul(z, both(0.3989422804014327f)), e, cdf);
+    } else if constexpr (ACT == CM_ACT_GELU_TANH) {
+        // s + z s (1 - s) 2u'
+        const F2 z2 = mul(z, z), s = gelu_tanh_gate(z, z2);
+        const F2 du = fma(z2, both(6.0f * kGeluC * kGeluA), both(2.0f * kGeluC));
+        return fma(mul(z, s), mul(fma(s, both(-1.0f), both(1.0f)), du), s);
+    } else if constexpr (ACT == CM_ACT_SILU) {
+        const F2 s = sigmoid_of(mul(z, both(-kLog2e)));
+        return mul(s, fma(z, fma(s, both(-1.0f), both(1.0f)), both(1.0f)));
+    } else {
+        return both(1.0f);
     }
 }
 
-// The same over a slice, the choice outside the loop.
+template <int ACT, int N>
+__device__ __forceinline__ void act_loop(float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 r = parts(act2<ACT>(pair(f[i], f[i + 1])));
+        f[i] = r.x;
+        f[i + 1] = r.y;
+    }
+}
+template <int ACT, int N>
+__device__ __forceinline__ void dact_loop(float (&f)[N], const float (&z)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 r = parts(mul(pair(f[i], f[i + 1]), dact2<ACT>(pair(z[i], z[i + 1]))));
+        f[i] = r.x;
+        f[i + 1] = r.y;
+    }
+}
+
+// f = act(f), and f *= act'(z); the choice of activation outside the loop.
 template <int N>
 __device__ __forceinline__ void apply_act(float (&f)[N], int act) {
     switch (act) {
-        case CM_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_RELU);
-            break;
-        case CM_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_GELU);
-            break;
-        case CM_ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_GELU_TANH);
-            break;
-        case CM_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act1(f[i], CM_ACT_SILU);
-            break;
+        case CM_ACT_RELU: act_loop<CM_ACT_RELU>(f); break;
+        case CM_ACT_GELU: act_loop<CM_ACT_GELU>(f); break;
+        case CM_ACT_GELU_TANH: act_loop<CM_ACT_GELU_TANH>(f); break;
+        case CM_ACT_SILU: act_loop<CM_ACT_SILU>(f); break;
         default: break;
     }
 }
 template <int N>
 __device__ __forceinline__ void mul_dact(float (&f)[N], const float (&z)[N], int act) {
     switch (act) {
-        case CM_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_RELU);
-            break;
-        case CM_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_GELU);
-            break;
-        case CM_ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_GELU_TANH);
-            break;
-        case CM_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] *= dact1(z[i], CM_ACT_SILU);
-            break;
+        case CM_ACT_RELU: dact_loop<CM_ACT_RELU>(f, z); break;
+        case CM_ACT_GELU: dact_loop<CM_ACT_GELU>(f, z); break;
+        case CM_ACT_GELU_TANH: dact_loop<CM_ACT_GELU_TANH>(f, z); break;
+        case CM_ACT_SILU: dact_loop<CM_ACT_SILU>(f, z); break;
         default: break;
     }
 }

@@ -346,6 +346,8 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
                 float f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                // the columns' biases lie one to a lane (as fast as reading them
+                // all from L1, and any address will do)
                 if (e.bias) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] += __shfl_sync(0xffffffffu, bsel, i);
