@@ -24,7 +24,9 @@
 // element's index, so that averages move however small the steps.
 //
 // Bound by memory: 28 bytes an element with bf16 gradients and parameters, a
-// master copy and fp32 states, 16.06 with 8-bit states.  A warp takes a block
+// master copy and fp32 states (59 M elements: 239 us, the rate of a copy), 16.06
+// with 8-bit states (50 M with fp32 gradients, 18.06: 168 us, 5.4 TB/s; there the
+// passes' arithmetic is not wholly under other warps' loads).  A warp takes a block
 // of 256 elements, a thread 8 neighbours of it, all its loads before the first
 // use.  The tensors' addresses are kernel parameters, so a step needs no copy
 // of a table to the device.
@@ -48,7 +50,7 @@ constexpr int kBlock = CM_ADAMW_BLOCK;
 constexpr int kAdamThreads = 256;
 constexpr int kAdamPass = kAdamThreads * 8;             // elements a CTA updates at a time
 // Passes of a CTA.  Four with codes, whose passes are long on arithmetic: finding
-// the tensor is paid once for them (50 M elements: 171 us, with one pass 183);
+// the tensor is paid once for them (50 M elements: 168 us, with one pass 180);
 // one without, where four would only put loads behind stores (59 M elements:
 // 242 us, with four 252).
 constexpr int kCodePasses = 4;

@@ -17,6 +17,12 @@
 // by the result, and TMA writes the buffer out.  Global memory thus sees whole
 // 128-byte rows, and what lies beyond the matrix is the tensor map's business.
 //
+// Bound by the tensor cores: 8192 x 8192 x 3584 takes 253.6 us, 1897 TFLOP/s, at
+// full clock; 8192 x 8192 x 28672 with GELU and the pre-activation kept 2.29 to
+// 2.39 ms, 1610 to 1680 TFLOP/s under the power cap.  With few K slices it is the
+// epilogue: 2.5 us a wave of tiles, GELU 2.7 more (two special-function
+// operations an element).
+//
 // Calls with too few tiles for all SMs split the tiles' K slices: see
 // cm_linear_split_kernel below.
 //
@@ -625,7 +631,8 @@ __device__ __forceinline__ void finish4(const LinearEpilogue &e, float (&v)[4][4
 // fp32 (the ring, whose loads have all been multiplied by then); after a
 // cluster barrier pair j finishes the j-th part of the columns, adding the
 // pairs' partial sums in their order.  No workspace, one launch, the same bits
-// every time.
+// every time.  200 x 8192 x 3584 takes 19.9 us on four pairs a tile, 26.3 on two
+// and 42.5 unsplit; the exchange and the summing cost 4 us (128 columns) to 6.5.
 template <int LAYOUT, int BN, int S>
 __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __grid_constant__ LinearPairParams p) {
     extern __shared__ uint8_t smem_raw[];

@@ -10,6 +10,12 @@
 // them in rank order, each for its share of the tokens, so one launch does it,
 // nothing passes through global memory, and the result does not depend on timing.
 //
+// Bound by HBM where the weights are large: one token through 28672 x 8192 takes
+// 69.7 us, 6738 GB/s.  A small call is bound by latency: one token through 4096 x
+// 2048 takes 6.6 us, of which 2.5 are its bytes; the rest is starting, the first
+// loads, and the sum over the cluster.  45 tokens through 8190 x 3579: 14.7 us for
+// 8.8 us of bytes.
+//
 // Roles (128 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the
 // MMAs; then all four warps run the epilogue (a thread owns one column, so a
 // warp's loads and stores are 32 neighbouring elements of one row).  Two CTAs
