@@ -63,6 +63,7 @@ bool map_written(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, i
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool misaligned(const void *p, cm_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (t == CM_F32 ? 3u : 1u)) != 0; }
 bool bad_dtype(cm_dtype t) { return t != CM_BF16 && t != CM_F32; }
 
 // A matrix the kernels read with TMA or write in 16-byte pieces.
@@ -276,6 +277,7 @@ cm_status cm_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_w
     CM_TRY(check_matrix(y, ldy, n));
     if (residual) CM_TRY(check_matrix(residual, ldr, n));
     if (preact) CM_TRY(check_matrix(preact, ldz, n));
+    if (misaligned(bias, bias_dtype)) return CM_ERR_ALIGNMENT;
     Device d;
     CM_TRY(device(&d));
     LinearEpilogue e = {};
@@ -342,7 +344,7 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
         CM_TRY(check_matrix(dy, lddy, n));
     }
     if (db && (!ws || ws_bytes < wgrad_workspace(M, n))) return CM_ERR_WORKSPACE;
-    if (db && !aligned16(ws)) return CM_ERR_ALIGNMENT;
+    if (db && (!aligned16(ws) || misaligned(db, db_dtype))) return CM_ERR_ALIGNMENT;
     Device d;
     CM_TRY(device(&d));
     if (M == 0) {   // the sum over no rows

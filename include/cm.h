@@ -585,7 +585,8 @@ cm_status cm_ag_gemm_noalloc_check_status(cm_stream_t stream, int32_t info[4]);
  * weight is stored [n][K] (CM_W_NK) or [K][n] (CM_W_KN).  Row strides must be
  * multiples of 8 elements and matrices 16-byte aligned (the tensor-map rule);
  * extents may be any positive number, and M may be 0 (nothing to do).
- * Outputs must not alias inputs.
+ * Outputs must not alias inputs.  The first call on a device looks up the
+ * kernels' attributes; make it outside any stream capture.
  *
  *  CM_ACT_RELU max(v, 0);  CM_ACT_GELU v (1 + erf(v / sqrt 2)) / 2;
  *  CM_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2;
@@ -608,7 +609,7 @@ typedef enum cm_act {
  *  Errors (synchronous, nothing enqueued): CM_ERR_INVALID_ARG for a null
  *  pointer or a bad enum; CM_ERR_SHAPE if M < 0, K or n is not positive, one
  *  exceeds 2^30, or a row stride is smaller than the row; CM_ERR_ALIGNMENT
- *  if a row stride or pointer is misaligned; CM_ERR_UNSUPPORTED on another
+ *  if a row stride or pointer is misaligned (bias by its element); CM_ERR_UNSUPPORTED on another
  *  device; CM_ERR_CUDA if a launch or tensor-map encoding fails.  Device-side
  *  waits that expire come from cm_linear_check_status.
  */

@@ -33,7 +33,7 @@ def test_linear(lib):
                dict(res=A, ldr=8), dict(z=A, ldz=16)):
         assert linear(lib, **kw) == cm.CM_ERR_SHAPE, kw
     for kw in (dict(x=A + 2), dict(w=A + 8), dict(y=A + 4), dict(ldx=65), dict(ldw=68), dict(ldy=36),
-               dict(res=A + 2, ldr=32), dict(z=A, ldz=33)):
+               dict(res=A + 2, ldr=32), dict(z=A, ldz=33), dict(bias=A + 1), dict(bias=A + 2, bias_dtype=1)):
         assert linear(lib, **kw) == cm.CM_ERR_ALIGNMENT, kw
     assert linear(lib, M=0, x=None, y=None) == cm.CM_OK
 
@@ -69,7 +69,7 @@ def test_wgrad(lib):
         assert call(**kw) == cm.CM_ERR_SHAPE, kw
     for kw in (dict(ws=None), dict(ws_bytes=16)):
         assert call(**kw) == cm.CM_ERR_WORKSPACE, kw
-    for kw in (dict(ws=A + 4), dict(dw=A + 4), dict(lddy=33)):
+    for kw in (dict(ws=A + 4), dict(dw=A + 4), dict(lddy=33), dict(db=A + 2), dict(db=A + 1, db_dtype=0)):
         assert call(**kw) == cm.CM_ERR_ALIGNMENT, kw
     assert cm.linear_wgrad_workspace_size(100, 64, 1000) >= 4000
     assert cm.linear_wgrad_workspace_size(-1, 64, 1000) == 0
