@@ -141,17 +141,17 @@ __device__ __forceinline__ float with_other(float v, float *slot, int rank) {
 
 // A parameter vector to shared memory as fp32, 1 (or 0) where there is none.
 // The first and second halves of the vectors lie in two planes of h8 / 2, so
-// that neighbouring threads read neighbouring 16 bytes.  Columns c0 .. c0 + h.
+// that neighbouring threads read neighbouring 16 bytes.
 // A group of `width` threads, t its place in it, covers the row with R vectors
 // a thread; all loads before the first store.
 template <int R>
-__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int c0, int h, int h8,
-                                            int width, int t) {
+__device__ __forceinline__ void stage_param(float *dst, const void *p, int f32, float null_value, int h, int h8, int width,
+                                            int t) {
     V8 v[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int c = (r * width + t) * 8;
-        v[r] = c < h ? load_param8(p, f32, null_value, c0 + c, c0 + h) : fill(0.0f);
+        v[r] = c < h ? load_param8(p, f32, null_value, c, h) : fill(0.0f);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -243,28 +243,21 @@ __device__ __forceinline__ V8 scaled(const V8 &x, float mean, float rstd, const 
 // rows share that, and the reads of gamma and beta (8192 x 8192 in bf16: 50 us
 // with two, 68 with one).  Rows longer than 8192 go one by one, to keep the
 // registers.  gamma and beta stay in shared memory as fp32.
-//
-// SPLIT: rows longer than 16384 are shared by a cluster of two CTAs, the first
-// half of the columns in one and the second in the other; they exchange a
-// row's sums through shared memory.
-template <typename X, typename Y, int R, int NR, int S, bool SPLIT>
+template <typename X, typename Y, int R, int NR, int S>
 __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(const __grid_constant__ NormParams p, int width) {
     let_next_start();
     wait_for_previous();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float sums[2][2][kRowBuf];
-    __shared__ float other[SPLIT ? 4 : 1];
-    static_assert(!SPLIT || NR == 1, "a cluster exchanges one row's sums");
     const Group g(width);
     const int t = int(threadIdx.x) - g.index * width, per = int(blockDim.x) / width;
-    const Columns cols(p.h, SPLIT);
-    const int h = cols.count, h8 = (cols.half + 7) / 8 * 8, c0 = cols.first;
+    const int h = int(p.h), h8 = (h + 7) / 8 * 8;
     float *const gamma = reinterpret_cast<float *>(smem), *const beta = gamma + h8;
     X *const ring = reinterpret_cast<X *>(beta + h8) + g.index * NR * h8;
     const int stage = per * NR * h8;
-    const int64_t step = int64_t(cols.ctas) * per * NR, row0 = (int64_t(cols.cta) * per + g.index) * NR;
+    const int64_t step = int64_t(gridDim.x) * per * NR, row0 = (int64_t(blockIdx.x) * per + g.index) * NR;
     int64_t ask_row = row0;
-    const X *ask_x = static_cast<const X *>(p.x) + row0 * p.ldx + c0;
+    const X *ask_x = static_cast<const X *>(p.x) + row0 * p.ldx;
     auto ask = [&](int st) {
 #pragma unroll
         for (int k = 0; k < NR; ++k)
@@ -280,13 +273,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(con
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) ask(k);
     if (g.index == 0) {
-        stage_param<R>(gamma, p.gamma, p.p_f32, 1.0f, c0, h, h8, width, t);
-        stage_param<R>(beta, p.beta, p.p_f32, 0.0f, c0, h, h8, width, t);
+        stage_param<R>(gamma, p.gamma, p.p_f32, 1.0f, h, h8, width, t);
+        stage_param<R>(beta, p.beta, p.p_f32, 0.0f, h, h8, width, t);
     }
     __syncthreads();
-    const float inv_h = 1.0f / float(p.h);
+    const float inv_h = 1.0f / float(h);
     int st = 0, flip = 0;
-    Y *y = static_cast<Y *>(p.out) + row0 * p.ldo + c0;
+    Y *y = static_cast<Y *>(p.out) + row0 * p.ldo;
     for (int64_t row = row0; row < p.rows; row += step) {
         ask(st == 0 ? S - 1 : st - 1);
         copy_wait<S - 1>();
@@ -302,16 +295,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(con
         rows_sum(total(f[0]), NR > 1 ? total(f[NR - 1]) : 0.0f, g, sums[flip][0], mean);
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
-            if (SPLIT) mean[k] = with_other(mean[k], &other[flip], cols.rank);
             mean[k] *= inv_h;
         }
         rows_sum(squares(f[0], mean[0], width, t, h), NR > 1 ? squares(f[NR - 1], mean[NR - 1], width, t, h) : 0.0f, g,
                  sums[flip][1], rstd);
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
-            if (SPLIT) rstd[k] = with_other(rstd[k], &other[2 + flip], cols.rank);
             rstd[k] = rsqrtf(rstd[k] * inv_h + p.eps);
-            if (t == 0 && c0 == 0 && (k == 0 || second)) {
+            if (t == 0 && (k == 0 || second)) {
                 if (p.mean) p.mean[row + k] = mean[k];
                 if (p.rstd) p.rstd[row + k] = rstd[k];
             }
@@ -329,7 +320,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(con
         flip ^= 1;
     }
     copy_wait<0>();
-    if (SPLIT) dev::cluster_sync();   // the other CTA has read this one's last sum
 }
 
 // Few rows: `width` threads hold a row in registers.
@@ -839,9 +829,9 @@ cudaError_t launch_ring(const NormParams &p, const RingPlan &r, bool split, cuda
                         split ? 2 : 1, stream, p, r.width);
 }
 
-template <typename X, typename Y, int R, int NR, int S, bool SPLIT = false>
+template <typename X, typename Y, int R, int NR, int S>
 cudaError_t forward_ring(const NormParams &p, const RingPlan &r, cudaStream_t stream) {
-    return launch_ring<cm_layer_norm_ring_kernel<X, Y, R, NR, S, SPLIT>>(p, r, SPLIT, stream);
+    return launch_ring<cm_layer_norm_ring_kernel<X, Y, R, NR, S>>(p, r, false, stream);
 }
 
 template <typename X, typename Y>
@@ -854,23 +844,27 @@ cudaError_t forward(const NormParams &p, cudaStream_t stream) {
         return launch_after(cm_layer_norm_any_kernel<X, Y>, dim3(unsigned(p.rows)), 512, 0, 1, stream, p);
     }
     const int sms = sm_count();
-    // the rings pay once a group has a few steps to run ahead on
-    if (RingPlan r = ring_plan((p.rows + 1) / 2, p.h, 2 * sizeof(X), 8, 4, 15, sms); vecs <= 1024 && r.ctas > 0) {
-        if (p.rows >= 4 * r.ctas * r.per) {
-            if (r.R == 4) return r.S == 3 ? forward_ring<X, Y, 4, 2, 3>(p, r, stream) : forward_ring<X, Y, 4, 2, 2>(p, r, stream);
-            if (r.S == 3)   // rows this short leave room for three
-                return r.R == 1 ? forward_ring<X, Y, 1, 2, 3>(p, r, stream) : forward_ring<X, Y, 2, 2, 3>(p, r, stream);
-        }
-    } else if (r = ring_plan(p.rows, p.h, sizeof(X), 8, 4, 15, sms); r.ctas > 0) {
-        if (p.rows >= 2 * r.ctas * r.per)
-            return r.S == 3 ? forward_ring<X, Y, 4, 1, 3>(p, r, stream) : forward_ring<X, Y, 4, 1, 2>(p, r, stream);
-    } else if (r = ring_plan(p.rows, (p.h + 15) / 16 * 8, sizeof(X), 8, 4, 1, sms / 2); r.ctas > 0) {
-        if (p.rows >= 2 * r.ctas)
-            return r.S == 3 ? forward_ring<X, Y, 4, 1, 3, true>(p, r, stream) : forward_ring<X, Y, 4, 1, 2, true>(p, r, stream);
-    }
-    // all of a row's loads at once
+    // the register kernel: all of a row's loads at once
     const int R = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
     const int width = row_width(vecs, R), per = std::max(1, 128 / width);
+    // The ring pays once that kernel would take more than two rounds of CTAs
+    // (1024 threads an SM).  Rows of 8192 in bf16: 152 rows 3.6 us in registers
+    // and 6.4 in the ring, 304 6.6 and 6.5, 600 12.3 and 6.6; rows of 2048:
+    // 1200 5.0 and 6.5, 2400 9.0 and 6.7.  Rows longer than 16384 fit no ring;
+    // 2000 of 28672 take 93 us.
+    if (p.rows > 2 * int64_t(sms) * std::max(1, 1024 / (width * per)) * per) {
+        if (vecs <= 1024) {
+            const RingPlan r = ring_plan((p.rows + 1) / 2, p.h, 2 * sizeof(X), 8, 4, 15, sms);
+            if (r.ctas > 0 && r.R == 4)
+                return r.S == 3 ? forward_ring<X, Y, 4, 2, 3>(p, r, stream) : forward_ring<X, Y, 4, 2, 2>(p, r, stream);
+            if (r.ctas > 0 && r.S == 3)   // rows this short leave room for three
+                return r.R == 1 ? forward_ring<X, Y, 1, 2, 3>(p, r, stream) : forward_ring<X, Y, 2, 2, 3>(p, r, stream);
+        } else {
+            const RingPlan r = ring_plan(p.rows, p.h, sizeof(X), 8, 4, 15, sms);
+            if (r.ctas > 0)
+                return r.S == 3 ? forward_ring<X, Y, 4, 1, 3>(p, r, stream) : forward_ring<X, Y, 4, 1, 2>(p, r, stream);
+        }
+    }
     const unsigned grid = unsigned((p.rows + per - 1) / per), threads = unsigned(width * per);
     return launch_after(R == 1   ? cm_layer_norm_kernel<X, Y, 1>
                         : R == 2 ? cm_layer_norm_kernel<X, Y, 2>

@@ -51,7 +51,8 @@ def s_of(h):
 SHAPES = [(1, 1, 0, 0), (1, 8, 0, 0), (3, 7, 0, 0), (5, 64, 0, 0), (2, 100, 4, 0), (9, 256, 0, 0), (33, 257, 7, 0),
           (1000, 512, 0, 0), (17, 777, 1, 3), (640, 1024, 8, 0), (3, 4096, 0, 0), (700, 4100, 4, 0), (2, 8192, 0, 1),
           (650, 8192, 0, 0), (4, 12288, 0, 0), (630, 12296, 16, 0), (5, 20000, 0, 0), (620, 16390, 2, 0),
-          (2, 32768, 0, 0), (2, 40000, 8, 0), (3, 50001, 0, 0), (20000, 96, 0, 0)]
+          (2, 32768, 0, 0), (2, 40000, 8, 0), (3, 50001, 0, 0), (20000, 96, 0, 0), (6000, 600, 0, 0),
+          (2501, 2048, 0, 0), (400, 20480, 0, 0)]
 DTYPES = [(BF, BF), (BF, F32), (F32, BF), (F32, F32)]
 
 
