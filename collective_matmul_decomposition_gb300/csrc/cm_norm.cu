@@ -767,12 +767,13 @@ int sm_count(int *device = nullptr) {
     return n;
 }
 
-// Chunks of rows for the column sums: enough CTAs for two rounds of the SMs,
-// at least 32 rows each; few rows are one chunk, whose sum is the result.
+// Chunks of rows for the column sums: enough CTAs for two rounds of the SMs, at
+// least 64 rows each, and no more than 128, whose sums the second launch adds in
+// 16 steps; few rows are one chunk, whose sum is the result.
 int64_t chunks_for(int64_t rows, int64_t cols) {
     if (rows <= 128) return 1;
     const int64_t blocks = (cols + 255) / 256;
-    return std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, std::max<int64_t>(1, 608 / blocks)));
+    return std::max<int64_t>(1, std::min({(rows + 63) / 64, std::max<int64_t>(1, 608 / blocks), int64_t(128)}));
 }
 
 constexpr int64_t kRingSmem = 224 * 1024;   // of 227 KB; the kernels' own buffers take up to 2
