@@ -425,7 +425,7 @@ def _matrix(name, t, shape, device, dtype=None):
 def _vector(name, t, n, device, dtype=None):
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements on CUDA device {device}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
@@ -442,10 +442,16 @@ def _dtype_of(name, t):
 
 def _extents(name, t):
     """(rows, columns, device) of the 2-D CUDA tensor that a call's other shapes follow from."""
-    if t.dim() != 2 or not t.is_cuda:
+    shape, device = t.shape, t.get_device()
+    if len(shape) != 2 or device < 0:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    r, c = t.shape
-    return r, c, t.get_device()
+    return shape[0], shape[1], device
+
+
+def _columns(name, t):
+    if t.ndim != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape[1]
 
 
 def _workspace(ws, device):
@@ -460,7 +466,7 @@ def cm_linear(x, w, y, bias=None, act: str = "none", residual=None, preact=None,
     """y [M][n] = act(x @ W^T + bias) + residual; preact receives x @ W^T + bias (bf16)."""
     lib = _library()
     M, K, dev = _extents("x", x)
-    n = _extents("y", y)[1]
+    n = _columns("y", y)
     layout = LAYOUTS[w_layout]
     xp, ldx = _matrix("x", x, (M, K), dev, _b16)
     wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
@@ -477,7 +483,7 @@ def cm_linear_dgrad(dy, w, dx, preact=None, act: str = "none", residual=None, w_
     """dx [M][K] = (dy @ W) * act'(preact) + residual; act and preact are those of the layer in front."""
     lib = _library()
     M, n, dev = _extents("dy", dy)
-    K = _extents("dx", dx)[1]
+    K = _columns("dx", dx)
     layout = LAYOUTS[w_layout]
     dyp, lddy = _matrix("dy", dy, (M, n), dev, _b16)
     wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
@@ -499,7 +505,7 @@ def cm_linear_wgrad(x, dy, dw, ws=None, db=None, accumulate: bool = False, w_lay
     ws (linear_wgrad_workspace_size bytes) is needed with db only."""
     lib = _library()
     M, K, dev = _extents("x", x)
-    n = _extents("dy", dy)[1]
+    n = _columns("dy", dy)
     layout = LAYOUTS[w_layout]
     xp, ldx = _matrix("x", x, (M, K), dev, _b16)
     dyp, lddy = _matrix("dy", dy, (M, n), dev, _b16)
