@@ -64,8 +64,8 @@ cudaError_t prepare_linear_strip(int device);
 cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream);
 int linear_strip_stages(int tok, int ring_bytes);
 
-// Tiles of 256 x 256 on CTA pairs, for calls with many of them.  A is the row
-// operand here, B the column operand.
+// Tiles of 256 rows x bn columns on CTA pairs.  A is the row operand here, B the
+// column operand.
 struct LinearPairParams {
     CUtensorMap tmA, tmB;
     CUtensorMap tmY;          // bf16: 64 x 32 boxes, fp32: 32 x 32

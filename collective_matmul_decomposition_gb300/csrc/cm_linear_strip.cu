@@ -16,7 +16,7 @@
 // loads, and the sum over the cluster.  45 tokens through 8190 x 3579: 14.7 us for
 // 8.8 us of bytes.
 //
-// Roles (128 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the
+// Roles (128 threads): a thread of warp 0 issues the TMA loads, one of warp 1 the
 // MMAs; then all four warps run the epilogue (a thread owns one column, so a
 // warp's loads and stores are 32 neighbouring elements of one row).  Two CTAs
 // fit on an SM: one's epilogue runs under the other's loads.
