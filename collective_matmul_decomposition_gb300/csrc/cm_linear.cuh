@@ -61,7 +61,10 @@ struct LinearStripParams {
 };
 
 // layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.
-cudaError_t prepare_linear_strip(int device);
+constexpr int kStripAlone = 216 * 1024, kStripShared = 108 * 1024;   // ring bytes of a CTA alone on its SM, of one of two
+// clusters[i]: clusters of i CTAs (2 to kStripMostSplits) that run together, one CTA an SM.
+constexpr int kStripMostSplits = 8;
+cudaError_t prepare_linear_strip(int sms, int *clusters);
 cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream);
 int linear_strip_stages(int tok, int ring_bytes);
 

@@ -80,7 +80,8 @@ cm_status check_extents(int64_t M, int64_t K, int64_t n) {
 
 struct Device {
     int id = 0, sms = 0;
-    int clusters[3] = {0, 0, 0};   // of 1, 2 and 4 pairs
+    int clusters[3] = {0, 0, 0};                    // of 1, 2 and 4 pairs
+    int strip_clusters[kStripMostSplits + 1] = {};  // of so many strip CTAs, one CTA an SM
     LinearStatus *status = nullptr;
 };
 
@@ -98,7 +99,7 @@ cm_status device(Device *d) {
             cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess)
             return CM_ERR_CUDA;
         if (major != 10 || minor != 3) return CM_ERR_UNSUPPORTED;
-        if (prepare_linear_strip(d->id) != cudaSuccess) return CM_ERR_CUDA;
+        if (prepare_linear_strip(c.sms, c.strip_clusters) != cudaSuccess) return CM_ERR_CUDA;
         if (prepare_linear_pair(c.sms, c.clusters) != cudaSuccess) return CM_ERR_CUDA;
         if (c.clusters[0] < 1) return CM_ERR_UNSUPPORTED;
         void *sp = nullptr;
@@ -133,36 +134,41 @@ struct Choice {
 };
 
 // The choice with the least estimated time.  The estimates' constants were
-// fitted to calls on one GB300 with weights from HBM, in us.
-//   pair: a K slice of 64 takes a wave of tiles 0.33 (256 columns) or 0.21
+// fitted to 110 random calls (up to 630 rows, K and columns from 256 to 16384)
+// on one GB300 with weights from HBM, in us; the choices take 2 % longer than
+// the best of each call on average, the worst 1.2 times as long.
+//   pair: a K slice of 64 takes a wave of tiles 0.32 (256 columns) or 0.21
 //     (128), but no wave is shorter than its epilogue, 2.9 or 2.0; a launch
-//     takes 2.5 beyond that, summing over a cluster's pairs 6.5 or 4.
-//   strip: a launch takes 4, and 0.02 a row of the tile; split, 5.5 and 0.045.
-//   Between, HBM gives 6.3 TB/s, the SMs read L2 (every tile its own copy of the
-//   rows) at 11 TB/s, and a slice takes 0.2.
+//     takes 3.8 beyond that, summing over a cluster's pairs 2.6 or 1.6.
+//   strip: a launch takes 3.4, and 0.04 a row of the tile; split, 3.7 and 0.063.
+//     A slice takes 0.125.
+//   Between, HBM and L2 (every tile its own copy of the rows) are given 8.5 and
+//   22 TB/s, since of what is not the longest a part shows as well.
 // Measured on both sides of where the choice changes (best strip / best pair):
-//   rows 45,  K 8190, cols 3579:  15.0 / 18.5     rows 100, K 8192,  cols 3584: 19.3 / 20.5
-//   rows 200, K 8192, cols 3584:  24.9 / 20.8     rows 256, K 12288, cols 4608: 37.4 / 31.2
-//   rows 100, K 1024, cols 2048:   7.0 / 6.5      rows 512, K 4096,  cols 4096: 22.9 / 18.7
+//   rows 45,  K 8190, cols 3579:  14.6 / 17.1     rows 100, K 8192,  cols 3584: 18.9 / 19.0
+//   rows 200, K 8192, cols 3584:  24.9 / 19.6     rows 256, K 12288, cols 4608: 37.4 / 29.5
+//   rows 100, K 1024, cols 2048:   7.0 / 6.5      rows 512, K 4096,  cols 4096: 22.9 / 17.7
+//   rows 272, K 4480, cols 14832: 40.3 / 46.8     rows 434, K 5552,  cols 11856: 73 / 59 (not looked at above 384)
 // between pair tiles (256 columns / 128 / 128 on two pairs a tile):
 //   rows 2048, K 12288, cols 4608:  129 / 161 / -     rows 1024, K 8192, cols 1024:  40.1 / 23.1 / 16.8
 // and between strips (one tile of rows / more, shorter ones):
-//   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  24.4 / 29.0 (three)
+//   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  22.8 / 29.0 (three)
 Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn) {
     Choice best;
     double least = 1e30;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t slices = up(k, kBK);
-    const double from_hbm = double(cols) * double(k) * 2.0 / 6.3e6;
+    const double from_hbm = double(cols) * double(k) * 2.0 / 8.5e6;
     // pair tiles waste what they have beyond `rows`: not worth a look below 33
     for (int bn = 256; bn >= 128 && rows > 32; bn /= 2) {
         const int64_t tiles = up(rows, 256) * up(cols, bn);
         for (int i = 0; i < 3; ++i) {
             const int splits = 1 << i;
             if (i > 0 && (tiles > d.clusters[i] || slices < 2 * splits)) break;
-            const double wave = std::max(double(up(slices, splits)) * (bn == 256 ? 0.33 : 0.21), bn == 256 ? 2.9 : 2.0);
-            const double t = 2.5 + (i == 0 ? 0.0 : bn == 256 ? 6.5 : 4.0) +
-                             std::max(double(up(tiles, d.clusters[i])) * wave, from_hbm);
+            const double wave = std::max(double(up(slices, splits)) * (bn == 256 ? 0.32 : 0.21), bn == 256 ? 2.9 : 2.0);
+            const double run = double(up(tiles, d.clusters[i])) * wave;
+            const double t = 3.8 + (i == 0 ? 0.0 : bn == 256 ? 2.6 : 1.6) + std::max(run, from_hbm) +
+                             0.22 * std::min(run, from_hbm);
             if (t < least) {
                 least = t;
                 best.pair = true;
@@ -171,18 +177,22 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
             }
         }
     }
-    for (int64_t parts = 1; parts <= 4 && rows <= 512; ++parts) {
+    for (int64_t parts = 1; parts <= 4 && rows <= 384; ++parts) {
         const int64_t unit = row_mn ? 64 : 16, tok = up(up(rows, parts), unit) * unit;
         if (tok > 256) continue;
         const int64_t tiles = up(rows, tok) * up(cols, 128);
-        const double from_l2 = double(tiles) * double(128 + tok) * double(k) * 2.0 / 11e6;
-        // unsplit, or split until there are two CTAs an SM; partial tiles of
-        // more than 128 rows do not fit two to an SM
-        const int64_t most = tok > 128 ? 1 : std::max<int64_t>(1, std::min({int64_t(8), 2 * d.sms / tiles, slices}));
+        const double from_l2 = double(tiles) * double(128 + tok) * double(k) * 2.0 / 22e6;
+        // unsplit, or split as far as all tiles' clusters run at once, two CTAs
+        // an SM (9 rows, K 3728, cols 5504: 43 tiles of seven CTAs each take
+        // 16.3 us, of six 10.4).  Partial tiles of more than 128 rows do not fit
+        // two to an SM
+        int64_t most = tok > 128 ? 1 : std::min<int64_t>(kStripMostSplits, slices);
+        while (most > 1 && tiles > 2 * d.strip_clusters[most]) --most;
         for (int64_t splits = 1; splits <= most; splits += std::max<int64_t>(1, most - 1)) {
-            const double run = 0.2 * double(up(slices, splits)) * double(up(tiles * splits, d.sms));
-            const double t = (splits > 1 ? 5.5 + 0.045 * double(tok) : 4.0 + 0.02 * double(tok)) +
-                             std::max({from_hbm, from_l2, run});
+            const double run = 0.125 * double(up(slices, splits)) * double(up(tiles * splits, d.sms));
+            const double longest = std::max({from_hbm, from_l2, run});
+            const double second = std::max(std::min(from_hbm, from_l2), std::min(std::max(from_hbm, from_l2), run));
+            const double t = (splits > 1 ? 3.7 + 0.063 * double(tok) : 3.4 + 0.04 * double(tok)) + longest + 0.5 * second;
             if (t >= least) continue;
             least = t;
             best.pair = false;
@@ -190,7 +200,7 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
             best.splits = int(splits);
             // a CTA has an SM to itself where there are SMs enough; clusters
             // of such CTAs only pack where half of them are
-            best.ring_bytes = (tiles * splits <= (splits == 1 ? d.sms : d.sms / 2) ? 216 : 108) * 1024;
+            best.ring_bytes = tiles * splits <= (splits == 1 ? d.sms : d.sms / 2) ? kStripAlone : kStripShared;
         }
     }
     return best;

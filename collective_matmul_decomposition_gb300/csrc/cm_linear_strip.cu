@@ -43,7 +43,6 @@ constexpr int kThreadsL = 128;
 constexpr int kTileCols = 128;
 constexpr int kStripA = kTileCols * kBK * 2;   // 16 KB of the column operand per slice
 constexpr int kStripMaxStages = 12;
-constexpr int kStripMost = 216 * 1024;         // ring bytes of a CTA that has an SM to itself
 
 struct StripSmem {
     uint8_t *ring;
@@ -348,17 +347,25 @@ int linear_strip_stages(int tok, int ring_bytes) {
     return std::min(kStripMaxStages, ring_bytes / (kStripA + tok * kBK * 2));
 }
 
-cudaError_t prepare_linear_strip(int device) {
-    static bool done[64] = {false};
-    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-    if (!done[device]) {
-        void (*fns[3])(LinearStripParams) = {cm_linear_strip_kernel<0>, cm_linear_strip_kernel<2>,
-                                             cm_linear_strip_kernel<3>};
-        for (auto fn : fns) {
-            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripMost + 1024);
-            if (e != cudaSuccess) return e;
-        }
-        done[device] = true;
+cudaError_t prepare_linear_strip(int sms, int *clusters) {
+    void (*fns[3])(LinearStripParams) = {cm_linear_strip_kernel<0>, cm_linear_strip_kernel<2>, cm_linear_strip_kernel<3>};
+    for (auto fn : fns) {
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripAlone + 1024);
+        if (e != cudaSuccess) return e;
+    }
+    for (int i = 2; i <= kStripMostSplits; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(sms / i * i));
+        cfg.blockDim = dim3(kThreadsL);
+        cfg.dynamicSmemBytes = kStripAlone + 1024;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(i);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], fns[0], &cfg);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
