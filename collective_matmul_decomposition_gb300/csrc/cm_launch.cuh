@@ -6,12 +6,6 @@
 // kernel has completed and its writes are visible.  Every kernel launched so
 // calls it in every thread before its first access to global memory, and
 // says with let_next_start() that its own successor may be set up in turn.
-//
-// One kernel may run beside its predecessor instead.  The predecessor calls
-// let_next_start() after its own wait, so that when its successor starts all
-// earlier kernels have completed; the successor touches nothing that the
-// predecessor writes and writes nothing that it reads, and waits in every thread
-// at its end, so that whoever waits for the successor has waited for both.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -55,7 +55,6 @@ struct LinearStripParams {
     int splits;         // CTAs of a cluster that share a tile's K slices
     int ring_bytes;     // shared memory for `stages` slices, and for a split tile's partial sums
     int stages;
-    int next_beside;    // the next launch may run beside this kernel
     LinearStatus *status;
     uint64_t timeout_ns;
 };
@@ -80,7 +79,6 @@ struct LinearPairParams {
     int kblocks, mtiles, ntiles, tiles;
     int bn;                   // columns of a tile: 256 or 128
     int band;                 // row tiles that run through all columns together
-    int next_beside;          // the next launch may run beside this kernel
     LinearStatus *status;
     uint64_t timeout_ns;
 };
@@ -91,19 +89,10 @@ struct LinearPairParams {
 cudaError_t prepare_linear_pair(int sms, int *clusters);
 cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int splits, int clusters, cudaStream_t stream);
 
-// Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu), in two
-// launches: partial sums per row chunk in `partial`, then their sum in chunk
-// order.  One chunk is summed to `out` by the first, and the second launches
-// nothing.  The first runs beside the kernel launched before it.
-struct ColumnSums {
-    const void *x;
-    int64_t ldx, rows, cols;
-    float *partial;   // colsum_chunks(rows, cols) x cols
-    void *out;
-    bool out_f32, accumulate;
-};
+// Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu): partial
+// sums per row chunk in `partial`, then their sum in chunk order.
 int64_t colsum_chunks(int64_t rows, int64_t cols);
-cudaError_t launch_colsum(const ColumnSums &c, cudaStream_t stream);
-cudaError_t launch_colsum_join(const ColumnSums &c, cudaStream_t stream);
+cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols, float *partial, void *out,
+                          bool out_f32, bool accumulate, cudaStream_t stream);
 
 }  // namespace cm

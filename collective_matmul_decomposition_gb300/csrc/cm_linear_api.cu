@@ -207,7 +207,7 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
 }
 
 cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const Operand &b, int64_t rows, int64_t cols,
-                       int64_t k, const LinearEpilogue &e, bool next_beside, cudaStream_t stream) {
+                       int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
     LinearPairParams p;
     p.e = e;
     p.rows = rows;
@@ -219,7 +219,6 @@ cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const
     if (int64_t(p.mtiles) * p.ntiles > 0x7fffffff) return CM_ERR_SHAPE;
     p.tiles = p.mtiles * p.ntiles;
     p.band = int(std::max<int64_t>(1, std::min<int64_t>(p.mtiles, kBandBytes / (int64_t(p.kblocks) * 256 * kBK * 2))));
-    p.next_beside = next_beside ? 1 : 0;
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
     if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, c.bn / 2) ||
@@ -235,12 +234,11 @@ cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const
     return launch_linear_pair(p, layout, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
-// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.  next_beside: the
-// next launch is one that runs beside this product.
+// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
-                  const LinearEpilogue &e, cudaStream_t stream, bool next_beside = false) {
+                  const LinearEpilogue &e, cudaStream_t stream) {
     const Choice c = choose(d, rows, cols, k, b.mn_major);
-    if (c.pair) return product_pair(d, c, a, b, rows, cols, k, e, next_beside, stream);
+    if (c.pair) return product_pair(d, c, a, b, rows, cols, k, e, stream);
     LinearStripParams p;
     p.e = e;
     p.rows = rows;
@@ -251,7 +249,6 @@ cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t r
     p.splits = c.splits;
     p.ring_bytes = c.ring_bytes;
     p.stages = linear_strip_stages(c.tok, c.ring_bytes);
-    p.next_beside = next_beside ? 1 : 0;
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
     if (!map_operand(&p.tmA, a, cols, k, 128) || !map_operand(&p.tmB, b, rows, k, c.tok)) return CM_ERR_CUDA;
@@ -370,19 +367,16 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
             return CM_ERR_CUDA;
         return CM_OK;
     }
+    if (db && launch_colsum(dy, lddy, M, n, static_cast<float *>(ws), db, db_dtype == CM_F32, accumulate != 0,
+                            stream) != cudaSuccess)
+        return CM_ERR_CUDA;
     LinearEpilogue e = {};
     e.y = dw;
     e.ldy = lddw;
     e.y_f32 = dw_dtype == CM_F32;
     e.accumulate = accumulate != 0;
     const Operand ox = {x, ldx, true}, ody = {dy, lddy, true};
-    const bool sums = db != nullptr;
-    CM_TRY(nk ? product(d, ox, ody, n, K, M, e, stream, sums) : product(d, ody, ox, K, n, M, e, stream, sums));
-    if (!sums) return CM_OK;
-    // The column sums run beside the product, on SMs that it leaves free or is done with.
-    const ColumnSums c = {dy, lddy, M, n, static_cast<float *>(ws), db, db_dtype == CM_F32, accumulate != 0};
-    if (launch_colsum(c, stream) != cudaSuccess || launch_colsum_join(c, stream) != cudaSuccess) return CM_ERR_CUDA;
-    return CM_OK;
+    return nk ? product(d, ox, ody, n, K, M, e, stream) : product(d, ody, ox, K, n, M, e, stream);
 }
 
 cm_status cm_linear_check_status(cm_stream_t stream_, int32_t info[4]) {

@@ -485,9 +485,8 @@ __device__ uint32_t open_pair(const LinearPairParams &p, LSmem &s, uint8_t *smem
     __syncthreads();
     cluster_sync();   // the CTAs' barriers exist before any cross-CTA arrival or load
     tc_fence_after();
-    if (!p.next_beside) let_next_start();
+    let_next_start();
     wait_for_previous();
-    if (p.next_beside) let_next_start();
     return *s.tmem_slot;
 }
 

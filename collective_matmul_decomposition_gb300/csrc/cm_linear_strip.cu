@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s.tmem_slot;
-    if (!p.next_beside) let_next_start();
+    let_next_start();
 
     const int split = p.splits > 1 ? int(cluster_ctarank()) : 0;
     const int tile = int(blockIdx.x) / p.splits;
@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         }
     __syncwarp();
     wait_for_previous();
-    if (p.next_beside) let_next_start();
 
     if (warp == 0) {
         if (elect_one()) {

@@ -662,15 +662,11 @@ __device__ __forceinline__ void put_sum(void *out, int f32, int accumulate, int6
 // Bound by memory for long sums, by the launch for short ones: a CTA takes a
 // chunk of rows and 256 columns, so that a row's reads are 512 neighbouring bytes.
 // Partial sums over the rows of chunk blockIdx.y.  STATS: [chunk][2][h] of
-// dy xh and dy; otherwise [chunk][h] of dy.  Without STATS it runs beside the
-// kernel before it, the product of the weight gradient, whose last tiles and few
-// CTAs leave SMs free.  A weight gradient with its bias's, beside / after it:
-//   rows 7954, 241 x 86: 14.7 / 18.0 us     rows 65536, 256 x 256: 38.5 / 50.5 us
-//   rows 1813, 483 x 24629: 69 / 74.5 us    rows 4096, 4096 x 4096: 87 / 87 us (all registers taken)
+// dy xh and dy; otherwise [chunk][h] of dy.
 template <typename X, typename Y, int V, bool STATS, int kY>
 __global__ void __launch_bounds__(32 * kY) cm_colsum_kernel(NormParams p) {
     let_next_start();
-    if constexpr (STATS) wait_for_previous();
+    wait_for_previous();
     __shared__ float sm[STATS ? 2 : 1][kY][32 * V];
     const int tx = int(threadIdx.x) & 31, ty = int(threadIdx.x) >> 5;
     const int64_t c = (int64_t(blockIdx.x) * 32 + tx) * V;
@@ -724,7 +720,6 @@ __global__ void __launch_bounds__(32 * kY) cm_colsum_kernel(NormParams p) {
             p.partial[int64_t(blockIdx.y) * p.h + cc] = sb;
         }
     }
-    if constexpr (!STATS) wait_for_previous();   // runs beside it
 }
 
 // out[c] (+)= sum over parts of partial[part * stride + c]: eight lanes take
@@ -947,27 +942,24 @@ cudaError_t launch_layer_norm_backward(const NormParams &p, cm_dtype x, cm_dtype
 
 int64_t colsum_chunks(int64_t rows, int64_t cols) { return chunks_for(rows, cols); }
 
-cudaError_t launch_colsum(const ColumnSums &c, cudaStream_t stream) {
+cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols, float *partial, void *out,
+                          bool out_f32, bool accumulate, cudaStream_t stream) {
     NormParams p = {};
-    p.dy = c.x;
-    p.lddy = c.ldx;
-    p.rows = c.rows;
-    p.h = c.cols;
-    p.partial = c.partial;
-    p.dbeta = c.out;
-    p.g_f32 = c.out_f32;
-    p.accumulate = c.accumulate;
-    const int64_t chunks = chunks_for(c.rows, c.cols);
-    return launch_after(chunks == 1 ? cm_colsum_kernel<bf16, bf16, 8, false, 32>
-                                    : cm_colsum_kernel<bf16, bf16, 8, false, kColY>,
-                        dim3(unsigned((c.cols + 255) / 256), unsigned(chunks)), 32 * (chunks == 1 ? 32 : kColY), 0, 1,
-                        stream, p);
-}
-
-cudaError_t launch_colsum_join(const ColumnSums &c, cudaStream_t stream) {
-    const int64_t chunks = chunks_for(c.rows, c.cols);
-    if (chunks == 1) return cudaSuccess;
-    return sum_parts(c.partial, chunks, c.cols, c.cols, c.out, nullptr, c.out_f32 ? 1 : 0, c.accumulate ? 1 : 0, stream);
+    p.dy = x;
+    p.lddy = ldx;
+    p.rows = rows;
+    p.h = cols;
+    p.partial = partial;
+    p.dbeta = out;
+    p.g_f32 = out_f32;
+    p.accumulate = accumulate;
+    const int64_t chunks = chunks_for(rows, cols);
+    const cudaError_t e = launch_after(chunks == 1 ? cm_colsum_kernel<bf16, bf16, 8, false, 32>
+                                                   : cm_colsum_kernel<bf16, bf16, 8, false, kColY>,
+                                       dim3(unsigned((cols + 255) / 256), unsigned(chunks)),
+                                       32 * (chunks == 1 ? 32 : kColY), 0, 1, stream, p);
+    if (e != cudaSuccess || chunks == 1) return e;
+    return sum_parts(partial, chunks, cols, cols, out, nullptr, out_f32 ? 1 : 0, accumulate ? 1 : 0, stream);
 }
 
 }  // namespace cm
