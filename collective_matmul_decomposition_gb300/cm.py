@@ -386,13 +386,14 @@ def plan_choose_einsum(n_ranks, m, K, n, rates, max_chunks=CM_MAX_CHUNKS):
 
 
 # torch's names that the calls below use, bound by _bind_torch at the first of them
-_torch = _b16 = _f32 = _raw_stream = None
+_torch = _b16 = _f32 = _raw_stream = _current_device = None
 
 
 def _bind_torch():
-    global _torch, _b16, _f32, _raw_stream
+    global _torch, _b16, _f32, _raw_stream, _current_device
     import torch
     _b16, _f32, _raw_stream = torch.bfloat16, torch.float32, torch._C._cuda_getCurrentRawStream
+    _current_device = torch._C._cuda_getDevice
     _torch = torch
 
 
@@ -403,7 +404,16 @@ def _library():
 
 
 def _stream_of(stream, device: int) -> int:
-    return stream.cuda_stream if stream is not None else _raw_stream(device)
+    """The stream that a call on tensors of that device is launched on.  The library launches on the current device,
+    and the default stream's handle is the same on all of them: another device's tensors are refused."""
+    if device != _current_device():
+        raise ValueError(f"the tensors are on CUDA device {device}, but device {_current_device()} is the current one "
+                         f"(call under torch.cuda.device({device}))")
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream is on CUDA device {stream.device_index}, the tensors are on device {device}")
+    return stream.cuda_stream
 
 
 def _matrix(name, t, shape, device, dtype=None):
@@ -519,9 +529,10 @@ def cm_linear_wgrad(x, dy, dw, ws=None, db=None, accumulate: bool = False, w_lay
 
 
 def cm_linear_check_status(stream=None):
-    """Synchronise and return (status, info[4]) of the linear kernels since the last read."""
+    """Synchronise and return (status, info[4]) of the linear kernels on the current device since the last read."""
+    lib = _library()
     info = (ctypes.c_int * 4)()
-    st = load().cm_linear_check_status(_stream_ptr(stream), info)
+    st = lib.cm_linear_check_status(_stream_of(stream, _current_device()), info)
     return st, list(info)
 
 
@@ -626,11 +637,11 @@ def cm_adamw(tensors: AdamWTensors, lr: float, beta1: float = 0.9, beta2: float 
     gradient; seed: not 0 rounds 8-bit states up or down at random, keeping their mean (a new seed each step)."""
     lib = _library()
     scale = None
+    dev = tensors.device.index if tensors.device is not None else _current_device()
     if grad_scale is not None:
-        if grad_scale.numel() != 1 or grad_scale.dtype is not _f32 or not grad_scale.is_cuda:
-            raise ValueError("grad_scale must be one fp32 CUDA element")
+        if grad_scale.numel() != 1 or grad_scale.dtype is not _f32 or grad_scale.get_device() != dev:
+            raise ValueError(f"grad_scale must be one fp32 element on CUDA device {dev}")
         scale = grad_scale.data_ptr()
-    dev = tensors.device.index if tensors.device is not None else _torch.cuda.current_device()
     st = lib.cm_adamw(tensors.array(), len(tensors), lr, beta1, beta2, eps, int(step), scale, seed,
                       _stream_of(stream, dev))
     if st:

@@ -585,8 +585,10 @@ cm_status cm_ag_gemm_noalloc_check_status(cm_stream_t stream, int32_t info[4]);
  * weight is stored [n][K] (CM_W_NK) or [K][n] (CM_W_KN).  Row strides must be
  * multiples of 8 elements and matrices 16-byte aligned (the tensor-map rule);
  * extents may be any positive number, and M may be 0 (nothing to do).
- * Outputs must not alias inputs.  The first call on a device looks up the
- * kernels' attributes; make it outside any stream capture.
+ * Outputs must not alias inputs.  These calls, like those of the layer norm and
+ * of AdamW below, launch on the calling thread's current device, which the
+ * stream and all memory must belong to.  The first call on a device looks up
+ * the kernels' attributes; make it outside any stream capture.
  *
  *  CM_ACT_RELU max(v, 0);  CM_ACT_GELU v (1 + erf(v / sqrt 2)) / 2;
  *  CM_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2;
