@@ -249,12 +249,16 @@ class Plan:
 
 
 def _stream_ptr(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    _library()
+    return ctypes.c_void_p(_stream_of(stream, _current_device()))
 
 
 def _ptr(t):
+    """The tensor's address; the library launches on the current device, so one of another GPU is refused."""
+    _library()
+    if t.is_cuda and t.get_device() != _current_device():
+        raise ValueError(f"a tensor is on CUDA device {t.get_device()}, but device {_current_device()} is the current "
+                         f"one (call under torch.cuda.device({t.get_device()}))")
     return ctypes.c_void_p(t.data_ptr())
 
 

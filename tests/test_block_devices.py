@@ -1,5 +1,5 @@
-"""The linear layer's, layer norm's and AdamW's bindings launch on the current device only: tensors (or a stream, or a
-gradient scale) of another one are refused before the library is called.  Stand-ins for tensors and library, no GPU."""
+"""The bindings launch on the current device only: tensors (or a stream, or a gradient scale) of another one are
+refused before the library is called.  Stand-ins for tensors and library, no GPU."""
 
 import pytest
 import torch
@@ -118,3 +118,33 @@ def test_scale_and_status(library):
     assert library.calls == []
     assert cm.cm_linear_check_status(Stream(0))[0] == 0
     assert cm.cm_linear_check_status()[0] == 0
+
+
+class Plan:
+    handle, N = None, 2
+
+
+def collectives(index, stream=None):
+    """The collective calls with tensors of that device (the library is a stand-in: their shapes do not matter)."""
+    x, w, y = Tensor(2, 4, 64, index=index), Tensor(2, 32, 64, index=index), Tensor(2, 8, 32, index=index)
+    a, b, c = (Tensor(4, 64, 64, index=index) for _ in range(3))
+    ws = Tensor(1024, dtype=torch.uint8, index=index)
+    return {
+        "cm_ag_gemm": lambda: cm.cm_ag_gemm(Plan, x, w, y, ws, "nk", stream=stream),
+        "cm_gemm_rs": lambda: cm.cm_gemm_rs(Plan, x, w, y, ws, "nk", stream=stream),
+        "cm_gemm_rs_pipelined": lambda: cm.cm_gemm_rs_pipelined(Plan, x, w, y, ws, "nk", stream=stream),
+        "cm_backward_pair": lambda: cm.cm_backward_pair(Plan, x, w, y, x, w, ws, stream=stream),
+        "cm_cannon_gemm": lambda: cm.cm_cannon_gemm(Plan, a, b, c, ws, stream=stream),
+        "cm_check_status": lambda: cm.cm_check_status(ws, stream),
+    }
+
+
+@pytest.mark.parametrize("name", list(collectives(0)))
+def test_collective_calls(library, name):
+    for wrong in (collectives(1), collectives(0, stream=Stream(1))):
+        with pytest.raises(ValueError, match="device"):
+            wrong[name]()
+    assert library.calls == []
+    collectives(0)[name]()
+    collectives(0, stream=Stream(0))[name]()
+    assert library.calls == [name, name]
