@@ -78,7 +78,7 @@ struct Table {
     float b1, b2, c1, c2;   // betas and 1 - beta
     float step, root_scale, eps;   // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
     const float *grad_scale;
-    uint32_t seed_lo, seed_hi;
+    uint32_t seed_key;   // of the seed's two halves
     bool seeded;
 };
 
@@ -138,8 +138,11 @@ __device__ __forceinline__ uint32_t encode2(float a, float b) {
     return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
 
-// 32 mixed bits of a counter (the finalizer of MurmurHash3).
-__device__ __forceinline__ uint32_t mix(uint32_t h) {
+// 32 mixed bits of a counter (the finalizer of MurmurHash3).  The random bits of
+// an element come from the seed, the tensor's place in the list and the index
+// in turn, each added to what the one before was mixed to: were they added up
+// unmixed, a tensor would get the bits that its neighbour had a seed earlier.
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
     h ^= h >> 16;
     h *= 0x85ebca6bu;
     h ^= h >> 13;
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kAdamThreads, 5) cm_adamw_kernel(const __grid_
             __syncwarp();   // every lane has read the block's old scales
             uint32_t bits[8] = {};
             if (t.seeded) {
-                const uint32_t key = mix(mix(uint32_t(s.i0 >> 32) + t.seed_hi) ^ (e.index + t.seed_lo));
+                const uint32_t key = mix(mix(t.seed_key + e.index) + uint32_t(s.i0 >> 32));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) bits[i] = mix((uint32_t(s.i0) + uint32_t(i)) ^ key);
             }
@@ -300,7 +303,7 @@ cudaError_t launch(const Table<kLargeTable> &all, bool codes, int64_t chunks, cu
     t.b1 = all.b1, t.b2 = all.b2, t.c1 = all.c1, t.c2 = all.c2;
     t.step = all.step, t.root_scale = all.root_scale, t.eps = all.eps;
     t.grad_scale = all.grad_scale;
-    t.seed_lo = all.seed_lo, t.seed_hi = all.seed_hi, t.seeded = all.seeded;
+    t.seed_key = all.seed_key, t.seeded = all.seeded;
     return launch_after(codes ? cm_adamw_kernel<CAP, true> : cm_adamw_kernel<CAP, false>, dim3(unsigned(chunks)),
                         kAdamThreads, 0, 1, stream, t);
 }
@@ -349,7 +352,7 @@ extern "C" cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double 
     t.root_scale = float(1.0 / std::sqrt(1.0 - std::pow(beta2, double(step))));
     t.eps = float(eps);
     t.grad_scale = grad_scale;
-    t.seed_lo = uint32_t(seed), t.seed_hi = uint32_t(seed >> 32), t.seeded = seed != 0;
+    t.seed_key = mix(mix(uint32_t(seed)) + uint32_t(seed >> 32)), t.seeded = seed != 0;
     int i = 0;
     while (i < count) {
         int64_t chunks = 0;
