@@ -47,23 +47,28 @@ __device__ __forceinline__ F2 gelu_tanh_gate(F2 v, F2 v2) {
     constexpr float k = -2.0f * kLog2e * kGeluC;
     return sigmoid_of(mul(v, fma(v2, both(k * kGeluA), both(k))));
 }
-// The normal distribution's integral up to v, and e = exp(-v^2 / 2).  By formula
-// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions, whose
-// error is at most 1.5e-7: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with
-// t = 1 / (1 + p x), for x = |v| / sqrt 2.  A third of erff's instructions.
+// The normal distribution's integral up to v, and e = exp(-v^2 / 2).  The near
+// tail is t q(t) e with t = 1 / (1 + p |v|), the form of formula 7.1.26 of
+// Abramowitz and Stegun's Handbook of Mathematical Functions, with eight
+// coefficients instead of its five, fitted here for the least relative error
+// (linear programming over 0 <= |v| <= 14): 9.5e-8, so that GELU keeps its
+// accuracy where it is small, which the handbook's absolute 1.5e-7 does not
+// (5e-4 of the value at v = -4, 1e-2 at -8).  What is left is the rounding of
+// the exponent, at most 1.5 v^2 2^-24.
 __device__ __forceinline__ F2 normal_cdf(F2 v, F2 &e) {
     const float2 s = parts(v);
-    constexpr float px = 0.3275911f * 0.7071067811865476f;
-    const F2 t = rcp_fast(pair(fmaf(px, fabsf(s.x), 1.0f), fmaf(px, fabsf(s.y), 1.0f)));
+    constexpr float p = 0.30405593f;
+    const F2 t = rcp_fast(pair(fmaf(p, fabsf(s.x), 1.0f), fmaf(p, fabsf(s.y), 1.0f)));
     e = exp2_fast(mul(mul(v, v), both(-0.5f * kLog2e)));
-    F2 q = fma(t, both(1.061405429f), both(-1.453152027f));
-    q = fma(t, q, both(1.421413741f));
-    q = fma(t, q, both(-0.284496736f));
-    q = fma(t, q, both(0.254829592f));
-    // q t e / 2 lies under the near tail; what is left to 1/2 goes by v's sign
-    const float2 d = parts(fma(mul(q, t), mul(e, both(-0.5f)), both(0.5f)));
-    const float2 h = parts(mul(mul(q, t), mul(e, both(0.5f))));
-    return pair(s.x < 0.0f ? h.x : 0.5f + d.x, s.y < 0.0f ? h.y : 0.5f + d.y);
+    F2 q = fma(t, both(0.036636885f), both(-0.15430708f));
+    q = fma(t, q, both(0.19037811f));
+    q = fma(t, q, both(-0.0415411f));
+    q = fma(t, q, both(0.122740515f));
+    q = fma(t, q, both(0.102677226f));
+    q = fma(t, q, both(0.12215613f));
+    q = fma(t, q, both(0.12125933f));
+    const float2 h = parts(mul(mul(q, t), e));
+    return pair(s.x < 0.0f ? h.x : 1.0f - h.x, s.y < 0.0f ? h.y : 1.0f - h.y);
 }
 
 // act(v) of a pair
