@@ -100,8 +100,10 @@ __device__ __forceinline__ F2 dact2(F2 z) {
         const F2 cdf = normal_cdf(z, e);
         return fma(mul(z, both(0.3989422804014327f)), e, cdf);
     } else if constexpr (ACT == CM_ACT_GELU_TANH) {
-        // s + z s (1 - s) 2u'
-        const F2 z2 = mul(z, z), s = gelu_tanh_gate(z, z2);
+        // s + z s (1 - s) 2u'.  Past |z| = 2^32, where s is 0 or 1 and the second
+        // term nothing, z^2 is held: it must not overflow to meet 1 - s = 0
+        const float2 sq = parts(mul(z, z));
+        const F2 z2 = pair(fminf(sq.x, 0x1p64f), fminf(sq.y, 0x1p64f)), s = gelu_tanh_gate(z, z2);
         const F2 du = fma(z2, both(6.0f * kGeluC * kGeluA), both(2.0f * kGeluC));
         return fma(mul(z, s), mul(fma(s, both(-1.0f), both(1.0f)), du), s);
     } else if constexpr (ACT == CM_ACT_SILU) {
