@@ -585,7 +585,8 @@ def cm_layer_norm_backward(x, dy, gamma, mean, rstd, dx, ws=None, dgamma=None, d
 
 
 class AdamWTensors:
-    """The tensors of an AdamW step (cm_adamw), listed once; holds references to them."""
+    """The tensors of an AdamW step (cm_adamw), listed once by their addresses.  The list keeps their memory allocated;
+    a tensor that is given other storage later (param.data = ...) is not followed there."""
 
     def __init__(self):
         self._rows, self._keep, self._array, self.device = [], [], None, None
@@ -626,7 +627,8 @@ class AdamWTensors:
             ptrs.append(t.data_ptr())
         self._rows.append(cm_adamw_tensor(*ptrs, n, float(weight_decay), _dtype_of("param", param),
                                           _dtype_of("grad", grad), bits))
-        self._keep.append((param, grad, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale))
+        # the storages, not the tensors, which may be given others
+        self._keep.append([t.untyped_storage() for _, t, _, _ in each if t is not None])
         self._array = None
 
     def array(self):
