@@ -614,19 +614,19 @@ class AdamWTensors:
                 ("exp_avg", exp_avg, n, None), ("exp_avg_sq", exp_avg_sq, n, None),
                 ("exp_avg_scale", exp_avg_scale, blocks, torch.float32),
                 ("exp_avg_sq_scale", exp_avg_sq_scale, blocks, torch.float32)]
-        ptrs = []
+        ptrs, device = [], self.device or param.device
         for name, t, count, dtype in each:
             if t is None:
                 ptrs.append(None)
                 continue
-            if not t.is_cuda or not t.is_contiguous() or t.numel() != count or (self.device or t.device) != t.device:
+            if not t.is_cuda or not t.is_contiguous() or t.numel() != count or t.device != device:
                 raise ValueError(f"{name} must be a contiguous tensor of {count} elements on one CUDA device")
             if dtype is not None and t.dtype != dtype:
                 raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-            self.device = t.device
             ptrs.append(t.data_ptr())
         self._rows.append(cm_adamw_tensor(*ptrs, n, float(weight_decay), _dtype_of("param", param),
                                           _dtype_of("grad", grad), bits))
+        self.device = device
         # the storages, not the tensors, which may be given others
         self._keep.append([t.untyped_storage() for _, t, _, _ in each if t is not None])
         self._array = None

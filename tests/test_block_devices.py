@@ -148,3 +148,17 @@ def test_collective_calls(library, name):
     collectives(0)[name]()
     collectives(0, stream=Stream(0))[name]()
     assert library.calls == [name, name]
+
+
+def test_a_refused_tensor_leaves_the_list_as_it_was():
+    t = cm.AdamWTensors()
+    flat = lambda index, n=512: Tensor(n, dtype=F32, index=index)   # noqa: E731
+    with pytest.raises(ValueError):
+        t.add(flat(1), flat(1, 511), flat(1), flat(1))
+    with pytest.raises(ValueError):
+        t.add(flat(1), flat(0), flat(1), flat(1))
+    with pytest.raises(TypeError):
+        t.add(Tensor(512, dtype=torch.float16), flat(1), flat(1), flat(1))
+    assert len(t) == 0 and t.device is None
+    t.add(flat(0), flat(0), flat(0), flat(0))
+    assert len(t) == 1 and t.device == torch.device("cuda", 0)
