@@ -51,7 +51,7 @@ EXPORTS = ["cm_plan", "cm_plan_destroy", "cm_plan_steps", "cm_plan_step", "cm_pl
            "cm_backward_pair_workspace_size", "cm_backward_pair",
            "cm_cannon_workspace_size", "cm_cannon_gemm", "cm_einsum_cost", "cm_plan_choose_einsum",
            "cm_linear", "cm_linear_dgrad", "cm_linear_wgrad", "cm_linear_wgrad_workspace_size",
-           "cm_linear_check_status", "cm_layer_norm", "cm_layer_norm_backward",
+           "cm_linear_choose", "cm_linear_check_status", "cm_layer_norm", "cm_layer_norm_backward",
            "cm_layer_norm_backward_workspace_size", "cm_adamw"]
 CM_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -69,6 +69,11 @@ class cm_task(ctypes.Structure):
                 ("wait_in", ctypes.c_int16 * 2), ("wait_free", ctypes.c_int16 * 2),
                 ("sig_fwd", ctypes.c_int16 * 2), ("sig_done", ctypes.c_int16),
                 ("step", ctypes.c_int16), ("stream", ctypes.c_int16), ("tile_group", ctypes.c_int16)]
+
+
+class cm_linear_tile(ctypes.Structure):
+    _fields_ = [("pair", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("splits", ctypes.c_int32),
+                ("ctas_per_sm", ctypes.c_int32)]
 
 
 class cm_adamw_tensor(ctypes.Structure):
@@ -160,6 +165,8 @@ def load():
     lib.cm_linear_wgrad.restype = i32
     lib.cm_linear_wgrad_workspace_size.argtypes = [i64, i64, i64]
     lib.cm_linear_wgrad_workspace_size.restype = sz
+    lib.cm_linear_choose.argtypes = [i64, i64, i64, i32, ctypes.POINTER(cm_linear_tile)]
+    lib.cm_linear_choose.restype = i32
     lib.cm_linear_check_status.argtypes = [p, ctypes.POINTER(i32)]
     lib.cm_linear_check_status.restype = i32
     lib.cm_layer_norm.argtypes = [p, i32, i64, p, p, i32, f32, p, i32, i64, p, p, i64, i64, p]
@@ -530,6 +537,13 @@ def cm_linear_wgrad(x, dy, dw, ws=None, db=None, accumulate: bool = False, w_lay
                              _stream_of(stream, dev))
     if st:
         raise CMError(st, "cm_linear_wgrad")
+
+
+def linear_choose(rows: int, cols: int, k: int, transposed: bool = False) -> cm_linear_tile:
+    """The tile that the current device computes a rows x cols product of k terms in (transposed: a weight gradient's)."""
+    tile = cm_linear_tile()
+    _check(load().cm_linear_choose(rows, cols, k, 1 if transposed else 0, ctypes.byref(tile)), "cm_linear_choose")
+    return tile
 
 
 def cm_linear_check_status(stream=None):

@@ -379,6 +379,21 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
     return nk ? product(d, ox, ody, n, K, M, e, stream) : product(d, ody, ox, K, n, M, e, stream);
 }
 
+cm_status cm_linear_choose(int64_t rows, int64_t cols, int64_t k, int transposed, cm_linear_tile *tile) {
+    if (!tile) return CM_ERR_INVALID_ARG;
+    if (rows == 0) return CM_ERR_SHAPE;
+    CM_TRY(check_extents(rows, k, cols));
+    Device d;
+    CM_TRY(device(&d));
+    const Choice c = choose(d, rows, cols, k, transposed != 0);
+    tile->pair = c.pair ? 1 : 0;
+    tile->rows = c.pair ? 256 : c.tok;
+    tile->cols = c.pair ? c.bn : 128;
+    tile->splits = c.splits;
+    tile->ctas_per_sm = !c.pair && c.ring_bytes == kStripShared ? 2 : 1;
+    return CM_OK;
+}
+
 cm_status cm_linear_check_status(cm_stream_t stream_, int32_t info[4]) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     Device d;

@@ -648,6 +648,23 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
                           int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes, cm_stream_t stream);
 
 /*
+ * cm_linear_choose -- how the calls above compute a product of `rows` x `cols`
+ * elements with k terms each on the current device; asks for no launch and
+ * no memory.  The forward call's product is M x n with k = K, the data
+ * gradient's M x K with k = n.  The weight gradient's (`transposed` not 0) has
+ * the weight's extents as it is stored, n x K or K x n, with k = M.
+ *  Errors: CM_ERR_INVALID_ARG (NULL), CM_ERR_SHAPE (an extent that is not
+ *  positive or exceeds 2^30), CM_ERR_CUDA or CM_ERR_UNSUPPORTED without a device.
+ */
+typedef struct cm_linear_tile {
+    int32_t pair;         /* 1: tiles on pairs of CTAs, 0: strips, one CTA each */
+    int32_t rows, cols;   /* of a tile */
+    int32_t splits;       /* pairs, or CTAs, of a cluster that share a tile's k terms */
+    int32_t ctas_per_sm;  /* that shared memory allows */
+} cm_linear_tile;
+cm_status cm_linear_choose(int64_t rows, int64_t cols, int64_t k, int transposed, cm_linear_tile *tile);
+
+/*
  * cm_linear_check_status -- synchronise `stream` and read the status word of
  * the linear kernels on the current device: CM_OK, or CM_ERR_TIMEOUT if a
  * bounded device-side wait has expired in some call since the word was last
