@@ -490,11 +490,25 @@ __device__ uint32_t open_pair(const LinearPairParams &p, LSmem &s, uint8_t *smem
     return *s.tmem_slot;
 }
 
-__device__ void close_pair(uint32_t tmem) {
+// After an expired wait.  The leader's barriers count both CTAs' loads, but
+// where the two gave up at different slices some complete no phase any more, and
+// nothing tells when they have landed.  A load takes a few microseconds: the CTA,
+// and with it its shared memory, stays for a millisecond after the last.
+constexpr uint64_t kSettleNs = 1000000;
+__device__ __noinline__ void settle() {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < kSettleNs) {
+    }
+}
+
+__device__ void close_pair(const LSmem &s, uint32_t tmem) {
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // no cross-CTA traffic is left when a CTA frees its tensor memory
     tc_fence_after();
+    // a slice that was not multiplied has kept both CTAs' accumulator waits from
+    // ending, so both are aborting
+    if (threadIdx.x == 0 && *s.abort) settle();
     if (threadIdx.x >> 5 == 1) {
         __syncwarp();
         tmem_dealloc_pair(tmem, kTmemCols);
@@ -520,7 +534,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
         else
             finish_tiles<false, BN>(p, s, tmem, rank);
     }
-    close_pair(tmem);
+    close_pair(s, tmem);
 }
 
 // ---- few tiles: K split over the pairs of a cluster ---------------------------------
@@ -711,7 +725,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
             finish4(p.e, v, bias, int64_t(row0) + r, kRows, int64_t(row0) + nrows, col, n);
         }
     }
-    close_pair(tmem);   // with its cluster barrier the peers have read this CTA's partial tile
+    close_pair(s, tmem);   // with its cluster barrier the peers have read this CTA's partial tile
 }
 
 cudaError_t pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, unsigned cluster, unsigned ctas,

@@ -240,11 +240,9 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                     phase ^= 1u;
                 }
             }
-            // only an aborting CTA can get here with a load whose slice nobody
-            // waits for: no load may still write this shared memory at exit
-            if (*s.abort)
-                for (int i = 0; i < p.stages && i < issued; ++i)
-                    drain_l(p, &s.full[i], i < stage ? phase : phase ^ 1u);
+            // no load may still write this shared memory at exit, should another
+            // role give up on it, now or later
+            for (int i = 0; i < p.stages && i < issued; ++i) drain_l(p, &s.full[i], i < stage ? phase : phase ^ 1u);
         }
         __syncwarp();
     } else if (warp == 1) {
