@@ -213,10 +213,10 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     __syncwarp();
     wait_for_previous();
 
+    int stage = 0, issued = 0;   // of the thread that loads, and of the one that multiplies
+    uint32_t phase = 0;
     if (warp == 0) {
         if (elect_one()) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_try_wait(&s.empty[stage], phase ^ 1u) && !wait_l(p, s, &s.empty[stage], phase ^ 1u, kLinSiteEmpty))
                     break;
@@ -240,9 +240,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                     phase ^= 1u;
                 }
             }
-            // no load may still write this shared memory at exit, should another
-            // role give up on it, now or later
-            for (int i = 0; i < p.stages && i < issued; ++i) drain_l(p, &s.full[i], i < stage ? phase : phase ^ 1u);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -250,8 +247,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             const uint32_t idesc = idesc_bf16(kTileCols, p.tok, B_MN, A_MN);
             constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kBLbo = B_MN ? 64 * kBK * 2 : 16;
             constexpr uint32_t kAStep = A_MN ? (16 * 128) >> 4 : 32 >> 4, kBStep = B_MN ? (16 * 128) >> 4 : 32 >> 4;
-            int stage = 0;
-            uint32_t phase = 0;
             bool ok = true;
             const uint64_t ad0 = desc_sw128(smem_u32(s.ring), kALbo, 1024);
             const uint64_t bd0 = desc_sw128(smem_u32(s.ring) + kStripA, kBLbo, 1024);
@@ -281,6 +276,12 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         __syncwarp();
     }
     const bool good = wait_l(p, s, s.acc, 0, kLinSiteAcc);
+    // The accumulator is complete once every load has landed.  If it was given up,
+    // the loading thread waits for what it issued: no load may still write this
+    // shared memory at exit.
+    if (!good) {
+        for (int i = 0; i < p.stages && i < issued; ++i) drain_l(p, &s.full[i], i < stage ? phase : phase ^ 1u);
+    }
     __syncwarp();
     tc_fence_after();
     const int nrows = int(min(int64_t(p.tok), p.rows - row0));
