@@ -226,6 +226,14 @@ __device__ __forceinline__ float squares(const Share<R> &s, float mean, int widt
     }
     return sum(add(q[0], q[1])) + tail;
 }
+// s / h from inv = 1 / h: the product, which is off by a unit of the last place
+// for many h, and its remainder's part, so that exact quotients come out exact.
+// The compiler's division costs 1 to 8 % of the ring kernel (65536 x 512 in bf16:
+// 27.1 us for 26.0, 100000 x 64: 27.1 for 25.1).
+__device__ __forceinline__ float quotient(float s, float h, float inv) {
+    const float q = s * inv, rest = fmaf(-q, h, s);
+    return rest == rest ? fmaf(rest, inv, q) : q;   // a sum that is not finite has no remainder
+}
 // (x - mean) rstd g + b; the difference first, so that a row of one value gives b
 // wherever the row's sum is exact (and the mean its quotient, rounded once)
 __device__ __forceinline__ V8 scaled(const V8 &x, float mean, float rstd, const V8 &g, const V8 &b) {
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) cm_layer_norm_ring_kernel(con
         float mean[NR], rstd[NR];
         rows_sum(total(f[0]), NR > 1 ? total(f[NR - 1]) : 0.0f, g, sums[flip][0], mean);
 #pragma unroll
-        for (int k = 0; k < NR; ++k) mean[k] /= float(h);   // not times 1/h, which is rounded: see scaled()
+        for (int k = 0; k < NR; ++k) mean[k] = quotient(mean[k], float(h), inv_h);
         rows_sum(squares(f[0], mean[0], width, t, h), NR > 1 ? squares(f[NR - 1], mean[NR - 1], width, t, h) : 0.0f, g,
                  sums[flip][1], rstd);
 #pragma unroll
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(1024) cm_layer_norm_kernel(NormParams p, int w
         f.x[r] = live && c < h ? load_row8(x, c, h) : fill(0.0f);
     }
     const float inv_h = 1.0f / float(h);
-    const float mean = row_sum(total(f), g, row_buf(sums[0], g, 1)) / float(h);
+    const float mean = quotient(row_sum(total(f), g, row_buf(sums[0], g, 1)), float(h), inv_h);
     const float rstd = rsqrtf(row_sum(squares(f, mean, width, t, h), g, row_buf(sums[1], g, 1)) * inv_h + p.eps);
     if (!live) return;
     if (t == 0) {
