@@ -134,9 +134,15 @@ struct Choice {
 };
 
 // The choice with the least estimated time.  The estimates' constants were
-// fitted to 110 random calls (up to 630 rows, K and columns from 256 to 16384)
-// on one GB300 with weights from HBM, in us; the choices take 2 % longer than
-// the best of each call on average, the worst 1.2 times as long.
+// fitted to 110 forward calls (up to 1000 rows, K and columns from 256 to 28672)
+// with [n][K] weights from HBM, bf16 outputs and nothing else in the epilogue, on
+// one GB300, in us: 89 calls at random and 21 picked, 11 of them for sizes that
+// this library runs elsewhere or that lie at a border below, ten for having been
+// chosen badly before.  The choices take 2 % longer than the best of each call on
+// average, the worst 1.2 times as long (33 rows, K 1048, cols 2864: 8.2 for 6.7).
+// Other layouts, the gradients and fp32 outputs use the same constants, which
+// were not fitted to them; the bytes of outputs, residuals and pre-activations
+// are not in the estimate.
 //   pair: a K slice of 64 takes a wave of tiles 0.32 (256 columns) or 0.21
 //     (128), but no wave is shorter than its epilogue, 2.9 or 2.0; a launch
 //     takes 3.8 beyond that, summing over a cluster's pairs 2.6 or 1.6.
@@ -184,8 +190,10 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
         const double from_l2 = double(tiles) * double(128 + tok) * double(k) * 2.0 / 22e6;
         // unsplit, or split as far as all tiles' clusters run at once, two CTAs
         // an SM (9 rows, K 3728, cols 5504: 43 tiles of seven CTAs each take
-        // 16.3 us, of six 10.4).  Partial tiles of more than 128 rows do not fit
-        // two to an SM
+        // 16.3 us, of six 10.4).  Partial tiles of up to 208 rows fit two to an SM,
+        // but the constants were fitted with splits of 128 rows at most: with splits
+        // up to 208, 21 of 400 random calls of 129 to 384 rows went otherwise, 12 of
+        // them faster (by up to 23 %) and five slower (by up to 38 %)
         int64_t most = tok > 128 ? 1 : std::min<int64_t>(kStripMostSplits, slices);
         while (most > 1 && tiles > 2 * d.strip_clusters[most]) --most;
         for (int64_t splits = 1; splits <= most; splits += std::max<int64_t>(1, most - 1)) {

@@ -20,8 +20,8 @@
 // Bound by the tensor cores: 8192 x 8192 x 3584 takes 253.6 us, 1897 TFLOP/s, at
 // full clock; 8192 x 8192 x 28672 with GELU and the pre-activation kept 2.29 to
 // 2.39 ms, 1610 to 1680 TFLOP/s under the power cap.  With few K slices it is the
-// epilogue: 2.5 us a wave of tiles, GELU 2.7 more (two special-function
-// operations an element).
+// epilogue: 2.5 us a wave of tiles, SiLU 1.4 more, GELU 2.6 (its tanh form 1.6);
+// 8192 x 64 x 8192 takes 34.7, 54.8, 71.0 and 56.7 us.
 //
 // Calls with too few tiles for all SMs split the tiles' K slices: see
 // cm_linear_split_kernel below.

@@ -12,7 +12,7 @@
 //
 // Bound by HBM where the weights are large: one token through 28672 x 8192 takes
 // 69.7 us, 6738 GB/s.  A small call is bound by latency: one token through 4096 x
-// 2048 takes 6.6 us, of which 2.5 are its bytes; the rest is starting, the first
+// 2048 takes 6.6 to 7.0 us, of which 2.5 are its bytes; the rest is starting, the first
 // loads, and the sum over the cluster.  45 tokens through 8190 x 3579: 14.7 us for
 // 8.8 us of bytes.
 //

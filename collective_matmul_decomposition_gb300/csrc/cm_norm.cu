@@ -8,7 +8,7 @@
 //
 // All are bound by memory, and short of it by the latency of a row's reductions:
 // 8192 x 8192 in bf16 takes 52 us forward (5.2 TB/s) and 97 us backward with
-// residual and parameter gradients (5.6 TB/s); 65536 x 512: 26.5 and 48.6 us.
+// residual and parameter gradients (5.5 TB/s); 65536 x 512: 26.3 and 48.6 us.
 //
 // Statistics and sums are fp32.  The variance is that of the centred values
 // (two passes over registers), so a row far from zero loses nothing.
@@ -668,6 +668,9 @@ __device__ __forceinline__ void put_sum(void *out, int f32, int accumulate, int6
 
 // Bound by memory for long sums, by the launch for short ones: a CTA takes a
 // chunk of rows and 256 columns, so that a row's reads are 512 neighbouring bytes.
+// A weight gradient without the bias's sums and with them: rows 300, 1024 x 1024
+// 4.9 and 9.4 us; 65536, 256 x 256 33 and 50; 1813, 483 x 24629 46 and 74; whether
+// the sums come before the product or after it is one.
 // Partial sums over the rows of chunk blockIdx.y.  STATS: [chunk][2][h] of
 // dy xh and dy; otherwise [chunk][h] of dy.
 template <typename X, typename Y, int V, bool STATS, int kY>

@@ -679,7 +679,8 @@ cm_status cm_linear_check_status(cm_stream_t stream, int32_t info[4]);
  *  x (x_dtype), y (y_dtype) with row strides; gamma, beta [h] (param_dtype),
  *  NULL for 1 and 0; mean, rstd [rows] fp32, NULL or written for the backward
  *  pass.  Any extent, stride and element-aligned address; rows of at most
- *  32768 elements with 16-byte aligned starts are read once.  y may be x.
+ *  32768 elements with 16-byte aligned starts are read once.  y may be x where
+ *  type and row stride are the same.
  *  Errors: as cm_linear (eps must not be negative or NaN; rows may be 0).
  */
 cm_status cm_layer_norm(const void *x, cm_dtype x_dtype, int64_t ldx, const void *gamma, const void *beta,
