@@ -52,7 +52,8 @@ EXPORTS = ["cm_plan", "cm_plan_destroy", "cm_plan_steps", "cm_plan_step", "cm_pl
            "cm_cannon_workspace_size", "cm_cannon_gemm", "cm_einsum_cost", "cm_plan_choose_einsum",
            "cm_linear", "cm_linear_dgrad", "cm_linear_wgrad", "cm_linear_wgrad_workspace_size",
            "cm_linear_choose", "cm_linear_check_status", "cm_layer_norm", "cm_layer_norm_backward",
-           "cm_layer_norm_backward_workspace_size", "cm_adamw"]
+           "cm_layer_norm_backward_workspace_size", "cm_adamw", "cm_embedding", "cm_embedding_backward",
+           "cm_embedding_backward_workspace_size"]
 CM_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -178,6 +179,12 @@ def load():
     lib.cm_layer_norm_backward_workspace_size.restype = sz
     lib.cm_adamw.argtypes = [p, i32, f64, f64, f64, f64, i64, p, ctypes.c_uint64, p]
     lib.cm_adamw.restype = i32
+    lib.cm_embedding.argtypes = [p, i32, i64, p, i32, i64, f32, p, i32, i64, i64, i64, i64, p]
+    lib.cm_embedding.restype = i32
+    lib.cm_embedding_backward.argtypes = [p, i32, i64, p, i32, i64, f32, p, i32, i64, i32, i64, i64, i64, p, sz, p]
+    lib.cm_embedding_backward.restype = i32
+    lib.cm_embedding_backward_workspace_size.argtypes = [i64, i64]
+    lib.cm_embedding_backward_workspace_size.restype = sz
     _lib = lib
     return lib
 
@@ -397,12 +404,13 @@ def plan_choose_einsum(n_ranks, m, K, n, rates, max_chunks=CM_MAX_CHUNKS):
 
 
 # torch's names that the calls below use, bound by _bind_torch at the first of them
-_torch = _b16 = _f32 = _raw_stream = _current_device = None
+_torch = _b16 = _f32 = _i32 = _i64 = _raw_stream = _current_device = None
 
 
 def _bind_torch():
-    global _torch, _b16, _f32, _raw_stream, _current_device
+    global _torch, _b16, _f32, _i32, _i64, _raw_stream, _current_device
     import torch
+    _i32, _i64 = torch.int32, torch.int64
     _b16, _f32, _raw_stream = torch.bfloat16, torch.float32, torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
     _torch = torch
@@ -666,6 +674,47 @@ def cm_adamw(tensors: AdamWTensors, lr: float, beta1: float = 0.9, beta2: float 
                       _stream_of(stream, dev))
     if st:
         raise CMError(st, "cm_adamw")
+
+
+def _index_vector(name, t, n, device):
+    """A contiguous vector of n token ids: (pointer, bits)."""
+    if t.dtype is not _i64 and t.dtype is not _i32:
+        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+    return _vector(name, t, n, device), 64 if t.dtype is _i64 else 32
+
+
+def cm_embedding(ids, w, y, scale: float = 1.0, first: int = 0, stream=None):
+    """y [tokens][h] = scale * w[ids - first]; zeros for ids that are negative or not of first .. first + n - 1."""
+    lib = _library()
+    n, h, dev = _extents("w", w)
+    tokens = ids.shape[0] if ids.ndim else 0
+    ip, bits = _index_vector("ids", ids, tokens, dev)
+    wp, ldw = _matrix("w", w, (n, h), dev)
+    yp, ldy = _matrix("y", y, (tokens, h), dev)
+    st = lib.cm_embedding(ip, bits, first, wp, _dtype_of("w", w), ldw, scale, yp, _dtype_of("y", y), ldy, tokens, n, h,
+                          _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_embedding")
+
+
+def embedding_backward_workspace_size(tokens: int, h: int) -> int:
+    return load().cm_embedding_backward_workspace_size(tokens, h)
+
+
+def cm_embedding_backward(dy, ids, dw, ws, scale: float = 1.0, first: int = 0, accumulate: bool = False, stream=None):
+    """dw [n][h] (+)= scale * the sum of the rows dy[t] with ids[t] = first + v (embedding_backward_workspace_size bytes
+    in ws); with accumulate, rows of dw without a token are left as they are, else they become zeros."""
+    lib = _library()
+    tokens, h, dev = _extents("dy", dy)
+    n = dw.shape[0]
+    ip, bits = _index_vector("ids", ids, tokens, dev)
+    dyp, lddy = _matrix("dy", dy, (tokens, h), dev)
+    dwp, lddw = _matrix("dw", dw, (n, h), dev)
+    wsp, ws_bytes = _workspace(ws, dev)
+    st = lib.cm_embedding_backward(dyp, _dtype_of("dy", dy), lddy, ip, bits, first, scale, dwp, _dtype_of("dw", dw), lddw,
+                                   1 if accumulate else 0, tokens, n, h, wsp, ws_bytes, _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_embedding_backward")
 
 
 def version() -> str:

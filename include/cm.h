@@ -746,6 +746,37 @@ typedef struct cm_adamw_tensor {
 cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double lr, double beta1, double beta2, double eps,
                    int64_t step, const float *grad_scale, uint64_t seed, cm_stream_t stream);
 
+/*
+ * cm_embedding -- y[t] = scale w[ids[t] - first] for each of `tokens` tokens,
+ * a row of h elements; zeros where ids[t] is negative or not one of the n rows
+ * that w holds, ids first .. first + n - 1 (a rank's slice of the vocabulary:
+ * the slices' results then add up to the whole one's).
+ *  ids: int32 or int64 (id_bits 32 or 64); w [n][h] (w_dtype) and y [tokens][h]
+ *  (y_dtype) with row strides.  Any extent, stride and element-aligned address;
+ *  rows that start on 16 bytes go in whole vectors.  y must not alias w.
+ *  Errors: as cm_linear (first must lie in 0 .. 2^30; tokens may be 0).
+ */
+cm_status cm_embedding(const void *ids, int id_bits, int64_t first, const void *w, cm_dtype w_dtype, int64_t ldw,
+                       float scale, void *y, cm_dtype y_dtype, int64_t ldy, int64_t tokens, int64_t n, int64_t h,
+                       cm_stream_t stream);
+
+/*
+ * cm_embedding_backward -- dw[v] = scale times the sum of dy[t] over the tokens
+ * with ids[t] = first + v; with `accumulate` it is added to what is there, and
+ * rows without a token are neither read nor written.  Other tokens (see above)
+ * count nowhere, and their dy is not read.  Sums are fp32 in the order of the
+ * tokens, in pieces that depend on the ids alone, rounded once: results do not
+ * depend on timing.
+ *  dy [tokens][h] (dy_dtype), dw [n][h] (dw_dtype); h at most 65535 * 256.
+ *  ws: cm_embedding_backward_workspace_size(tokens, h) bytes, 16-byte aligned;
+ *  no initialisation; calls that share it must be ordered on the GPU.
+ *  Errors: as cm_embedding, and CM_ERR_WORKSPACE.
+ */
+size_t cm_embedding_backward_workspace_size(int64_t tokens, int64_t h);
+cm_status cm_embedding_backward(const void *dy, cm_dtype dy_dtype, int64_t lddy, const void *ids, int id_bits,
+                                int64_t first, float scale, void *dw, cm_dtype dw_dtype, int64_t lddw, int accumulate,
+                                int64_t tokens, int64_t n, int64_t h, void *ws, size_t ws_bytes, cm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
