@@ -50,7 +50,8 @@ EXPORTS = ["cm_plan", "cm_plan_destroy", "cm_plan_steps", "cm_plan_step", "cm_pl
            "cm_gemm_rs_pipelined_workspace_size", "cm_gemm_rs_pipelined",
            "cm_backward_pair_workspace_size", "cm_backward_pair",
            "cm_cannon_workspace_size", "cm_cannon_gemm", "cm_einsum_cost", "cm_plan_choose_einsum",
-           "cm_linear", "cm_linear_dgrad", "cm_linear_wgrad", "cm_linear_wgrad_workspace_size",
+           "cm_linear", "cm_linear_dgrad", "cm_linear_gated", "cm_linear_gated_dgrad", "cm_linear_wgrad",
+           "cm_linear_wgrad_workspace_size",
            "cm_linear_choose", "cm_linear_check_status", "cm_layer_norm", "cm_layer_norm_backward",
            "cm_layer_norm_backward_workspace_size", "cm_adamw", "cm_embedding", "cm_embedding_backward",
            "cm_embedding_backward_workspace_size"]
@@ -162,6 +163,10 @@ def load():
     lib.cm_linear.restype = i32
     lib.cm_linear_dgrad.argtypes = [p, i64, p, i64, i32, p, i64, i32, p, i64, p, i32, i64, i64, i64, i64, p]
     lib.cm_linear_dgrad.restype = i32
+    lib.cm_linear_gated.argtypes = [p, i64, p, p, i64, i32, p, p, i32, i32, p, p, i64, p, i64, i64, i64, i64, p]
+    lib.cm_linear_gated.restype = i32
+    lib.cm_linear_gated_dgrad.argtypes = [p, i64, p, i64, i32, p, p, i64, i32, p, p, i64, i64, i64, i64, p]
+    lib.cm_linear_gated_dgrad.restype = i32
     lib.cm_linear_wgrad.argtypes = [p, i64, p, i64, p, i32, i64, i32, p, i32, i32, i64, i64, i64, p, sz, p]
     lib.cm_linear_wgrad.restype = i32
     lib.cm_linear_wgrad_workspace_size.argtypes = [i64, i64, i64]
@@ -523,6 +528,53 @@ def cm_linear_dgrad(dy, w, dx, preact=None, act: str = "none", residual=None, w_
                              M, K, n, _stream_of(stream, dev))
     if st:
         raise CMError(st, "cm_linear_dgrad")
+
+
+def _matrices(names, ts, shape, device, dtype):
+    """Two matrices of one shape and row stride: (pointers, row stride)."""
+    (p0, ld0), (p1, ld1) = (_matrix(name, t, shape, device, dtype) for name, t in zip(names, ts))
+    if ld0 != ld1:
+        raise ValueError(f"{names[0]} and {names[1]} must have one row stride, not {ld0} and {ld1}")
+    return p0, p1, ld0
+
+
+def cm_linear_gated(x, w_gate, w_up, y, act: str = "silu", bias_gate=None, bias_up=None, z_gate=None, z_up=None,
+                    w_layout: str = "nk", stream=None):
+    """y [M][n] = act(g) * u, g = x @ Wg^T + bias_gate, u = x @ Wu^T + bias_up; z_gate and z_up receive g and u (bf16)."""
+    lib = _library()
+    M, K, dev = _extents("x", x)
+    n = _columns("y", y)
+    layout = LAYOUTS[w_layout]
+    if (bias_gate is None) != (bias_up is None) or (z_gate is None) != (z_up is None):
+        raise ValueError("biases and pre-activations are given for both projections or for neither")
+    if bias_gate is not None and bias_gate.dtype is not bias_up.dtype:
+        raise TypeError("bias_gate and bias_up must have one dtype")
+    xp, ldx = _matrix("x", x, (M, K), dev, _b16)
+    gp, up, ldw = _matrices(("w_gate", "w_up"), (w_gate, w_up), (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
+    yp, ldy = _matrix("y", y, (M, n), dev, _b16)
+    zg, zu, ldz = _matrices(("z_gate", "z_up"), (z_gate, z_up), (M, n), dev, _b16) if z_gate is not None else (None, None, 0)
+    st = lib.cm_linear_gated(xp, ldx, gp, up, ldw, layout, _vector("bias_gate", bias_gate, n, dev),
+                             _vector("bias_up", bias_up, n, dev), _dtype_of("bias_gate", bias_gate), ACTS[act], zg, zu, ldz,
+                             yp, ldy, M, K, n, _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear_gated")
+
+
+def cm_linear_gated_dgrad(dy, w, dz_gate, dz_up, z_gate, z_up, act: str = "silu", w_layout: str = "nk", stream=None):
+    """With d = dy @ W (the down projection's weight) and the z of cm_linear_gated: dz_gate [M][K] = d * z_up *
+    act'(z_gate), dz_up [M][K] = d * act(z_gate)."""
+    lib = _library()
+    M, n, dev = _extents("dy", dy)
+    K = _columns("dz_gate", dz_gate)
+    layout = LAYOUTS[w_layout]
+    dyp, lddy = _matrix("dy", dy, (M, n), dev, _b16)
+    wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
+    zg, zu, ldz = _matrices(("z_gate", "z_up"), (z_gate, z_up), (M, K), dev, _b16)
+    dg, du, lddz = _matrices(("dz_gate", "dz_up"), (dz_gate, dz_up), (M, K), dev, _b16)
+    st = lib.cm_linear_gated_dgrad(dyp, lddy, wp, ldw, layout, zg, zu, ldz, ACTS[act], dg, du, lddz, M, K, n,
+                                   _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear_gated_dgrad")
 
 
 def linear_wgrad_workspace_size(M: int, K: int, n: int) -> int:

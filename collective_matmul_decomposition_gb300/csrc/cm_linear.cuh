@@ -26,7 +26,20 @@ struct LinearEpilogue {
     int act;            // cm_act
     int dact;
     int accumulate;
+    // of the gated kernels (LinearMode): the up projection's bias, and its z read or written
+    const void *bias2;
+    const void *zin2;   // bf16
+    void *z2;           // bf16
 };
+
+// What a kernel's epilogue computes.
+//   kLinPlain  LinearEpilogue's chain.
+//   kLinGated  two products of the same rows, g with the first column operand and u
+//              with the second: g += bias, u += bias2; z = bf16(g), z2 = bf16(u) if
+//              kept; y = act(g) u.
+//   kLinGateGrad  D is the gradient of such a y: z = D zin2 act'(zin), y = D act(zin)
+//              (zin = g, zin2 = u as they were kept; y is u's gradient, z is g's).
+enum LinearMode { kLinPlain = 0, kLinGated = 1, kLinGateGrad = 2 };
 
 // Device status of the linear kernels: {code, tile, CTA, site} of the first
 // bounded wait that expired since it was last read.
@@ -47,6 +60,7 @@ enum LinearSite : uint32_t {
 struct LinearStripParams {
     CUtensorMap tmA;    // column operand: [n][K] (K-major) or [K][n]
     CUtensorMap tmB;    // row operand: [rows][K] (K-major) or [K][rows]
+    CUtensorMap tmA2;   // gated: the second column operand; a tile then has 64 columns of each
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks;        // 64-wide K slices
@@ -59,12 +73,12 @@ struct LinearStripParams {
     uint64_t timeout_ns;
 };
 
-// layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.
+// layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.  The gated modes take 0 and 2.
 constexpr int kStripAlone = 216 * 1024, kStripShared = 108 * 1024;   // ring bytes of a CTA alone on its SM, of one of two
 // clusters[i]: clusters of i CTAs (2 to kStripMostSplits) that run together, one CTA an SM.
 constexpr int kStripMostSplits = 8;
 cudaError_t prepare_linear_strip(int sms, int *clusters);
-cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream);
+cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, LinearMode mode, cudaStream_t stream);
 int linear_strip_stages(int tok, int ring_bytes);
 
 // Tiles of 256 rows x bn columns on CTA pairs.  A is the row operand here, B the
@@ -74,6 +88,7 @@ struct LinearPairParams {
     CUtensorMap tmY;          // bf16: 64 x 32 boxes, fp32: 32 x 32
     CUtensorMap tmZ;          // pre-activation kept (bf16 y only), 64 x 32
     CUtensorMap tmIn0, tmIn1; // residual (or y, to be added to) and pre-activation read; bf16 y only
+    CUtensorMap tmB2, tmZ2;   // gated: the second column operand, and its z kept
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks, mtiles, ntiles, tiles;
@@ -83,11 +98,13 @@ struct LinearPairParams {
     uint64_t timeout_ns;
 };
 
-// layout: bit 0 = B MN-major, bit 1 = A MN-major.  splits: 1 (persistent, on
+// layout: bit 0 = B MN-major, bit 1 = A MN-major; the gated modes take 0 and 1, and
+// kLinGated tiles of 256 columns, half of them of each operand.  splits: 1 (persistent, on
 // `clusters` pairs), or 2 or 4 pairs a cluster that share a tile's K slices,
 // one cluster a tile.  clusters[i]: clusters of 2^i pairs that run together.
 cudaError_t prepare_linear_pair(int sms, int *clusters);
-cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int splits, int clusters, cudaStream_t stream);
+cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode mode, int splits, int clusters,
+                               cudaStream_t stream);
 
 // Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu): partial
 // sums per row chunk in `partial`, then their sum in chunk order.

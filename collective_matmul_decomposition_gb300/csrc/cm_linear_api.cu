@@ -159,14 +159,16 @@ struct Choice {
 //   rows 2048, K 12288, cols 4608:  129 / 161 / -     rows 1024, K 8192, cols 1024:  40.1 / 23.1 / 16.8
 // and between strips (one tile of rows / more, shorter ones):
 //   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  22.8 / 29.0 (three)
-Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn) {
+// A gated product is estimated as one of the columns of both its operands; its
+// pair tiles have 256 of them (`wide`).
+Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn, bool wide = false) {
     Choice best;
     double least = 1e30;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t slices = up(k, kBK);
     const double from_hbm = double(cols) * double(k) * 2.0 / 8.5e6;
     // pair tiles waste what they have beyond `rows`: not worth a look below 33
-    for (int bn = 256; bn >= 128 && rows > 32; bn /= 2) {
+    for (int bn = 256; bn >= (wide ? 256 : 128) && rows > 32; bn /= 2) {
         const int64_t tiles = up(rows, 256) * up(cols, bn);
         for (int i = 0; i < 3; ++i) {
             const int splits = 1 << i;
@@ -214,8 +216,9 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
     return best;
 }
 
-cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const Operand &b, int64_t rows, int64_t cols,
-                       int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
+// a2: the second column operand of a gated product, else NULL.
+cm_status product_pair(const Device &d, const Choice &c, LinearMode mode, const Operand &a, const Operand *a2, const Operand &b,
+                       int64_t rows, int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
     LinearPairParams p;
     p.e = e;
     p.rows = rows;
@@ -223,30 +226,39 @@ cm_status product_pair(const Device &d, const Choice &c, const Operand &a, const
     p.bn = c.bn;
     p.kblocks = int((k + kBK - 1) / kBK);
     p.mtiles = int((rows + 255) / 256);
-    p.ntiles = int((cols + c.bn - 1) / c.bn);
+    const int tile_cols = mode == kLinGated ? c.bn / 2 : c.bn;
+    p.ntiles = int((cols + tile_cols - 1) / tile_cols);
     if (int64_t(p.mtiles) * p.ntiles > 0x7fffffff) return CM_ERR_SHAPE;
     p.tiles = p.mtiles * p.ntiles;
     p.band = int(std::max<int64_t>(1, std::min<int64_t>(p.mtiles, kBandBytes / (int64_t(p.kblocks) * 256 * kBK * 2))));
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
     if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, c.bn / 2) ||
-        !map_written(&p.tmY, e.y, rows, cols, e.ldy, e.y_f32 != 0))
+        (a2 && !map_operand(&p.tmB2, *a2, cols, k, c.bn / 2)) || !map_written(&p.tmY, e.y, rows, cols, e.ldy, e.y_f32 != 0))
         return CM_ERR_CUDA;
-    if (!e.y_f32) {
+    if (mode == kLinGateGrad) {
+        if (!map_written(&p.tmZ, e.z, rows, cols, e.ldz, false) || !map_rows(&p.tmIn0, e.zin2, rows, cols, e.ldzin, 32) ||
+            !map_rows(&p.tmIn1, e.zin, rows, cols, e.ldzin, 32))
+            return CM_ERR_CUDA;
+    } else if (mode == kLinGated) {
+        if (e.z && (!map_written(&p.tmZ, e.z, rows, cols, e.ldz, false) || !map_written(&p.tmZ2, e.z2, rows, cols, e.ldz, false)))
+            return CM_ERR_CUDA;
+    } else if (!e.y_f32) {
         if (e.z && !map_written(&p.tmZ, e.z, rows, cols, e.ldz, false)) return CM_ERR_CUDA;
         if (e.accumulate && !map_rows(&p.tmIn0, e.y, rows, cols, e.ldy, 32)) return CM_ERR_CUDA;
         if (e.res && !map_rows(&p.tmIn0, e.res, rows, cols, e.ldr, 32)) return CM_ERR_CUDA;
         if (e.dact && !map_rows(&p.tmIn1, e.zin, rows, cols, e.ldzin, 32)) return CM_ERR_CUDA;
     }
     const int layout = (a.mn_major ? 1 : 0) | (b.mn_major ? 2 : 0);
-    return launch_linear_pair(p, layout, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+    return launch_linear_pair(p, layout, mode, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
-// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e.
+// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e; a2: see product_pair().
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
-                  const LinearEpilogue &e, cudaStream_t stream) {
-    const Choice c = choose(d, rows, cols, k, b.mn_major);
-    if (c.pair) return product_pair(d, c, a, b, rows, cols, k, e, stream);
+                  const LinearEpilogue &e, cudaStream_t stream, LinearMode mode = kLinPlain, const Operand *a2 = nullptr) {
+    const bool gated = mode == kLinGated;
+    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated);
+    if (c.pair) return product_pair(d, c, mode, a, a2, b, rows, cols, k, e, stream);
     LinearStripParams p;
     p.e = e;
     p.rows = rows;
@@ -259,9 +271,11 @@ cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t r
     p.stages = linear_strip_stages(c.tok, c.ring_bytes);
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
-    if (!map_operand(&p.tmA, a, cols, k, 128) || !map_operand(&p.tmB, b, rows, k, c.tok)) return CM_ERR_CUDA;
+    if (!map_operand(&p.tmA, a, cols, k, gated ? 64 : 128) || (gated && !map_operand(&p.tmA2, *a2, cols, k, 64)) ||
+        !map_operand(&p.tmB, b, rows, k, c.tok))
+        return CM_ERR_CUDA;
     const int layout = (b.mn_major ? 1 : 0) | (a.mn_major ? 2 : 0);
-    return launch_linear_strip(p, layout, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+    return launch_linear_strip(p, layout, mode, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
 size_t wgrad_workspace(int64_t M, int64_t n) {
@@ -340,6 +354,65 @@ cm_status cm_linear_dgrad(const void *dy, int64_t lddy, const void *w, int64_t l
     e.ldr = ldr;
     // W stored [n][K]: its K columns are contiguous, the contracted n is not
     return product(d, {w, ldw, wlayout == CM_W_NK}, {dy, lddy, false}, M, K, n, e, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cm_status cm_linear_gated(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw, cm_wlayout wlayout,
+                          const void *bias_gate, const void *bias_up, cm_dtype bias_dtype, cm_act act, void *z_gate,
+                          void *z_up, int64_t ldz, void *y, int64_t ldy, int64_t M, int64_t K, int64_t n,
+                          cm_stream_t stream) {
+    NvtxRange range("cm_linear_gated");
+    if ((bias_gate && bad_dtype(bias_dtype)) || (wlayout != CM_W_KN && wlayout != CM_W_NK) || act < CM_ACT_NONE ||
+        act > CM_ACT_SILU || !bias_gate != !bias_up || !z_gate != !z_up)
+        return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    if (n > kMaxExtent / 2) return CM_ERR_SHAPE;
+    if (M == 0) return CM_OK;
+    CM_TRY(check_matrix(x, ldx, K));
+    for (const void *w : {w_gate, w_up}) CM_TRY(check_matrix(w, ldw, wlayout == CM_W_NK ? K : n));
+    CM_TRY(check_matrix(y, ldy, n));
+    if (z_gate)
+        for (const void *z : {z_gate, z_up}) CM_TRY(check_matrix(z, ldz, n));
+    if (misaligned(bias_gate, bias_dtype) || misaligned(bias_up, bias_dtype)) return CM_ERR_ALIGNMENT;
+    Device d;
+    CM_TRY(device(&d));
+    LinearEpilogue e = {};
+    e.y = y;
+    e.ldy = ldy;
+    e.bias = bias_gate;
+    e.bias2 = bias_up;
+    e.bias_f32 = bias_dtype == CM_F32;
+    e.act = act;
+    e.z = z_gate;
+    e.z2 = z_up;
+    e.ldz = ldz;
+    const Operand gate = {w_gate, ldw, wlayout == CM_W_KN}, up = {w_up, ldw, wlayout == CM_W_KN};
+    return product(d, gate, {x, ldx, false}, M, n, K, e, reinterpret_cast<cudaStream_t>(stream), kLinGated, &up);
+}
+
+cm_status cm_linear_gated_dgrad(const void *dy, int64_t lddy, const void *w, int64_t ldw, cm_wlayout wlayout,
+                                const void *z_gate, const void *z_up, int64_t ldz, cm_act act, void *dz_gate, void *dz_up,
+                                int64_t lddz, int64_t M, int64_t K, int64_t n, cm_stream_t stream) {
+    NvtxRange range("cm_linear_gated_dgrad");
+    if ((wlayout != CM_W_KN && wlayout != CM_W_NK) || act < CM_ACT_NONE || act > CM_ACT_SILU) return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    if (M == 0) return CM_OK;
+    CM_TRY(check_matrix(dy, lddy, n));
+    CM_TRY(check_matrix(w, ldw, wlayout == CM_W_NK ? K : n));
+    for (const void *z : {z_gate, z_up}) CM_TRY(check_matrix(z, ldz, K));
+    for (const void *z : {dz_gate, dz_up}) CM_TRY(check_matrix(z, lddz, K));
+    Device d;
+    CM_TRY(device(&d));
+    LinearEpilogue e = {};
+    e.y = dz_up;
+    e.ldy = lddz;
+    e.z = dz_gate;
+    e.ldz = lddz;
+    e.act = act;
+    e.zin = z_gate;
+    e.zin2 = z_up;
+    e.ldzin = ldz;
+    return product(d, {w, ldw, wlayout == CM_W_NK}, {dy, lddy, false}, M, K, n, e, reinterpret_cast<cudaStream_t>(stream),
+                   kLinGateGrad);
 }
 
 size_t cm_linear_wgrad_workspace_size(int64_t M, int64_t K, int64_t n) {

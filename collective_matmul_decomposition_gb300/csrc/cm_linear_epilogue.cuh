@@ -155,11 +155,54 @@ __device__ __forceinline__ void mul_dact(float (&f)[N], const float (&z)[N], int
     }
 }
 
-__device__ __forceinline__ float load_bias(const LinearEpilogue &e, int64_t c) {
-    if (!e.bias) return 0.0f;
-    return e.bias_f32 ? static_cast<const float *>(e.bias)[c]
-                      : __bfloat162float(static_cast<const __nv_bfloat16 *>(e.bias)[c]);
+// g becomes act(g) u.
+template <int ACT, int N>
+__device__ __forceinline__ void gate_loop(float (&g)[N], const float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 r = parts(mul(act2<ACT>(pair(g[i], g[i + 1])), pair(u[i], u[i + 1])));
+        g[i] = r.x;
+        g[i + 1] = r.y;
+    }
 }
+template <int N>
+__device__ __forceinline__ void apply_gate(float (&g)[N], const float (&u)[N], int act) {
+    switch (act) {
+        case CM_ACT_RELU: gate_loop<CM_ACT_RELU>(g, u); break;
+        case CM_ACT_GELU: gate_loop<CM_ACT_GELU>(g, u); break;
+        case CM_ACT_GELU_TANH: gate_loop<CM_ACT_GELU_TANH>(g, u); break;
+        case CM_ACT_SILU: gate_loop<CM_ACT_SILU>(g, u); break;
+        default: gate_loop<CM_ACT_NONE>(g, u); break;
+    }
+}
+// From d, the gradient of act(g) u: g becomes d u act'(g), its own gradient, and u becomes d act(g).
+template <int ACT, int N>
+__device__ __forceinline__ void gate_grad_loop(const float (&d)[N], float (&g)[N], float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const F2 dd = pair(d[i], d[i + 1]), gg = pair(g[i], g[i + 1]);
+        const float2 dg = parts(mul(mul(dd, pair(u[i], u[i + 1])), dact2<ACT>(gg)));
+        const float2 du = parts(mul(dd, act2<ACT>(gg)));
+        g[i] = dg.x, g[i + 1] = dg.y;
+        u[i] = du.x, u[i + 1] = du.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void gate_grad(const float (&d)[N], float (&g)[N], float (&u)[N], int act) {
+    switch (act) {
+        case CM_ACT_RELU: gate_grad_loop<CM_ACT_RELU>(d, g, u); break;
+        case CM_ACT_GELU: gate_grad_loop<CM_ACT_GELU>(d, g, u); break;
+        case CM_ACT_GELU_TANH: gate_grad_loop<CM_ACT_GELU_TANH>(d, g, u); break;
+        case CM_ACT_SILU: gate_grad_loop<CM_ACT_SILU>(d, g, u); break;
+        default: gate_grad_loop<CM_ACT_NONE>(d, g, u); break;
+    }
+}
+
+__device__ __forceinline__ float load_bias(const void *bias, int f32, int64_t c) {
+    if (!bias) return 0.0f;
+    return f32 ? static_cast<const float *>(bias)[c] : __bfloat162float(static_cast<const __nv_bfloat16 *>(bias)[c]);
+}
+__device__ __forceinline__ float load_bias(const LinearEpilogue &e, int64_t c) { return load_bias(e.bias, e.bias_f32, c); }
 
 }  // namespace
 }  // namespace lin

@@ -116,20 +116,23 @@ struct Share {
     uint32_t leader;
 };
 
-template <int LAYOUT, int BN>
+template <int LAYOUT, int BN, int MODE>
 __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, int rank) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
     const uint32_t full_leader = mapa_shared(smem_u32(s.full), w.leader);
     const uint32_t a0 = smem_u32(s.a0), b0 = smem_u32(s.b0);
-    const uint64_t tma = reinterpret_cast<uint64_t>(&p.tmA), tmb = reinterpret_cast<uint64_t>(&p.tmB);
+    // gated: the pair's even CTA stages the gate's columns, the odd one the up projection's,
+    // so that half of each CTA's accumulator columns belong to either
+    const uint64_t tma = reinterpret_cast<uint64_t>(&p.tmA);
+    const uint64_t tmb = reinterpret_cast<uint64_t>(MODE == kLinGated && rank ? &p.tmB2 : &p.tmB);
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int t = w.first; t < p.tiles && ok; t += w.step) {
         int mt, nt;
         tile_at(p, t, mt, nt);
-        const int row0 = mt * kTile + rank * kHalf, col0 = nt * BN + rank * (BN / 2);
+        const int row0 = mt * kTile + rank * kHalf, col0 = MODE == kLinGated ? nt * (BN / 2) : nt * BN + rank * (BN / 2);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
             if (!mbar_try_wait(s.empty + stage, phase ^ 1u) &&
                 !wait_p(p, s, s.empty + stage, phase ^ 1u, kLinSiteEmpty, t)) {
@@ -264,8 +267,8 @@ __device__ __noinline__ void store_rest(const LinearPairParams &p, uint8_t *buf0
         if (i < n) z[i] = __float2bfloat16_rn(f[i]);
 }
 
-// F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).
-template <bool F32, int BN>
+// F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).  MODE: kLinPlain or kLinGateGrad.
+template <bool F32, int BN, int MODE>
 __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t tmem, int rank) {
     constexpr int kChunk = F32 ? 32 : 64, kCols = BN / 2;   // columns of a warp
     const LinearEpilogue &e = p.e;
@@ -276,7 +279,9 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
     const uint32_t tempty_leader = mapa_shared(smem_u32(&s.tempty[0]), 0);
     // inputs by TMA: the residual or the old value, and the pre-activation.
     // With an fp32 y those are bf16 beside 4-byte chunks: read directly.
-    const bool in0 = !F32 && (e.res || e.accumulate), in1 = !F32 && e.dact;
+    // The gate's gradients read both z and write one gradient over each.
+    constexpr bool kGate = MODE == kLinGateGrad;
+    const bool in0 = kGate || (!F32 && (e.res || e.accumulate)), in1 = kGate || (!F32 && e.dact);
     const uint32_t in_bytes = uint32_t(in0 ? kEpiBuf : 0) + uint32_t(in1 ? kEpiBuf : 0);
     // the second buffer holds the pre-activation if there is one; else chunks
     // take turns with the two, so that one is filled while the other is written out
@@ -352,6 +357,21 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
                 float f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                if constexpr (kGate) {
+                    float g[32], u[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        unpack8(*piece(buf1, lane, h * 4 + j), g + 8 * j);
+                        unpack8(*piece(buf0, lane, h * 4 + j), u + 8 * j);
+                    }
+                    lin::gate_grad(f, g, u, e.act);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        *piece(buf1, lane, h * 4 + j) = pack8(g + 8 * j);
+                        *piece(buf0, lane, h * 4 + j) = pack8(u + 8 * j);
+                    }
+                    continue;
+                }
                 // the columns' biases lie one to a lane (as fast as reading them
                 // all from L1, and any address will do)
                 if (e.bias) {
@@ -446,6 +466,105 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
     __syncwarp();
 }
 
+// The columns behind a row's last whole 16-byte piece, n of them, from element `at` of the buffer's row.
+__device__ __noinline__ void store_tail(uint8_t *buf, void *m, int64_t ld, int64_t row, int64_t col, int at, int n, int r) {
+    float f[8];
+    unpack8(*piece(buf, r, at >> 3), f);
+    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(m) + row * ld + col;
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) y[i] = __float2bfloat16_rn(f[i]);
+}
+
+// The gated product: of a tile's 256 accumulator columns the first 128 are g, the
+// others u of the same 128 columns.  A warp owns 32 rows x 64 of those.  Up to three
+// matrices leave through its two buffers in turn (y, then z of both); each reads the
+// accumulator again, which costs less than holding 128 columns in registers.
+// Bound by the tensor cores where the products are long (4096 x 8192 x 28672 with both
+// z kept), by the epilogue below some 16 K slices a tile.
+__device__ void finish_gated(const LinearPairParams &p, const LSmem &s, uint32_t tmem, int rank) {
+    constexpr int BN = 256, kCols = 64;
+    const LinearEpilogue &e = p.e;
+    const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
+    const int quad = ew & 3, half = ew >> 2;
+    uint8_t *const bufs = s.epi + ew * 2 * kEpiBuf;
+    uint8_t *buf = bufs;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    const int rest = int(p.cols % 8);
+    const int64_t whole = p.cols - rest;
+    const int outs = e.z ? 3 : 1;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = int(blockIdx.x) >> 1; t < p.tiles; t += int(gridDim.x) >> 1) {
+        int mt, nt;
+        tile_at(p, t, mt, nt);
+        const int row0 = mt * kTile + rank * kHalf + quad * 32, c0 = nt * (BN / 2) + half * kCols;
+        const bool live = row0 < p.rows && c0 < p.cols;
+        float bg[2], bu[2];   // the columns' biases lie one to a lane
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 32 * h + lane;
+            bg[h] = c < p.cols ? lin::load_bias(e.bias, e.bias_f32, c) : 0.0f;
+            bu[h] = c < p.cols ? lin::load_bias(e.bias2, e.bias_f32, c) : 0.0f;
+        }
+        bool ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
+        auto load = [&](int first, int h, float (&f)[32], const float (&b)[2]) {
+            uint32_t v[32];
+            tmem_ld32(taddr + uint32_t(first + 32 * h), v);
+            tmem_wait_ld_regs(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+            if (e.bias) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] += __shfl_sync(0xffffffffu, h ? b[1] : b[0], i);
+            }
+        };
+        for (int o = 0; live && o < outs; ++o) {
+            if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has been read out
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float f[32];
+                if (o == 0) {
+                    float u[32];
+                    load(0, h, f, bg);
+                    load(BN / 2, h, u, bu);
+                    lin::apply_gate(f, u, e.act);
+                } else if (o == 1) {
+                    load(0, h, f, bg);
+                } else {
+                    load(BN / 2, h, f, bu);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *piece(buf, lane, h * 4 + j) = pack8(f + 8 * j);
+            }
+            if (rest && c0 + kCols > whole && int64_t(row0) + lane < p.rows)
+                store_tail(buf, o == 0 ? e.y : o == 1 ? e.z : e.z2, o == 0 ? e.ldy : e.ldz, int64_t(row0) + lane, whole,
+                           int(whole - c0), rest, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (c0 < whole) tma_store_3d(o == 0 ? &p.tmY : o == 1 ? &p.tmZ : &p.tmZ2, buf, c0, row0, 0);
+                bulk_commit();
+            }
+            buf = buf == bufs ? bufs + kEpiBuf : bufs;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
+        if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+        }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+}
+
 // Shared memory, barriers and tensor memory of a CTA.  Returns the accumulators' address.
 template <int BN>
 __device__ uint32_t open_pair(const LinearPairParams &p, LSmem &s, uint8_t *smem_raw) {
@@ -515,7 +634,7 @@ __device__ void close_pair(const LSmem &s, uint32_t tmem) {
     }
 }
 
-template <int LAYOUT, int BN>
+template <int LAYOUT, int BN, int MODE>
 __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __grid_constant__ LinearPairParams p) {
     extern __shared__ uint8_t smem_raw[];
     LSmem s;
@@ -523,16 +642,18 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     const int warp = int(threadIdx.x) >> 5, rank = int(cluster_ctarank());
     const Share w = {int(blockIdx.x) >> 1, int(gridDim.x) >> 1, 0, p.kblocks, 0u};
     if (warp == 0) {
-        if (elect_one()) load_tiles<LAYOUT, BN>(p, s, w, rank);
+        if (elect_one()) load_tiles<LAYOUT, BN, MODE>(p, s, w, rank);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) multiply_tiles<LAYOUT, BN>(p, s, w, tmem);
         __syncwarp();
     } else if (warp >= 4) {
-        if (p.e.y_f32)
-            finish_tiles<true, BN>(p, s, tmem, rank);
+        if constexpr (MODE == kLinGated)
+            finish_gated(p, s, tmem, rank);
+        else if (MODE == kLinPlain && p.e.y_f32)
+            finish_tiles<true, BN, kLinPlain>(p, s, tmem, rank);
         else
-            finish_tiles<false, BN>(p, s, tmem, rank);
+            finish_tiles<false, BN, MODE>(p, s, tmem, rank);
     }
     close_pair(s, tmem);
 }
@@ -640,6 +761,25 @@ __device__ __forceinline__ void finish4(const LinearEpilogue &e, float (&v)[4][4
     }
 }
 
+// The same for the gate's gradients: v is the gradient of act(g) u.
+__device__ __forceinline__ void finish4_gate_grad(const LinearEpilogue &e, float (&v)[4][4], int64_t row, int64_t step,
+                                                  int64_t end, int64_t col, int n) {
+    float g[4][4], u[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bool live = row + k * step < end;
+        get4(e.zin, (row + k * step) * e.ldzin + col, live ? n : 0, g[k]);
+        get4(e.zin2, (row + k * step) * e.ldzin + col, live ? n : 0, u[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (row + k * step >= end) continue;
+        lin::gate_grad(v[k], g[k], u[k], e.act);
+        put4(e.z, (row + k * step) * e.ldz + col, n, g[k]);
+        put4(e.y, (row + k * step) * e.ldy + col, n, u[k]);
+    }
+}
+
 // A cluster of S pairs computes one tile, pair j the j-th part of its K slices.
 // Each CTA leaves its 128 rows of the partial tile in its own shared memory as
 // fp32 (the ring, whose loads have all been multiplied by then); after a
@@ -647,7 +787,7 @@ __device__ __forceinline__ void finish4(const LinearEpilogue &e, float (&v)[4][4
 // pairs' partial sums in their order.  No workspace, one launch, the same bits
 // every time.  200 x 8192 x 3584 takes 19.9 us on four pairs a tile, 26.3 on two
 // and 42.5 unsplit; the exchange and the summing cost 4 us (128 columns) to 6.5.
-template <int LAYOUT, int BN, int S>
+template <int LAYOUT, int BN, int S, int MODE>
 __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __grid_constant__ LinearPairParams p) {
     extern __shared__ uint8_t smem_raw[];
     static_assert(kHalf * BN * 4 <= kRingBytes, "a partial tile fits in the ring");
@@ -664,7 +804,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
     const int nrows = int(max(int64_t(0), min(int64_t(kHalf), p.rows - row0)));
     bool good = true;
     if (warp == 0) {
-        if (elect_one()) load_tiles<LAYOUT, BN>(p, s, w, rank);
+        if (elect_one()) load_tiles<LAYOUT, BN, MODE>(p, s, w, rank);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) multiply_tiles<LAYOUT, BN>(p, s, w, tmem);
@@ -693,21 +833,25 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
     // reached all the same
     __syncthreads();
     cluster_sync();
-    constexpr int kCols = BN / S, kLanes = kCols / 4, kRows = kLThreads / kLanes;   // threads a row, rows at a time
+    // gated: pair j finishes the j-th part of the gate's columns with the up projection's
+    constexpr int kTileCols = MODE == kLinGated ? BN / 2 : BN;
+    constexpr int kCols = kTileCols / S, kLanes = kCols / 4, kRows = kLThreads / kLanes;   // threads a row, rows at a time
     const int c = part * kCols + int(threadIdx.x) % kLanes * 4;
-    const int64_t col = int64_t(nt) * BN + c;
+    const int64_t col = int64_t(nt) * kTileCols + c;
     const int n = int(max(int64_t(0), min(int64_t(4), p.cols - col)));
     if (n > 0) {
         float bias[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) bias[i] = i < n ? lin::load_bias(p.e, col + i) : 0.0f;
+        [[maybe_unused]] float bias2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias2[i] = MODE == kLinGated && i < n ? lin::load_bias(p.e.bias2, p.e.bias_f32, col + i) : 0.0f;
         uint32_t base[S];
 #pragma unroll
         for (int j = 0; j < S; ++j) base[j] = mapa_shared(smem_u32(s.a0), uint32_t(2 * j + rank));
         for (int r = int(threadIdx.x) / kLanes; r < nrows; r += 4 * kRows) {
-            float v[4][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            // the sum of row r + k kRows, columns at .. at + 3, over the pairs in their order
+            auto sum = [&](int k, int at, float (&v)[4]) {
                 float4 q[S];
 #pragma unroll
                 for (int j = 0; j < S; ++j) {
@@ -715,14 +859,37 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
                     if (r + k * kRows < nrows)
                         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                                      : "=f"(q[j].x), "=f"(q[j].y), "=f"(q[j].z), "=f"(q[j].w)
-                                     : "r"(base[j] + partial_at<BN>(r + k * kRows, c / 4))
+                                     : "r"(base[j] + partial_at<BN>(r + k * kRows, at / 4))
                                      : "memory");
                 }
-                v[k][0] = q[0].x, v[k][1] = q[0].y, v[k][2] = q[0].z, v[k][3] = q[0].w;
+                v[0] = q[0].x, v[1] = q[0].y, v[2] = q[0].z, v[3] = q[0].w;
 #pragma unroll
-                for (int j = 1; j < S; ++j) v[k][0] += q[j].x, v[k][1] += q[j].y, v[k][2] += q[j].z, v[k][3] += q[j].w;
+                for (int j = 1; j < S; ++j) v[0] += q[j].x, v[1] += q[j].y, v[2] += q[j].z, v[3] += q[j].w;
+            };
+            float v[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum(k, c, v[k]);
+            if constexpr (MODE == kLinGated) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float u[4];
+                    sum(k, BN / 2 + c, u);
+                    if (r + k * kRows >= nrows) continue;
+                    const int64_t row = int64_t(row0) + r + k * kRows;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[k][i] += bias[i], u[i] += bias2[i];
+                    if (p.e.z) {
+                        put4(p.e.z, row * p.e.ldz + col, n, v[k]);
+                        put4(p.e.z2, row * p.e.ldz + col, n, u);
+                    }
+                    lin::apply_gate(v[k], u, p.e.act);
+                    put4(p.e.y, row * p.e.ldy + col, n, v[k]);
+                }
+            } else if constexpr (MODE == kLinGateGrad) {
+                finish4_gate_grad(p.e, v, int64_t(row0) + r, kRows, int64_t(row0) + nrows, col, n);
+            } else {
+                finish4(p.e, v, bias, int64_t(row0) + r, kRows, int64_t(row0) + nrows, col, n);
             }
-            finish4(p.e, v, bias, int64_t(row0) + r, kRows, int64_t(row0) + nrows, col, n);
         }
     }
     close_pair(s, tmem);   // with its cluster barrier the peers have read this CTA's partial tile
@@ -746,42 +913,65 @@ cudaError_t pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, unsi
 
 using PairKernel = void (*)(LinearPairParams);
 
-// By operand layout (0, 1, 3), tile columns and pairs of a cluster.
-PairKernel pair_kernel(int layout, int bn, int splits) {
-    static const PairKernel table[3][2][3] = {
-        {{cm_linear_pair_kernel<0, 256>, cm_linear_split_kernel<0, 256, 2>, cm_linear_split_kernel<0, 256, 4>},
-         {cm_linear_pair_kernel<0, 128>, cm_linear_split_kernel<0, 128, 2>, cm_linear_split_kernel<0, 128, 4>}},
-        {{cm_linear_pair_kernel<1, 256>, cm_linear_split_kernel<1, 256, 2>, cm_linear_split_kernel<1, 256, 4>},
-         {cm_linear_pair_kernel<1, 128>, cm_linear_split_kernel<1, 128, 2>, cm_linear_split_kernel<1, 128, 4>}},
-        {{cm_linear_pair_kernel<3, 256>, cm_linear_split_kernel<3, 256, 2>, cm_linear_split_kernel<3, 256, 4>},
-         {cm_linear_pair_kernel<3, 128>, cm_linear_split_kernel<3, 128, 2>, cm_linear_split_kernel<3, 128, 4>}}};
-    const int l = layout == 0 ? 0 : layout == 1 ? 1 : layout == 3 ? 2 : -1;
-    const int b = bn == 256 ? 0 : bn == 128 ? 1 : -1, sp = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : -1;
-    return l < 0 || b < 0 || sp < 0 ? nullptr : table[l][b][sp];
+// By operand layout (0, 1, 3; the gated modes have 0 and 1), tile columns (the
+// gated product has 256) and pairs of a cluster.
+template <int LAYOUT, int MODE>
+PairKernel pair_kernel_of(int bn, int splits) {
+    if (bn == 256)
+        return splits == 1   ? cm_linear_pair_kernel<LAYOUT, 256, MODE>
+               : splits == 2 ? cm_linear_split_kernel<LAYOUT, 256, 2, MODE>
+               : splits == 4 ? cm_linear_split_kernel<LAYOUT, 256, 4, MODE>
+                             : nullptr;
+    if constexpr (MODE != kLinGated) {
+        if (bn == 128)
+            return splits == 1   ? cm_linear_pair_kernel<LAYOUT, 128, MODE>
+                   : splits == 2 ? cm_linear_split_kernel<LAYOUT, 128, 2, MODE>
+                   : splits == 4 ? cm_linear_split_kernel<LAYOUT, 128, 4, MODE>
+                                 : nullptr;
+    }
+    return nullptr;
+}
+
+PairKernel pair_kernel(int layout, LinearMode mode, int bn, int splits) {
+    if (mode == kLinGated)
+        return layout == 0   ? pair_kernel_of<0, kLinGated>(bn, splits)
+               : layout == 1 ? pair_kernel_of<1, kLinGated>(bn, splits)
+                             : nullptr;
+    if (mode == kLinGateGrad)
+        return layout == 0   ? pair_kernel_of<0, kLinGateGrad>(bn, splits)
+               : layout == 1 ? pair_kernel_of<1, kLinGateGrad>(bn, splits)
+                             : nullptr;
+    return layout == 0   ? pair_kernel_of<0, kLinPlain>(bn, splits)
+           : layout == 1 ? pair_kernel_of<1, kLinPlain>(bn, splits)
+           : layout == 3 ? pair_kernel_of<3, kLinPlain>(bn, splits)
+                         : nullptr;
 }
 
 }  // namespace
 
 cudaError_t prepare_linear_pair(int sms, int *clusters) {
-    for (int layout : {0, 1, 3})
-        for (int bn : {256, 128})
-            for (int i = 0; i < 3; ++i) {
-                const int splits = 1 << i;
-                const PairKernel fn = pair_kernel(layout, bn, splits);
-                cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
-                if (e != cudaSuccess) return e;
-                if (layout != 0 || bn != 256) continue;
-                cudaLaunchConfig_t cfg;
-                cudaLaunchAttribute attr[1];
-                pair_config(cfg, attr, unsigned(2 * splits), unsigned(sms / (2 * splits) * (2 * splits)), nullptr);
-                e = cudaOccupancyMaxActiveClusters(&clusters[i], fn, &cfg);
-                if (e != cudaSuccess) return e;
-            }
+    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad})
+        for (int layout : {0, 1, 3})
+            for (int bn : {256, 128})
+                for (int i = 0; i < 3; ++i) {
+                    const int splits = 1 << i;
+                    const PairKernel fn = pair_kernel(layout, mode, bn, splits);
+                    if (!fn) continue;
+                    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
+                    if (e != cudaSuccess) return e;
+                    if (mode != kLinPlain || layout != 0 || bn != 256) continue;
+                    cudaLaunchConfig_t cfg;
+                    cudaLaunchAttribute attr[1];
+                    pair_config(cfg, attr, unsigned(2 * splits), unsigned(sms / (2 * splits) * (2 * splits)), nullptr);
+                    e = cudaOccupancyMaxActiveClusters(&clusters[i], fn, &cfg);
+                    if (e != cudaSuccess) return e;
+                }
     return cudaSuccess;
 }
 
-cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, int splits, int clusters, cudaStream_t stream) {
-    const PairKernel fn = pair_kernel(layout, p.bn, splits);
+cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode mode, int splits, int clusters,
+                               cudaStream_t stream) {
+    const PairKernel fn = pair_kernel(layout, mode, p.bn, splits);
     if (!fn) return cudaErrorInvalidValue;
     // split: one cluster a tile; else persistent
     const int n = splits > 1 ? p.tiles : std::max(1, std::min(clusters, p.tiles));

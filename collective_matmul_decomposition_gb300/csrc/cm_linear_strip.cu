@@ -153,7 +153,63 @@ __device__ __forceinline__ void finish(const LinearEpilogue &e, float (&v)[kBatc
     }
 }
 
-template <int LAYOUT>
+// The same for the gate's gradients: v is the gradient of act(g) u.
+__device__ __forceinline__ void finish_gate_grad(const LinearEpilogue &e, float (&v)[kBatch], int64_t row0, int64_t step,
+                                                 int64_t end, int64_t col) {
+    float g[kBatch], u[kBatch];
+    const int64_t in = row0 * e.ldzin + col;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const bool live = row0 + k * step < end;
+        g[k] = live ? __bfloat162float(static_cast<const __nv_bfloat16 *>(e.zin)[in + k * step * e.ldzin]) : 0.0f;
+        u[k] = live ? __bfloat162float(static_cast<const __nv_bfloat16 *>(e.zin2)[in + k * step * e.ldzin]) : 0.0f;
+    }
+    lin::gate_grad(v, g, u, e.act);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        if (row0 + k * step >= end) continue;
+        static_cast<__nv_bfloat16 *>(e.z)[(row0 + k * step) * e.ldz + col] = __float2bfloat16_rn(g[k]);
+        static_cast<__nv_bfloat16 *>(e.y)[(row0 + k * step) * e.ldy + col] = __float2bfloat16_rn(u[k]);
+    }
+}
+
+// The gated product of the rows t, t + step, ... below `end` of a tile: the partial
+// tiles of `splits` CTAs, [token][64 gate columns, 64 up columns], are summed in
+// rank order; a thread takes one column of every other of those rows.
+__device__ __forceinline__ void finish_gated(const LinearEpilogue &e, const float *part, int splits, int t0, int step, int end,
+                                             int64_t row0, int64_t col0, int64_t cols) {
+    constexpr int kPairs = 4;
+    const int j = int(threadIdx.x) & 63;
+    const int64_t col = col0 + j;
+    if (col >= cols) return;
+    const float bg = lin::load_bias(e.bias, e.bias_f32, col), bu = lin::load_bias(e.bias2, e.bias_f32, col);
+    for (int t = t0 + (int(threadIdx.x) >> 6) * step; t < end; t += 2 * kPairs * step) {
+        float g[kPairs], u[kPairs];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            const int at = (t + 2 * k * step) * kTileCols + j;
+            const bool live = t + 2 * k * step < end;
+            g[k] = u[k] = 0.0f;
+            if (!live) continue;
+            g[k] = (splits > 1 ? cluster_sum(smem_u32(part + at), splits) : part[at]) + bg;
+            u[k] = (splits > 1 ? cluster_sum(smem_u32(part + at + 64), splits) : part[at + 64]) + bu;
+        }
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            const int64_t row = row0 + t + 2 * k * step;
+            if (!e.z || t + 2 * k * step >= end) continue;
+            static_cast<__nv_bfloat16 *>(e.z)[row * e.ldz + col] = __float2bfloat16_rn(g[k]);
+            static_cast<__nv_bfloat16 *>(e.z2)[row * e.ldz + col] = __float2bfloat16_rn(u[k]);
+        }
+        lin::apply_gate(g, u, e.act);
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k)
+            if (t + 2 * k * step < end)
+                static_cast<__nv_bfloat16 *>(e.y)[(row0 + t + 2 * k * step) * e.ldy + col] = __float2bfloat16_rn(g[k]);
+    }
+}
+
+template <int LAYOUT, int MODE>
 __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid_constant__ LinearStripParams p) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     extern __shared__ uint8_t smem_raw[];
@@ -195,7 +251,11 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const int split = p.splits > 1 ? int(cluster_ctarank()) : 0;
     const int tile = int(blockIdx.x) / p.splits;
     const int ct = tile / p.row_tiles, rt = tile - ct * p.row_tiles;
-    const int col0 = ct * kTileCols, row0 = rt * p.tok;
+    constexpr bool kGated = MODE == kLinGated;
+    const int col0 = ct * (kGated ? kTileCols / 2 : kTileCols), row0 = rt * p.tok;
+    // gated: the tile's second 64 columns are the second operand's
+    const CUtensorMap *const second = kGated ? &p.tmA2 : &p.tmA;
+    const int col1 = kGated ? col0 : col0 + 64;
     const int kb0 = int(int64_t(p.kblocks) * split / p.splits), kb1 = int(int64_t(p.kblocks) * (split + 1) / p.splits);
     const uint32_t stage_bytes = uint32_t(kStripA + p.tok * kBK * 2);
 
@@ -205,9 +265,11 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     if (warp == 0 && elect_one())
         for (int kb = kb0; kb < min(kb1, kb0 + p.stages); ++kb) {
             if (A_MN) {
-                for (int j = 0; j < kTileCols / 64; ++j) tma_prefetch_3d(&p.tmA, col0 + 64 * j, kb * kBK, 0);
+                tma_prefetch_3d(&p.tmA, col0, kb * kBK, 0);
+                tma_prefetch_3d(second, col1, kb * kBK, 0);
             } else {
                 tma_prefetch_3d(&p.tmA, kb * kBK, col0, 0);
+                if (kGated) tma_prefetch_3d(second, kb * kBK, col1, 0);
             }
         }
     __syncwarp();
@@ -223,10 +285,11 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 uint8_t *sa = s.ring + uint32_t(stage) * stage_bytes, *sb = sa + kStripA;
                 mbar_expect_tx(&s.full[stage], stage_bytes);
                 if (A_MN) {
-                    for (int j = 0; j < kTileCols / 64; ++j)
-                        tma_load_3d(sa + j * (64 * kBK * 2), &p.tmA, &s.full[stage], col0 + 64 * j, kb * kBK, 0);
+                    tma_load_3d(sa, &p.tmA, &s.full[stage], col0, kb * kBK, 0);
+                    tma_load_3d(sa + 64 * kBK * 2, second, &s.full[stage], col1, kb * kBK, 0);
                 } else {
                     tma_load_3d(sa, &p.tmA, &s.full[stage], kb * kBK, col0, 0);
+                    if (kGated) tma_load_3d(sa + 64 * kBK * 2, second, &s.full[stage], kb * kBK, col1, 0);
                 }
                 if (B_MN) {
                     for (int j = 0; j < p.tok / 64; ++j)
@@ -287,8 +350,28 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const int nrows = int(min(int64_t(p.tok), p.rows - row0));
     const int64_t col = int64_t(col0) + threadIdx.x;
     const uint32_t taddr = tmem + (uint32_t(warp * 32) << 16);
-    const float bias = col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
-    if (p.splits == 1) {
+    const float bias = !kGated && col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
+    if (kGated && p.splits == 1) {
+        // gate and up columns lie in different threads' lanes: they meet in the ring,
+        // whose loads have all been multiplied, 128 tokens at a time
+        constexpr int kBlock = 128;
+        static_assert(kBlock * kTileCols * 4 <= kStripShared, "a block of tokens fits in the ring");
+        float *part = reinterpret_cast<float *>(s.ring);
+        for (int b = 0; b < nrows; b += kBlock) {
+            const int end = min(nrows - b, kBlock);
+            for (int t0 = 0; t0 < end; t0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(taddr + uint32_t(b + t0), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (t0 + i < end) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
+            }
+            __syncthreads();
+            if (good) finish_gated(p.e, part, 1, 0, 1, end, int64_t(row0) + b, col0, p.cols);
+            __syncthreads();
+        }
+    } else if (p.splits == 1) {
         for (int t0 = 0; t0 < nrows; t0 += 32) {
             uint32_t v[32];
             tmem_ld32(taddr + uint32_t(t0), v);
@@ -300,7 +383,10 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                         float f[kBatch];
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) f[k] = __uint_as_float(v[b + k]);
-                        finish(p.e, f, bias, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
+                        if constexpr (MODE == kLinGateGrad)
+                            finish_gate_grad(p.e, f, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
+                        else
+                            finish(p.e, f, bias, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
                     }
             }
         }
@@ -318,7 +404,9 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         }
         if (!good) *s.abort = 1;
         cluster_sync();
-        if (col < p.cols && good)
+        if (kGated) {
+            if (good) finish_gated(p.e, part, p.splits, split, p.splits, nrows, row0, col0, p.cols);
+        } else if (col < p.cols && good)
             for (int t = split; t < nrows; t += p.splits * kBatch) {
                 float f[kBatch];
 #pragma unroll
@@ -326,7 +414,10 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                     f[k] = t + k * p.splits < nrows
                                ? cluster_sum(smem_u32(part + (t + k * p.splits) * kTileCols + int(threadIdx.x)), p.splits)
                                : 0.0f;
-                finish(p.e, f, bias, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
+                if constexpr (MODE == kLinGateGrad)
+                    finish_gate_grad(p.e, f, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
+                else
+                    finish(p.e, f, bias, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
             }
         cluster_sync();   // the peers have read this CTA's partial tile
     }
@@ -339,6 +430,26 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     }
 }
 
+using StripKernel = void (*)(LinearStripParams);
+
+StripKernel strip_kernel(int layout, LinearMode mode) {
+    switch (mode) {
+        case kLinGated:
+            return layout == 0   ? cm_linear_strip_kernel<0, kLinGated>
+                   : layout == 2 ? cm_linear_strip_kernel<2, kLinGated>
+                                 : nullptr;
+        case kLinGateGrad:
+            return layout == 0   ? cm_linear_strip_kernel<0, kLinGateGrad>
+                   : layout == 2 ? cm_linear_strip_kernel<2, kLinGateGrad>
+                                 : nullptr;
+        default:
+            return layout == 0   ? cm_linear_strip_kernel<0, kLinPlain>
+                   : layout == 2 ? cm_linear_strip_kernel<2, kLinPlain>
+                   : layout == 3 ? cm_linear_strip_kernel<3, kLinPlain>
+                                 : nullptr;
+    }
+}
+
 }  // namespace
 
 int linear_strip_stages(int tok, int ring_bytes) {
@@ -346,11 +457,13 @@ int linear_strip_stages(int tok, int ring_bytes) {
 }
 
 cudaError_t prepare_linear_strip(int sms, int *clusters) {
-    void (*fns[3])(LinearStripParams) = {cm_linear_strip_kernel<0>, cm_linear_strip_kernel<2>, cm_linear_strip_kernel<3>};
-    for (auto fn : fns) {
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripAlone + 1024);
-        if (e != cudaSuccess) return e;
-    }
+    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad})
+        for (int layout : {0, 2, 3}) {
+            const StripKernel fn = strip_kernel(layout, mode);
+            if (!fn) continue;
+            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripAlone + 1024);
+            if (e != cudaSuccess) return e;
+        }
     for (int i = 2; i <= kStripMostSplits; ++i) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(sms / i * i));
@@ -362,20 +475,17 @@ cudaError_t prepare_linear_strip(int sms, int *clusters) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], fns[0], &cfg);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[i], strip_kernel(0, kLinPlain), &cfg);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, cudaStream_t stream) {
-    const int64_t col_tiles = (p.cols + kTileCols - 1) / kTileCols;
-    const int64_t grid = col_tiles * p.row_tiles * p.splits;
+cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, LinearMode mode, cudaStream_t stream) {
+    const int64_t tile_cols = mode == kLinGated ? kTileCols / 2 : kTileCols;
+    const int64_t grid = (p.cols + tile_cols - 1) / tile_cols * p.row_tiles * p.splits;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    void (*fn)(LinearStripParams) = layout == 0   ? cm_linear_strip_kernel<0>
-                                    : layout == 2 ? cm_linear_strip_kernel<2>
-                                    : layout == 3 ? cm_linear_strip_kernel<3>
-                                                  : nullptr;
+    const StripKernel fn = strip_kernel(layout, mode);
     if (!fn) return cudaErrorInvalidValue;
     return launch_after(fn, dim3(unsigned(grid)), kThreadsL, size_t(p.ring_bytes) + 1024, unsigned(p.splits), stream, p);
 }

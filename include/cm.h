@@ -634,6 +634,34 @@ cm_status cm_linear_dgrad(const void *dy, int64_t lddy, const void *w, int64_t l
                           cm_stream_t stream);
 
 /*
+ * cm_linear_gated -- the gated product in front of an MLP's down projection:
+ *   g = x Wg^T + bias_gate;  u = x Wu^T + bias_up;  y = act(g) u.
+ *  x [M][K]; w_gate, w_up [n][K] or [K][n] (`wlayout`), both of row stride ldw:
+ *  two matrices, or the halves of one [2n][K]; y [M][n] bf16.  bias_gate and
+ *  bias_up [n] (bias_dtype) are both given or both NULL, and so are z_gate and
+ *  z_up [M][n] bf16, both of row stride ldz, which receive g and u (rounded to
+ *  bf16) for the backward pass.  n at most 2^29.  Errors as cm_linear.
+ */
+cm_status cm_linear_gated(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw, cm_wlayout wlayout,
+                          const void *bias_gate, const void *bias_up, cm_dtype bias_dtype, cm_act act, void *z_gate,
+                          void *z_up, int64_t ldz, void *y, int64_t ldy, int64_t M, int64_t K, int64_t n,
+                          cm_stream_t stream);
+
+/*
+ * cm_linear_gated_dgrad -- back through the down projection and the gate: with
+ * d = dy W and the g and u that cm_linear_gated kept,
+ *   dz_gate = d u act'(g);  dz_up = d act(g).
+ *  dy [M][n], w [n][K] or [K][n] the down projection's; z_gate, z_up [M][K]
+ *  (row stride ldz); dz_gate, dz_up [M][K] bf16 (row stride lddz).  Where the
+ *  two lie side by side in one [M][2K] matrix, and the gate's and up
+ *  projection's weights one below the other, cm_linear_dgrad and
+ *  cm_linear_wgrad take both at once.  Errors as cm_linear.
+ */
+cm_status cm_linear_gated_dgrad(const void *dy, int64_t lddy, const void *w, int64_t ldw, cm_wlayout wlayout,
+                                const void *z_gate, const void *z_up, int64_t ldz, cm_act act, void *dz_gate, void *dz_up,
+                                int64_t lddz, int64_t M, int64_t K, int64_t n, cm_stream_t stream);
+
+/*
  * cm_linear_wgrad -- dw = dy^T x (laid out as the weight is, `wlayout`) and,
  * if db is not NULL, db = the sum of dy's rows; with `accumulate` both are
  * added to what is there.  x [M][K], dy [M][n] bf16; dw (dw_dtype); db [n]
