@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["cm_kernel.cu", "cm_kernel_pair.cu", "cm_api.cu", "cm_plan.cpp", "cm_noalloc.cu", "cm_cost.cpp", "cm_reduce.cu",
            "cm_linear_strip.cu", "cm_linear_pair.cu", "cm_linear_api.cu", "cm_norm.cu", "cm_norm_api.cu", "cm_adamw.cu",
-           "cm_embedding.cu"]
+           "cm_embedding.cu", "cm_head.cu"]
 HEADERS = ["cm_internal.h", "cm_kernel.cuh", "cm_device.cuh", "cm_kernel_common.cuh",
            "cm_linear.cuh", "cm_linear_epilogue.cuh", "cm_norm.cuh", "cm_vec.cuh", "cm_launch.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

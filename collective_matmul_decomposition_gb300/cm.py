@@ -51,7 +51,8 @@ EXPORTS = ["cm_plan", "cm_plan_destroy", "cm_plan_steps", "cm_plan_step", "cm_pl
            "cm_backward_pair_workspace_size", "cm_backward_pair",
            "cm_cannon_workspace_size", "cm_cannon_gemm", "cm_einsum_cost", "cm_plan_choose_einsum",
            "cm_linear", "cm_linear_dgrad", "cm_linear_gated", "cm_linear_gated_dgrad", "cm_linear_wgrad",
-           "cm_linear_wgrad_workspace_size",
+           "cm_linear_wgrad_workspace_size", "cm_linear_cross_entropy", "cm_linear_cross_entropy_workspace_size",
+           "cm_linear_cross_entropy_backward", "cm_linear_cross_entropy_backward_workspace_size",
            "cm_linear_choose", "cm_linear_check_status", "cm_layer_norm", "cm_layer_norm_backward",
            "cm_layer_norm_backward_workspace_size", "cm_adamw", "cm_embedding", "cm_embedding_backward",
            "cm_embedding_backward_workspace_size"]
@@ -171,6 +172,14 @@ def load():
     lib.cm_linear_wgrad.restype = i32
     lib.cm_linear_wgrad_workspace_size.argtypes = [i64, i64, i64]
     lib.cm_linear_wgrad_workspace_size.restype = sz
+    lib.cm_linear_cross_entropy.argtypes = [p, i64, p, i64, i32, p, i32, i64, i64, p, p, p, i64, i64, i64, p, sz, p]
+    lib.cm_linear_cross_entropy.restype = i32
+    lib.cm_linear_cross_entropy_backward.argtypes = [p, i64, p, i64, i32, p, i32, i64, i64, p, p, p, p, i32, i64, p, i32, i64,
+                                                     i32, i64, i64, i64, p, sz, p]
+    lib.cm_linear_cross_entropy_backward.restype = i32
+    for name in ("cm_linear_cross_entropy_workspace_size", "cm_linear_cross_entropy_backward_workspace_size"):
+        getattr(lib, name).argtypes = [i64, i64, i64]
+        getattr(lib, name).restype = sz
     lib.cm_linear_choose.argtypes = [i64, i64, i64, i32, ctypes.POINTER(cm_linear_tile)]
     lib.cm_linear_choose.restype = i32
     lib.cm_linear_check_status.argtypes = [p, ctypes.POINTER(i32)]
@@ -599,6 +608,64 @@ def cm_linear_wgrad(x, dy, dw, ws=None, db=None, accumulate: bool = False, w_lay
         raise CMError(st, "cm_linear_wgrad")
 
 
+def _index_vector(name, t, n, device):
+    """A contiguous vector of n token ids: (pointer, bits)."""
+    if t.dtype is not _i64 and t.dtype is not _i32:
+        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+    return _vector(name, t, n, device), 64 if t.dtype is _i64 else 32
+
+
+def linear_cross_entropy_workspace_size(M: int, K: int, n: int) -> int:
+    return load().cm_linear_cross_entropy_workspace_size(M, K, n)
+
+
+def cm_linear_cross_entropy(x, w, targets, loss, lse, ws, picked=None, first: int = 0, vocab=None, w_layout: str = "nk",
+                            stream=None):
+    """loss [M] = lse - picked of the logits x @ W^T, which are not kept (fp32; loss, lse and picked may each be None).
+    targets [M] int32 or int64; negative ones leave their row out.  w holds the ids first .. first + n - 1 of `vocab`
+    (None: first + n).  ws: linear_cross_entropy_workspace_size bytes."""
+    lib = _library()
+    M, K, dev = _extents("x", x)
+    layout = LAYOUTS[w_layout]
+    n = w.shape[layout != CM_W_NK]
+    xp, ldx = _matrix("x", x, (M, K), dev, _b16)
+    wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
+    tp, bits = _index_vector("targets", targets, M, dev)
+    wsp, ws_bytes = _workspace(ws, dev)
+    st = lib.cm_linear_cross_entropy(xp, ldx, wp, ldw, layout, tp, bits, first, first + n if vocab is None else vocab,
+                                     _vector("loss", loss, M, dev, _f32), _vector("lse", lse, M, dev, _f32),
+                                     _vector("picked", picked, M, dev, _f32), M, K, n, wsp, ws_bytes, _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear_cross_entropy")
+
+
+def linear_cross_entropy_backward_workspace_size(M: int, K: int, n: int) -> int:
+    return load().cm_linear_cross_entropy_backward_workspace_size(M, K, n)
+
+
+def cm_linear_cross_entropy_backward(x, w, targets, lse, dloss, ws, dx=None, dw=None, dlse=None, first: int = 0, vocab=None,
+                                     accumulate: bool = False, w_layout: str = "nk", stream=None):
+    """The gradients of sum(dloss * loss + dlse * lse): dx [M][K], and dw (+)= in the weight's layout (both optional).
+    lse [M] as the forward call wrote it, or joined over all slices; ws: linear_cross_entropy_backward_workspace_size."""
+    lib = _library()
+    M, K, dev = _extents("x", x)
+    layout = LAYOUTS[w_layout]
+    n = w.shape[layout != CM_W_NK]
+    xp, ldx = _matrix("x", x, (M, K), dev, _b16)
+    wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
+    dxp, lddx = _matrix("dx", dx, (M, K), dev) if dx is not None else (None, 0)
+    dwp, lddw = _matrix("dw", dw, (n, K) if layout == CM_W_NK else (K, n), dev) if dw is not None else (None, 0)
+    tp, bits = _index_vector("targets", targets, M, dev)
+    wsp, ws_bytes = _workspace(ws, dev)
+    st = lib.cm_linear_cross_entropy_backward(xp, ldx, wp, ldw, layout, tp, bits, first, first + n if vocab is None else vocab,
+                                              _vector("lse", lse, M, dev, _f32), _vector("dloss", dloss, M, dev, _f32),
+                                              _vector("dlse", dlse, M, dev, _f32), dxp, _dtype_of("dx", dx), lddx, dwp,
+                                              _dtype_of("dw", dw), lddw, 1 if accumulate else 0, M, K, n, wsp, ws_bytes,
+                                              _stream_of(stream, dev))
+    if st:
+        raise CMError(st, "cm_linear_cross_entropy_backward")
+
+
 def linear_choose(rows: int, cols: int, k: int, transposed: bool = False) -> cm_linear_tile:
     """The tile that the current device computes a rows x cols product of k terms in (transposed: a weight gradient's)."""
     tile = cm_linear_tile()
@@ -726,13 +793,6 @@ def cm_adamw(tensors: AdamWTensors, lr: float, beta1: float = 0.9, beta2: float 
                       _stream_of(stream, dev))
     if st:
         raise CMError(st, "cm_adamw")
-
-
-def _index_vector(name, t, n, device):
-    """A contiguous vector of n token ids: (pointer, bits)."""
-    if t.dtype is not _i64 and t.dtype is not _i32:
-        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
-    return _vector(name, t, n, device), 64 if t.dtype is _i64 else 32
 
 
 def cm_embedding(ids, w, y, scale: float = 1.0, first: int = 0, stream=None):

@@ -30,6 +30,7 @@ struct LinearEpilogue {
     const void *bias2;
     const void *zin2;   // bf16
     void *z2;           // bf16
+    const float *scale; // device: multiplies D first; NULL for 1
 };
 
 // What a kernel's epilogue computes.
@@ -39,7 +40,31 @@ struct LinearEpilogue {
 //              kept; y = act(g) u.
 //   kLinGateGrad  D is the gradient of such a y: z = D zin2 act'(zin), y = D act(zin)
 //              (zin = g, zin2 = u as they were kept; y is u's gradient, z is g's).
-enum LinearMode { kLinPlain = 0, kLinGated = 1, kLinGateGrad = 2 };
+//   kLinStats  D are logits: of each row and each half of a tile's columns the largest
+//              and the sum of exp(. - largest), and the target's logit (LinearHead).
+//   kLinSoftGrad  y = exp(D - lse) grad, less hit where the column is the target.
+enum LinearMode { kLinPlain = 0, kLinGated = 1, kLinGateGrad = 2, kLinStats = 3, kLinSoftGrad = 4 };
+
+// The loss over a vocabulary, by slots: the rows that have a target, in order.
+struct LinearHead {
+    const int32_t *target;   // column of the weights' slice, or kNotHere, kNoToken
+    const float *lse2;       // lse log2(e)
+    const float *grad, *hit;
+    float2 *stat;            // [part][stride]: {largest, sum}, two parts a tile of columns
+    float *picked;           // the target's logit, where it lies in the slice
+    int64_t stride;          // slots there may be
+    int64_t first;           // column of the slice that the product's first one is
+};
+constexpr int32_t kNotHere = -1, kNoToken = -2;   // of another slice; beyond the vocabulary
+
+// A product of the slots' rows: how many there are is known on the device only.
+struct LinearLive {
+    const int32_t *count;    // NULL: all rows
+    int skip;                // tiles of rows behind the last slot are left out (else they are computed as zeros)
+    int of_k;                // it limits the contracted extent, not the rows
+    int whole_is;            // where every row is a slot, tmWhole stands for tmA (1) or tmB (2)
+    int64_t whole;           // rows there are
+};
 
 // Device status of the linear kernels: {code, tile, CTA, site} of the first
 // bounded wait that expired since it was last read.
@@ -89,6 +114,9 @@ struct LinearPairParams {
     CUtensorMap tmZ;          // pre-activation kept (bf16 y only), 64 x 32
     CUtensorMap tmIn0, tmIn1; // residual (or y, to be added to) and pre-activation read; bf16 y only
     CUtensorMap tmB2, tmZ2;   // gated: the second column operand, and its z kept
+    CUtensorMap tmWhole;      // see LinearLive
+    LinearLive live;          // persistent kernels only
+    LinearHead head;
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks, mtiles, ntiles, tiles;
@@ -99,7 +127,8 @@ struct LinearPairParams {
 };
 
 // layout: bit 0 = B MN-major, bit 1 = A MN-major; the gated modes take 0 and 1, and
-// kLinGated tiles of 256 columns, half of them of each operand.  splits: 1 (persistent, on
+// kLinGated tiles of 256 columns, half of them of each operand; the head's modes have
+// 0 and 1, tiles of 256 columns and no splits.  splits: 1 (persistent, on
 // `clusters` pairs), or 2 or 4 pairs a cluster that share a tile's K slices,
 // one cluster a tile.  clusters[i]: clusters of 2^i pairs that run together.
 cudaError_t prepare_linear_pair(int sms, int *clusters);
@@ -111,5 +140,48 @@ cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode
 int64_t colsum_chunks(int64_t rows, int64_t cols);
 cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols, float *partial, void *out,
                           bool out_f32, bool accumulate, cudaStream_t stream);
+
+// Rows that have a target, gathered (cm_head.cu).  Slot j is the j-th of them.
+struct HeadRows {
+    const void *targets;
+    int target_bits;
+    int64_t first, n, vocab;     // the slice's ids, and how many there are in all
+    int64_t rows, K;
+    const void *x;               // bf16 [rows][ldx]
+    int64_t ldx;
+    void *xs;                    // the slots' rows, [rows][ldxs]; zeros behind the last up to a multiple of 64, or all
+    int64_t ldxs;
+    int always;                  // gather where every row is a slot too, and write zeros to all rows behind
+    int32_t *count;
+    int32_t *row_of;             // by slot (forward), NULL
+    int32_t *slot_of;            // by row (backward), -1 for none; NULL
+    int32_t *target;             // by slot
+    float *picked;               // by slot, zeroed (forward)
+    float *loss, *lse_out, *picked_out;   // by row, zeros for rows without a target (forward); may be NULL
+    const float *lse, *dloss, *dlse;      // by row (backward); dlse may be NULL
+    float *lse2, *grad, *hit, *scale;     // by slot, and one (backward)
+};
+cudaError_t launch_head_rows(const HeadRows &p, cudaStream_t stream);
+
+struct HeadJoin {
+    const float2 *stat;          // [parts][stride]
+    int64_t parts, stride;
+    const int32_t *count, *row_of, *target;
+    const float *picked;
+    float *loss, *lse, *picked_out;
+};
+cudaError_t launch_head_join(const HeadJoin &p, cudaStream_t stream);
+
+// dx[row] = scale sum[slot_of[row]], zeros for rows without a slot.
+struct HeadScatter {
+    const float *sum;            // [slot][ld], ld a multiple of 8
+    int64_t ld;
+    const int32_t *slot_of;
+    const float *scale;
+    void *dx;
+    int dx_f32;
+    int64_t lddx, rows, K;
+};
+cudaError_t launch_head_scatter(const HeadScatter &p, cudaStream_t stream);
 
 }  // namespace cm

@@ -216,11 +216,22 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
     return best;
 }
 
-// a2: the second column operand of a gated product, else NULL.
-cm_status product_pair(const Device &d, const Choice &c, LinearMode mode, const Operand &a, const Operand *a2, const Operand &b,
-                       int64_t rows, int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
+// What a product is beyond a plain one.
+struct Kind {
+    LinearMode mode = kLinPlain;
+    const Operand *a2 = nullptr;      // gated: the second column operand
+    LinearLive live = {};             // of the slots' rows
+    const Operand *whole = nullptr;   // what tmWhole maps
+    LinearHead head = {};
+};
+
+cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b, int64_t rows,
+                       int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
+    const LinearMode mode = kind.mode;
     LinearPairParams p;
     p.e = e;
+    p.live = kind.live;
+    p.head = kind.head;
     p.rows = rows;
     p.cols = cols;
     p.bn = c.bn;
@@ -234,7 +245,12 @@ cm_status product_pair(const Device &d, const Choice &c, LinearMode mode, const 
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
     if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, c.bn / 2) ||
-        (a2 && !map_operand(&p.tmB2, *a2, cols, k, c.bn / 2)) || !map_written(&p.tmY, e.y, rows, cols, e.ldy, e.y_f32 != 0))
+        (kind.a2 && !map_operand(&p.tmB2, *kind.a2, cols, k, c.bn / 2)) ||
+        (e.y && !map_written(&p.tmY, e.y, rows, cols, e.ldy, e.y_f32 != 0)))
+        return CM_ERR_CUDA;
+    // the row operand is A of a tile here (1), the column operand B (2)
+    if (kind.whole && !(kind.live.whole_is == 1 ? map_operand(&p.tmWhole, *kind.whole, rows, k, 128)
+                                                : map_operand(&p.tmWhole, *kind.whole, cols, k, c.bn / 2)))
         return CM_ERR_CUDA;
     if (mode == kLinGateGrad) {
         if (!map_written(&p.tmZ, e.z, rows, cols, e.ldz, false) || !map_rows(&p.tmIn0, e.zin2, rows, cols, e.ldzin, 32) ||
@@ -243,7 +259,7 @@ cm_status product_pair(const Device &d, const Choice &c, LinearMode mode, const 
     } else if (mode == kLinGated) {
         if (e.z && (!map_written(&p.tmZ, e.z, rows, cols, e.ldz, false) || !map_written(&p.tmZ2, e.z2, rows, cols, e.ldz, false)))
             return CM_ERR_CUDA;
-    } else if (!e.y_f32) {
+    } else if (mode == kLinPlain && !e.y_f32) {
         if (e.z && !map_written(&p.tmZ, e.z, rows, cols, e.ldz, false)) return CM_ERR_CUDA;
         if (e.accumulate && !map_rows(&p.tmIn0, e.y, rows, cols, e.ldy, 32)) return CM_ERR_CUDA;
         if (e.res && !map_rows(&p.tmIn0, e.res, rows, cols, e.ldr, 32)) return CM_ERR_CUDA;
@@ -253,12 +269,14 @@ cm_status product_pair(const Device &d, const Choice &c, LinearMode mode, const 
     return launch_linear_pair(p, layout, mode, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
-// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e; a2: see product_pair().
+// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e; all rows, no head.
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
-                  const LinearEpilogue &e, cudaStream_t stream, LinearMode mode = kLinPlain, const Operand *a2 = nullptr) {
+                  const LinearEpilogue &e, cudaStream_t stream, const Kind &kind = {}) {
+    const LinearMode mode = kind.mode;
+    const Operand *const a2 = kind.a2;
     const bool gated = mode == kLinGated;
     const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated);
-    if (c.pair) return product_pair(d, c, mode, a, a2, b, rows, cols, k, e, stream);
+    if (c.pair) return product_pair(d, c, kind, a, b, rows, cols, k, e, stream);
     LinearStripParams p;
     p.e = e;
     p.rows = rows;
@@ -276,6 +294,85 @@ cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t r
         return CM_ERR_CUDA;
     const int layout = (b.mn_major ? 1 : 0) | (a.mn_major ? 2 : 0);
     return launch_linear_strip(p, layout, mode, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+}
+
+// ---- the loss over a vocabulary -----------------------------------------------------
+// Pieces of a workspace, one behind the other, each on 256 bytes.
+struct Carve {
+    uint8_t *base;
+    size_t used = 0;
+    explicit Carve(void *p) : base(static_cast<uint8_t *>(p)) {}
+    template <typename T>
+    T *take(size_t n) {
+        T *const at = reinterpret_cast<T *>(base + used);
+        used += (n * sizeof(T) + 255) / 256 * 256;
+        return at;
+    }
+};
+
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+struct LossSpace {
+    int32_t *count, *row_of, *target;
+    float *picked;
+    uint16_t *xs;
+    float2 *stat;
+    int64_t parts;
+};
+LossSpace loss_space(Carve &c, int64_t M, int64_t K, int64_t n) {
+    LossSpace s;
+    s.parts = (n + 255) / 256 * 2;
+    s.count = c.take<int32_t>(1);
+    s.row_of = c.take<int32_t>(size_t(M));
+    s.target = c.take<int32_t>(size_t(M));
+    s.picked = c.take<float>(size_t(M));
+    s.xs = c.take<uint16_t>(size_t(M) * size_t(up8(K)));
+    s.stat = c.take<float2>(size_t(s.parts) * size_t(M));
+    return s;
+}
+
+// Columns of the vocabulary whose logits' gradients are there at a time: the
+// workspace holds them in bf16, 256 MB of them or 2048 columns.
+constexpr int64_t kLossGradBytes = int64_t(256) << 20;
+int64_t loss_grad_columns(int64_t M, int64_t n) {
+    const int64_t most = std::max<int64_t>(2048, kLossGradBytes / (2 * M) / 256 * 256);
+    if (n <= most) return n;
+    const int64_t chunks = (n + most - 1) / most;
+    return ((n + chunks - 1) / chunks + 255) / 256 * 256;
+}
+
+struct LossGradSpace {
+    int32_t *count, *slot_of, *target;
+    float *scale, *lse2, *grad, *hit, *sum;
+    uint16_t *xs, *p;
+    int64_t columns, ldp, lds;
+};
+LossGradSpace loss_grad_space(Carve &c, int64_t M, int64_t K, int64_t n) {
+    LossGradSpace s;
+    s.columns = loss_grad_columns(M, n);
+    s.ldp = up8(s.columns);
+    s.lds = up8(K);
+    s.count = c.take<int32_t>(1);
+    s.scale = c.take<float>(1);
+    s.slot_of = c.take<int32_t>(size_t(M));
+    s.target = c.take<int32_t>(size_t(M));
+    s.lse2 = c.take<float>(size_t(M));
+    s.grad = c.take<float>(size_t(M));
+    s.hit = c.take<float>(size_t(M));
+    s.xs = c.take<uint16_t>(size_t(M) * size_t(s.lds));
+    s.p = c.take<uint16_t>(size_t(M) * size_t(s.ldp));
+    s.sum = c.take<float>(size_t(M) * size_t(s.lds));
+    return s;
+}
+
+cm_status check_head(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout, const void *targets,
+                     int target_bits, int64_t first, int64_t vocab, int64_t K, int64_t n) {
+    if (!targets || first < 0 || first > kMaxExtent || vocab < first + n || vocab > 2 * kMaxExtent) return CM_ERR_INVALID_ARG;
+    const cm_status st = check_matrix(x, ldx, K);
+    if (st != CM_OK) return st;
+    const cm_status sw = check_matrix(w, ldw, wlayout == CM_W_NK ? K : n);
+    if (sw != CM_OK) return sw;
+    return (reinterpret_cast<uintptr_t>(targets) & (target_bits == 64 ? 7u : 3u)) != 0 ? CM_ERR_ALIGNMENT : CM_OK;
 }
 
 size_t wgrad_workspace(int64_t M, int64_t n) {
@@ -386,7 +483,10 @@ cm_status cm_linear_gated(const void *x, int64_t ldx, const void *w_gate, const 
     e.z2 = z_up;
     e.ldz = ldz;
     const Operand gate = {w_gate, ldw, wlayout == CM_W_KN}, up = {w_up, ldw, wlayout == CM_W_KN};
-    return product(d, gate, {x, ldx, false}, M, n, K, e, reinterpret_cast<cudaStream_t>(stream), kLinGated, &up);
+    Kind kind;
+    kind.mode = kLinGated;
+    kind.a2 = &up;
+    return product(d, gate, {x, ldx, false}, M, n, K, e, reinterpret_cast<cudaStream_t>(stream), kind);
 }
 
 cm_status cm_linear_gated_dgrad(const void *dy, int64_t lddy, const void *w, int64_t ldw, cm_wlayout wlayout,
@@ -411,8 +511,9 @@ cm_status cm_linear_gated_dgrad(const void *dy, int64_t lddy, const void *w, int
     e.zin = z_gate;
     e.zin2 = z_up;
     e.ldzin = ldz;
-    return product(d, {w, ldw, wlayout == CM_W_NK}, {dy, lddy, false}, M, K, n, e, reinterpret_cast<cudaStream_t>(stream),
-                   kLinGateGrad);
+    Kind kind;
+    kind.mode = kLinGateGrad;
+    return product(d, {w, ldw, wlayout == CM_W_NK}, {dy, lddy, false}, M, K, n, e, reinterpret_cast<cudaStream_t>(stream), kind);
 }
 
 size_t cm_linear_wgrad_workspace_size(int64_t M, int64_t K, int64_t n) {
@@ -458,6 +559,183 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
     e.accumulate = accumulate != 0;
     const Operand ox = {x, ldx, true}, ody = {dy, lddy, true};
     return nk ? product(d, ox, ody, n, K, M, e, stream) : product(d, ody, ox, K, n, M, e, stream);
+}
+
+size_t cm_linear_cross_entropy_workspace_size(int64_t M, int64_t K, int64_t n) {
+    if (check_extents(M, K, n) != CM_OK) return 0;
+    Carve c(nullptr);
+    loss_space(c, M, K, n);
+    return c.used;
+}
+
+cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout,
+                                  const void *targets, int target_bits, int64_t first, int64_t vocab, float *loss, float *lse,
+                                  float *picked, int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes,
+                                  cm_stream_t stream_) {
+    NvtxRange range("cm_linear_cross_entropy");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if ((wlayout != CM_W_KN && wlayout != CM_W_NK) || (target_bits != 32 && target_bits != 64)) return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    if (M == 0) return CM_OK;
+    CM_TRY(check_head(x, ldx, w, ldw, wlayout, targets, target_bits, first, vocab, K, n));
+    if (!ws || ws_bytes < cm_linear_cross_entropy_workspace_size(M, K, n)) return CM_ERR_WORKSPACE;
+    if (!aligned16(ws) || misaligned(loss, CM_F32) || misaligned(lse, CM_F32) || misaligned(picked, CM_F32)) return CM_ERR_ALIGNMENT;
+    Device d;
+    CM_TRY(device(&d));
+    Carve carve(ws);
+    const LossSpace s = loss_space(carve, M, K, n);
+    HeadRows r = {};
+    r.targets = targets;
+    r.target_bits = target_bits;
+    r.first = first;
+    r.n = n;
+    r.vocab = vocab;
+    r.rows = M;
+    r.K = K;
+    r.x = x;
+    r.ldx = ldx;
+    r.xs = s.xs;
+    r.ldxs = up8(K);
+    r.count = s.count;
+    r.row_of = s.row_of;
+    r.target = s.target;
+    r.picked = s.picked;
+    r.loss = loss;
+    r.lse_out = lse;
+    r.picked_out = picked;
+    if (launch_head_rows(r, stream) != cudaSuccess) return CM_ERR_CUDA;
+    const Operand rows = {s.xs, up8(K), false}, all = {x, ldx, false};
+    Kind kind;
+    kind.mode = kLinStats;
+    kind.live = {s.count, 1, 0, 1, M};
+    kind.whole = &all;
+    kind.head.target = s.target;
+    kind.head.stat = s.stat;
+    kind.head.picked = s.picked;
+    kind.head.stride = M;
+    Choice c;
+    c.pair = true;
+    CM_TRY(product_pair(d, c, kind, {w, ldw, wlayout == CM_W_KN}, rows, M, n, K, {}, stream));
+    const HeadJoin j = {s.stat, s.parts, M, s.count, s.row_of, s.target, s.picked, loss, lse, picked};
+    return launch_head_join(j, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+}
+
+size_t cm_linear_cross_entropy_backward_workspace_size(int64_t M, int64_t K, int64_t n) {
+    if (check_extents(M, K, n) != CM_OK) return 0;
+    if (M == 0) return 256;
+    Carve c(nullptr);
+    loss_grad_space(c, M, K, n);
+    return c.used;
+}
+
+cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout,
+                                           const void *targets, int target_bits, int64_t first, int64_t vocab,
+                                           const float *lse, const float *dloss, const float *dlse, void *dx,
+                                           cm_dtype dx_dtype, int64_t lddx, void *dw, cm_dtype dw_dtype, int64_t lddw,
+                                           int accumulate, int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes,
+                                           cm_stream_t stream_) {
+    NvtxRange range("cm_linear_cross_entropy_backward");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if ((wlayout != CM_W_KN && wlayout != CM_W_NK) || (target_bits != 32 && target_bits != 64) || (dx && bad_dtype(dx_dtype)) ||
+        (dw && bad_dtype(dw_dtype)))
+        return CM_ERR_INVALID_ARG;
+    CM_TRY(check_extents(M, K, n));
+    const bool nk = wlayout == CM_W_NK;
+    if (dw) CM_TRY(check_matrix(dw, lddw, nk ? K : n));
+    if (M == 0) {   // the sum over no rows
+        const size_t es = dw_dtype == CM_F32 ? 4 : 2;
+        if (dw && !accumulate && cudaMemset2DAsync(dw, size_t(lddw) * es, 0, size_t(nk ? K : n) * es, size_t(nk ? n : K), stream) != cudaSuccess)
+            return CM_ERR_CUDA;
+        return CM_OK;
+    }
+    if (!lse || !dloss) return CM_ERR_INVALID_ARG;
+    CM_TRY(check_head(x, ldx, w, ldw, wlayout, targets, target_bits, first, vocab, K, n));
+    if (dx) CM_TRY(check_matrix(dx, lddx, K));
+    if (!ws || ws_bytes < cm_linear_cross_entropy_backward_workspace_size(M, K, n)) return CM_ERR_WORKSPACE;
+    if (!aligned16(ws) || misaligned(lse, CM_F32) || misaligned(dloss, CM_F32) || misaligned(dlse, CM_F32)) return CM_ERR_ALIGNMENT;
+    if (!dx && !dw) return CM_OK;
+    Device d;
+    CM_TRY(device(&d));
+    Carve carve(ws);
+    const LossGradSpace s = loss_grad_space(carve, M, K, n);
+    // the two products behind a chunk's logits; tiles that are split, and strips, take all rows
+    const Choice cx = choose(d, M, K, s.columns, false), cw = choose(d, nk ? s.columns : K, nk ? K : s.columns, M, true);
+    const bool counted = (!dx || (cx.pair && cx.splits == 1)) && (!dw || (cw.pair && cw.splits == 1));
+    HeadRows r = {};
+    r.targets = targets;
+    r.target_bits = target_bits;
+    r.first = first;
+    r.n = n;
+    r.vocab = vocab;
+    r.rows = M;
+    r.K = K;
+    r.x = x;
+    r.ldx = ldx;
+    r.xs = s.xs;
+    r.ldxs = s.lds;
+    r.always = !counted;
+    r.count = s.count;
+    r.slot_of = s.slot_of;
+    r.target = s.target;
+    r.lse = lse;
+    r.dloss = dloss;
+    r.dlse = dlse;
+    r.lse2 = s.lse2;
+    r.grad = s.grad;
+    r.hit = s.hit;
+    r.scale = s.scale;
+    if (launch_head_rows(r, stream) != cudaSuccess) return CM_ERR_CUDA;
+    const Operand rows = {s.xs, s.lds, false}, rows_t = {s.xs, s.lds, true}, all = {x, ldx, false}, all_t = {x, ldx, true};
+    for (int64_t c0 = 0; c0 < n; c0 += s.columns) {
+        const int64_t cols = std::min(s.columns, n - c0);
+        const void *const wc = static_cast<const uint16_t *>(w) + (nk ? c0 * ldw : c0);
+        Kind kind;
+        kind.mode = kLinSoftGrad;
+        kind.live = {s.count, counted ? 1 : 0, 0, counted ? 1 : 0, M};
+        kind.whole = counted ? &all : nullptr;
+        kind.head.target = s.target;
+        kind.head.lse2 = s.lse2;
+        kind.head.grad = s.grad;
+        kind.head.hit = s.hit;
+        kind.head.first = c0;
+        Choice c;
+        c.pair = true;
+        LinearEpilogue e = {};
+        e.y = s.p;
+        e.ldy = s.ldp;
+        CM_TRY(product_pair(d, c, kind, {wc, ldw, !nk}, rows, M, cols, K, e, stream));
+        if (dx) {
+            e = {};
+            e.y = s.sum;
+            e.ldy = s.lds;
+            e.y_f32 = 1;
+            e.accumulate = c0 > 0;
+            const Operand a = {wc, ldw, nk}, b = {s.p, s.ldp, false};
+            Kind plain;
+            if (counted) plain.live = {s.count, 1, 0, 0, M};
+            CM_TRY(counted ? product_pair(d, cx, plain, a, b, M, K, cols, e, stream) : product(d, a, b, M, K, cols, e, stream));
+        }
+        if (dw) {
+            e = {};
+            e.y = static_cast<uint8_t *>(dw) + (nk ? c0 * lddw : c0) * (dw_dtype == CM_F32 ? 4 : 2);
+            e.ldy = lddw;
+            e.y_f32 = dw_dtype == CM_F32;
+            e.accumulate = accumulate != 0;
+            e.scale = s.scale;
+            const Operand pt = {s.p, s.ldp, true};
+            Kind plain;
+            if (counted) {
+                plain.live = {s.count, 0, 1, nk ? 2 : 1, M};
+                plain.whole = &all_t;
+            }
+            const int64_t dr = nk ? cols : K, dc = nk ? K : cols;
+            const Operand &a = nk ? rows_t : pt, &b = nk ? pt : rows_t;
+            CM_TRY(counted ? product_pair(d, cw, plain, a, b, dr, dc, M, e, stream) : product(d, a, b, dr, dc, M, e, stream));
+        }
+    }
+    if (!dx) return CM_OK;
+    const HeadScatter g = {s.sum, s.lds, s.slot_of, s.scale, dx, dx_dtype == CM_F32, lddx, M, K};
+    return launch_head_scatter(g, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
 cm_status cm_linear_choose(int64_t rows, int64_t cols, int64_t k, int transposed, cm_linear_tile *tile) {

@@ -100,21 +100,48 @@ __device__ void drain_p(const LinearPairParams &p, uint64_t *bar, uint32_t parit
         if (globaltimer() - t0 > p.timeout_ns) break;
 }
 
-__device__ __forceinline__ void tile_at(const LinearPairParams &p, int t, int &mt, int &nt) {
+__device__ __forceinline__ void tile_at(const LinearPairParams &p, int mtiles, int t, int &mt, int &nt) {
     const int per_band = p.band * p.ntiles;
     const int b = t / per_band;
-    const int rows = min(p.band, p.mtiles - b * p.band);
+    const int rows = min(p.band, mtiles - b * p.band);
     const int u = t - b * per_band;
     nt = u / rows;
     mt = b * p.band + (u - nt * rows);
 }
 
 // The tiles and K slices of a CTA's pair: first, first + step, ... below
-// p.tiles, each over slices kb0 .. kb1 - 1.  `leader` is the pair's even CTA.
+// `tiles`, each over slices kb0 .. kb1 - 1.  `leader` is the pair's even CTA.
 struct Share {
     int first, step, kb0, kb1;
     uint32_t leader;
+    int tiles, mtiles;
+    int64_t rows;
+    const CUtensorMap *a, *b;   // the operands' maps
 };
+
+// A persistent kernel's share, cut down to the slots where they are counted.
+template <int MODE>
+__device__ __forceinline__ Share share_of(const LinearPairParams &p, int rank) {
+    // gated: the pair's even CTA stages the gate's columns, the odd one the up projection's,
+    // so that half of each CTA's accumulator columns belong to either
+    Share w = {int(blockIdx.x) >> 1, int(gridDim.x) >> 1, 0, p.kblocks, 0u, p.tiles, p.mtiles, p.rows, &p.tmA,
+               MODE == kLinGated && rank ? &p.tmB2 : &p.tmB};
+    if (MODE != kLinGated && MODE != kLinGateGrad && p.live.count) {
+        const int n = *p.live.count;
+        // where there is none, one slice or one row of tiles is computed all the same:
+        // the slots behind the last are zeros
+        if (p.live.of_k) {
+            w.kb1 = max(1, min(p.kblocks, (n + kBK - 1) / kBK));
+        } else {
+            w.rows = n;
+            if (p.live.skip) w.mtiles = max(1, (n + kTile - 1) / kTile);
+            w.tiles = w.mtiles * p.ntiles;
+        }
+        if (n == p.live.whole && p.live.whole_is == 1) w.a = &p.tmWhole;
+        if (n == p.live.whole && p.live.whole_is == 2) w.b = &p.tmWhole;
+    }
+    return w;
+}
 
 template <int LAYOUT, int BN, int MODE>
 __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, int rank) {
@@ -122,16 +149,13 @@ __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Shar
     constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
     const uint32_t full_leader = mapa_shared(smem_u32(s.full), w.leader);
     const uint32_t a0 = smem_u32(s.a0), b0 = smem_u32(s.b0);
-    // gated: the pair's even CTA stages the gate's columns, the odd one the up projection's,
-    // so that half of each CTA's accumulator columns belong to either
-    const uint64_t tma = reinterpret_cast<uint64_t>(&p.tmA);
-    const uint64_t tmb = reinterpret_cast<uint64_t>(MODE == kLinGated && rank ? &p.tmB2 : &p.tmB);
+    const uint64_t tma = reinterpret_cast<uint64_t>(w.a), tmb = reinterpret_cast<uint64_t>(w.b);
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (int t = w.first; t < p.tiles && ok; t += w.step) {
+    for (int t = w.first; t < w.tiles && ok; t += w.step) {
         int mt, nt;
-        tile_at(p, t, mt, nt);
+        tile_at(p, w.mtiles, t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf, col0 = MODE == kLinGated ? nt * (BN / 2) : nt * BN + rank * (BN / 2);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
             if (!mbar_try_wait(s.empty + stage, phase ^ 1u) &&
@@ -182,7 +206,7 @@ __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, const 
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     const uint16_t both = uint16_t(3u << w.leader);   // the pair's CTAs
-    for (int t = w.first; t < p.tiles && ok; t += w.step) {
+    for (int t = w.first; t < w.tiles && ok; t += w.step) {
         if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * BN);
@@ -269,7 +293,7 @@ __device__ __noinline__ void store_rest(const LinearPairParams &p, uint8_t *buf0
 
 // F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).  MODE: kLinPlain or kLinGateGrad.
 template <bool F32, int BN, int MODE>
-__device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t tmem, int rank) {
+__device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int kChunk = F32 ? 32 : 64, kCols = BN / 2;   // columns of a warp
     const LinearEpilogue &e = p.e;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
@@ -296,11 +320,11 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
     uint32_t acc_phase = 0, in_phase = 0;
     bool pending = false;   // inputs asked for and not yet waited for
     bool ok = true;
-    for (int t = int(blockIdx.x) >> 1; t < p.tiles && ok; t += int(gridDim.x) >> 1) {
+    for (int t = w.first; t < w.tiles && ok; t += w.step) {
         int mt, nt;
-        tile_at(p, t, mt, nt);
+        tile_at(p, w.mtiles, t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf + quad * 32, cbase = nt * BN + half * kCols;
-        const int nch = row0 < p.rows && cbase < p.cols ? min(kCols, int(min(p.cols - cbase, int64_t(kCols))) + kChunk - 1) / kChunk : 0;
+        const int nch = row0 < w.rows && cbase < p.cols ? min(kCols, int(min(p.cols - cbase, int64_t(kCols))) + kChunk - 1) / kChunk : 0;
         float bias[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -357,6 +381,11 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
                 float f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                if (!kGate && e.scale) {
+                    const float scale = *e.scale;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] *= scale;
+                }
                 if constexpr (kGate) {
                     float g[32], u[32];
 #pragma unroll
@@ -405,7 +434,7 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, uint32_t
                 } else {
                     const int64_t row = int64_t(row0) + lane;
                     const int col = cbase + ch * kChunk;
-                    const bool live = row < p.rows;
+                    const bool live = row < w.rows;
                     auto at = [&](const void *m, int64_t ld, int i) {
                         return live && col + i < p.cols
                                    ? __bfloat162float(static_cast<const __nv_bfloat16 *>(m)[row * ld + col + i])
@@ -482,7 +511,7 @@ __device__ __noinline__ void store_tail(uint8_t *buf, void *m, int64_t ld, int64
 // accumulator again, which costs less than holding 128 columns in registers.
 // Bound by the tensor cores where the products are long (4096 x 8192 x 28672 with both
 // z kept), by the epilogue below some 16 K slices a tile.
-__device__ void finish_gated(const LinearPairParams &p, const LSmem &s, uint32_t tmem, int rank) {
+__device__ void finish_gated(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = 64;
     const LinearEpilogue &e = p.e;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
@@ -495,9 +524,9 @@ __device__ void finish_gated(const LinearPairParams &p, const LSmem &s, uint32_t
     const int outs = e.z ? 3 : 1;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = int(blockIdx.x) >> 1; t < p.tiles; t += int(gridDim.x) >> 1) {
+    for (int t = w.first; t < w.tiles; t += w.step) {
         int mt, nt;
-        tile_at(p, t, mt, nt);
+        tile_at(p, w.mtiles, t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf + quad * 32, c0 = nt * (BN / 2) + half * kCols;
         const bool live = row0 < p.rows && c0 < p.cols;
         float bg[2], bu[2];   // the columns' biases lie one to a lane
@@ -552,6 +581,153 @@ __device__ void finish_gated(const LinearPairParams &p, const LSmem &s, uint32_t
                 bulk_commit();
             }
             buf = buf == bufs ? bufs + kEpiBuf : bufs;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
+        if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+        }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+}
+
+// The statistics of a softmax over the columns, without the logits: a thread owns one
+// row and half of the tile's columns, and goes through them 32 at a time with the
+// running maximum m and sum s of exp2(v log2(e) - m), all in fp32:
+//   m' = max(m, max v);  s' = s exp2(m - m') + sum exp2(v - m').
+// What is not a column counts as -infinity.  A NaN stays one through the sum.
+__device__ void finish_stats(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+    constexpr int BN = 256, kCols = BN / 2;
+    const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
+    const int quad = ew & 3, half = ew >> 2;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = w.first; t < w.tiles; t += w.step) {
+        int mt, nt;
+        tile_at(p, w.mtiles, t, mt, nt);
+        const int row0 = mt * kTile + rank * kHalf + quad * 32, row = row0 + lane;
+        const int64_t c0 = int64_t(nt) * BN + half * kCols;
+        // the target's place among the warp's columns; -1 if it is not there
+        const int64_t target = row < w.rows ? p.head.target[row] : kNotHere, left = target - p.head.first - c0;
+        const int at = target >= 0 && left >= 0 && left < kCols ? int(left) : -1;
+        bool ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
+        float m = -INFINITY, sum = 0.0f, picked = 0.0f;
+        if (row0 < w.rows) {
+#pragma unroll 1
+            for (int c = 0; c < kCols && c0 + c < p.cols; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(taddr + uint32_t(c), v);
+                tmem_wait_ld_regs(v);
+                float f[32];
+                const int n = int(min(int64_t(32), p.cols - c0 - c));
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                if (__any_sync(0xffffffffu, at >= c && at < c + 32)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) picked = at == c + i ? f[i] : picked;
+                }
+                if (n < 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = i < n ? f[i] : -INFINITY;
+                }
+                float top = f[0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) top = fmaxf(top, f[i]);
+                const float next = fmaxf(m, top * lin::kLog2e);
+                const float base = next == -INFINITY ? 0.0f : next;   // no number yet: exp2(-inf - 0) is 0
+                sum *= lin::exp2_fast(m - base);
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part[i & 3] += lin::exp2_fast(fmaf(f[i], lin::kLog2e, -base));
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                m = next;
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
+        if (row < w.rows) {
+            p.head.stat[(int64_t(nt) * 2 + half) * p.head.stride + row] = make_float2(m, sum);
+            if (at >= 0 && c0 + at < p.cols) p.head.picked[row] = picked;
+        }
+        if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+        }
+    }
+    __syncwarp();
+}
+
+// The gradient of the logits, bf16: exp(D - lse) grad, less hit in the target's column.
+// Rows behind the last slot are zeros up to the tile's end.
+__device__ void finish_softgrad(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+    constexpr int BN = 256, kCols = BN / 2, kChunk = 64;
+    const LinearEpilogue &e = p.e;
+    const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
+    const int quad = ew & 3, half = ew >> 2;
+    uint8_t *const bufs = s.epi + ew * 2 * kEpiBuf;
+    uint8_t *buf = bufs;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    const int rest = int(p.cols % 8);
+    const int64_t whole = p.cols - rest;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = w.first; t < w.tiles; t += w.step) {
+        int mt, nt;
+        tile_at(p, w.mtiles, t, mt, nt);
+        const int row0 = mt * kTile + rank * kHalf + quad * 32, row = row0 + lane;
+        const int cbase = nt * BN + half * kCols;
+        const bool slot = row < w.rows;
+        const float lse2 = slot ? p.head.lse2[row] : 0.0f, grad = slot ? p.head.grad[row] : 0.0f;
+        const float hit = slot ? p.head.hit[row] : 0.0f;
+        const int64_t target = slot ? p.head.target[row] : kNotHere, left = target - p.head.first - cbase;
+        const int at = target >= 0 && left >= 0 && left < kCols ? int(left) : -1;
+        bool ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
+        if (row0 < p.rows) {
+#pragma unroll 1
+            for (int c = 0; c < kCols && cbase + c < p.cols; c += kChunk) {
+                if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has been read out
+                __syncwarp();
+                const int c0 = cbase + c;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+                    tmem_ld32(taddr + uint32_t(c + 32 * h), v);
+                    tmem_wait_ld_regs(v);
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        f[i] = slot ? lin::exp2_fast(fmaf(__uint_as_float(v[i]), lin::kLog2e, -lse2)) * grad : 0.0f;
+                    const int here = at - c - 32 * h;
+                    if (__any_sync(0xffffffffu, at >= 0 && here >= 0 && here < 32)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] -= at >= 0 && here == i ? hit : 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) *piece(buf, lane, h * 4 + j) = pack8(f + 8 * j);
+                }
+                if (rest && c0 + kChunk > whole && row < p.rows)
+                    store_tail(buf, e.y, e.ldy, row, whole, int(whole - c0), rest, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (c0 < whole) tma_store_3d(&p.tmY, buf, c0, row0, 0);
+                    bulk_commit();
+                }
+                buf = buf == bufs ? bufs + kEpiBuf : bufs;
+            }
         }
         tc_fence_before();
         __syncwarp();
@@ -640,7 +816,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     LSmem s;
     const uint32_t tmem = open_pair<BN>(p, s, smem_raw);
     const int warp = int(threadIdx.x) >> 5, rank = int(cluster_ctarank());
-    const Share w = {int(blockIdx.x) >> 1, int(gridDim.x) >> 1, 0, p.kblocks, 0u};
+    const Share w = share_of<MODE>(p, rank);
     if (warp == 0) {
         if (elect_one()) load_tiles<LAYOUT, BN, MODE>(p, s, w, rank);
         __syncwarp();
@@ -649,11 +825,15 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
         __syncwarp();
     } else if (warp >= 4) {
         if constexpr (MODE == kLinGated)
-            finish_gated(p, s, tmem, rank);
+            finish_gated(p, s, w, tmem, rank);
+        else if constexpr (MODE == kLinStats)
+            finish_stats(p, s, w, tmem, rank);
+        else if constexpr (MODE == kLinSoftGrad)
+            finish_softgrad(p, s, w, tmem, rank);
         else if (MODE == kLinPlain && p.e.y_f32)
-            finish_tiles<true, BN, kLinPlain>(p, s, tmem, rank);
+            finish_tiles<true, BN, kLinPlain>(p, s, w, tmem, rank);
         else
-            finish_tiles<false, BN, MODE>(p, s, tmem, rank);
+            finish_tiles<false, BN, MODE>(p, s, w, tmem, rank);
     }
     close_pair(s, tmem);
 }
@@ -697,6 +877,13 @@ __device__ __forceinline__ void put4(void *m, int64_t at, int n, const float (&f
 __device__ __forceinline__ void finish4(const LinearEpilogue &e, float (&v)[4][4], const float (&bias)[4], int64_t row,
                                         int64_t step, int64_t end, int64_t col, int n) {
     float in[4][4];
+    if (e.scale) {
+        const float scale = *e.scale;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[k][i] *= scale;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -797,9 +984,9 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
     const int crank = int(cluster_ctarank()), rank = crank & 1, part = crank >> 1;
     const int tile = int(blockIdx.x) / (2 * S);
     const Share w = {tile, p.tiles, int(int64_t(p.kblocks) * part / S), int(int64_t(p.kblocks) * (part + 1) / S),
-                     uint32_t(crank & ~1)};
+                     uint32_t(crank & ~1), p.tiles, p.mtiles, p.rows, &p.tmA, MODE == kLinGated && rank ? &p.tmB2 : &p.tmB};
     int mt, nt;
-    tile_at(p, tile, mt, nt);
+    tile_at(p, p.mtiles, tile, mt, nt);
     const int row0 = mt * kTile + rank * kHalf;
     const int nrows = int(max(int64_t(0), min(int64_t(kHalf), p.rows - row0)));
     bool good = true;
@@ -917,12 +1104,14 @@ using PairKernel = void (*)(LinearPairParams);
 // gated product has 256) and pairs of a cluster.
 template <int LAYOUT, int MODE>
 PairKernel pair_kernel_of(int bn, int splits) {
-    if (bn == 256)
+    if constexpr (MODE == kLinStats || MODE == kLinSoftGrad)
+        return bn == 256 && splits == 1 ? cm_linear_pair_kernel<LAYOUT, 256, MODE> : nullptr;
+    else if (bn == 256)
         return splits == 1   ? cm_linear_pair_kernel<LAYOUT, 256, MODE>
                : splits == 2 ? cm_linear_split_kernel<LAYOUT, 256, 2, MODE>
                : splits == 4 ? cm_linear_split_kernel<LAYOUT, 256, 4, MODE>
                              : nullptr;
-    if constexpr (MODE != kLinGated) {
+    if constexpr (MODE == kLinPlain || MODE == kLinGateGrad) {
         if (bn == 128)
             return splits == 1   ? cm_linear_pair_kernel<LAYOUT, 128, MODE>
                    : splits == 2 ? cm_linear_split_kernel<LAYOUT, 128, 2, MODE>
@@ -933,14 +1122,14 @@ PairKernel pair_kernel_of(int bn, int splits) {
 }
 
 PairKernel pair_kernel(int layout, LinearMode mode, int bn, int splits) {
-    if (mode == kLinGated)
-        return layout == 0   ? pair_kernel_of<0, kLinGated>(bn, splits)
-               : layout == 1 ? pair_kernel_of<1, kLinGated>(bn, splits)
-                             : nullptr;
-    if (mode == kLinGateGrad)
-        return layout == 0   ? pair_kernel_of<0, kLinGateGrad>(bn, splits)
-               : layout == 1 ? pair_kernel_of<1, kLinGateGrad>(bn, splits)
-                             : nullptr;
+    const auto two = [&](PairKernel nk, PairKernel kn) { return layout == 0 ? nk : layout == 1 ? kn : nullptr; };
+    switch (mode) {
+        case kLinGated: return two(pair_kernel_of<0, kLinGated>(bn, splits), pair_kernel_of<1, kLinGated>(bn, splits));
+        case kLinGateGrad: return two(pair_kernel_of<0, kLinGateGrad>(bn, splits), pair_kernel_of<1, kLinGateGrad>(bn, splits));
+        case kLinStats: return two(pair_kernel_of<0, kLinStats>(bn, splits), pair_kernel_of<1, kLinStats>(bn, splits));
+        case kLinSoftGrad: return two(pair_kernel_of<0, kLinSoftGrad>(bn, splits), pair_kernel_of<1, kLinSoftGrad>(bn, splits));
+        default: break;
+    }
     return layout == 0   ? pair_kernel_of<0, kLinPlain>(bn, splits)
            : layout == 1 ? pair_kernel_of<1, kLinPlain>(bn, splits)
            : layout == 3 ? pair_kernel_of<3, kLinPlain>(bn, splits)
@@ -950,7 +1139,7 @@ PairKernel pair_kernel(int layout, LinearMode mode, int bn, int splits) {
 }  // namespace
 
 cudaError_t prepare_linear_pair(int sms, int *clusters) {
-    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad})
+    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad, kLinStats, kLinSoftGrad})
         for (int layout : {0, 1, 3})
             for (int bn : {256, 128})
                 for (int i = 0; i < 3; ++i) {

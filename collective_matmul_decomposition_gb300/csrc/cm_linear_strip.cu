@@ -105,6 +105,11 @@ constexpr int kBatch = 8;
 __device__ __forceinline__ void finish(const LinearEpilogue &e, float (&v)[kBatch], float bias, int64_t row0, int64_t step,
                                        int64_t end, int64_t col) {
     float in[kBatch];
+    if (e.scale) {
+        const float scale = *e.scale;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] *= scale;
+    }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) v[k] += bias;
     if (e.z) {

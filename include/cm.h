@@ -676,6 +676,50 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
                           int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes, cm_stream_t stream);
 
 /*
+ * cm_linear_cross_entropy -- the loss of each of M rows over a vocabulary, or of
+ * a rank's slice of one, whose logits z = x W^T are never written:
+ *   lse = log sum_v exp(z_v);  picked = z_t, t the row's target;  loss = lse - picked.
+ *  x [M][K] bf16; w [n][K] or [K][n] (`wlayout`) bf16, the rows (columns) of ids
+ *  first .. first + n - 1 of a vocabulary of `vocab` ids; targets [M] int32 or
+ *  int64 (target_bits 32 or 64).  loss, lse, picked [M] fp32, each may be NULL.
+ *  A negative target leaves its row out: its outputs are 0, and x is not used
+ *  there.  Where a target lies outside of the slice, picked is 0: over ranks that
+ *  hold a slice each, log sum_ranks exp(lse) less the sum of picked is the loss of
+ *  the whole.  A target of `vocab` or more has a NaN loss.  Products, maxima and
+ *  sums are fp32.  first at most 2^30, vocab at least first + n and at most 2^31.
+ *  ws: cm_linear_cross_entropy_workspace_size(M, K, n) bytes, 16-byte aligned; no
+ *  initialisation; calls that share it must be ordered on the GPU.  Results do not
+ *  depend on timing.  Errors as cm_linear, and CM_ERR_WORKSPACE.
+ */
+size_t cm_linear_cross_entropy_workspace_size(int64_t M, int64_t K, int64_t n);
+cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout,
+                                  const void *targets, int target_bits, int64_t first, int64_t vocab, float *loss, float *lse,
+                                  float *picked, int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes,
+                                  cm_stream_t stream);
+
+/*
+ * cm_linear_cross_entropy_backward -- the gradients of sum(dloss loss + dlse lse):
+ *   dz = exp(z - lse) (dloss + dlse), less dloss in the target's column;
+ *   dx = dz W;  dw (+)= dz^T x, laid out as the weight is.
+ *  Arguments as in the forward call; lse [M] fp32 as that wrote it, or the log
+ *  sum over all slices (dx is then this slice's share: the slices' dx add up, and
+ *  each dw is whole).  dloss [M] fp32, dlse [M] fp32 or NULL (zeros).  dx [M][K]
+ *  (dx_dtype) and dw (dw_dtype) may each be NULL; with `accumulate` dw is added to.
+ *  Rows without a target give zeros and count nowhere; their lse, dloss and dlse
+ *  are not used.  The logits are computed again, some columns at a time, and dz is
+ *  rounded to bf16 for the products (relative to the largest of the finite
+ *  |dloss|, |dloss + dlse|); sums are fp32.
+ *  ws: cm_linear_cross_entropy_backward_workspace_size(M, K, n) bytes, as above.
+ */
+size_t cm_linear_cross_entropy_backward_workspace_size(int64_t M, int64_t K, int64_t n);
+cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout,
+                                           const void *targets, int target_bits, int64_t first, int64_t vocab,
+                                           const float *lse, const float *dloss, const float *dlse, void *dx,
+                                           cm_dtype dx_dtype, int64_t lddx, void *dw, cm_dtype dw_dtype, int64_t lddw,
+                                           int accumulate, int64_t M, int64_t K, int64_t n, void *ws, size_t ws_bytes,
+                                           cm_stream_t stream);
+
+/*
  * cm_linear_choose -- how the calls above compute a product of `rows` x `cols`
  * elements with k terms each on the current device; asks for no launch and
  * no memory.  The forward call's product is M x n with k = K, the data
