@@ -7,21 +7,23 @@
 // are sorted by (row, token) first, so that every row of dw is summed and written
 // once, in one order, whatever the timing:
 //   1. tiles of 1024 keys (row << 32 | token) are sorted in shared memory;
-//   2. up to 64 sorted runs at a time become one: a key's place is its place in
+//   2. up to 32 sorted runs at a time become one: a key's place is its place in
 //      its own run plus the number of smaller keys in each other run, found by
 //      bisection; keys are all different, so no two meet.  Again while runs are left;
-//   3. a token that occurs often would make one warp sum many rows: the aligned
-//      pieces of 32 and 256 sorted tokens that lie in one row of dw are summed first
-//      (a warp, or the eight warps of a CTA, each), into the workspace;
-//   4. the first token of each row's run owns the row: its warps add up what the
-//      pieces have left over and the pieces, in sorted order.  Where dw is not
-//      added to, the other CTAs of the same launch write zeros to the absent rows.
+//   3. a warp takes an aligned piece of 16 sorted tokens and 256 columns, and writes
+//      the sums of the rows whose tokens all lie in it.  A row that goes on beyond
+//      the piece, or came from the one before, leaves its part in the workspace;
+//   4. the parts of such a row are added in order by a warp, or where there are
+//      many by the warps of a CTA, each neighbouring ones, then the warps' sums.
+// Where dw is not added to, further CTAs of launch 3 write zeros to the absent rows.
 #include <cuda_bf16.h>
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
+#include "cm_device.cuh"
 #include "cm_internal.h"
 #include "cm_launch.cuh"
 #include "cm_vec.cuh"
@@ -32,6 +34,7 @@ namespace {
 using namespace vec;
 
 constexpr int64_t kMaxExtent = int64_t(1) << 30;
+constexpr int64_t kMostColumns = 65535 * 256;   // blocks of columns are counted by the grid's second extent
 constexpr uint32_t kNoRow = 0xffffffffu;   // the row of a token that is not of the slice: sorted last
 
 struct NvtxRange {
@@ -96,43 +99,40 @@ struct LookupParams {
     const void *w;
     void *y;
     int64_t ldw, ldy, tokens;
-    int h;
+    int h, width;
     float scale;
 };
 
 constexpr int kLookThreads = 256, kLookBatch = 4;
 
-// A CTA takes 1024 vectors of eight, counted through all tokens' rows, so that
-// any row length fills it; a thread has four loads under way before its first store.
+// `width` (a power of two up to 256) neighbouring threads share a row, each with
+// four of its vectors under way before its first store; rows of more than 1024
+// vectors take several CTAs.  No division: counted through all rows' vectors, 16384
+// tokens of 8192 elements took 101 us instead of 70.
 template <typename W, typename Y, bool VEC>
 __global__ void __launch_bounds__(kLookThreads) cm_embedding_kernel(const LookupParams p) {
     let_next_start();
     wait_for_previous();
-    const uint32_t per_row = uint32_t(p.h + 7) / 8;
-    const int64_t v0 = int64_t(blockIdx.x) * (kLookThreads * kLookBatch);
-    const int64_t t0 = v0 / per_row;
-    const uint32_t off = uint32_t(v0 - t0 * per_row) + threadIdx.x;
+    const int lane = int(threadIdx.x) & (p.width - 1), rows = kLookThreads / p.width;
+    const int64_t t = int64_t(blockIdx.x) * rows + int(threadIdx.x) / p.width;
+    if (t >= p.tokens) return;
+    const int c0 = (int(blockIdx.y) * kLookBatch * p.width + lane) * 8, step = p.width * 8;
+    const uint32_t row = row_of(p.ids, t);
+    const W *from = static_cast<const W *>(p.w) + int64_t(row == kNoRow ? 0 : row) * p.ldw;
+    Y *to = static_cast<Y *>(p.y) + t * p.ldy;
     V8 v[kLookBatch];
 #pragma unroll
     for (int k = 0; k < kLookBatch; ++k) {
-        const uint32_t o = off + uint32_t(k * kLookThreads), r = o / per_row;
-        const int64_t t = t0 + r;
-        const int c = int(o - r * per_row) * 8;
-        const uint32_t row = t < p.tokens ? row_of(p.ids, t) : kNoRow;
         v[k] = fill(0.0f);
-        if (row != kNoRow) v[k] = scaled(get8<VEC>(static_cast<const W *>(p.w) + int64_t(row) * p.ldw, c, p.h), p.scale);
+        if (row != kNoRow && c0 + k * step < p.h) v[k] = get8<VEC>(from, c0 + k * step, p.h);
     }
 #pragma unroll
-    for (int k = 0; k < kLookBatch; ++k) {
-        const uint32_t o = off + uint32_t(k * kLookThreads), r = o / per_row;
-        const int64_t t = t0 + r;
-        const int c = int(o - r * per_row) * 8;
-        if (t < p.tokens) put8<VEC>(static_cast<Y *>(p.y) + t * p.ldy, c, p.h, v[k]);
-    }
+    for (int k = 0; k < kLookBatch; ++k)
+        if (c0 + k * step < p.h) put8<VEC>(to, c0 + k * step, p.h, scaled(v[k], p.scale));
 }
 
 // ---- tokens sorted by row -----------------------------------------------------------
-constexpr int kSortTile = 1024, kMergeRuns = 64, kMergeThreads = 256;
+constexpr int kSortTile = 1024, kMergeRuns = 32, kMergeThreads = 256;
 
 __device__ __forceinline__ uint64_t lesser(uint64_t a, uint64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ uint64_t greater(uint64_t a, uint64_t b) { return a < b ? b : a; }
@@ -176,21 +176,47 @@ __device__ __forceinline__ uint32_t smaller(const uint64_t *in, uint32_t n, uint
     return lo;
 }
 
-// Groups of up to kMergeRuns sorted runs of `run` keys become one run each.
+// Groups of up to kMergeRuns sorted runs of `run` keys (a power of two) become one
+// run each.  Earlier runs hold earlier tokens: of equal rows theirs come first, so rows
+// alone are compared.  A group of the first round is bisected in shared memory
+// (kShared: its rows, 128 KB at most; 16384 tokens: 8 us, in global memory 21 to 28).
+template <bool kShared>
 __global__ void __launch_bounds__(kMergeThreads) cm_embedding_merge_kernel(const uint64_t *in, uint64_t *out, int64_t tokens,
                                                                            int64_t run) {
+    extern __shared__ uint32_t rows[];
     let_next_start();
     wait_for_previous();
-    const int64_t i = int64_t(blockIdx.x) * kMergeThreads + threadIdx.x;
+    // run is a multiple of a CTA's keys: they all lie in one run
+    const int64_t i0 = int64_t(blockIdx.x) * kMergeThreads, i = i0 + threadIdx.x;
+    const int own = int(i0 / run % kMergeRuns);
+    const int64_t base = i0 / run / kMergeRuns * kMergeRuns * run;
+    const int64_t n = min(tokens - base, int64_t(kMergeRuns) * run);   // keys of the group
+    if (kShared) {
+        for (int j = int(threadIdx.x); j < int(n); j += kMergeThreads) rows[j] = uint32_t(in[base + j] >> 32);
+        __syncthreads();
+    }
     if (i >= tokens) return;
-    const int64_t own = i / run, group = own / kMergeRuns * kMergeRuns, base = group * run;
     const uint64_t k = in[i];
-    int64_t place = i - own * run;
-    const int runs = int(min(int64_t(kMergeRuns), (tokens - base + run - 1) / run));
-#pragma unroll 4
-    for (int r = 0; r < runs; ++r) {
-        const int64_t b = base + r * run;
-        if (group + r != own) place += smaller(in + b, uint32_t(min(run, tokens - b)), k);
+    const uint32_t row = uint32_t(k >> 32);
+    int64_t place = i - base - own * run;
+    constexpr int kAtOnce = 8;   // runs whose bisections do not wait for one another
+    for (int r0 = 0; int64_t(r0) * run < n; r0 += kAtOnce) {
+        uint32_t at[kAtOnce], left[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            at[j] = 0;
+            left[j] = r0 + j == own ? 0u : uint32_t(max(int64_t(0), min(run, n - (r0 + j) * run)));
+        }
+        for (uint32_t step = uint32_t(run); step; step >>= 1)
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (at[j] + step > left[j]) continue;
+                const int64_t b = int64_t(r0 + j) * run + at[j] + step - 1;
+                const uint32_t other = kShared ? rows[b] : uint32_t(in[base + b] >> 32);
+                if (other < row || (other == row && r0 + j < own)) at[j] += step;
+            }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) place += at[j];
     }
     out[base + place] = k;
 }
@@ -200,92 +226,68 @@ struct SumParams {
     const uint64_t *keys;    // sorted
     const void *dy;
     void *dw;
-    float *pieces;           // [ceil(tokens / 32)][h, rounded up to 8]: sums of aligned pieces, NULL where none are made
+    float *parts;            // [ceil(tokens / 16)][2][h, rounded up to 8]: of a row from the piece before, and into the next
     int64_t lddy, lddw, tokens, rows;
     int h;
     float scale;
     int accumulate;
-    int64_t sum_ctas;        // CTAs that sum; those behind them write zeros
+    int64_t sum_ctas, zero_ctas;   // that sum, and that write zeros
 };
 
-constexpr int kPiece = 32, kWhole = 256;   // sorted tokens of a warp's piece, and of a CTA's
-constexpr int kAtOnce = 8;                 // rows under way at a time
+constexpr int kPiece = 16;                 // sorted tokens of a warp
+constexpr int kAtOnce = 4;                 // rows under way at a time, and where dw is added to as many of its
 
 __device__ __forceinline__ uint32_t row_at(const SumParams &p, int64_t i) { return uint32_t(p.keys[i] >> 32); }
-// The aligned piece of n sorted tokens at i lies in one row of dw.
-__device__ __forceinline__ bool one_row(const SumParams &p, int64_t i, int n, uint32_t row) {
-    return i % n == 0 && i + n <= p.tokens && row_at(p, i + n - 1) == row;
+__device__ __forceinline__ float *part_at(const SumParams &p, int64_t piece, int into_next, int c) {
+    return p.parts + (piece * 2 + into_next) * ((p.h + 7) / 8 * 8) + c;
 }
 
-__device__ __forceinline__ float *piece_at(const SumParams &p, int64_t i, int c) {
-    return p.pieces + (i / kPiece) * ((p.h + 7) / 8 * 8) + c;
+template <bool VEC, typename DW>
+__device__ __forceinline__ V8 old_row(const SumParams &p, uint32_t row, int c) {
+    return get8<VEC>(static_cast<const DW *>(p.dw) + int64_t(row) * p.lddw, c, p.h);
+}
+template <bool VEC, typename DW>
+__device__ __forceinline__ void put_row(const SumParams &p, const V8 &acc, const V8 &old, uint32_t row, int c) {
+    V8 v = scaled(acc, p.scale);
+    if (p.accumulate) add_to(v, old);
+    put8<VEC>(static_cast<DW *>(p.dw) + int64_t(row) * p.lddw, c, p.h, v);
 }
 
-// Sum over sorted tokens i .. i + n - 1 of column c .. c + 7, in order.
-template <bool VEC, typename DY>
-__device__ __forceinline__ void add_tokens(const SumParams &p, V8 &acc, int64_t i, int n, int c) {
-    for (int j = 0; j < n; j += kAtOnce) {
-        V8 v[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            v[k] = fill(0.0f);
-            if (j + k < n)
-                v[k] = get8<VEC>(static_cast<const DY *>(p.dy) + int64_t(uint32_t(p.keys[i + j + k])) * p.lddy, c, p.h);
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-            if (j + k < n) add_to(acc, v[k]);
-    }
-}
-
-// grid: aligned pieces of 256 sorted tokens x column blocks of 256.  A warp sums 32
-// tokens; where all 256 lie in one row, the eight sums are added in order.
-template <typename DY, bool VEC>
-__global__ void __launch_bounds__(256) cm_embedding_pieces_kernel(const SumParams p) {
-    __shared__ V8 part[8][32];
-    let_next_start();
-    wait_for_previous();
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    const int64_t i0 = int64_t(blockIdx.x) * kWhole, i = i0 + warp * kPiece;
-    const int c = int(blockIdx.y) * 256 + lane * 8;
-    const uint32_t row0 = row_at(p, i0);
-    const bool whole = row0 != kNoRow && one_row(p, i0, kWhole, row0);   // the same in every thread
-    const uint32_t row = i < p.tokens ? row_at(p, i) : kNoRow;
-    if (c < p.h && row != kNoRow && (whole || one_row(p, i, kPiece, row))) {
-        V8 acc = fill(0.0f);
-        add_tokens<VEC, DY>(p, acc, i, kPiece, c);
-        if (whole)
-            part[warp][lane] = acc;
-        else
-            store8(piece_at(p, i, c), acc);
-    }
-    if (!whole) return;
-    __syncthreads();
-    if (warp == 0 && c < p.h) {
-        V8 acc = part[0][lane];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) add_to(acc, part[w][lane]);
-        store8(piece_at(p, i0, c), acc);
-    }
-}
-
-// Rows of dw without a token, 64 to a CTA: zeros.
-constexpr int kZeroRows = 64;
+// Rows of dw without a token, 64 to a CTA: zeros.  Rows of whole 16-byte pieces are
+// written by bulk copies of a block of zeros, the others element by element.
+constexpr int kZeroRows = 64, kZeroBytes = 8192;
 template <typename DW, bool VEC>
 __device__ void zero_absent(const SumParams &p, int64_t v0) {
     __shared__ unsigned long long seen;
     __shared__ int64_t bounds[2];
+    __shared__ __align__(128) uint4 zeros[VEC ? kZeroBytes / 16 : 1];
     const int n = int(min(int64_t(kZeroRows), p.rows - v0));
     if (threadIdx.x == 0) seen = 0;
     if (threadIdx.x < 2) {   // first sorted token of row v0, and of the row behind the last
         const uint64_t k = uint64_t(v0 + (threadIdx.x ? n : 0)) << 32;
         bounds[threadIdx.x] = smaller(p.keys, uint32_t(p.tokens), k);
     }
+    if (VEC)
+        for (int i = threadIdx.x; i < kZeroBytes / 16; i += blockDim.x) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     for (int64_t i = bounds[0] + threadIdx.x; i < bounds[1]; i += blockDim.x)
         if (i == bounds[0] || row_at(p, i) != row_at(p, i - 1)) atomicOr(&seen, 1ull << (row_at(p, i) - v0));
+    if (VEC) dev::fence_proxy_async_smem();
     __syncthreads();
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const int64_t bytes = int64_t(p.h) * int64_t(sizeof(DW));
+    if (VEC && bytes % 16 == 0) {
+        if (warp) return;
+        for (int r = lane; r < n; r += 32) {
+            if (seen >> r & 1) continue;
+            uint8_t *row = static_cast<uint8_t *>(p.dw) + (v0 + r) * p.lddw * int64_t(sizeof(DW));
+            for (int64_t at = 0; at < bytes; at += kZeroBytes)
+                dev::bulk_store(row + at, zeros, uint32_t(min(bytes - at, int64_t(kZeroBytes))));
+        }
+        dev::bulk_commit();
+        dev::bulk_wait<0>();
+        return;
+    }
     const V8 zero = fill(0.0f);
     for (int r = warp; r < n; r += int(blockDim.x) >> 5) {
         if (seen >> r & 1) continue;
@@ -294,45 +296,131 @@ __device__ void zero_absent(const SumParams &p, int64_t v0) {
     }
 }
 
-// A warp for each sorted token and 256 columns; those of a row's first token sum the row.
+// A warp for each aligned piece of 16 sorted tokens and 256 columns.  The CTAs that write
+// zeros lie between those that sum, so that one's stores cover the other's latencies.
 template <typename DY, typename DW, bool VEC>
 __global__ void __launch_bounds__(256) cm_embedding_sum_kernel(const SumParams p) {
     let_next_start();
     wait_for_previous();
-    if (int64_t(blockIdx.x) >= p.sum_ctas) {
-        zero_absent<DW, VEC>(p, (int64_t(blockIdx.x) - p.sum_ctas) * kZeroRows);
+    const int64_t zeros_before = int64_t(blockIdx.x) * p.zero_ctas / gridDim.x;
+    if ((int64_t(blockIdx.x) + 1) * p.zero_ctas / gridDim.x > zeros_before) {
+        zero_absent<DW, VEC>(p, zeros_before * kZeroRows);
         return;
     }
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    const int64_t blocks = (p.h + 255) / 256, unit = int64_t(blockIdx.x) * 8 + warp;
-    int64_t i = unit / blocks;
-    const int c = int(unit - i * blocks) * 256 + lane * 8;
-    if (i >= p.tokens) return;
-    const uint32_t row = row_at(p, i);
-    if (row == kNoRow || (i > 0 && row_at(p, i - 1) == row)) return;
+    const int64_t blocks = (p.h + 255) / 256, unit = (int64_t(blockIdx.x) - zeros_before) * 8 + warp, piece = unit / blocks;
+    const int c = int(unit - piece * blocks) * 256 + lane * 8;
+    const int64_t i0 = piece * kPiece, i = i0 + lane;
+    if (i0 >= p.tokens) return;
+    // a lane holds one token: its row, and whether it is the row's first or last in the piece
+    const uint64_t key = lane < kPiece && i < p.tokens ? p.keys[i] : ~uint64_t(0);
+    const uint32_t row = uint32_t(key >> 32), token = uint32_t(key);
+    const uint32_t before = __shfl_up_sync(0xffffffffu, row, 1), behind = __shfl_down_sync(0xffffffffu, row, 1);
+    const uint32_t live = __ballot_sync(0xffffffffu, row != kNoRow);   // sorted: the first ones
+    if (live == 0) return;
+    const uint32_t first = __ballot_sync(0xffffffffu, lane == 0 || before != row);
+    const uint32_t last = __ballot_sync(0xffffffffu, lane == kPiece - 1 || behind != row);
+    const bool from_before = i0 > 0 && row_at(p, i0 - 1) == __shfl_sync(0xffffffffu, row, 0);
+    const bool into_next = i0 + kPiece < p.tokens && row_at(p, i0 + kPiece) == __shfl_sync(0xffffffffu, row, kPiece - 1);
+    const int n = __popc(live);
+    // rows that go on in another piece: their parts go to the workspace
+    const uint32_t apart = (from_before ? last & (0u - last) : 0u) | (into_next ? 1u << (kPiece - 1) : 0u);
     V8 acc = fill(0.0f);
-    while (true) {   // the same way in all lanes
-        // up to 32 tokens of the row, as far as the next aligned piece
-        const int64_t at = i + lane;
-        const bool mine = at < p.tokens && row_at(p, at) == row;
-        const uint32_t live = __ballot_sync(0xffffffffu, mine);
-        int n = live == 0xffffffffu ? 32 : __ffs(~live) - 1;   // sorted: the row's tokens come first
-        if (n == 0) break;
-        if (p.pieces && i % kPiece == 0 && n == kPiece) {
-            const bool whole = one_row(p, i, kWhole, row);
-            if (c < p.h) add_to(acc, load8(piece_at(p, i, c)));
-            i += whole ? kWhole : kPiece;
-            continue;
+    for (int j = 0; j < n; j += kAtOnce) {
+        V8 v[kAtOnce], old[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const uint32_t t = __shfl_sync(0xffffffffu, token, j + k), r = __shfl_sync(0xffffffffu, row, j + k);
+            v[k] = old[k] = fill(0.0f);
+            if (j + k >= n || c >= p.h) continue;
+            v[k] = get8<VEC>(static_cast<const DY *>(p.dy) + int64_t(t) * p.lddy, c, p.h);
+            if (p.accumulate && ((last & ~apart) >> (j + k) & 1)) old[k] = old_row<VEC, DW>(p, r, c);
         }
-        if (p.pieces) n = min(n, kPiece - int(i % kPiece));
-        if (c < p.h) add_tokens<VEC, DY>(p, acc, i, n, c);
-        i += n;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int at = j + k;
+            const uint32_t r = __shfl_sync(0xffffffffu, row, at);
+            if (at >= n || c >= p.h) continue;
+            if (first >> at & 1) acc = fill(0.0f);
+            add_to(acc, v[k]);
+            if (!(last >> at & 1)) continue;
+            if (apart >> at & 1)   // the piece's first row, where it came from before; else the last, which goes on
+                store8(part_at(p, piece, from_before && (last & ((1u << at) - 1)) == 0 ? 0 : 1, c), acc);
+            else
+                put_row<VEC, DW>(p, acc, old[k], r, c);
+        }
     }
-    if (c >= p.h) return;
-    DW *out = static_cast<DW *>(p.dw) + int64_t(row) * p.lddw;
-    acc = scaled(acc, p.scale);
-    if (p.accumulate) add_to(acc, get8<VEC>(out, c, p.h));
-    put8<VEC>(out, c, p.h, acc);
+}
+
+// The sum of parts k0 .. k1 - 1, in order, of the row that goes on from `piece` into
+// the next: that piece's second part, and the first ones of the pieces behind.
+__device__ __forceinline__ V8 add_parts(const SumParams &p, int64_t piece, int64_t k0, int64_t k1, int c) {
+    constexpr int kParts = 8;
+    V8 acc = fill(0.0f);
+    for (int64_t k = k0; k < k1; k += kParts) {
+        V8 v[kParts];
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {
+            v[j] = fill(0.0f);
+            if (k + j < k1) v[j] = load8(part_at(p, piece + k + j, k + j == 0, c));
+        }
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) add_to(acc, v[j]);
+    }
+    return acc;
+}
+
+// The rows that lie in several pieces.  A CTA looks at 32 pieces, a lane at each, for
+// rows that begin there and go on; columns of 256.  A warp adds the parts of up to
+// 32 pieces; longer rows are shared by the CTA's warps, each with a run of their parts.
+template <typename DW, bool VEC>
+__global__ void __launch_bounds__(256) cm_embedding_join_kernel(const SumParams p) {
+    __shared__ V8 sums[8][32];
+    let_next_start();
+    wait_for_previous();
+    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31, c = int(blockIdx.y) * 256 + lane * 8;
+    const int64_t piece0 = int64_t(blockIdx.x) * 32, end = (piece0 + lane + 1) * kPiece;   // of the lane's piece
+    uint32_t row = kNoRow;
+    if (end < p.tokens) {
+        row = row_at(p, end);
+        if (row_at(p, end - 1) != row) row = kNoRow;
+        // began earlier
+        if (end > kPiece && row_at(p, end - kPiece) == row && row_at(p, end - kPiece - 1) == row) row = kNoRow;
+    }
+    const uint32_t owners = __ballot_sync(0xffffffffu, row != kNoRow);   // the same in every warp
+    uint32_t longer = 0;
+    for (uint32_t left = owners, at = 0; left; left &= left - 1, ++at) {
+        const int o = __ffs(left) - 1;
+        const uint32_t r = __shfl_sync(0xffffffffu, row, o);
+        const int64_t piece = piece0 + o, i = (piece + 2 + lane) * kPiece;
+        // pieces behind the next that hold some of the row
+        const uint32_t more = __ballot_sync(0xffffffffu, i < p.tokens && row_at(p, i) == r);
+        if (more == 0xffffffffu) longer |= 1u << o;
+        if (more == 0xffffffffu || int(at % 8) != warp || c >= p.h) continue;
+        const V8 old = p.accumulate ? old_row<VEC, DW>(p, r, c) : fill(0.0f);
+        put_row<VEC, DW>(p, add_parts(p, piece, 0, 2 + __popc(more), c), old, r, c);
+    }
+    for (; longer; longer &= longer - 1) {   // the same in every warp
+        const int o = __ffs(longer) - 1;
+        const uint32_t r = __shfl_sync(0xffffffffu, row, o);
+        const int64_t piece = piece0 + o;
+        int64_t n = 2;   // pieces that hold some of the row
+        while (true) {
+            const int64_t i = (piece + n + threadIdx.x) * kPiece;
+            const int more = __syncthreads_count(i < p.tokens && row_at(p, i) == r);
+            n += more;
+            if (more < int(blockDim.x)) break;
+        }
+        if (c < p.h) sums[warp][lane] = add_parts(p, piece, n * warp / 8, n * (warp + 1) / 8, c);
+        __syncthreads();
+        if (warp == 0 && c < p.h) {
+            V8 acc = sums[0][lane];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) add_to(acc, sums[w][lane]);
+            put_row<VEC, DW>(p, acc, p.accumulate ? old_row<VEC, DW>(p, r, c) : fill(0.0f), r, c);
+        }
+        __syncthreads();
+    }
 }
 
 // ---- launches -----------------------------------------------------------------------
@@ -359,17 +447,30 @@ cm_status check_extents(int64_t tokens, int64_t rows, int64_t h) {
 }
 
 template <typename W, typename Y>
-cudaError_t lookup(const LookupParams &p, bool vec, int64_t ctas, cudaStream_t stream) {
-    return launch_after(vec ? cm_embedding_kernel<W, Y, true> : cm_embedding_kernel<W, Y, false>, dim3(unsigned(ctas)),
-                        kLookThreads, 0, 1, stream, p);
+cudaError_t lookup(const LookupParams &p, bool vec, cudaStream_t stream) {
+    const int rows = kLookThreads / p.width, per = kLookBatch * p.width * 8;
+    const dim3 grid(unsigned((p.tokens + rows - 1) / rows), unsigned((p.h + per - 1) / per));
+    return launch_after(vec ? cm_embedding_kernel<W, Y, true> : cm_embedding_kernel<W, Y, false>, grid, kLookThreads, 0, 1, stream, p);
 }
 
-// The workspace: keys twice, then the pieces' sums.
+// The workspace: keys twice, then the parts.
 size_t key_bytes(int64_t tokens) { return (size_t(tokens) * sizeof(uint64_t) + 255) / 256 * 256; }
-bool has_pieces(int64_t tokens) { return tokens >= 2 * kPiece; }
 size_t backward_workspace(int64_t tokens, int64_t h) {
-    const size_t pieces = has_pieces(tokens) ? size_t((tokens + kPiece - 1) / kPiece) * size_t((h + 7) / 8 * 8) * sizeof(float) : 0;
-    return 2 * key_bytes(tokens) + pieces + 256;
+    // one piece has no neighbours
+    const size_t parts = tokens > kPiece ? size_t((tokens + kPiece - 1) / kPiece) * 2 * size_t((h + 7) / 8 * 8) * sizeof(float) : 0;
+    return 2 * key_bytes(tokens) + parts + 256;
+}
+
+// Leave to use more than 48 KB of shared memory; asked for once a device.
+cudaError_t allow_shared() {
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess || (device < 64 && (done.load(std::memory_order_relaxed) >> device & 1))) return e;
+    const cudaError_t set = cudaFuncSetAttribute(cm_embedding_merge_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kMergeRuns * kSortTile * int(sizeof(uint32_t)));
+    if (set == cudaSuccess && device < 64) done.fetch_or(uint64_t(1) << device, std::memory_order_relaxed);
+    return set;
 }
 
 // Sorted keys of all tokens; in either half of the workspace.
@@ -377,8 +478,14 @@ cudaError_t sort_tokens(const Ids &ids, int64_t tokens, uint64_t *a, uint64_t *b
     cudaError_t e = launch_after(cm_embedding_sort_kernel, dim3(unsigned((tokens + kSortTile - 1) / kSortTile)), kSortTile, 0, 1,
                                  stream, ids, tokens, a);
     for (int64_t run = kSortTile; run < tokens && e == cudaSuccess; run *= kMergeRuns) {
-        e = launch_after(cm_embedding_merge_kernel, dim3(unsigned((tokens + kMergeThreads - 1) / kMergeThreads)), kMergeThreads,
-                         0, 1, stream, static_cast<const uint64_t *>(a), b, tokens, run);
+        const dim3 grid(unsigned((tokens + kMergeThreads - 1) / kMergeThreads));
+        const size_t smem = size_t(std::min<int64_t>(tokens, kMergeRuns * kSortTile)) * sizeof(uint32_t);
+        if (run > kSortTile)
+            e = launch_after(cm_embedding_merge_kernel<false>, grid, kMergeThreads, 0, 1, stream, static_cast<const uint64_t *>(a), b,
+                             tokens, run);
+        else if (smem <= 48 * 1024 || (e = allow_shared()) == cudaSuccess)
+            e = launch_after(cm_embedding_merge_kernel<true>, grid, kMergeThreads, smem, 1, stream, static_cast<const uint64_t *>(a), b,
+                             tokens, run);
         std::swap(a, b);
     }
     *sorted = a;
@@ -387,14 +494,11 @@ cudaError_t sort_tokens(const Ids &ids, int64_t tokens, uint64_t *a, uint64_t *b
 
 template <typename DY, typename DW, bool VEC>
 cudaError_t sum_rows(const SumParams &p, cudaStream_t stream) {
-    if (p.pieces) {
-        const cudaError_t e = launch_after(cm_embedding_pieces_kernel<DY, VEC>,
-                                           dim3(unsigned((p.tokens + kWhole - 1) / kWhole), unsigned((p.h + 255) / 256)), 256, 0, 1,
-                                           stream, p);
-        if (e != cudaSuccess) return e;
-    }
-    const int64_t zeros = p.accumulate ? 0 : (p.rows + kZeroRows - 1) / kZeroRows;
-    return launch_after(cm_embedding_sum_kernel<DY, DW, VEC>, dim3(unsigned(p.sum_ctas + zeros)), 256, 0, 1, stream, p);
+    const cudaError_t e =
+        launch_after(cm_embedding_sum_kernel<DY, DW, VEC>, dim3(unsigned(p.sum_ctas + p.zero_ctas)), 256, 0, 1, stream, p);
+    if (e != cudaSuccess || p.tokens <= kPiece) return e;
+    return launch_after(cm_embedding_join_kernel<DW, VEC>, dim3(unsigned((p.tokens + 32 * kPiece - 1) / (32 * kPiece)), unsigned((p.h + 255) / 256)), 256,
+                        0, 1, stream, p);
 }
 
 template <typename DY, typename DW>
@@ -424,15 +528,16 @@ cm_status cm_embedding(const void *ids, int id_bits, int64_t first, const void *
     CM_TRY(check_ids(ids, id_bits, first));
     CM_TRY(check_rows(w, w_dtype, ldw, h));
     CM_TRY(check_rows(y, y_dtype, ldy, h));
-    const int64_t per_cta = kLookThreads * kLookBatch, ctas = (tokens * ((h + 7) / 8) + per_cta - 1) / per_cta;
-    if (ctas > 0x7fffffff) return CM_ERR_SHAPE;
-    const LookupParams p = {{ids, first, n, id_bits}, w, y, ldw, ldy, tokens, int(h), scale};
+    if (h > kMostColumns) return CM_ERR_SHAPE;
+    int width = 1;
+    while (width < kLookThreads && width * kLookBatch * 8 < h) width *= 2;
+    const LookupParams p = {{ids, first, n, id_bits}, w, y, ldw, ldy, tokens, int(h), width, scale};
     const bool vec = whole_vectors(w, w_dtype, ldw) && whole_vectors(y, y_dtype, ldy);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = w_dtype == CM_F32 ? y_dtype == CM_F32 ? lookup<float, float>(p, vec, ctas, s)
-                                                                : lookup<float, bf16>(p, vec, ctas, s)
-                          : y_dtype == CM_F32 ? lookup<bf16, float>(p, vec, ctas, s)
-                                              : lookup<bf16, bf16>(p, vec, ctas, s);
+    const cudaError_t e = w_dtype == CM_F32 ? y_dtype == CM_F32 ? lookup<float, float>(p, vec, s)
+                                                                : lookup<float, bf16>(p, vec, s)
+                          : y_dtype == CM_F32 ? lookup<bf16, float>(p, vec, s)
+                                              : lookup<bf16, bf16>(p, vec, s);
     return e == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
@@ -460,15 +565,16 @@ cm_status cm_embedding_backward(const void *dy, cm_dtype dy_dtype, int64_t lddy,
     if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0) return CM_ERR_ALIGNMENT;
     const int64_t blocks = (h + 255) / 256;
     SumParams p = {};
-    p.sum_ctas = (tokens * blocks + 7) / 8;
-    if (blocks > 65535 || p.sum_ctas + n / kZeroRows + 1 > 0x7fffffff) return CM_ERR_SHAPE;
+    p.sum_ctas = ((tokens + kPiece - 1) / kPiece * blocks + 7) / 8;
+    p.zero_ctas = accumulate ? 0 : (n + kZeroRows - 1) / kZeroRows;
+    if (h > kMostColumns || p.sum_ctas + p.zero_ctas > 0x7fffffff) return CM_ERR_SHAPE;
     uint8_t *base = static_cast<uint8_t *>(ws);
     if (sort_tokens({ids, first, n, id_bits}, tokens, reinterpret_cast<uint64_t *>(base),
                     reinterpret_cast<uint64_t *>(base + key_bytes(tokens)), &p.keys, stream) != cudaSuccess)
         return CM_ERR_CUDA;
     p.dy = dy;
     p.dw = dw;
-    p.pieces = has_pieces(tokens) ? reinterpret_cast<float *>(base + 2 * key_bytes(tokens)) : nullptr;
+    p.parts = reinterpret_cast<float *>(base + 2 * key_bytes(tokens));
     p.lddy = lddy;
     p.lddw = lddw;
     p.tokens = tokens;

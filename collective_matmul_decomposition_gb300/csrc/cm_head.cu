@@ -17,7 +17,7 @@ namespace {
 
 using namespace vec;
 
-constexpr int kRowsThreads = 256, kRowsOfCta = 64;
+constexpr int kRowsThreads = 256, kRowsMost = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int64_t target_of(const HeadRows &p, int64_t row) {
@@ -31,20 +31,21 @@ __device__ __forceinline__ float larger(float a, float b) {
     return b <= 3.0e38f ? fmaxf(a, b) : a;
 }
 
-// A CTA places 64 rows.  It counts all rows' targets itself, which costs a pass over
-// them from L2 (rows^2 / 64 of them in all, little beside the products' rows K n),
-// and saves a launch and a scan across CTAs.
+// A CTA places 8 to 64 rows (`per`: 1003 rows of 4101 elements in 64s 86 us, on 16
+// SMs).  It counts all rows' targets itself, which costs a pass over them from L2
+// (rows^2 / per of them in all, little beside the products' rows K n), and saves a
+// launch and a scan across CTAs.
 //
 // The gradients' factors are kept relative to the largest of them (scale), by which the
 // results are multiplied at the end in fp32: the bf16 gradient of a logit then does not
 // carry the rounding of a common factor such as 1 / rows.
-__global__ void __launch_bounds__(kRowsThreads) cm_head_rows_kernel(const HeadRows p) {
+__global__ void __launch_bounds__(kRowsThreads) cm_head_rows_kernel(const HeadRows p, int per) {
     __shared__ int counts[2][kRowsThreads / 32];
     __shared__ float tops[kRowsThreads / 32];
-    __shared__ int slots[kRowsOfCta];
+    __shared__ int slots[kRowsMost];
     let_next_start();
     wait_for_previous();
-    const int64_t r0 = int64_t(blockIdx.x) * kRowsOfCta, r1 = min(p.rows, r0 + kRowsOfCta);
+    const int64_t r0 = int64_t(blockIdx.x) * per, r1 = min(p.rows, r0 + per);
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
     int before = 0, all = 0;
     float top = 0.0f;
@@ -75,15 +76,14 @@ __global__ void __launch_bounds__(kRowsThreads) cm_head_rows_kernel(const HeadRo
         if (p.scale) *p.scale = scale;
     }
     if (warp == 0) {   // the CTA's rows, in order
-#pragma unroll
-        for (int i = 0; i < kRowsOfCta; i += 32) {
+        for (int i = 0; i < per; i += 32) {
             const int64_t r = r0 + i + lane;
             const int64_t t = r < r1 ? target_of(p, r) : -1;
             const uint32_t live = __ballot_sync(0xffffffffu, t >= 0);
             const int slot = t >= 0 ? before + __popc(live & ((1u << lane) - 1)) : -1;
             before += __popc(live);
-            slots[i + lane] = slot;
             if (r >= r1) continue;
+            slots[i + lane] = slot;
             if (p.slot_of) p.slot_of[r] = slot;
             if (slot < 0) {
                 if (p.loss) p.loss[r] = 0.0f;
@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(256) cm_head_scatter_kernel(const HeadScatter 
 }  // namespace
 
 cudaError_t launch_head_rows(const HeadRows &p, cudaStream_t stream) {
-    return launch_after(cm_head_rows_kernel, dim3(unsigned((p.rows + kRowsOfCta - 1) / kRowsOfCta)), kRowsThreads, 0, 1, stream, p);
+    const int per = int(std::max<int64_t>(8, std::min<int64_t>(kRowsMost, p.rows / 512 / 8 * 8)));
+    return launch_after(cm_head_rows_kernel, dim3(unsigned((p.rows + per - 1) / per)), kRowsThreads, 0, 1, stream, p, per);
 }
 cudaError_t launch_head_join(const HeadJoin &p, cudaStream_t stream) {
     return launch_after(cm_head_join_kernel, dim3(unsigned((p.stride + 31) / 32)), 32 * kJoinWarps, 0, 1, stream, p);

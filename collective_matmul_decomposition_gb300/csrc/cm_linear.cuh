@@ -50,7 +50,7 @@ struct LinearHead {
     const int32_t *target;   // column of the weights' slice, or kNotHere, kNoToken
     const float *lse2;       // lse log2(e)
     const float *grad, *hit;
-    float2 *stat;            // [part][stride]: {largest, sum}, two parts a tile of columns
+    float2 *stat;            // [part][stride]: {largest, sum} of 128 columns
     float *picked;           // the target's logit, where it lies in the slice
     int64_t stride;          // slots there may be
     int64_t first;           // column of the slice that the product's first one is
@@ -94,11 +94,13 @@ struct LinearStripParams {
     int splits;         // CTAs of a cluster that share a tile's K slices
     int ring_bytes;     // shared memory for `stages` slices, and for a split tile's partial sums
     int stages;
+    LinearHead head;    // of the head's modes: 128 columns a part
+    const int32_t *count;   // slots there are
     LinearStatus *status;
     uint64_t timeout_ns;
 };
 
-// layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.  The gated modes take 0 and 2.
+// layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.  The other modes than kLinPlain take 0 and 2.
 constexpr int kStripAlone = 216 * 1024, kStripShared = 108 * 1024;   // ring bytes of a CTA alone on its SM, of one of two
 // clusters[i]: clusters of i CTAs (2 to kStripMostSplits) that run together, one CTA an SM.
 constexpr int kStripMostSplits = 8;

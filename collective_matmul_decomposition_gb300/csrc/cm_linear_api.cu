@@ -269,14 +269,9 @@ cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const
     return launch_linear_pair(p, layout, mode, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
-// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e; all rows, no head.
-cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
-                  const LinearEpilogue &e, cudaStream_t stream, const Kind &kind = {}) {
-    const LinearMode mode = kind.mode;
-    const Operand *const a2 = kind.a2;
-    const bool gated = mode == kLinGated;
-    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated);
-    if (c.pair) return product_pair(d, c, kind, a, b, rows, cols, k, e, stream);
+cm_status product_strip(const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b, int64_t rows,
+                        int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
+    const bool gated = kind.mode == kLinGated;
     LinearStripParams p;
     p.e = e;
     p.rows = rows;
@@ -287,13 +282,31 @@ cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t r
     p.splits = c.splits;
     p.ring_bytes = c.ring_bytes;
     p.stages = linear_strip_stages(c.tok, c.ring_bytes);
+    p.head = kind.head;
+    p.count = kind.live.count;
     p.status = d.status;
     p.timeout_ns = kLinearTimeoutNs;
-    if (!map_operand(&p.tmA, a, cols, k, gated ? 64 : 128) || (gated && !map_operand(&p.tmA2, *a2, cols, k, 64)) ||
+    if (!map_operand(&p.tmA, a, cols, k, gated ? 64 : 128) || (gated && !map_operand(&p.tmA2, *kind.a2, cols, k, 64)) ||
         !map_operand(&p.tmB, b, rows, k, c.tok))
         return CM_ERR_CUDA;
     const int layout = (b.mn_major ? 1 : 0) | (a.mn_major ? 2 : 0);
-    return launch_linear_strip(p, layout, mode, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+    return launch_linear_strip(p, layout, kind.mode, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
+}
+
+// D [rows][cols] = B [rows][k] A [cols][k]^T with the epilogue e, of all rows.
+cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
+                  const LinearEpilogue &e, cudaStream_t stream, const Kind &kind = {}) {
+    const bool gated = kind.mode == kLinGated;
+    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated);
+    return c.pair ? product_pair(d, c, kind, a, b, rows, cols, k, e, stream) : product_strip(d, c, kind, a, b, rows, cols, k, e, stream);
+}
+
+// Logits, whose columns are as many as the vocabulary's: strips where choose() takes
+// them, else whole pair tiles.
+Choice choose_logits(const Device &d, int64_t rows, int64_t cols, int64_t k) {
+    Choice c = choose(d, rows, cols, k, false, true);
+    if (c.pair) c.splits = 1;
+    return c;
 }
 
 // ---- the loss over a vocabulary -----------------------------------------------------
@@ -317,17 +330,15 @@ struct LossSpace {
     float *picked;
     uint16_t *xs;
     float2 *stat;
-    int64_t parts;
 };
 LossSpace loss_space(Carve &c, int64_t M, int64_t K, int64_t n) {
     LossSpace s;
-    s.parts = (n + 255) / 256 * 2;
     s.count = c.take<int32_t>(1);
     s.row_of = c.take<int32_t>(size_t(M));
     s.target = c.take<int32_t>(size_t(M));
     s.picked = c.take<float>(size_t(M));
     s.xs = c.take<uint16_t>(size_t(M) * size_t(up8(K)));
-    s.stat = c.take<float2>(size_t(s.parts) * size_t(M));
+    s.stat = c.take<float2>(size_t((n + 255) / 256 * 2) * size_t(M));
     return s;
 }
 
@@ -603,6 +614,8 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
     r.loss = loss;
     r.lse_out = lse;
     r.picked_out = picked;
+    const Choice c = choose_logits(d, M, n, K);
+    r.always = !c.pair;
     if (launch_head_rows(r, stream) != cudaSuccess) return CM_ERR_CUDA;
     const Operand rows = {s.xs, up8(K), false}, all = {x, ldx, false};
     Kind kind;
@@ -613,10 +626,10 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
     kind.head.stat = s.stat;
     kind.head.picked = s.picked;
     kind.head.stride = M;
-    Choice c;
-    c.pair = true;
-    CM_TRY(product_pair(d, c, kind, {w, ldw, wlayout == CM_W_KN}, rows, M, n, K, {}, stream));
-    const HeadJoin j = {s.stat, s.parts, M, s.count, s.row_of, s.target, s.picked, loss, lse, picked};
+    const Operand weights = {w, ldw, wlayout == CM_W_KN};
+    CM_TRY(c.pair ? product_pair(d, c, kind, weights, rows, M, n, K, {}, stream)
+                  : product_strip(d, c, kind, weights, rows, M, n, K, {}, stream));
+    const HeadJoin j = {s.stat, c.pair ? (n + 255) / 256 * 2 : (n + 127) / 128, M, s.count, s.row_of, s.target, s.picked, loss, lse, picked};
     return launch_head_join(j, stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
 
@@ -658,9 +671,10 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
     CM_TRY(device(&d));
     Carve carve(ws);
     const LossGradSpace s = loss_grad_space(carve, M, K, n);
-    // the two products behind a chunk's logits; tiles that are split, and strips, take all rows
+    // a chunk's logits and the two products behind them; tiles that are split, and strips, take all rows
+    const Choice cp = choose_logits(d, M, s.columns, K);
     const Choice cx = choose(d, M, K, s.columns, false), cw = choose(d, nk ? s.columns : K, nk ? K : s.columns, M, true);
-    const bool counted = (!dx || (cx.pair && cx.splits == 1)) && (!dw || (cw.pair && cw.splits == 1));
+    const bool counted = cp.pair && (!dx || (cx.pair && cx.splits == 1)) && (!dw || (cw.pair && cw.splits == 1));
     HeadRows r = {};
     r.targets = targets;
     r.target_bits = target_bits;
@@ -698,12 +712,12 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
         kind.head.grad = s.grad;
         kind.head.hit = s.hit;
         kind.head.first = c0;
-        Choice c;
-        c.pair = true;
         LinearEpilogue e = {};
         e.y = s.p;
         e.ldy = s.ldp;
-        CM_TRY(product_pair(d, c, kind, {wc, ldw, !nk}, rows, M, cols, K, e, stream));
+        const Operand weights = {wc, ldw, !nk};
+        CM_TRY(cp.pair ? product_pair(d, cp, kind, weights, rows, M, cols, K, e, stream)
+                       : product_strip(d, cp, kind, weights, rows, M, cols, K, e, stream));
         if (dx) {
             e = {};
             e.y = s.sum;

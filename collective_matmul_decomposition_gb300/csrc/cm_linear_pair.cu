@@ -1122,7 +1122,7 @@ PairKernel pair_kernel_of(int bn, int splits) {
 }
 
 PairKernel pair_kernel(int layout, LinearMode mode, int bn, int splits) {
-    const auto two = [&](PairKernel nk, PairKernel kn) { return layout == 0 ? nk : layout == 1 ? kn : nullptr; };
+    const auto two = [&](PairKernel k_major, PairKernel mn_major) { return layout == 0 ? k_major : layout == 1 ? mn_major : nullptr; };
     switch (mode) {
         case kLinGated: return two(pair_kernel_of<0, kLinGated>(bn, splits), pair_kernel_of<1, kLinGated>(bn, splits));
         case kLinGateGrad: return two(pair_kernel_of<0, kLinGateGrad>(bn, splits), pair_kernel_of<1, kLinGateGrad>(bn, splits));

@@ -214,6 +214,61 @@ __device__ __forceinline__ void finish_gated(const LinearEpilogue &e, const floa
     }
 }
 
+// The same for the logits' gradients: exp(v - lse) grad, less hit in the target's
+// column; zeros behind the last slot.
+__device__ __forceinline__ void finish_softgrad(const LinearEpilogue &e, const LinearHead &h, int count, float (&v)[kBatch],
+                                                int64_t row0, int64_t step, int64_t end, int64_t col) {
+    float lse2[kBatch], grad[kBatch], hit[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int64_t row = row0 + k * step;
+        lse2[k] = grad[k] = hit[k] = 0.0f;
+        if (row >= end || row >= count) continue;
+        lse2[k] = h.lse2[row];
+        grad[k] = h.grad[row];
+        hit[k] = h.target[row] == h.first + col ? h.hit[row] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int64_t row = row0 + k * step;
+        if (row >= end) continue;
+        const float p = row < count ? lin::exp2_fast(fmaf(v[k], lin::kLog2e, -lse2[k])) * grad[k] - hit[k] : 0.0f;
+        static_cast<__nv_bfloat16 *>(e.y)[row * e.ldy + col] = __float2bfloat16_rn(p);
+    }
+}
+
+// The softmax statistics of a tile's 128 columns for the rows t0, t0 + step, ... below
+// `end`: a warp takes every fourth of those rows, a lane four neighbouring columns.  The
+// partial tiles are summed as above.
+__device__ __forceinline__ void finish_stats(const LinearHead &h, int count, const float *part, int splits, int t0, int step,
+                                             int end, int64_t row0, int64_t col0, int64_t cols) {
+    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    for (int t = t0 + warp * step; t < end && row0 + t < count; t += 4 * step) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = t * kTileCols + lane * 4 + i;
+            f[i] = splits > 1 ? cluster_sum(smem_u32(part + at), splits) : part[at];
+        }
+        const int64_t row = row0 + t, col = col0 + lane * 4, target = h.target[row];
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (target == col + i && col + i < cols) h.picked[row] = f[i];
+            if (col + i >= cols) f[i] = -INFINITY;
+            top = fmaxf(top, f[i]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m = top * lin::kLog2e, base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += lin::exp2_fast(fmaf(f[i], lin::kLog2e, -base));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) h.stat[col0 / kTileCols * h.stride + row] = make_float2(m, sum);
+    }
+}
+
 template <int LAYOUT, int MODE>
 __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid_constant__ LinearStripParams p) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
@@ -356,9 +411,11 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const int64_t col = int64_t(col0) + threadIdx.x;
     const uint32_t taddr = tmem + (uint32_t(warp * 32) << 16);
     const float bias = !kGated && col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
-    if (kGated && p.splits == 1) {
-        // gate and up columns lie in different threads' lanes: they meet in the ring,
-        // whose loads have all been multiplied, 128 tokens at a time
+    constexpr bool kStats = MODE == kLinStats;
+    [[maybe_unused]] const int count = kStats || MODE == kLinSoftGrad ? *p.count : 0;
+    if ((kGated || kStats) && p.splits == 1) {
+        // gate and up columns, or those of a row's sum, lie in different threads' lanes:
+        // they meet in the ring, whose loads have all been multiplied, 128 tokens at a time
         constexpr int kBlock = 128;
         static_assert(kBlock * kTileCols * 4 <= kStripShared, "a block of tokens fits in the ring");
         float *part = reinterpret_cast<float *>(s.ring);
@@ -373,7 +430,11 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                     if (t0 + i < end) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
             }
             __syncthreads();
-            if (good) finish_gated(p.e, part, 1, 0, 1, end, int64_t(row0) + b, col0, p.cols);
+            if constexpr (kStats) {
+                if (good) finish_stats(p.head, count, part, 1, 0, 1, end, int64_t(row0) + b, col0, p.cols);
+            } else {
+                if (good) finish_gated(p.e, part, 1, 0, 1, end, int64_t(row0) + b, col0, p.cols);
+            }
             __syncthreads();
         }
     } else if (p.splits == 1) {
@@ -390,6 +451,8 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                         for (int k = 0; k < kBatch; ++k) f[k] = __uint_as_float(v[b + k]);
                         if constexpr (MODE == kLinGateGrad)
                             finish_gate_grad(p.e, f, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
+                        else if constexpr (MODE == kLinSoftGrad)
+                            finish_softgrad(p.e, p.head, count, f, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
                         else
                             finish(p.e, f, bias, int64_t(row0) + t0 + b, 1, int64_t(row0) + nrows, col);
                     }
@@ -409,8 +472,10 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         }
         if (!good) *s.abort = 1;
         cluster_sync();
-        if (kGated) {
+        if constexpr (kGated) {
             if (good) finish_gated(p.e, part, p.splits, split, p.splits, nrows, row0, col0, p.cols);
+        } else if constexpr (kStats) {
+            if (good) finish_stats(p.head, count, part, p.splits, split, p.splits, nrows, row0, col0, p.cols);
         } else if (col < p.cols && good)
             for (int t = split; t < nrows; t += p.splits * kBatch) {
                 float f[kBatch];
@@ -421,6 +486,8 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                                : 0.0f;
                 if constexpr (MODE == kLinGateGrad)
                     finish_gate_grad(p.e, f, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
+                else if constexpr (MODE == kLinSoftGrad)
+                    finish_softgrad(p.e, p.head, count, f, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
                 else
                     finish(p.e, f, bias, int64_t(row0) + t, p.splits, int64_t(row0) + nrows, col);
             }
@@ -438,15 +505,12 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
 using StripKernel = void (*)(LinearStripParams);
 
 StripKernel strip_kernel(int layout, LinearMode mode) {
+    const auto two = [&](StripKernel k_major, StripKernel mn_major) { return layout == 0 ? k_major : layout == 2 ? mn_major : nullptr; };
     switch (mode) {
-        case kLinGated:
-            return layout == 0   ? cm_linear_strip_kernel<0, kLinGated>
-                   : layout == 2 ? cm_linear_strip_kernel<2, kLinGated>
-                                 : nullptr;
-        case kLinGateGrad:
-            return layout == 0   ? cm_linear_strip_kernel<0, kLinGateGrad>
-                   : layout == 2 ? cm_linear_strip_kernel<2, kLinGateGrad>
-                                 : nullptr;
+        case kLinGated: return two(cm_linear_strip_kernel<0, kLinGated>, cm_linear_strip_kernel<2, kLinGated>);
+        case kLinGateGrad: return two(cm_linear_strip_kernel<0, kLinGateGrad>, cm_linear_strip_kernel<2, kLinGateGrad>);
+        case kLinStats: return two(cm_linear_strip_kernel<0, kLinStats>, cm_linear_strip_kernel<2, kLinStats>);
+        case kLinSoftGrad: return two(cm_linear_strip_kernel<0, kLinSoftGrad>, cm_linear_strip_kernel<2, kLinSoftGrad>);
         default:
             return layout == 0   ? cm_linear_strip_kernel<0, kLinPlain>
                    : layout == 2 ? cm_linear_strip_kernel<2, kLinPlain>
@@ -462,7 +526,7 @@ int linear_strip_stages(int tok, int ring_bytes) {
 }
 
 cudaError_t prepare_linear_strip(int sms, int *clusters) {
-    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad})
+    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad, kLinStats, kLinSoftGrad})
         for (int layout : {0, 2, 3}) {
             const StripKernel fn = strip_kernel(layout, mode);
             if (!fn) continue;

@@ -826,7 +826,8 @@ cm_status cm_adamw(const cm_adamw_tensor *tensors, int count, double lr, double 
  *  ids: int32 or int64 (id_bits 32 or 64); w [n][h] (w_dtype) and y [tokens][h]
  *  (y_dtype) with row strides.  Any extent, stride and element-aligned address;
  *  rows that start on 16 bytes go in whole vectors.  y must not alias w.
- *  Errors: as cm_linear (first must lie in 0 .. 2^30; tokens may be 0).
+ *  Errors: as cm_linear (first must lie in 0 .. 2^30, h is at most 65535 * 256;
+ *  tokens may be 0).
  */
 cm_status cm_embedding(const void *ids, int id_bits, int64_t first, const void *w, cm_dtype w_dtype, int64_t ldw,
                        float scale, void *y, cm_dtype y_dtype, int64_t ldy, int64_t tokens, int64_t n, int64_t h,
