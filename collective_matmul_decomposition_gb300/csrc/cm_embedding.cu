@@ -20,10 +20,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 
-#include "cm_device.cuh"
 #include "cm_internal.h"
 #include "cm_launch.cuh"
 #include "cm_vec.cuh"
@@ -139,7 +137,7 @@ __device__ __forceinline__ uint64_t greater(uint64_t a, uint64_t b) { return a <
 
 // One key a thread, bitonic: partners less than a warp apart by shuffles, the
 // others through shared memory.
-__global__ void __launch_bounds__(kSortTile) cm_embedding_sort_kernel(const Ids ids, int64_t tokens, uint64_t *keys) {
+__global__ void __launch_bounds__(kSortTile) cm_embedding_sort_kernel(const Ids ids, int64_t tokens, uint64_t *keys, uint32_t *rows) {
     __shared__ uint64_t s[kSortTile];
     let_next_start();
     wait_for_previous();
@@ -161,64 +159,66 @@ __global__ void __launch_bounds__(kSortTile) cm_embedding_sort_kernel(const Ids 
             const bool low = (i & d) == 0, up = (i & size) == 0;   // up: ascending (all of it in the last round)
             k = low == up ? lesser(k, other) : greater(k, other);
         }
-    if (t < tokens) keys[t] = k;
+    if (t < tokens) keys[t] = k, rows[t] = uint32_t(k >> 32);
 }
 
-// Keys of in[0 .. n) that are smaller than k.
-__device__ __forceinline__ uint32_t smaller(const uint64_t *in, uint32_t n, uint64_t k) {
-    uint32_t lo = 0;
-    while (n > 0) {
-        const uint32_t half = n >> 1;
-        const bool right = in[lo + half] < k;
-        lo = right ? lo + half + 1 : lo;
-        n = right ? n - half - 1 : half;
-    }
-    return lo;
-}
-
-// Groups of up to kMergeRuns sorted runs of `run` keys (a power of two) become one
-// run each.  Earlier runs hold earlier tokens: of equal rows theirs come first, so rows
-// alone are compared.  A group of the first round is bisected in shared memory
-// (kShared: its rows, 128 KB at most; 16384 tokens: 8 us, in global memory 21 to 28).
-template <bool kShared>
-__global__ void __launch_bounds__(kMergeThreads) cm_embedding_merge_kernel(const uint64_t *in, uint64_t *out, int64_t tokens,
-                                                                           int64_t run) {
-    extern __shared__ uint32_t rows[];
+// Groups of up to 32 sorted runs of `run` keys (a power of two) become one run each.
+// Earlier runs hold earlier tokens: of equal rows theirs come first, so rows alone are
+// compared.  Of each run 32 rows at equal distances lie in shared memory, where a
+// bisection begins; in the first round the 32 rows that are left of a run are one line
+// of cache.  A thread bisects eight runs at a time, whose loads do not wait for one
+// another.
+constexpr int kSamples = 32;
+__global__ void __launch_bounds__(kMergeThreads) cm_embedding_merge_kernel(const uint64_t *in, const uint32_t *rows_in, uint64_t *out,
+                                                                           uint32_t *rows_out, uint32_t tokens, uint32_t run) {
+    __shared__ uint32_t sample[kMergeRuns * kSamples];
     let_next_start();
     wait_for_previous();
     // run is a multiple of a CTA's keys: they all lie in one run
-    const int64_t i0 = int64_t(blockIdx.x) * kMergeThreads, i = i0 + threadIdx.x;
-    const int own = int(i0 / run % kMergeRuns);
-    const int64_t base = i0 / run / kMergeRuns * kMergeRuns * run;
-    const int64_t n = min(tokens - base, int64_t(kMergeRuns) * run);   // keys of the group
-    if (kShared) {
-        for (int j = int(threadIdx.x); j < int(n); j += kMergeThreads) rows[j] = uint32_t(in[base + j] >> 32);
-        __syncthreads();
+    const uint32_t i0 = blockIdx.x * kMergeThreads, i = i0 + threadIdx.x;
+    const uint32_t own = i0 / run % kMergeRuns, base = (i0 / run - own) * run, stride = run / kSamples;
+    const int shift = __ffs(int(stride)) - 1;
+    const uint32_t n = min(uint64_t(tokens - base), uint64_t(kMergeRuns) * run);   // keys of the group
+    const uint32_t *const rows = rows_in + base;
+#pragma unroll
+    for (uint32_t j = threadIdx.x; j < kMergeRuns * kSamples; j += kMergeThreads) {
+        const uint64_t at = uint64_t(j + 1) * stride - 1;
+        sample[j] = at < n ? rows[at] : 0u;
     }
+    __syncthreads();
     if (i >= tokens) return;
     const uint64_t k = in[i];
     const uint32_t row = uint32_t(k >> 32);
-    int64_t place = i - base - own * run;
-    constexpr int kAtOnce = 8;   // runs whose bisections do not wait for one another
-    for (int r0 = 0; int64_t(r0) * run < n; r0 += kAtOnce) {
+    uint32_t place = i - base - own * run;
+    constexpr uint32_t kAtOnce = 8;
+    for (uint32_t r0 = 0; r0 < kMergeRuns && uint64_t(r0) * run < n; r0 += kAtOnce) {
         uint32_t at[kAtOnce], left[kAtOnce];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (uint32_t j = 0; j < kAtOnce; ++j) {
+            const uint64_t first = uint64_t(r0 + j) * run;
             at[j] = 0;
-            left[j] = r0 + j == own ? 0u : uint32_t(max(int64_t(0), min(run, n - (r0 + j) * run)));
+            left[j] = r0 + j == own || first >= n ? 0u : min(run, n - uint32_t(first));
         }
-        for (uint32_t step = uint32_t(run); step; step >>= 1)
+        uint32_t step = run;
+        for (; step >= stride; step >>= 1)
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
+            for (uint32_t j = 0; j < kAtOnce; ++j) {
                 if (at[j] + step > left[j]) continue;
-                const int64_t b = int64_t(r0 + j) * run + at[j] + step - 1;
-                const uint32_t other = kShared ? rows[b] : uint32_t(in[base + b] >> 32);
-                if (other < row || (other == row && r0 + j < own)) at[j] += step;
+                const uint32_t other = sample[(r0 + j) * kSamples + ((at[j] + step) >> shift) - 1];
+                if (other < row || (r0 + j < own && other == row)) at[j] += step;
+            }
+        for (; step; step >>= 1)
+#pragma unroll
+            for (uint32_t j = 0; j < kAtOnce; ++j) {
+                if (at[j] + step > left[j]) continue;
+                const uint32_t other = rows[(r0 + j) * run + at[j] + step - 1];
+                if (other < row || (r0 + j < own && other == row)) at[j] += step;
             }
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) place += at[j];
+        for (uint32_t j = 0; j < kAtOnce; ++j) place += at[j];
     }
     out[base + place] = k;
+    rows_out[base + place] = row;
 }
 
 // ---- sums of rows -------------------------------------------------------------------
@@ -231,7 +231,7 @@ struct SumParams {
     int h;
     float scale;
     int accumulate;
-    int64_t sum_ctas, zero_ctas;   // that sum, and that write zeros
+    int64_t sum_ctas;
 };
 
 constexpr int kPiece = 16;                 // sorted tokens of a warp
@@ -253,62 +253,65 @@ __device__ __forceinline__ void put_row(const SumParams &p, const V8 &acc, const
     put8<VEC>(static_cast<DW *>(p.dw) + int64_t(row) * p.lddw, c, p.h, v);
 }
 
-// Rows of dw without a token, 64 to a CTA: zeros.  Rows of whole 16-byte pieces are
-// written by bulk copies of a block of zeros, the others element by element.
-constexpr int kZeroRows = 64, kZeroBytes = 8192;
+// Rows of dw without a token: zeros.  A warp a row, which it looks up among the sorted
+// tokens, 32 probes a round.  A launch of its own with little in it but stores, and CTAs
+// that leave as soon as theirs are out, so that the SMs write one moving front:
+// 131072 x 4096 fp32 in 290 us (a memset takes 277); with 32 rows a warp it was 359, with
+// rows a persistent CTA's 320 to 500.
 template <typename DW, bool VEC>
-__device__ void zero_absent(const SumParams &p, int64_t v0) {
-    __shared__ unsigned long long seen;
-    __shared__ int64_t bounds[2];
-    __shared__ __align__(128) uint4 zeros[VEC ? kZeroBytes / 16 : 1];
-    const int n = int(min(int64_t(kZeroRows), p.rows - v0));
-    if (threadIdx.x == 0) seen = 0;
-    if (threadIdx.x < 2) {   // first sorted token of row v0, and of the row behind the last
-        const uint64_t k = uint64_t(v0 + (threadIdx.x ? n : 0)) << 32;
-        bounds[threadIdx.x] = smaller(p.keys, uint32_t(p.tokens), k);
-    }
-    if (VEC)
-        for (int i = threadIdx.x; i < kZeroBytes / 16; i += blockDim.x) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    for (int64_t i = bounds[0] + threadIdx.x; i < bounds[1]; i += blockDim.x)
-        if (i == bounds[0] || row_at(p, i) != row_at(p, i - 1)) atomicOr(&seen, 1ull << (row_at(p, i) - v0));
-    if (VEC) dev::fence_proxy_async_smem();
-    __syncthreads();
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    const int64_t bytes = int64_t(p.h) * int64_t(sizeof(DW));
-    if (VEC && bytes % 16 == 0) {
-        if (warp) return;
-        for (int r = lane; r < n; r += 32) {
-            if (seen >> r & 1) continue;
-            uint8_t *row = static_cast<uint8_t *>(p.dw) + (v0 + r) * p.lddw * int64_t(sizeof(DW));
-            for (int64_t at = 0; at < bytes; at += kZeroBytes)
-                dev::bulk_store(row + at, zeros, uint32_t(min(bytes - at, int64_t(kZeroBytes))));
-        }
-        dev::bulk_commit();
-        dev::bulk_wait<0>();
-        return;
-    }
-    const V8 zero = fill(0.0f);
-    for (int r = warp; r < n; r += int(blockDim.x) >> 5) {
-        if (seen >> r & 1) continue;
-        DW *row = static_cast<DW *>(p.dw) + (v0 + r) * p.lddw;
-        for (int c = lane * 8; c < p.h; c += 256) put8<VEC>(row, c, p.h, zero);
-    }
-}
-
-// A warp for each aligned piece of 16 sorted tokens and 256 columns.  The CTAs that write
-// zeros lie between those that sum, so that one's stores cover the other's latencies.
-template <typename DY, typename DW, bool VEC>
-__global__ void __launch_bounds__(256) cm_embedding_sum_kernel(const SumParams p) {
+__global__ void __launch_bounds__(256) cm_embedding_zero_kernel(const SumParams p) {
     let_next_start();
     wait_for_previous();
-    const int64_t zeros_before = int64_t(blockIdx.x) * p.zero_ctas / gridDim.x;
-    if ((int64_t(blockIdx.x) + 1) * p.zero_ctas / gridDim.x > zeros_before) {
-        zero_absent<DW, VEC>(p, zeros_before * kZeroRows);
-        return;
+    const int lane = int(threadIdx.x) & 31;
+    const int64_t v = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (v >= p.rows) return;
+    int64_t lo = 0, n = p.tokens;   // rows of tokens [.. lo) are smaller, of [lo + n ..) not
+    while (n > 0) {
+        const int64_t step = (n + 31) / 32, at = min(n, int64_t(lane + 1) * step) - 1;   // probes repeat at the end
+        const uint32_t row = row_at(p, lo + at);
+        if (__any_sync(0xffffffffu, row == v)) return;
+        const int64_t right = min(n, __popc(__ballot_sync(0xffffffffu, row < v)) * step);
+        lo += right;
+        n = min(step - 1, n - right);
     }
+    constexpr int kPer = 16 / int(sizeof(DW));
+    const int whole = VEC ? p.h / kPer : 0;   // 16-byte pieces of a row
+    DW *row = static_cast<DW *>(p.dw) + v * p.lddw;
+#pragma unroll 8
+    for (int i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(row)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int c = whole * kPer + lane; c < p.h; c += 32) from_f(row + c, 0.0f);
+}
+
+// Eight neighbouring elements as they were loaded: of bf16 half the registers of the
+// numbers, so that more warps fit on an SM.
+template <typename T, bool VEC>
+struct Raw8 {
+    V8 v;
+    __device__ __forceinline__ void load(const T *row, int c, int h) { v = get8<VEC>(row, c, h); }
+    __device__ __forceinline__ V8 get() const { return v; }
+};
+template <>
+struct Raw8<bf16, true> {
+    uint4 w;
+    __device__ __forceinline__ void load(const bf16 *row, int c, int h) {
+        if (c + 8 <= h) {
+            w = *reinterpret_cast<const uint4 *>(row + c);
+            return;
+        }
+        const V8 v = load_row8(row, c, h);
+        w = make_uint4(pack(v.p[0]), pack(v.p[1]), pack(v.p[2]), pack(v.p[3]));
+    }
+    __device__ __forceinline__ V8 get() const { return {{unpack(w.x), unpack(w.y), unpack(w.z), unpack(w.w)}}; }
+};
+
+// A warp for each aligned piece of 16 sorted tokens and 256 columns; ADD: dw is added to.
+// Four rows, and as many old ones of dw, are under way at a time.
+template <typename DY, typename DW, bool VEC, bool ADD>
+__global__ void __launch_bounds__(256, ADD || sizeof(DY) == 4 || !VEC ? 2 : 4) cm_embedding_sum_kernel(const SumParams p) {
+    let_next_start();
+    wait_for_previous();
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    const int64_t blocks = (p.h + 255) / 256, unit = (int64_t(blockIdx.x) - zeros_before) * 8 + warp, piece = unit / blocks;
+    const int64_t blocks = (p.h + 255) / 256, unit = int64_t(blockIdx.x) * 8 + warp, piece = unit / blocks;
     const int c = int(unit - piece * blocks) * 256 + lane * 8;
     const int64_t i0 = piece * kPiece, i = i0 + lane;
     if (i0 >= p.tokens) return;
@@ -326,15 +329,17 @@ __global__ void __launch_bounds__(256) cm_embedding_sum_kernel(const SumParams p
     // rows that go on in another piece: their parts go to the workspace
     const uint32_t apart = (from_before ? last & (0u - last) : 0u) | (into_next ? 1u << (kPiece - 1) : 0u);
     V8 acc = fill(0.0f);
+#pragma unroll 1
     for (int j = 0; j < n; j += kAtOnce) {
-        V8 v[kAtOnce], old[kAtOnce];
+        Raw8<DY, VEC> v[kAtOnce];
+        [[maybe_unused]] V8 old[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
             const uint32_t t = __shfl_sync(0xffffffffu, token, j + k), r = __shfl_sync(0xffffffffu, row, j + k);
-            v[k] = old[k] = fill(0.0f);
             if (j + k >= n || c >= p.h) continue;
-            v[k] = get8<VEC>(static_cast<const DY *>(p.dy) + int64_t(t) * p.lddy, c, p.h);
-            if (p.accumulate && ((last & ~apart) >> (j + k) & 1)) old[k] = old_row<VEC, DW>(p, r, c);
+            v[k].load(static_cast<const DY *>(p.dy) + int64_t(t) * p.lddy, c, p.h);
+            if constexpr (ADD)
+                if ((last & ~apart) >> (j + k) & 1) old[k] = old_row<VEC, DW>(p, r, c);
         }
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
@@ -342,12 +347,15 @@ __global__ void __launch_bounds__(256) cm_embedding_sum_kernel(const SumParams p
             const uint32_t r = __shfl_sync(0xffffffffu, row, at);
             if (at >= n || c >= p.h) continue;
             if (first >> at & 1) acc = fill(0.0f);
-            add_to(acc, v[k]);
+            add_to(acc, v[k].get());
             if (!(last >> at & 1)) continue;
-            if (apart >> at & 1)   // the piece's first row, where it came from before; else the last, which goes on
+            if (apart >> at & 1) {   // the piece's first row, where it came from before; else the last, which goes on
                 store8(part_at(p, piece, from_before && (last & ((1u << at) - 1)) == 0 ? 0 : 1, c), acc);
-            else
-                put_row<VEC, DW>(p, acc, old[k], r, c);
+                continue;
+            }
+            V8 sum = scaled(acc, p.scale);
+            if constexpr (ADD) add_to(sum, old[k]);
+            put8<VEC>(static_cast<DW *>(p.dw) + int64_t(r) * p.lddw, c, p.h, sum);
         }
     }
 }
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(256) cm_embedding_sum_kernel(const SumParams p
 // The sum of parts k0 .. k1 - 1, in order, of the row that goes on from `piece` into
 // the next: that piece's second part, and the first ones of the pieces behind.
 __device__ __forceinline__ V8 add_parts(const SumParams &p, int64_t piece, int64_t k0, int64_t k1, int c) {
-    constexpr int kParts = 8;
+    constexpr int kParts = 4;
     V8 acc = fill(0.0f);
     for (int64_t k = k0; k < k1; k += kParts) {
         V8 v[kParts];
@@ -370,18 +378,19 @@ __device__ __forceinline__ V8 add_parts(const SumParams &p, int64_t piece, int64
     return acc;
 }
 
-// The rows that lie in several pieces.  A CTA looks at 32 pieces, a lane at each, for
+// The rows that lie in several pieces.  A CTA looks at 16 pieces, a lane at each, for
 // rows that begin there and go on; columns of 256.  A warp adds the parts of up to
 // 32 pieces; longer rows are shared by the CTA's warps, each with a run of their parts.
+constexpr int kJoinPieces = 16;
 template <typename DW, bool VEC>
-__global__ void __launch_bounds__(256) cm_embedding_join_kernel(const SumParams p) {
+__global__ void __launch_bounds__(256, 3) cm_embedding_join_kernel(const SumParams p) {
     __shared__ V8 sums[8][32];
     let_next_start();
     wait_for_previous();
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31, c = int(blockIdx.y) * 256 + lane * 8;
-    const int64_t piece0 = int64_t(blockIdx.x) * 32, end = (piece0 + lane + 1) * kPiece;   // of the lane's piece
+    const int64_t piece0 = int64_t(blockIdx.x) * kJoinPieces, end = (piece0 + lane + 1) * kPiece;   // of the lane's piece
     uint32_t row = kNoRow;
-    if (end < p.tokens) {
+    if (lane < kJoinPieces && end < p.tokens) {
         row = row_at(p, end);
         if (row_at(p, end - 1) != row) row = kNoRow;
         // began earlier
@@ -453,52 +462,53 @@ cudaError_t lookup(const LookupParams &p, bool vec, cudaStream_t stream) {
     return launch_after(vec ? cm_embedding_kernel<W, Y, true> : cm_embedding_kernel<W, Y, false>, grid, kLookThreads, 0, 1, stream, p);
 }
 
-// The workspace: keys twice, then the parts.
-size_t key_bytes(int64_t tokens) { return (size_t(tokens) * sizeof(uint64_t) + 255) / 256 * 256; }
-size_t backward_workspace(int64_t tokens, int64_t h) {
+// The workspace: keys and their rows twice, then the parts.
+struct Space {
+    uint64_t *keys[2];
+    uint32_t *rows[2];
+    float *parts;
+    size_t bytes;
+};
+Space backward_space(void *ws, int64_t tokens, int64_t h) {
+    Space s;
+    uint8_t *const base = static_cast<uint8_t *>(ws);
+    size_t used = 0;
+    const auto take = [&](size_t bytes) {
+        void *const at = base + used;
+        used += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    for (auto &k : s.keys) k = static_cast<uint64_t *>(take(size_t(tokens) * 8));
+    for (auto &r : s.rows) r = static_cast<uint32_t *>(take(size_t(tokens) * 4));
     // one piece has no neighbours
-    const size_t parts = tokens > kPiece ? size_t((tokens + kPiece - 1) / kPiece) * 2 * size_t((h + 7) / 8 * 8) * sizeof(float) : 0;
-    return 2 * key_bytes(tokens) + parts + 256;
+    s.parts = static_cast<float *>(take(tokens > kPiece ? size_t((tokens + kPiece - 1) / kPiece) * 2 * size_t((h + 7) / 8 * 8) * 4 : 256));
+    s.bytes = used;
+    return s;
 }
 
-// Leave to use more than 48 KB of shared memory; asked for once a device.
-cudaError_t allow_shared() {
-    static std::atomic<uint64_t> done{0};
-    int device = 0;
-    const cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess || (device < 64 && (done.load(std::memory_order_relaxed) >> device & 1))) return e;
-    const cudaError_t set = cudaFuncSetAttribute(cm_embedding_merge_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 kMergeRuns * kSortTile * int(sizeof(uint32_t)));
-    if (set == cudaSuccess && device < 64) done.fetch_or(uint64_t(1) << device, std::memory_order_relaxed);
-    return set;
-}
-
-// Sorted keys of all tokens; in either half of the workspace.
-cudaError_t sort_tokens(const Ids &ids, int64_t tokens, uint64_t *a, uint64_t *b, const uint64_t **sorted, cudaStream_t stream) {
+// Sorted keys of all tokens, in either half of the workspace.
+cudaError_t sort_tokens(const Ids &ids, int64_t tokens, const Space &s, const uint64_t **sorted, cudaStream_t stream) {
     cudaError_t e = launch_after(cm_embedding_sort_kernel, dim3(unsigned((tokens + kSortTile - 1) / kSortTile)), kSortTile, 0, 1,
-                                 stream, ids, tokens, a);
-    for (int64_t run = kSortTile; run < tokens && e == cudaSuccess; run *= kMergeRuns) {
-        const dim3 grid(unsigned((tokens + kMergeThreads - 1) / kMergeThreads));
-        const size_t smem = size_t(std::min<int64_t>(tokens, kMergeRuns * kSortTile)) * sizeof(uint32_t);
-        if (run > kSortTile)
-            e = launch_after(cm_embedding_merge_kernel<false>, grid, kMergeThreads, 0, 1, stream, static_cast<const uint64_t *>(a), b,
-                             tokens, run);
-        else if (smem <= 48 * 1024 || (e = allow_shared()) == cudaSuccess)
-            e = launch_after(cm_embedding_merge_kernel<true>, grid, kMergeThreads, smem, 1, stream, static_cast<const uint64_t *>(a), b,
-                             tokens, run);
-        std::swap(a, b);
-    }
-    *sorted = a;
+                                 stream, ids, tokens, s.keys[0], s.rows[0]);
+    int at = 0;
+    for (int64_t run = kSortTile; run < tokens && e == cudaSuccess; run *= kMergeRuns, at ^= 1)
+        e = launch_after(cm_embedding_merge_kernel, dim3(unsigned((tokens + kMergeThreads - 1) / kMergeThreads)), kMergeThreads,
+                         0, 1, stream, static_cast<const uint64_t *>(s.keys[at]), static_cast<const uint32_t *>(s.rows[at]),
+                         s.keys[at ^ 1], s.rows[at ^ 1], uint32_t(tokens), uint32_t(run));
+    *sorted = s.keys[at];
     return e;
 }
 
 template <typename DY, typename DW, bool VEC>
 cudaError_t sum_rows(const SumParams &p, cudaStream_t stream) {
-    const cudaError_t e =
-        launch_after(cm_embedding_sum_kernel<DY, DW, VEC>, dim3(unsigned(p.sum_ctas + p.zero_ctas)), 256, 0, 1, stream, p);
+    cudaError_t e = cudaSuccess;
+    if (!p.accumulate) e = launch_after(cm_embedding_zero_kernel<DW, VEC>, dim3(unsigned((p.rows + 7) / 8)), 256, 0, 1, stream, p);
+    if (e == cudaSuccess)
+        e = launch_after(p.accumulate ? cm_embedding_sum_kernel<DY, DW, VEC, true> : cm_embedding_sum_kernel<DY, DW, VEC, false>,
+                         dim3(unsigned(p.sum_ctas)), 256, 0, 1, stream, p);
     if (e != cudaSuccess || p.tokens <= kPiece) return e;
-    return launch_after(cm_embedding_join_kernel<DW, VEC>, dim3(unsigned((p.tokens + 32 * kPiece - 1) / (32 * kPiece)), unsigned((p.h + 255) / 256)), 256,
-                        0, 1, stream, p);
+    return launch_after(cm_embedding_join_kernel<DW, VEC>,
+                        dim3(unsigned((p.tokens + kJoinPieces * kPiece - 1) / (kJoinPieces * kPiece)), unsigned((p.h + 255) / 256)), 256, 0, 1, stream, p);
 }
 
 template <typename DY, typename DW>
@@ -542,7 +552,7 @@ cm_status cm_embedding(const void *ids, int id_bits, int64_t first, const void *
 }
 
 size_t cm_embedding_backward_workspace_size(int64_t tokens, int64_t h) {
-    return check_extents(tokens, 1, h) == CM_OK ? backward_workspace(tokens, h) : 0;
+    return check_extents(tokens, 1, h) == CM_OK ? backward_space(nullptr, tokens, h).bytes : 0;
 }
 
 cm_status cm_embedding_backward(const void *dy, cm_dtype dy_dtype, int64_t lddy, const void *ids, int id_bits, int64_t first,
@@ -561,20 +571,17 @@ cm_status cm_embedding_backward(const void *dy, cm_dtype dy_dtype, int64_t lddy,
     }
     CM_TRY(check_ids(ids, id_bits, first));
     CM_TRY(check_rows(dy, dy_dtype, lddy, h));
-    if (!ws || ws_bytes < backward_workspace(tokens, h)) return CM_ERR_WORKSPACE;
+    const Space space = backward_space(ws, tokens, h);
+    if (!ws || ws_bytes < space.bytes) return CM_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0) return CM_ERR_ALIGNMENT;
     const int64_t blocks = (h + 255) / 256;
     SumParams p = {};
     p.sum_ctas = ((tokens + kPiece - 1) / kPiece * blocks + 7) / 8;
-    p.zero_ctas = accumulate ? 0 : (n + kZeroRows - 1) / kZeroRows;
-    if (h > kMostColumns || p.sum_ctas + p.zero_ctas > 0x7fffffff) return CM_ERR_SHAPE;
-    uint8_t *base = static_cast<uint8_t *>(ws);
-    if (sort_tokens({ids, first, n, id_bits}, tokens, reinterpret_cast<uint64_t *>(base),
-                    reinterpret_cast<uint64_t *>(base + key_bytes(tokens)), &p.keys, stream) != cudaSuccess)
-        return CM_ERR_CUDA;
+    if (h > kMostColumns || p.sum_ctas > 0x7fffffff) return CM_ERR_SHAPE;
+    if (sort_tokens({ids, first, n, id_bits}, tokens, space, &p.keys, stream) != cudaSuccess) return CM_ERR_CUDA;
     p.dy = dy;
     p.dw = dw;
-    p.parts = reinterpret_cast<float *>(base + 2 * key_bytes(tokens));
+    p.parts = space.parts;
     p.lddy = lddy;
     p.lddw = lddw;
     p.tokens = tokens;

@@ -31,7 +31,7 @@ __device__ __forceinline__ float larger(float a, float b) {
     return b <= 3.0e38f ? fmaxf(a, b) : a;
 }
 
-// A CTA places 8 to 64 rows (`per`: 1003 rows of 4101 elements in 64s 86 us, on 16
+// A CTA places 4 to 64 rows (`per`: 1003 rows of 4101 elements in 64s 86 us, on 16
 // SMs).  It counts all rows' targets itself, which costs a pass over them from L2
 // (rows^2 / per of them in all, little beside the products' rows K n), and saves a
 // launch and a scan across CTAs.
@@ -108,18 +108,18 @@ __global__ void __launch_bounds__(kRowsThreads) cm_head_rows_kernel(const HeadRo
     const int K = int(p.K), nv = (K + 7) / 8;
     const bf16 *x = static_cast<const bf16 *>(p.x);
     bf16 *xs = static_cast<bf16 *>(p.xs);
-    for (int i = warp; i < int(r1 - r0); i += kRowsThreads / 32) {
-        if (slots[i] < 0) continue;
-        const bf16 *from = x + (r0 + i) * p.ldx;
-        bf16 *to = xs + int64_t(slots[i]) * p.ldxs;
-        for (int v = lane; v < nv; v += 128) {   // four loads before the first store
-            V8 f[4];
+    const int total = int(r1 - r0) * nv;
+    for (int at = int(threadIdx.x); at < total; at += 4 * kRowsThreads) {   // four loads before the first store
+        V8 f[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (v + 32 * k < nv) f[k] = load_row8(from, (v + 32 * k) * 8, K);
+        for (int k = 0; k < 4; ++k) {
+            const int j = at + k * kRowsThreads, i = j / nv;
+            if (j < total && slots[i] >= 0) f[k] = load_row8(x + (r0 + i) * p.ldx, (j - i * nv) * 8, K);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (v + 32 * k < nv) store_row8(to, (v + 32 * k) * 8, K, f[k]);
+        for (int k = 0; k < 4; ++k) {
+            const int j = at + k * kRowsThreads, i = j / nv;
+            if (j < total && slots[i] >= 0) store_row8(xs + int64_t(slots[i]) * p.ldxs, (j - i * nv) * 8, K, f[k]);
         }
     }
     // zeros behind the last slot: where a product's contraction reads on to its slice's end
@@ -172,25 +172,25 @@ template <typename T>
 __global__ void __launch_bounds__(256) cm_head_scatter_kernel(const HeadScatter p) {
     let_next_start();
     wait_for_previous();
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31, K = int(p.K);
-    const int64_t row = int64_t(blockIdx.x) * 8 + warp;
+    const int half = int(threadIdx.x) >> 7, at = int(threadIdx.x) & 127, K = int(p.K);
+    const int64_t row = int64_t(blockIdx.x) * 2 + half;
     if (row >= p.rows) return;
     const int32_t slot = p.slot_of[row];
     const float scale = *p.scale;
     T *to = static_cast<T *>(p.dx) + row * p.lddx;
     const float *from = p.sum + int64_t(max(slot, 0)) * p.ld;
-    for (int c = lane * 8; c < K; c += 1024) {
+    for (int c = at * 8; c < K; c += 4096) {
         V8 f[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             f[k] = fill(0.0f);
-            if (slot >= 0 && c + 256 * k < K) f[k] = load_row8(from, c + 256 * k, K);
+            if (slot >= 0 && c + 1024 * k < K) f[k] = load_row8(from, c + 1024 * k, K);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[k].p[i] = mul(f[k].p[i], both(scale));
-            if (c + 256 * k < K) store_row8(to, c + 256 * k, K, f[k]);
+            if (c + 1024 * k < K) store_row8(to, c + 1024 * k, K, f[k]);
         }
     }
 }
@@ -198,14 +198,14 @@ __global__ void __launch_bounds__(256) cm_head_scatter_kernel(const HeadScatter 
 }  // namespace
 
 cudaError_t launch_head_rows(const HeadRows &p, cudaStream_t stream) {
-    const int per = int(std::max<int64_t>(8, std::min<int64_t>(kRowsMost, p.rows / 512 / 8 * 8)));
+    const int per = int(std::max<int64_t>(4, std::min<int64_t>(kRowsMost, p.rows / 512 / 4 * 4)));
     return launch_after(cm_head_rows_kernel, dim3(unsigned((p.rows + per - 1) / per)), kRowsThreads, 0, 1, stream, p, per);
 }
 cudaError_t launch_head_join(const HeadJoin &p, cudaStream_t stream) {
     return launch_after(cm_head_join_kernel, dim3(unsigned((p.stride + 31) / 32)), 32 * kJoinWarps, 0, 1, stream, p);
 }
 cudaError_t launch_head_scatter(const HeadScatter &p, cudaStream_t stream) {
-    return launch_after(p.dx_f32 ? cm_head_scatter_kernel<float> : cm_head_scatter_kernel<bf16>, dim3(unsigned((p.rows + 7) / 8)), 256, 0,
+    return launch_after(p.dx_f32 ? cm_head_scatter_kernel<float> : cm_head_scatter_kernel<bf16>, dim3(unsigned((p.rows + 1) / 2)), 256, 0,
                         1, stream, p);
 }
 

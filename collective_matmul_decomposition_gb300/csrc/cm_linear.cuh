@@ -137,6 +137,10 @@ cudaError_t prepare_linear_pair(int sms, int *clusters);
 cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode mode, int splits, int clusters,
                                cudaStream_t stream);
 
+// Two plain products of 256-column tiles in one launch, the first of layout 0 or 1 with
+// an fp32 y, the second of layout 3.
+cudaError_t launch_linear_two(const LinearPairParams &p0, int layout0, const LinearPairParams &p1, int clusters, cudaStream_t stream);
+
 // Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu): partial
 // sums per row chunk in `partial`, then their sum in chunk order.
 int64_t colsum_chunks(int64_t rows, int64_t cols);

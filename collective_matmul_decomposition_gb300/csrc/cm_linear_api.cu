@@ -225,10 +225,9 @@ struct Kind {
     LinearHead head = {};
 };
 
-cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b, int64_t rows,
-                       int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
+cm_status pair_params(LinearPairParams &p, const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b,
+                      int64_t rows, int64_t cols, int64_t k, const LinearEpilogue &e) {
     const LinearMode mode = kind.mode;
-    LinearPairParams p;
     p.e = e;
     p.live = kind.live;
     p.head = kind.head;
@@ -265,6 +264,15 @@ cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const
         if (e.res && !map_rows(&p.tmIn0, e.res, rows, cols, e.ldr, 32)) return CM_ERR_CUDA;
         if (e.dact && !map_rows(&p.tmIn1, e.zin, rows, cols, e.ldzin, 32)) return CM_ERR_CUDA;
     }
+    return CM_OK;
+}
+
+cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b, int64_t rows,
+                       int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
+    LinearPairParams p;
+    const cm_status st = pair_params(p, d, c, kind, a, b, rows, cols, k, e);
+    if (st != CM_OK) return st;
+    const LinearMode mode = kind.mode;
     const int layout = (a.mn_major ? 1 : 0) | (b.mn_major ? 2 : 0);
     return launch_linear_pair(p, layout, mode, c.splits, d.clusters[0], stream) == cudaSuccess ? CM_OK : CM_ERR_CUDA;
 }
@@ -323,7 +331,8 @@ struct Carve {
     }
 };
 
-int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+// Whole 128-byte lines: the rows of a box that a product loads then do not straddle them.
+int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 
 struct LossSpace {
     int32_t *count, *row_of, *target;
@@ -337,7 +346,7 @@ LossSpace loss_space(Carve &c, int64_t M, int64_t K, int64_t n) {
     s.row_of = c.take<int32_t>(size_t(M));
     s.target = c.take<int32_t>(size_t(M));
     s.picked = c.take<float>(size_t(M));
-    s.xs = c.take<uint16_t>(size_t(M) * size_t(up8(K)));
+    s.xs = c.take<uint16_t>(size_t(M) * size_t(up64(K)));
     s.stat = c.take<float2>(size_t((n + 255) / 256 * 2) * size_t(M));
     return s;
 }
@@ -361,8 +370,8 @@ struct LossGradSpace {
 LossGradSpace loss_grad_space(Carve &c, int64_t M, int64_t K, int64_t n) {
     LossGradSpace s;
     s.columns = loss_grad_columns(M, n);
-    s.ldp = up8(s.columns);
-    s.lds = up8(K);
+    s.ldp = up64(s.columns);
+    s.lds = up64(K);
     s.count = c.take<int32_t>(1);
     s.scale = c.take<float>(1);
     s.slot_of = c.take<int32_t>(size_t(M));
@@ -606,7 +615,7 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
     r.x = x;
     r.ldx = ldx;
     r.xs = s.xs;
-    r.ldxs = up8(K);
+    r.ldxs = up64(K);
     r.count = s.count;
     r.row_of = s.row_of;
     r.target = s.target;
@@ -617,7 +626,7 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
     const Choice c = choose_logits(d, M, n, K);
     r.always = !c.pair;
     if (launch_head_rows(r, stream) != cudaSuccess) return CM_ERR_CUDA;
-    const Operand rows = {s.xs, up8(K), false}, all = {x, ldx, false};
+    const Operand rows = {s.xs, up64(K), false}, all = {x, ldx, false};
     Kind kind;
     kind.mode = kLinStats;
     kind.live = {s.count, 1, 0, 1, M};
@@ -718,34 +727,35 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
         const Operand weights = {wc, ldw, !nk};
         CM_TRY(cp.pair ? product_pair(d, cp, kind, weights, rows, M, cols, K, e, stream)
                        : product_strip(d, cp, kind, weights, rows, M, cols, K, e, stream));
-        if (dx) {
-            e = {};
-            e.y = s.sum;
-            e.ldy = s.lds;
-            e.y_f32 = 1;
-            e.accumulate = c0 > 0;
-            const Operand a = {wc, ldw, nk}, b = {s.p, s.ldp, false};
-            Kind plain;
-            if (counted) plain.live = {s.count, 1, 0, 0, M};
-            CM_TRY(counted ? product_pair(d, cx, plain, a, b, M, K, cols, e, stream) : product(d, a, b, M, K, cols, e, stream));
+        // dx's part of the chunk, added up in fp32, and the chunk's rows (columns) of dw
+        LinearEpilogue ex = {}, ew = {};
+        ex.y = s.sum;
+        ex.ldy = s.lds;
+        ex.y_f32 = 1;
+        ex.accumulate = c0 > 0;
+        ew.y = static_cast<uint8_t *>(dw) + (nk ? c0 * lddw : c0) * (dw_dtype == CM_F32 ? 4 : 2);
+        ew.ldy = lddw;
+        ew.y_f32 = dw_dtype == CM_F32;
+        ew.accumulate = accumulate != 0;
+        ew.scale = s.scale;
+        const Operand ax = {wc, ldw, nk}, bx = {s.p, s.ldp, false}, pt = {s.p, s.ldp, true};
+        const Operand &aw = nk ? rows_t : pt, &bw = nk ? pt : rows_t;
+        const int64_t dr = nk ? cols : K, dc = nk ? K : cols;
+        Kind kx, kw;
+        if (counted) {
+            kx.live = {s.count, 1, 0, 0, M};
+            kw.live = {s.count, 0, 1, nk ? 2 : 1, M};
+            kw.whole = &all_t;
         }
-        if (dw) {
-            e = {};
-            e.y = static_cast<uint8_t *>(dw) + (nk ? c0 * lddw : c0) * (dw_dtype == CM_F32 ? 4 : 2);
-            e.ldy = lddw;
-            e.y_f32 = dw_dtype == CM_F32;
-            e.accumulate = accumulate != 0;
-            e.scale = s.scale;
-            const Operand pt = {s.p, s.ldp, true};
-            Kind plain;
-            if (counted) {
-                plain.live = {s.count, 0, 1, nk ? 2 : 1, M};
-                plain.whole = &all_t;
-            }
-            const int64_t dr = nk ? cols : K, dc = nk ? K : cols;
-            const Operand &a = nk ? rows_t : pt, &b = nk ? pt : rows_t;
-            CM_TRY(counted ? product_pair(d, cw, plain, a, b, dr, dc, M, e, stream) : product(d, a, b, dr, dc, M, e, stream));
+        if (dx && dw && counted && cx.bn == 256 && cw.bn == 256) {
+            LinearPairParams px, pw;
+            CM_TRY(pair_params(px, d, cx, kx, ax, bx, M, K, cols, ex));
+            CM_TRY(pair_params(pw, d, cw, kw, aw, bw, dr, dc, M, ew));
+            if (launch_linear_two(px, nk ? 1 : 0, pw, d.clusters[0], stream) != cudaSuccess) return CM_ERR_CUDA;
+            continue;
         }
+        if (dx) CM_TRY(counted ? product_pair(d, cx, kx, ax, bx, M, K, cols, ex, stream) : product(d, ax, bx, M, K, cols, ex, stream));
+        if (dw) CM_TRY(counted ? product_pair(d, cw, kw, aw, bw, dr, dc, M, ew, stream) : product(d, aw, bw, dr, dc, M, ew, stream));
     }
     if (!dx) return CM_OK;
     const HeadScatter g = {s.sum, s.lds, s.slot_of, s.scale, dx, dx_dtype == CM_F32, lddx, M, K};

@@ -155,6 +155,31 @@ __device__ __forceinline__ void mul_dact(float (&f)[N], const float (&z)[N], int
     }
 }
 
+// act(z) and act'(z) of a pair, by the same steps as act2 and dact2 but with their common
+// exponential and reciprocal taken once.
+template <int ACT>
+__device__ __forceinline__ F2 act_and_slope(F2 z, F2 &slope) {
+    if constexpr (ACT == CM_ACT_GELU) {
+        F2 e;
+        const F2 cdf = normal_cdf(z, e);
+        slope = fma(mul(z, both(0.3989422804014327f)), e, cdf);
+        return mul(z, cdf);
+    } else if constexpr (ACT == CM_ACT_GELU_TANH) {
+        const float2 sq = parts(mul(z, z));   // held as in dact2
+        const F2 z2 = pair(fminf(sq.x, 0x1p64f), fminf(sq.y, 0x1p64f)), s = gelu_tanh_gate(z, z2);
+        const F2 du = fma(z2, both(6.0f * kGeluC * kGeluA), both(2.0f * kGeluC)), zs = mul(z, s);
+        slope = fma(zs, mul(fma(s, both(-1.0f), both(1.0f)), du), s);
+        return zs;
+    } else if constexpr (ACT == CM_ACT_SILU) {
+        const F2 s = sigmoid_of(mul(z, both(-kLog2e)));
+        slope = mul(s, fma(z, fma(s, both(-1.0f), both(1.0f)), both(1.0f)));
+        return mul(z, s);
+    } else {
+        slope = dact2<ACT>(z);
+        return act2<ACT>(z);
+    }
+}
+
 // g becomes act(g) u.
 template <int ACT, int N>
 __device__ __forceinline__ void gate_loop(float (&g)[N], const float (&u)[N]) {
@@ -180,9 +205,10 @@ template <int ACT, int N>
 __device__ __forceinline__ void gate_grad_loop(const float (&d)[N], float (&g)[N], float (&u)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const F2 dd = pair(d[i], d[i + 1]), gg = pair(g[i], g[i + 1]);
-        const float2 dg = parts(mul(mul(dd, pair(u[i], u[i + 1])), dact2<ACT>(gg)));
-        const float2 du = parts(mul(dd, act2<ACT>(gg)));
+        const F2 dd = pair(d[i], d[i + 1]);
+        F2 slope;
+        const F2 a = act_and_slope<ACT>(pair(g[i], g[i + 1]), slope);
+        const float2 dg = parts(mul(mul(dd, pair(u[i], u[i + 1])), slope)), du = parts(mul(dd, a));
         g[i] = dg.x, g[i + 1] = dg.y;
         u[i] = du.x, u[i + 1] = du.y;
     }

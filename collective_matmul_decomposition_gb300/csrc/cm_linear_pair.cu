@@ -119,6 +119,16 @@ struct Share {
     const CUtensorMap *a, *b;   // the operands' maps
 };
 
+// Where a role stands in the ring of stages and in the two accumulators, from one
+// share to the next.
+struct Flow {
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    uint32_t issued = 0;      // of the loads
+    uint32_t in_phase = 0;    // of the epilogue's inputs
+    bool ok = true;           // no wait has expired
+};
+
 // A persistent kernel's share, cut down to the slots where they are counted.
 template <int MODE>
 __device__ __forceinline__ Share share_of(const LinearPairParams &p, int rank) {
@@ -144,15 +154,15 @@ __device__ __forceinline__ Share share_of(const LinearPairParams &p, int rank) {
 }
 
 template <int LAYOUT, int BN, int MODE>
-__device__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, int rank) {
+__device__ __forceinline__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, int rank, Flow &flow) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
     const uint32_t full_leader = mapa_shared(smem_u32(s.full), w.leader);
     const uint32_t a0 = smem_u32(s.a0), b0 = smem_u32(s.b0);
     const uint64_t tma = reinterpret_cast<uint64_t>(w.a), tmb = reinterpret_cast<uint64_t>(w.b);
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
-    bool ok = true;
+    int stage = flow.stage;
+    uint32_t phase = flow.phase, issued = flow.issued;
+    bool ok = flow.ok;
     for (int t = w.first; t < w.tiles && ok; t += w.step) {
         int mt, nt;
         tile_at(p, w.mtiles, t, mt, nt);
@@ -187,27 +197,35 @@ __device__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Shar
             }
         }
     }
-    // the leader's barriers count both CTAs' loads: once they complete no load
-    // is still writing this pair's shared memory
+    flow.stage = stage, flow.phase = phase, flow.issued = issued, flow.ok = ok;
+}
+
+// The leader's barriers count both CTAs' loads: once they complete no load
+// is still writing this pair's shared memory.
+template <int BN>
+__device__ __forceinline__ void drain_loads(const LinearPairParams &p, const LSmem &s, int rank, const Flow &flow) {
     if (rank == 0)
-        for (int i = 0; i < kStages; ++i)
-            if (uint32_t(i) < issued) drain_p(p, &s.full[i], i < stage ? phase : phase ^ 1u);
+        for (int i = 0; i < Tile<BN>::kStages; ++i)
+            if (uint32_t(i) < flow.issued) drain_p(p, &s.full[i], i < flow.stage ? flow.phase : flow.phase ^ 1u);
 }
 
 template <int LAYOUT, int BN>
-__device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem) {
+__device__ __forceinline__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, Flow &flow) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
     constexpr uint32_t kIdesc = idesc_bf16(kTile, BN, B_MN, A_MN);
     constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kBLbo = B_MN ? 64 * kBK * 2 : 16;
     constexpr uint32_t kAStep = A_MN ? (16 * 128) >> 4 : 32 >> 4, kBStep = B_MN ? (16 * 128) >> 4 : 32 >> 4;
     const uint64_t ad0 = desc_sw128(smem_u32(s.a0), kALbo, 1024), bd0 = desc_sw128(smem_u32(s.b0), kBLbo, 1024);
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    bool ok = true;
+    int stage = flow.stage, acc = flow.acc;
+    uint32_t phase = flow.phase, acc_phase = flow.acc_phase;
+    bool ok = flow.ok;
     const uint16_t both = uint16_t(3u << w.leader);   // the pair's CTAs
     for (int t = w.first; t < w.tiles && ok; t += w.step) {
-        if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) break;
+        if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) {
+            ok = false;
+            break;
+        }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * BN);
         bool ready = mbar_test_wait(s.full + stage, phase);   // looked at ahead, so that its latency overlaps the issue
@@ -236,6 +254,10 @@ __device__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, const 
             acc_phase ^= 1u;
         }
     }
+    flow.stage = stage, flow.phase = phase, flow.acc = acc, flow.acc_phase = acc_phase, flow.ok = ok;
+}
+
+__device__ __forceinline__ void drain_products(const LinearPairParams &p, const LSmem &s) {
     mma_commit_pair(s.drain);
     drain_p(p, s.drain, 0);
 }
@@ -293,7 +315,8 @@ __device__ __noinline__ void store_rest(const LinearPairParams &p, uint8_t *buf0
 
 // F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).  MODE: kLinPlain or kLinGateGrad.
 template <bool F32, int BN, int MODE>
-__device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+__device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank,
+                                             Flow &flow) {
     constexpr int kChunk = F32 ? 32 : 64, kCols = BN / 2;   // columns of a warp
     const LinearEpilogue &e = p.e;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
@@ -316,10 +339,10 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, const Sh
     constexpr int kPiece = F32 ? 4 : 8;
     const int rest = int(p.cols % kPiece);
     const int64_t whole = p.cols - rest;
-    int acc = 0;
-    uint32_t acc_phase = 0, in_phase = 0;
+    int acc = flow.acc;
+    uint32_t acc_phase = flow.acc_phase, in_phase = flow.in_phase;
     bool pending = false;   // inputs asked for and not yet waited for
-    bool ok = true;
+    bool ok = flow.ok;
     for (int t = w.first; t < w.tiles && ok; t += w.step) {
         int mt, nt;
         tile_at(p, w.mtiles, t, mt, nt);
@@ -493,6 +516,7 @@ __device__ void finish_tiles(const LinearPairParams &p, const LSmem &s, const Sh
         bulk_wait<0>();
     }
     __syncwarp();
+    flow.acc = acc, flow.acc_phase = acc_phase, flow.in_phase = in_phase, flow.ok = ok;
 }
 
 // The columns behind a row's last whole 16-byte piece, n of them, from element `at` of the buffer's row.
@@ -818,12 +842,21 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     const int warp = int(threadIdx.x) >> 5, rank = int(cluster_ctarank());
     const Share w = share_of<MODE>(p, rank);
     if (warp == 0) {
-        if (elect_one()) load_tiles<LAYOUT, BN, MODE>(p, s, w, rank);
+        if (elect_one()) {
+            Flow flow;
+            load_tiles<LAYOUT, BN, MODE>(p, s, w, rank, flow);
+            drain_loads<BN>(p, s, rank, flow);
+        }
         __syncwarp();
     } else if (warp == 1) {
-        if (rank == 0 && elect_one()) multiply_tiles<LAYOUT, BN>(p, s, w, tmem);
+        if (rank == 0 && elect_one()) {
+            Flow flow;
+            multiply_tiles<LAYOUT, BN>(p, s, w, tmem, flow);
+            drain_products(p, s);
+        }
         __syncwarp();
     } else if (warp >= 4) {
+        [[maybe_unused]] Flow flow;
         if constexpr (MODE == kLinGated)
             finish_gated(p, s, w, tmem, rank);
         else if constexpr (MODE == kLinStats)
@@ -831,9 +864,73 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
         else if constexpr (MODE == kLinSoftGrad)
             finish_softgrad(p, s, w, tmem, rank);
         else if (MODE == kLinPlain && p.e.y_f32)
-            finish_tiles<true, BN, kLinPlain>(p, s, w, tmem, rank);
+            finish_tiles<true, BN, kLinPlain>(p, s, w, tmem, rank, flow);
         else
-            finish_tiles<false, BN, MODE>(p, s, w, tmem, rank);
+            finish_tiles<false, BN, MODE>(p, s, w, tmem, rank, flow);
+    }
+    close_pair(s, tmem);
+}
+
+// ---- two products, one behind the other, in one launch ------------------------------
+// Long tiles (of p0) leave pairs idle in their last round: with r tiles in it, all but r
+// of them.  Those take q of the second product's shorter tiles each meanwhile, as
+// many as a long one's K slices hold, and what is left of them goes round all pairs.
+// The same tiles as in two launches, in fixed order.  Gradients of the loss, 1003 rows
+// (653 of them counted), 4101 x 16381, dx and dw: 160 us in two launches.
+struct TwoShares {
+    Share w0, idle, rest;
+};
+__device__ __forceinline__ TwoShares two_shares(const LinearPairParams &p0, const LinearPairParams &p1, int rank) {
+    constexpr int kLeast = 9;   // slices that the epilogue of a tile takes as long as
+    TwoShares t;
+    t.w0 = share_of<kLinPlain>(p0, rank);
+    t.idle = t.rest = share_of<kLinPlain>(p1, rank);
+    const int n = int(gridDim.x) >> 1, c = int(blockIdx.x) >> 1, r = t.w0.tiles % n;
+    const int q = (t.w0.kb1 - t.w0.kb0) / max(t.rest.kb1 - t.rest.kb0, kLeast);
+    const bool idle = r > 0 && c >= r;
+    t.idle.step = 1;
+    t.idle.first = idle ? int(min(int64_t(t.rest.tiles), int64_t(c - r) * q)) : 0;
+    t.idle.tiles = idle ? int(min(int64_t(t.rest.tiles), int64_t(c - r + 1) * q)) : 0;
+    const int given = r > 0 ? int(min(int64_t(t.rest.tiles), int64_t(n - r) * q)) : 0;
+    t.rest.first = min(t.rest.tiles, given) + c;
+    return t;
+}
+
+// L0: the first product's layout; the second's operands are both MN-major (3).
+template <int L0>
+__global__ void __launch_bounds__(kLThreads, 1) cm_linear_two_kernel(const __grid_constant__ LinearPairParams p0,
+                                                                     const __grid_constant__ LinearPairParams p1) {
+    extern __shared__ uint8_t smem_raw[];
+    LSmem s;
+    const uint32_t tmem = open_pair<256>(p0, s, smem_raw);
+    const int warp = int(threadIdx.x) >> 5, rank = int(cluster_ctarank());
+    const TwoShares t = two_shares(p0, p1, rank);
+    Flow flow;
+    if (warp == 0) {
+        if (elect_one()) {
+            load_tiles<L0, 256, kLinPlain>(p0, s, t.w0, rank, flow);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) load_tiles<3, 256, kLinPlain>(p1, s, i ? t.rest : t.idle, rank, flow);
+            drain_loads<256>(p0, s, rank, flow);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {
+            multiply_tiles<L0, 256>(p0, s, t.w0, tmem, flow);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) multiply_tiles<3, 256>(p1, s, i ? t.rest : t.idle, tmem, flow);
+            drain_products(p0, s);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        finish_tiles<true, 256, kLinPlain>(p0, s, t.w0, tmem, rank, flow);   // fp32 sums
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (p1.e.y_f32)
+                finish_tiles<true, 256, kLinPlain>(p1, s, i ? t.rest : t.idle, tmem, rank, flow);
+            else
+                finish_tiles<false, 256, kLinPlain>(p1, s, i ? t.rest : t.idle, tmem, rank, flow);
+        }
     }
     close_pair(s, tmem);
 }
@@ -991,10 +1088,18 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
     const int nrows = int(max(int64_t(0), min(int64_t(kHalf), p.rows - row0)));
     bool good = true;
     if (warp == 0) {
-        if (elect_one()) load_tiles<LAYOUT, BN, MODE>(p, s, w, rank);
+        if (elect_one()) {
+            Flow flow;
+            load_tiles<LAYOUT, BN, MODE>(p, s, w, rank, flow);
+            drain_loads<BN>(p, s, rank, flow);
+        }
         __syncwarp();
     } else if (warp == 1) {
-        if (rank == 0 && elect_one()) multiply_tiles<LAYOUT, BN>(p, s, w, tmem);
+        if (rank == 0 && elect_one()) {
+            Flow flow;
+            multiply_tiles<LAYOUT, BN>(p, s, w, tmem, flow);
+            drain_products(p, s);
+        }
         __syncwarp();
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
@@ -1139,6 +1244,10 @@ PairKernel pair_kernel(int layout, LinearMode mode, int bn, int splits) {
 }  // namespace
 
 cudaError_t prepare_linear_pair(int sms, int *clusters) {
+    for (auto fn : {cm_linear_two_kernel<0>, cm_linear_two_kernel<1>}) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
+        if (e != cudaSuccess) return e;
+    }
     for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad, kLinStats, kLinSoftGrad})
         for (int layout : {0, 1, 3})
             for (int bn : {256, 128})
@@ -1165,6 +1274,12 @@ cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode
     // split: one cluster a tile; else persistent
     const int n = splits > 1 ? p.tiles : std::max(1, std::min(clusters, p.tiles));
     return launch_after(fn, dim3(unsigned(2 * splits * n)), kLThreads, size_t(kLSmem), unsigned(2 * splits), stream, p);
+}
+
+cudaError_t launch_linear_two(const LinearPairParams &p0, int layout0, const LinearPairParams &p1, int clusters, cudaStream_t stream) {
+    const auto fn = layout0 == 0 ? cm_linear_two_kernel<0> : layout0 == 1 ? cm_linear_two_kernel<1> : nullptr;
+    if (!fn || p0.bn != 256 || p1.bn != 256) return cudaErrorInvalidValue;
+    return launch_after(fn, dim3(unsigned(2 * clusters)), kLThreads, size_t(kLSmem), 2u, stream, p0, p1);
 }
 
 }  // namespace cm

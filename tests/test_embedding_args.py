@@ -60,7 +60,7 @@ def test_backward(lib):
 def test_workspace_sizes(lib):
     size = cm.embedding_backward_workspace_size
     assert size(-1, 8) == 0 and size(8, 0) == 0
-    assert 0 < size(0, 8) <= size(1, 8) <= size(16, 8) < size(17, 8)
+    assert 0 < size(0, 8) <= size(1, 8) <= size(16, 64) < size(17, 64)
     assert size(8192, 4096) < 8192 * 4096 * 2 * 2 // 7   # two sevenths of the gradient's rows
 
 
