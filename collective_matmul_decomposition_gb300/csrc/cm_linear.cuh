@@ -30,7 +30,7 @@ struct LinearEpilogue {
     const void *bias2;
     const void *zin2;   // bf16
     void *z2;           // bf16
-    const float *scale; // device: multiplies D first; NULL for 1
+    const float *scale; // kLinCounted; on the device, NULL for 1
 };
 
 // What a kernel's epilogue computes.
@@ -43,7 +43,10 @@ struct LinearEpilogue {
 //   kLinStats  D are logits: of each row and each half of a tile's columns the largest
 //              and the sum of exp(. - largest), and the target's logit (LinearHead).
 //   kLinSoftGrad  y = exp(D - lse) grad, less hit where the column is the target.
-enum LinearMode { kLinPlain = 0, kLinGated = 1, kLinGateGrad = 2, kLinStats = 3, kLinSoftGrad = 4 };
+//   kLinCounted  kLinPlain with D times `scale` first, of rows that are counted on the
+//              device (LinearLive).  A mode of its own: the two checks cost a plain
+//              weight gradient of few slices a tile 0.6 us of 7.6.
+enum LinearMode { kLinPlain = 0, kLinGated = 1, kLinGateGrad = 2, kLinStats = 3, kLinSoftGrad = 4, kLinCounted = 5 };
 
 // The loss over a vocabulary, by slots: the rows that have a target, in order.
 struct LinearHead {
@@ -85,7 +88,6 @@ enum LinearSite : uint32_t {
 struct LinearStripParams {
     CUtensorMap tmA;    // column operand: [n][K] (K-major) or [K][n]
     CUtensorMap tmB;    // row operand: [rows][K] (K-major) or [K][rows]
-    CUtensorMap tmA2;   // gated: the second column operand; a tile then has 64 columns of each
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks;        // 64-wide K slices
@@ -94,18 +96,23 @@ struct LinearStripParams {
     int splits;         // CTAs of a cluster that share a tile's K slices
     int ring_bytes;     // shared memory for `stages` slices, and for a split tile's partial sums
     int stages;
-    LinearHead head;    // of the head's modes: 128 columns a part
-    const int32_t *count;   // slots there are
     LinearStatus *status;
     uint64_t timeout_ns;
 };
 
-// layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.  The other modes than kLinPlain take 0 and 2.
+// And of the modes that need more (kernel parameters are copied at each launch).
+struct LinearStripMore : LinearStripParams {
+    CUtensorMap tmA2;       // gated: the second column operand; a tile then has 64 columns of each
+    LinearHead head;        // of the head's modes: 128 columns a part
+    const int32_t *count;   // slots there are
+};
+
+// layout: bit 0 = row operand MN-major, bit 1 = column operand MN-major.  The other modes take 0 and 2; there is no kLinCounted.
 constexpr int kStripAlone = 216 * 1024, kStripShared = 108 * 1024;   // ring bytes of a CTA alone on its SM, of one of two
 // clusters[i]: clusters of i CTAs (2 to kStripMostSplits) that run together, one CTA an SM.
 constexpr int kStripMostSplits = 8;
 cudaError_t prepare_linear_strip(int sms, int *clusters);
-cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, LinearMode mode, cudaStream_t stream);
+cudaError_t launch_linear_strip(const LinearStripMore &p, int layout, LinearMode mode, cudaStream_t stream);
 int linear_strip_stages(int tok, int ring_bytes);
 
 // Tiles of 256 rows x bn columns on CTA pairs.  A is the row operand here, B the
@@ -115,10 +122,6 @@ struct LinearPairParams {
     CUtensorMap tmY;          // bf16: 64 x 32 boxes, fp32: 32 x 32
     CUtensorMap tmZ;          // pre-activation kept (bf16 y only), 64 x 32
     CUtensorMap tmIn0, tmIn1; // residual (or y, to be added to) and pre-activation read; bf16 y only
-    CUtensorMap tmB2, tmZ2;   // gated: the second column operand, and its z kept
-    CUtensorMap tmWhole;      // see LinearLive
-    LinearLive live;          // persistent kernels only
-    LinearHead head;
     LinearEpilogue e;
     int64_t rows, cols;
     int kblocks, mtiles, ntiles, tiles;
@@ -128,18 +131,26 @@ struct LinearPairParams {
     uint64_t timeout_ns;
 };
 
+// And of the modes that need more.
+struct LinearPairMore : LinearPairParams {
+    CUtensorMap tmB2, tmZ2;   // gated: the second column operand, and its z kept
+    CUtensorMap tmWhole;      // see LinearLive
+    LinearLive live;          // of the head's modes and kLinCounted
+    LinearHead head;
+};
+
 // layout: bit 0 = B MN-major, bit 1 = A MN-major; the gated modes take 0 and 1, and
 // kLinGated tiles of 256 columns, half of them of each operand; the head's modes have
-// 0 and 1, tiles of 256 columns and no splits.  splits: 1 (persistent, on
+// 0 and 1, tiles of 256 columns and no splits; kLinCounted has no splits.  splits: 1 (persistent, on
 // `clusters` pairs), or 2 or 4 pairs a cluster that share a tile's K slices,
 // one cluster a tile.  clusters[i]: clusters of 2^i pairs that run together.
 cudaError_t prepare_linear_pair(int sms, int *clusters);
-cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode mode, int splits, int clusters,
+cudaError_t launch_linear_pair(const LinearPairMore &p, int layout, LinearMode mode, int splits, int clusters,
                                cudaStream_t stream);
 
-// Two plain products of 256-column tiles in one launch, the first of layout 0 or 1 with
+// Two products (kLinCounted) of 256-column tiles in one launch, the first of layout 0 or 1 with
 // an fp32 y, the second of layout 3.
-cudaError_t launch_linear_two(const LinearPairParams &p0, int layout0, const LinearPairParams &p1, int clusters, cudaStream_t stream);
+cudaError_t launch_linear_two(const LinearPairMore &p0, int layout0, const LinearPairMore &p1, int clusters, cudaStream_t stream);
 
 // Column sums out[c] (+)= sum_r x[r][c] of a bf16 matrix (cm_norm.cu): partial
 // sums per row chunk in `partial`, then their sum in chunk order.

@@ -225,7 +225,7 @@ struct Kind {
     LinearHead head = {};
 };
 
-cm_status pair_params(LinearPairParams &p, const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b,
+cm_status pair_params(LinearPairMore &p, const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b,
                       int64_t rows, int64_t cols, int64_t k, const LinearEpilogue &e) {
     const LinearMode mode = kind.mode;
     p.e = e;
@@ -258,7 +258,7 @@ cm_status pair_params(LinearPairParams &p, const Device &d, const Choice &c, con
     } else if (mode == kLinGated) {
         if (e.z && (!map_written(&p.tmZ, e.z, rows, cols, e.ldz, false) || !map_written(&p.tmZ2, e.z2, rows, cols, e.ldz, false)))
             return CM_ERR_CUDA;
-    } else if (mode == kLinPlain && !e.y_f32) {
+    } else if ((mode == kLinPlain || mode == kLinCounted) && !e.y_f32) {
         if (e.z && !map_written(&p.tmZ, e.z, rows, cols, e.ldz, false)) return CM_ERR_CUDA;
         if (e.accumulate && !map_rows(&p.tmIn0, e.y, rows, cols, e.ldy, 32)) return CM_ERR_CUDA;
         if (e.res && !map_rows(&p.tmIn0, e.res, rows, cols, e.ldr, 32)) return CM_ERR_CUDA;
@@ -269,7 +269,7 @@ cm_status pair_params(LinearPairParams &p, const Device &d, const Choice &c, con
 
 cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b, int64_t rows,
                        int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
-    LinearPairParams p;
+    LinearPairMore p;
     const cm_status st = pair_params(p, d, c, kind, a, b, rows, cols, k, e);
     if (st != CM_OK) return st;
     const LinearMode mode = kind.mode;
@@ -280,7 +280,7 @@ cm_status product_pair(const Device &d, const Choice &c, const Kind &kind, const
 cm_status product_strip(const Device &d, const Choice &c, const Kind &kind, const Operand &a, const Operand &b, int64_t rows,
                         int64_t cols, int64_t k, const LinearEpilogue &e, cudaStream_t stream) {
     const bool gated = kind.mode == kLinGated;
-    LinearStripParams p;
+    LinearStripMore p;
     p.e = e;
     p.rows = rows;
     p.cols = cols;
@@ -680,10 +680,13 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
     CM_TRY(device(&d));
     Carve carve(ws);
     const LossGradSpace s = loss_grad_space(carve, M, K, n);
-    // a chunk's logits and the two products behind them; tiles that are split, and strips, take all rows
-    const Choice cp = choose_logits(d, M, s.columns, K);
-    const Choice cx = choose(d, M, K, s.columns, false), cw = choose(d, nk ? s.columns : K, nk ? K : s.columns, M, true);
-    const bool counted = cp.pair && (!dx || (cx.pair && cx.splits == 1)) && (!dw || (cw.pair && cw.splits == 1));
+    // a chunk's logits and the two products behind them; tiles that are split, and strips, take all rows.
+    // dw's are not split: its extents are the weights', and its epilogue scales
+    const Choice cp = choose_logits(d, M, s.columns, K), cx = choose(d, M, K, s.columns, false);
+    Choice cw = choose(d, nk ? s.columns : K, nk ? K : s.columns, M, true);
+    if (!cw.pair) cw = Choice{true, 128};
+    cw.splits = 1;
+    const bool counted = cp.pair && (!dx || (cx.pair && cx.splits == 1));
     HeadRows r = {};
     r.targets = targets;
     r.target_bits = target_bits;
@@ -742,20 +745,22 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
         const Operand &aw = nk ? rows_t : pt, &bw = nk ? pt : rows_t;
         const int64_t dr = nk ? cols : K, dc = nk ? K : cols;
         Kind kx, kw;
+        kw.mode = kLinCounted;
         if (counted) {
+            kx.mode = kLinCounted;
             kx.live = {s.count, 1, 0, 0, M};
             kw.live = {s.count, 0, 1, nk ? 2 : 1, M};
             kw.whole = &all_t;
         }
         if (dx && dw && counted && cx.bn == 256 && cw.bn == 256) {
-            LinearPairParams px, pw;
+            LinearPairMore px, pw;
             CM_TRY(pair_params(px, d, cx, kx, ax, bx, M, K, cols, ex));
             CM_TRY(pair_params(pw, d, cw, kw, aw, bw, dr, dc, M, ew));
             if (launch_linear_two(px, nk ? 1 : 0, pw, d.clusters[0], stream) != cudaSuccess) return CM_ERR_CUDA;
             continue;
         }
         if (dx) CM_TRY(counted ? product_pair(d, cx, kx, ax, bx, M, K, cols, ex, stream) : product(d, ax, bx, M, K, cols, ex, stream));
-        if (dw) CM_TRY(counted ? product_pair(d, cw, kw, aw, bw, dr, dc, M, ew, stream) : product(d, aw, bw, dr, dc, M, ew, stream));
+        if (dw) CM_TRY(product_pair(d, cw, kw, aw, bw, dr, dc, M, ew, stream));
     }
     if (!dx) return CM_OK;
     const HeadScatter g = {s.sum, s.lds, s.slot_of, s.scale, dx, dx_dtype == CM_F32, lddx, M, K};

@@ -228,7 +228,11 @@ __device__ __forceinline__ float load_bias(const void *bias, int f32, int64_t c)
     if (!bias) return 0.0f;
     return f32 ? static_cast<const float *>(bias)[c] : __bfloat162float(static_cast<const __nv_bfloat16 *>(bias)[c]);
 }
-__device__ __forceinline__ float load_bias(const LinearEpilogue &e, int64_t c) { return load_bias(e.bias, e.bias_f32, c); }
+__device__ __forceinline__ float load_bias(const LinearEpilogue &e, int64_t c) {
+    if (!e.bias) return 0.0f;
+    return e.bias_f32 ? static_cast<const float *>(e.bias)[c]
+                      : __bfloat162float(static_cast<const __nv_bfloat16 *>(e.bias)[c]);
+}
 
 }  // namespace
 }  // namespace lin

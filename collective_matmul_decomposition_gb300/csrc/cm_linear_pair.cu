@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cm_device.cuh"
 #include "cm_kernel.cuh"
@@ -109,15 +110,43 @@ __device__ __forceinline__ void tile_at(const LinearPairParams &p, int mtiles, i
     mt = b * p.band + (u - nt * rows);
 }
 
+// Modes whose products may end at the last slot (LinearLive), and the parameters of each.
+template <int MODE>
+constexpr bool kIsCounted = MODE == kLinStats || MODE == kLinSoftGrad || MODE == kLinCounted;
+template <int MODE>
+using PairParams = std::conditional_t<MODE == kLinPlain || MODE == kLinGateGrad, LinearPairParams, LinearPairMore>;
+
 // The tiles and K slices of a CTA's pair: first, first + step, ... below
 // `tiles`, each over slices kb0 .. kb1 - 1.  `leader` is the pair's even CTA.
 struct Share {
     int first, step, kb0, kb1;
     uint32_t leader;
+    // of the counted modes; the others have these from the parameters, at no register
     int tiles, mtiles;
     int64_t rows;
     const CUtensorMap *a, *b;   // the operands' maps
 };
+template <int MODE>
+__device__ __forceinline__ int tiles_of(const LinearPairParams &p, const Share &w) {
+    return kIsCounted<MODE> ? w.tiles : p.tiles;
+}
+template <int MODE>
+__device__ __forceinline__ int mtiles_of(const LinearPairParams &p, const Share &w) {
+    return kIsCounted<MODE> ? w.mtiles : p.mtiles;
+}
+template <int MODE>
+__device__ __forceinline__ int64_t rows_of(const LinearPairParams &p, const Share &w) {
+    return kIsCounted<MODE> ? w.rows : p.rows;
+}
+// of a persistent kernel's epilogue
+template <int MODE>
+__device__ __forceinline__ int first_of(const Share &w) {
+    return kIsCounted<MODE> ? w.first : int(blockIdx.x) >> 1;
+}
+template <int MODE>
+__device__ __forceinline__ int step_of(const Share &w) {
+    return kIsCounted<MODE> ? w.step : int(gridDim.x) >> 1;
+}
 
 // Where a role stands in the ring of stages and in the two accumulators, from one
 // share to the next.
@@ -131,12 +160,10 @@ struct Flow {
 
 // A persistent kernel's share, cut down to the slots where they are counted.
 template <int MODE>
-__device__ __forceinline__ Share share_of(const LinearPairParams &p, int rank) {
-    // gated: the pair's even CTA stages the gate's columns, the odd one the up projection's,
-    // so that half of each CTA's accumulator columns belong to either
-    Share w = {int(blockIdx.x) >> 1, int(gridDim.x) >> 1, 0, p.kblocks, 0u, p.tiles, p.mtiles, p.rows, &p.tmA,
-               MODE == kLinGated && rank ? &p.tmB2 : &p.tmB};
-    if (MODE != kLinGated && MODE != kLinGateGrad && p.live.count) {
+__device__ __forceinline__ Share share_of(const PairParams<MODE> &p) {
+    Share w = {int(blockIdx.x) >> 1, int(gridDim.x) >> 1, 0, p.kblocks, 0u, p.tiles, p.mtiles, p.rows, &p.tmA, &p.tmB};
+    if constexpr (kIsCounted<MODE>) {
+        if (!p.live.count) return w;
         const int n = *p.live.count;
         // where there is none, one slice or one row of tiles is computed all the same:
         // the slots behind the last are zeros
@@ -154,18 +181,23 @@ __device__ __forceinline__ Share share_of(const LinearPairParams &p, int rank) {
 }
 
 template <int LAYOUT, int BN, int MODE>
-__device__ __forceinline__ void load_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, int rank, Flow &flow) {
+__device__ __forceinline__ void load_tiles(const PairParams<MODE> &p, const LSmem &s, const Share &w, int rank, Flow &flow) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
     const uint32_t full_leader = mapa_shared(smem_u32(s.full), w.leader);
     const uint32_t a0 = smem_u32(s.a0), b0 = smem_u32(s.b0);
-    const uint64_t tma = reinterpret_cast<uint64_t>(w.a), tmb = reinterpret_cast<uint64_t>(w.b);
+    uint64_t tma = reinterpret_cast<uint64_t>(&p.tmA), tmb = reinterpret_cast<uint64_t>(&p.tmB);
+    if constexpr (kIsCounted<MODE>) tma = reinterpret_cast<uint64_t>(w.a), tmb = reinterpret_cast<uint64_t>(w.b);
+    // gated: the pair's even CTA stages the gate's columns, the odd one the up projection's,
+    // so that half of each CTA's accumulator columns belong to either
+    if constexpr (MODE == kLinGated)
+        if (rank) tmb = reinterpret_cast<uint64_t>(&p.tmB2);
     int stage = flow.stage;
     uint32_t phase = flow.phase, issued = flow.issued;
     bool ok = flow.ok;
-    for (int t = w.first; t < w.tiles && ok; t += w.step) {
+    for (int t = w.first; t < tiles_of<MODE>(p, w) && ok; t += w.step) {
         int mt, nt;
-        tile_at(p, w.mtiles, t, mt, nt);
+        tile_at(p, mtiles_of<MODE>(p, w), t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf, col0 = MODE == kLinGated ? nt * (BN / 2) : nt * BN + rank * (BN / 2);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
             if (!mbar_try_wait(s.empty + stage, phase ^ 1u) &&
@@ -209,7 +241,7 @@ __device__ __forceinline__ void drain_loads(const LinearPairParams &p, const LSm
             if (uint32_t(i) < flow.issued) drain_p(p, &s.full[i], i < flow.stage ? flow.phase : flow.phase ^ 1u);
 }
 
-template <int LAYOUT, int BN>
+template <int LAYOUT, int BN, int MODE>
 __device__ __forceinline__ void multiply_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, Flow &flow) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     constexpr int kStages = Tile<BN>::kStages, kB = Tile<BN>::kB;
@@ -221,7 +253,7 @@ __device__ __forceinline__ void multiply_tiles(const LinearPairParams &p, const 
     uint32_t phase = flow.phase, acc_phase = flow.acc_phase;
     bool ok = flow.ok;
     const uint16_t both = uint16_t(3u << w.leader);   // the pair's CTAs
-    for (int t = w.first; t < w.tiles && ok; t += w.step) {
+    for (int t = w.first; t < tiles_of<MODE>(p, w) && ok; t += w.step) {
         if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) {
             ok = false;
             break;
@@ -313,7 +345,7 @@ __device__ __noinline__ void store_rest(const LinearPairParams &p, uint8_t *buf0
         if (i < n) z[i] = __float2bfloat16_rn(f[i]);
 }
 
-// F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).  MODE: kLinPlain or kLinGateGrad.
+// F32: y is fp32 (chunks of 32 columns), otherwise bf16 (64 columns).  MODE: kLinPlain, kLinGateGrad or kLinCounted.
 template <bool F32, int BN, int MODE>
 __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank,
                                              Flow &flow) {
@@ -343,11 +375,11 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
     uint32_t acc_phase = flow.acc_phase, in_phase = flow.in_phase;
     bool pending = false;   // inputs asked for and not yet waited for
     bool ok = flow.ok;
-    for (int t = w.first; t < w.tiles && ok; t += w.step) {
+    for (int t = first_of<MODE>(w); t < tiles_of<MODE>(p, w) && ok; t += step_of<MODE>(w)) {
         int mt, nt;
-        tile_at(p, w.mtiles, t, mt, nt);
+        tile_at(p, mtiles_of<MODE>(p, w), t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf + quad * 32, cbase = nt * BN + half * kCols;
-        const int nch = row0 < w.rows && cbase < p.cols ? min(kCols, int(min(p.cols - cbase, int64_t(kCols))) + kChunk - 1) / kChunk : 0;
+        const int nch = row0 < rows_of<MODE>(p, w) && cbase < p.cols ? min(kCols, int(min(p.cols - cbase, int64_t(kCols))) + kChunk - 1) / kChunk : 0;
         float bias[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -404,7 +436,7 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
                 float f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                if (!kGate && e.scale) {
+                if (MODE == kLinCounted && e.scale) {
                     const float scale = *e.scale;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] *= scale;
@@ -457,7 +489,7 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
                 } else {
                     const int64_t row = int64_t(row0) + lane;
                     const int col = cbase + ch * kChunk;
-                    const bool live = row < w.rows;
+                    const bool live = row < rows_of<MODE>(p, w);
                     auto at = [&](const void *m, int64_t ld, int i) {
                         return live && col + i < p.cols
                                    ? __bfloat162float(static_cast<const __nv_bfloat16 *>(m)[row * ld + col + i])
@@ -535,7 +567,7 @@ __device__ __noinline__ void store_tail(uint8_t *buf, void *m, int64_t ld, int64
 // accumulator again, which costs less than holding 128 columns in registers.
 // Bound by the tensor cores where the products are long (4096 x 8192 x 28672 with both
 // z kept), by the epilogue below some 16 K slices a tile.
-__device__ void finish_gated(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+__device__ void finish_gated(const LinearPairMore &p, const LSmem &s, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = 64;
     const LinearEpilogue &e = p.e;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
@@ -548,9 +580,9 @@ __device__ void finish_gated(const LinearPairParams &p, const LSmem &s, const Sh
     const int outs = e.z ? 3 : 1;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = w.first; t < w.tiles; t += w.step) {
+    for (int t = int(blockIdx.x) >> 1; t < p.tiles; t += int(gridDim.x) >> 1) {
         int mt, nt;
-        tile_at(p, w.mtiles, t, mt, nt);
+        tile_at(p, p.mtiles, t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf + quad * 32, c0 = nt * (BN / 2) + half * kCols;
         const bool live = row0 < p.rows && c0 < p.cols;
         float bg[2], bu[2];   // the columns' biases lie one to a lane
@@ -623,7 +655,7 @@ __device__ void finish_gated(const LinearPairParams &p, const LSmem &s, const Sh
 // running maximum m and sum s of exp2(v log2(e) - m), all in fp32:
 //   m' = max(m, max v);  s' = s exp2(m - m') + sum exp2(v - m').
 // What is not a column counts as -infinity.  A NaN stays one through the sum.
-__device__ void finish_stats(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+__device__ void finish_stats(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = BN / 2;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
     const int quad = ew & 3, half = ew >> 2;
@@ -692,7 +724,7 @@ __device__ void finish_stats(const LinearPairParams &p, const LSmem &s, const Sh
 
 // The gradient of the logits, bf16: exp(D - lse) grad, less hit in the target's column.
 // Rows behind the last slot are zeros up to the tile's end.
-__device__ void finish_softgrad(const LinearPairParams &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+__device__ void finish_softgrad(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = BN / 2, kChunk = 64;
     const LinearEpilogue &e = p.e;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
@@ -835,12 +867,12 @@ __device__ void close_pair(const LSmem &s, uint32_t tmem) {
 }
 
 template <int LAYOUT, int BN, int MODE>
-__global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __grid_constant__ LinearPairParams p) {
+__global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __grid_constant__ PairParams<MODE> p) {
     extern __shared__ uint8_t smem_raw[];
     LSmem s;
     const uint32_t tmem = open_pair<BN>(p, s, smem_raw);
     const int warp = int(threadIdx.x) >> 5, rank = int(cluster_ctarank());
-    const Share w = share_of<MODE>(p, rank);
+    const Share w = share_of<MODE>(p);
     if (warp == 0) {
         if (elect_one()) {
             Flow flow;
@@ -851,20 +883,20 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             Flow flow;
-            multiply_tiles<LAYOUT, BN>(p, s, w, tmem, flow);
+            multiply_tiles<LAYOUT, BN, MODE>(p, s, w, tmem, flow);
             drain_products(p, s);
         }
         __syncwarp();
     } else if (warp >= 4) {
         [[maybe_unused]] Flow flow;
         if constexpr (MODE == kLinGated)
-            finish_gated(p, s, w, tmem, rank);
+            finish_gated(p, s, tmem, rank);
         else if constexpr (MODE == kLinStats)
             finish_stats(p, s, w, tmem, rank);
         else if constexpr (MODE == kLinSoftGrad)
             finish_softgrad(p, s, w, tmem, rank);
-        else if (MODE == kLinPlain && p.e.y_f32)
-            finish_tiles<true, BN, kLinPlain>(p, s, w, tmem, rank, flow);
+        else if (MODE != kLinGateGrad && p.e.y_f32)
+            finish_tiles<true, BN, MODE == kLinGateGrad ? kLinPlain : MODE>(p, s, w, tmem, rank, flow);
         else
             finish_tiles<false, BN, MODE>(p, s, w, tmem, rank, flow);
     }
@@ -880,11 +912,11 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
 struct TwoShares {
     Share w0, idle, rest;
 };
-__device__ __forceinline__ TwoShares two_shares(const LinearPairParams &p0, const LinearPairParams &p1, int rank) {
+__device__ __forceinline__ TwoShares two_shares(const LinearPairMore &p0, const LinearPairMore &p1) {
     constexpr int kLeast = 9;   // slices that the epilogue of a tile takes as long as
     TwoShares t;
-    t.w0 = share_of<kLinPlain>(p0, rank);
-    t.idle = t.rest = share_of<kLinPlain>(p1, rank);
+    t.w0 = share_of<kLinCounted>(p0);
+    t.idle = t.rest = share_of<kLinCounted>(p1);
     const int n = int(gridDim.x) >> 1, c = int(blockIdx.x) >> 1, r = t.w0.tiles % n;
     const int q = (t.w0.kb1 - t.w0.kb0) / max(t.rest.kb1 - t.rest.kb0, kLeast);
     const bool idle = r > 0 && c >= r;
@@ -898,38 +930,38 @@ __device__ __forceinline__ TwoShares two_shares(const LinearPairParams &p0, cons
 
 // L0: the first product's layout; the second's operands are both MN-major (3).
 template <int L0>
-__global__ void __launch_bounds__(kLThreads, 1) cm_linear_two_kernel(const __grid_constant__ LinearPairParams p0,
-                                                                     const __grid_constant__ LinearPairParams p1) {
+__global__ void __launch_bounds__(kLThreads, 1) cm_linear_two_kernel(const __grid_constant__ LinearPairMore p0,
+                                                                     const __grid_constant__ LinearPairMore p1) {
     extern __shared__ uint8_t smem_raw[];
     LSmem s;
     const uint32_t tmem = open_pair<256>(p0, s, smem_raw);
     const int warp = int(threadIdx.x) >> 5, rank = int(cluster_ctarank());
-    const TwoShares t = two_shares(p0, p1, rank);
+    const TwoShares t = two_shares(p0, p1);
     Flow flow;
     if (warp == 0) {
         if (elect_one()) {
-            load_tiles<L0, 256, kLinPlain>(p0, s, t.w0, rank, flow);
+            load_tiles<L0, 256, kLinCounted>(p0, s, t.w0, rank, flow);
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) load_tiles<3, 256, kLinPlain>(p1, s, i ? t.rest : t.idle, rank, flow);
+            for (int i = 0; i < 2; ++i) load_tiles<3, 256, kLinCounted>(p1, s, i ? t.rest : t.idle, rank, flow);
             drain_loads<256>(p0, s, rank, flow);
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            multiply_tiles<L0, 256>(p0, s, t.w0, tmem, flow);
+            multiply_tiles<L0, 256, kLinCounted>(p0, s, t.w0, tmem, flow);
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) multiply_tiles<3, 256>(p1, s, i ? t.rest : t.idle, tmem, flow);
+            for (int i = 0; i < 2; ++i) multiply_tiles<3, 256, kLinCounted>(p1, s, i ? t.rest : t.idle, tmem, flow);
             drain_products(p0, s);
         }
         __syncwarp();
     } else if (warp >= 4) {
-        finish_tiles<true, 256, kLinPlain>(p0, s, t.w0, tmem, rank, flow);   // fp32 sums
+        finish_tiles<true, 256, kLinCounted>(p0, s, t.w0, tmem, rank, flow);   // fp32 sums
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             if (p1.e.y_f32)
-                finish_tiles<true, 256, kLinPlain>(p1, s, i ? t.rest : t.idle, tmem, rank, flow);
+                finish_tiles<true, 256, kLinCounted>(p1, s, i ? t.rest : t.idle, tmem, rank, flow);
             else
-                finish_tiles<false, 256, kLinPlain>(p1, s, i ? t.rest : t.idle, tmem, rank, flow);
+                finish_tiles<false, 256, kLinCounted>(p1, s, i ? t.rest : t.idle, tmem, rank, flow);
         }
     }
     close_pair(s, tmem);
@@ -974,13 +1006,6 @@ __device__ __forceinline__ void put4(void *m, int64_t at, int n, const float (&f
 __device__ __forceinline__ void finish4(const LinearEpilogue &e, float (&v)[4][4], const float (&bias)[4], int64_t row,
                                         int64_t step, int64_t end, int64_t col, int n) {
     float in[4][4];
-    if (e.scale) {
-        const float scale = *e.scale;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[k][i] *= scale;
-    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -1072,7 +1097,7 @@ __device__ __forceinline__ void finish4_gate_grad(const LinearEpilogue &e, float
 // every time.  200 x 8192 x 3584 takes 19.9 us on four pairs a tile, 26.3 on two
 // and 42.5 unsplit; the exchange and the summing cost 4 us (128 columns) to 6.5.
 template <int LAYOUT, int BN, int S, int MODE>
-__global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __grid_constant__ LinearPairParams p) {
+__global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __grid_constant__ PairParams<MODE> p) {
     extern __shared__ uint8_t smem_raw[];
     static_assert(kHalf * BN * 4 <= kRingBytes, "a partial tile fits in the ring");
     LSmem s;
@@ -1081,7 +1106,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
     const int crank = int(cluster_ctarank()), rank = crank & 1, part = crank >> 1;
     const int tile = int(blockIdx.x) / (2 * S);
     const Share w = {tile, p.tiles, int(int64_t(p.kblocks) * part / S), int(int64_t(p.kblocks) * (part + 1) / S),
-                     uint32_t(crank & ~1), p.tiles, p.mtiles, p.rows, &p.tmA, MODE == kLinGated && rank ? &p.tmB2 : &p.tmB};
+                     uint32_t(crank & ~1), p.tiles, p.mtiles, p.rows, &p.tmA, &p.tmB};
     int mt, nt;
     tile_at(p, p.mtiles, tile, mt, nt);
     const int row0 = mt * kTile + rank * kHalf;
@@ -1097,7 +1122,7 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_split_kernel(const __g
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             Flow flow;
-            multiply_tiles<LAYOUT, BN>(p, s, w, tmem, flow);
+            multiply_tiles<LAYOUT, BN, MODE>(p, s, w, tmem, flow);
             drain_products(p, s);
         }
         __syncwarp();
@@ -1203,80 +1228,91 @@ cudaError_t pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, unsi
     return cudaSuccess;
 }
 
-using PairKernel = void (*)(LinearPairParams);
+template <int MODE>
+using PairKernel = void (*)(PairParams<MODE>);
 
-// By operand layout (0, 1, 3; the gated modes have 0 and 1), tile columns (the
-// gated product has 256) and pairs of a cluster.
-template <int LAYOUT, int MODE>
-PairKernel pair_kernel_of(int bn, int splits) {
-    if constexpr (MODE == kLinStats || MODE == kLinSoftGrad)
-        return bn == 256 && splits == 1 ? cm_linear_pair_kernel<LAYOUT, 256, MODE> : nullptr;
-    else if (bn == 256)
-        return splits == 1   ? cm_linear_pair_kernel<LAYOUT, 256, MODE>
-               : splits == 2 ? cm_linear_split_kernel<LAYOUT, 256, 2, MODE>
-               : splits == 4 ? cm_linear_split_kernel<LAYOUT, 256, 4, MODE>
-                             : nullptr;
-    if constexpr (MODE == kLinPlain || MODE == kLinGateGrad) {
-        if (bn == 128)
-            return splits == 1   ? cm_linear_pair_kernel<LAYOUT, 128, MODE>
-                   : splits == 2 ? cm_linear_split_kernel<LAYOUT, 128, 2, MODE>
-                   : splits == 4 ? cm_linear_split_kernel<LAYOUT, 128, 4, MODE>
-                                 : nullptr;
+// By operand layout (0, 1, 3), tile columns and pairs of a cluster; what a mode does
+// not have is NULL.
+template <int MODE, int LAYOUT>
+PairKernel<MODE> pair_kernel_of(int bn, int splits) {
+    constexpr bool kSplits = !kIsCounted<MODE>, kNarrow = MODE == kLinPlain || MODE == kLinGateGrad || MODE == kLinCounted;
+    if (bn == 256 && splits == 1) return cm_linear_pair_kernel<LAYOUT, 256, MODE>;
+    if constexpr (kNarrow)
+        if (bn == 128 && splits == 1) return cm_linear_pair_kernel<LAYOUT, 128, MODE>;
+    if constexpr (kSplits) {
+        if (bn == 256 && splits == 2) return cm_linear_split_kernel<LAYOUT, 256, 2, MODE>;
+        if (bn == 256 && splits == 4) return cm_linear_split_kernel<LAYOUT, 256, 4, MODE>;
+    }
+    if constexpr (kSplits && kNarrow) {
+        if (bn == 128 && splits == 2) return cm_linear_split_kernel<LAYOUT, 128, 2, MODE>;
+        if (bn == 128 && splits == 4) return cm_linear_split_kernel<LAYOUT, 128, 4, MODE>;
     }
     return nullptr;
 }
-
-PairKernel pair_kernel(int layout, LinearMode mode, int bn, int splits) {
-    const auto two = [&](PairKernel k_major, PairKernel mn_major) { return layout == 0 ? k_major : layout == 1 ? mn_major : nullptr; };
-    switch (mode) {
-        case kLinGated: return two(pair_kernel_of<0, kLinGated>(bn, splits), pair_kernel_of<1, kLinGated>(bn, splits));
-        case kLinGateGrad: return two(pair_kernel_of<0, kLinGateGrad>(bn, splits), pair_kernel_of<1, kLinGateGrad>(bn, splits));
-        case kLinStats: return two(pair_kernel_of<0, kLinStats>(bn, splits), pair_kernel_of<1, kLinStats>(bn, splits));
-        case kLinSoftGrad: return two(pair_kernel_of<0, kLinSoftGrad>(bn, splits), pair_kernel_of<1, kLinSoftGrad>(bn, splits));
-        default: break;
-    }
-    return layout == 0   ? pair_kernel_of<0, kLinPlain>(bn, splits)
-           : layout == 1 ? pair_kernel_of<1, kLinPlain>(bn, splits)
-           : layout == 3 ? pair_kernel_of<3, kLinPlain>(bn, splits)
-                         : nullptr;
+template <int MODE>
+PairKernel<MODE> pair_kernel(int layout, int bn, int splits) {
+    if (layout == 0) return pair_kernel_of<MODE, 0>(bn, splits);
+    if (layout == 1) return pair_kernel_of<MODE, 1>(bn, splits);
+    if constexpr (MODE == kLinPlain || MODE == kLinCounted)
+        if (layout == 3) return pair_kernel_of<MODE, 3>(bn, splits);
+    return nullptr;
 }
 
-}  // namespace
-
-cudaError_t prepare_linear_pair(int sms, int *clusters) {
-    for (auto fn : {cm_linear_two_kernel<0>, cm_linear_two_kernel<1>}) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
-        if (e != cudaSuccess) return e;
-    }
-    for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad, kLinStats, kLinSoftGrad})
-        for (int layout : {0, 1, 3})
-            for (int bn : {256, 128})
-                for (int i = 0; i < 3; ++i) {
-                    const int splits = 1 << i;
-                    const PairKernel fn = pair_kernel(layout, mode, bn, splits);
-                    if (!fn) continue;
-                    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
-                    if (e != cudaSuccess) return e;
-                    if (mode != kLinPlain || layout != 0 || bn != 256) continue;
-                    cudaLaunchConfig_t cfg;
-                    cudaLaunchAttribute attr[1];
-                    pair_config(cfg, attr, unsigned(2 * splits), unsigned(sms / (2 * splits) * (2 * splits)), nullptr);
-                    e = cudaOccupancyMaxActiveClusters(&clusters[i], fn, &cfg);
+template <int MODE>
+cudaError_t prepare_pair() {
+    for (int layout : {0, 1, 3})
+        for (int bn : {256, 128})
+            for (int splits : {1, 2, 4})
+                if (const auto fn = pair_kernel<MODE>(layout, bn, splits)) {
+                    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem);
                     if (e != cudaSuccess) return e;
                 }
     return cudaSuccess;
 }
 
-cudaError_t launch_linear_pair(const LinearPairParams &p, int layout, LinearMode mode, int splits, int clusters,
-                               cudaStream_t stream) {
-    const PairKernel fn = pair_kernel(layout, mode, p.bn, splits);
+template <int MODE>
+cudaError_t launch_pair(const LinearPairMore &p, int layout, int splits, int clusters, cudaStream_t stream) {
+    const auto fn = pair_kernel<MODE>(layout, p.bn, splits);
     if (!fn) return cudaErrorInvalidValue;
     // split: one cluster a tile; else persistent
     const int n = splits > 1 ? p.tiles : std::max(1, std::min(clusters, p.tiles));
-    return launch_after(fn, dim3(unsigned(2 * splits * n)), kLThreads, size_t(kLSmem), unsigned(2 * splits), stream, p);
+    return launch_after(fn, dim3(unsigned(2 * splits * n)), kLThreads, size_t(kLSmem), unsigned(2 * splits), stream,
+                        static_cast<const PairParams<MODE> &>(p));
 }
 
-cudaError_t launch_linear_two(const LinearPairParams &p0, int layout0, const LinearPairParams &p1, int clusters, cudaStream_t stream) {
+}  // namespace
+
+cudaError_t prepare_linear_pair(int sms, int *clusters) {
+    cudaError_t e = cudaSuccess;
+    for (auto prepare : {prepare_pair<kLinPlain>, prepare_pair<kLinGated>, prepare_pair<kLinGateGrad>, prepare_pair<kLinStats>,
+                         prepare_pair<kLinSoftGrad>, prepare_pair<kLinCounted>})
+        if ((e = prepare()) != cudaSuccess) return e;
+    for (auto fn : {cm_linear_two_kernel<0>, cm_linear_two_kernel<1>})
+        if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLSmem)) != cudaSuccess) return e;
+    for (int i = 0; i < 3; ++i) {
+        const int splits = 1 << i;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[1];
+        pair_config(cfg, attr, unsigned(2 * splits), unsigned(sms / (2 * splits) * (2 * splits)), nullptr);
+        if ((e = cudaOccupancyMaxActiveClusters(&clusters[i], pair_kernel<kLinPlain>(0, 256, splits), &cfg)) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_linear_pair(const LinearPairMore &p, int layout, LinearMode mode, int splits, int clusters,
+                               cudaStream_t stream) {
+    switch (mode) {
+        case kLinPlain: return launch_pair<kLinPlain>(p, layout, splits, clusters, stream);
+        case kLinGated: return launch_pair<kLinGated>(p, layout, splits, clusters, stream);
+        case kLinGateGrad: return launch_pair<kLinGateGrad>(p, layout, splits, clusters, stream);
+        case kLinStats: return launch_pair<kLinStats>(p, layout, splits, clusters, stream);
+        case kLinSoftGrad: return launch_pair<kLinSoftGrad>(p, layout, splits, clusters, stream);
+        case kLinCounted: return launch_pair<kLinCounted>(p, layout, splits, clusters, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_linear_two(const LinearPairMore &p0, int layout0, const LinearPairMore &p1, int clusters, cudaStream_t stream) {
     const auto fn = layout0 == 0 ? cm_linear_two_kernel<0> : layout0 == 1 ? cm_linear_two_kernel<1> : nullptr;
     if (!fn || p0.bn != 256 || p1.bn != 256) return cudaErrorInvalidValue;
     return launch_after(fn, dim3(unsigned(2 * clusters)), kLThreads, size_t(kLSmem), 2u, stream, p0, p1);

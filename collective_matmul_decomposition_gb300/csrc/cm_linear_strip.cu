@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cm_device.cuh"
 #include "cm_kernel.cuh"
@@ -105,11 +106,6 @@ constexpr int kBatch = 8;
 __device__ __forceinline__ void finish(const LinearEpilogue &e, float (&v)[kBatch], float bias, int64_t row0, int64_t step,
                                        int64_t end, int64_t col) {
     float in[kBatch];
-    if (e.scale) {
-        const float scale = *e.scale;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) v[k] *= scale;
-    }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) v[k] += bias;
     if (e.z) {
@@ -269,8 +265,11 @@ __device__ __forceinline__ void finish_stats(const LinearHead &h, int count, con
     }
 }
 
+template <int MODE>
+using StripParams = std::conditional_t<MODE == kLinPlain || MODE == kLinGateGrad, LinearStripParams, LinearStripMore>;
+
 template <int LAYOUT, int MODE>
-__global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid_constant__ LinearStripParams p) {
+__global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid_constant__ StripParams<MODE> p) {
     constexpr bool B_MN = (LAYOUT & 1) != 0, A_MN = (LAYOUT & 2) != 0;
     extern __shared__ uint8_t smem_raw[];
     StripSmem s;
@@ -313,9 +312,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const int ct = tile / p.row_tiles, rt = tile - ct * p.row_tiles;
     constexpr bool kGated = MODE == kLinGated;
     const int col0 = ct * (kGated ? kTileCols / 2 : kTileCols), row0 = rt * p.tok;
-    // gated: the tile's second 64 columns are the second operand's
-    const CUtensorMap *const second = kGated ? &p.tmA2 : &p.tmA;
-    const int col1 = kGated ? col0 : col0 + 64;
     const int kb0 = int(int64_t(p.kblocks) * split / p.splits), kb1 = int(int64_t(p.kblocks) * (split + 1) / p.splits);
     const uint32_t stage_bytes = uint32_t(kStripA + p.tok * kBK * 2);
 
@@ -324,12 +320,16 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     // values all the same: the loads below, which come after it, read L2.
     if (warp == 0 && elect_one())
         for (int kb = kb0; kb < min(kb1, kb0 + p.stages); ++kb) {
-            if (A_MN) {
-                tma_prefetch_3d(&p.tmA, col0, kb * kBK, 0);
-                tma_prefetch_3d(second, col1, kb * kBK, 0);
+            if constexpr (kGated) {   // 64 columns of each operand
+                for (const CUtensorMap *m : {&p.tmA, &p.tmA2})
+                    if (A_MN)
+                        tma_prefetch_3d(m, col0, kb * kBK, 0);
+                    else
+                        tma_prefetch_3d(m, kb * kBK, col0, 0);
+            } else if (A_MN) {
+                for (int j = 0; j < kTileCols / 64; ++j) tma_prefetch_3d(&p.tmA, col0 + 64 * j, kb * kBK, 0);
             } else {
                 tma_prefetch_3d(&p.tmA, kb * kBK, col0, 0);
-                if (kGated) tma_prefetch_3d(second, kb * kBK, col1, 0);
             }
         }
     __syncwarp();
@@ -344,12 +344,19 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                     break;
                 uint8_t *sa = s.ring + uint32_t(stage) * stage_bytes, *sb = sa + kStripA;
                 mbar_expect_tx(&s.full[stage], stage_bytes);
-                if (A_MN) {
-                    tma_load_3d(sa, &p.tmA, &s.full[stage], col0, kb * kBK, 0);
-                    tma_load_3d(sa + 64 * kBK * 2, second, &s.full[stage], col1, kb * kBK, 0);
+                if constexpr (kGated) {
+                    if (A_MN) {
+                        tma_load_3d(sa, &p.tmA, &s.full[stage], col0, kb * kBK, 0);
+                        tma_load_3d(sa + 64 * kBK * 2, &p.tmA2, &s.full[stage], col0, kb * kBK, 0);
+                    } else {
+                        tma_load_3d(sa, &p.tmA, &s.full[stage], kb * kBK, col0, 0);
+                        tma_load_3d(sa + 64 * kBK * 2, &p.tmA2, &s.full[stage], kb * kBK, col0, 0);
+                    }
+                } else if (A_MN) {
+                    for (int j = 0; j < kTileCols / 64; ++j)
+                        tma_load_3d(sa + j * (64 * kBK * 2), &p.tmA, &s.full[stage], col0 + 64 * j, kb * kBK, 0);
                 } else {
                     tma_load_3d(sa, &p.tmA, &s.full[stage], kb * kBK, col0, 0);
-                    if (kGated) tma_load_3d(sa + 64 * kBK * 2, second, &s.full[stage], kb * kBK, col1, 0);
                 }
                 if (B_MN) {
                     for (int j = 0; j < p.tok / 64; ++j)
@@ -412,7 +419,8 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const uint32_t taddr = tmem + (uint32_t(warp * 32) << 16);
     const float bias = !kGated && col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
     constexpr bool kStats = MODE == kLinStats;
-    [[maybe_unused]] const int count = kStats || MODE == kLinSoftGrad ? *p.count : 0;
+    [[maybe_unused]] int count = 0;
+    if constexpr (kStats || MODE == kLinSoftGrad) count = *p.count;
     if ((kGated || kStats) && p.splits == 1) {
         // gate and up columns, or those of a row's sum, lie in different threads' lanes:
         // they meet in the ring, whose loads have all been multiplied, 128 tokens at a time
@@ -503,19 +511,29 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
 }
 
 using StripKernel = void (*)(LinearStripParams);
+using StripMoreKernel = void (*)(LinearStripMore);
 
 StripKernel strip_kernel(int layout, LinearMode mode) {
-    const auto two = [&](StripKernel k_major, StripKernel mn_major) { return layout == 0 ? k_major : layout == 2 ? mn_major : nullptr; };
+    if (mode == kLinGateGrad)
+        return layout == 0   ? cm_linear_strip_kernel<0, kLinGateGrad>
+               : layout == 2 ? cm_linear_strip_kernel<2, kLinGateGrad>
+                             : nullptr;
+    if (mode != kLinPlain) return nullptr;
+    return layout == 0   ? cm_linear_strip_kernel<0, kLinPlain>
+           : layout == 2 ? cm_linear_strip_kernel<2, kLinPlain>
+           : layout == 3 ? cm_linear_strip_kernel<3, kLinPlain>
+                         : nullptr;
+}
+
+StripMoreKernel strip_more_kernel(int layout, LinearMode mode) {
+    const auto two = [&](StripMoreKernel k_major, StripMoreKernel mn_major) {
+        return layout == 0 ? k_major : layout == 2 ? mn_major : nullptr;
+    };
     switch (mode) {
         case kLinGated: return two(cm_linear_strip_kernel<0, kLinGated>, cm_linear_strip_kernel<2, kLinGated>);
-        case kLinGateGrad: return two(cm_linear_strip_kernel<0, kLinGateGrad>, cm_linear_strip_kernel<2, kLinGateGrad>);
         case kLinStats: return two(cm_linear_strip_kernel<0, kLinStats>, cm_linear_strip_kernel<2, kLinStats>);
         case kLinSoftGrad: return two(cm_linear_strip_kernel<0, kLinSoftGrad>, cm_linear_strip_kernel<2, kLinSoftGrad>);
-        default:
-            return layout == 0   ? cm_linear_strip_kernel<0, kLinPlain>
-                   : layout == 2 ? cm_linear_strip_kernel<2, kLinPlain>
-                   : layout == 3 ? cm_linear_strip_kernel<3, kLinPlain>
-                                 : nullptr;
+        default: return nullptr;
     }
 }
 
@@ -526,13 +544,16 @@ int linear_strip_stages(int tok, int ring_bytes) {
 }
 
 cudaError_t prepare_linear_strip(int sms, int *clusters) {
+    const auto prepare = [](const void *fn) {
+        return fn ? cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripAlone + 1024) : cudaSuccess;
+    };
     for (LinearMode mode : {kLinPlain, kLinGated, kLinGateGrad, kLinStats, kLinSoftGrad})
-        for (int layout : {0, 2, 3}) {
-            const StripKernel fn = strip_kernel(layout, mode);
-            if (!fn) continue;
-            cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStripAlone + 1024);
-            if (e != cudaSuccess) return e;
-        }
+        for (int layout : {0, 2, 3})
+            for (const void *fn : {reinterpret_cast<const void *>(strip_kernel(layout, mode)),
+                                   reinterpret_cast<const void *>(strip_more_kernel(layout, mode))}) {
+                const cudaError_t e = prepare(fn);
+                if (e != cudaSuccess) return e;
+            }
     for (int i = 2; i <= kStripMostSplits; ++i) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(sms / i * i));
@@ -550,13 +571,16 @@ cudaError_t prepare_linear_strip(int sms, int *clusters) {
     return cudaSuccess;
 }
 
-cudaError_t launch_linear_strip(const LinearStripParams &p, int layout, LinearMode mode, cudaStream_t stream) {
+cudaError_t launch_linear_strip(const LinearStripMore &p, int layout, LinearMode mode, cudaStream_t stream) {
     const int64_t tile_cols = mode == kLinGated ? kTileCols / 2 : kTileCols;
     const int64_t grid = (p.cols + tile_cols - 1) / tile_cols * p.row_tiles * p.splits;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    const StripKernel fn = strip_kernel(layout, mode);
+    const size_t smem = size_t(p.ring_bytes) + 1024;
+    if (const StripKernel fn = strip_kernel(layout, mode))
+        return launch_after(fn, dim3(unsigned(grid)), kThreadsL, smem, unsigned(p.splits), stream, static_cast<const LinearStripParams &>(p));
+    const StripMoreKernel fn = strip_more_kernel(layout, mode);
     if (!fn) return cudaErrorInvalidValue;
-    return launch_after(fn, dim3(unsigned(grid)), kThreadsL, size_t(p.ring_bytes) + 1024, unsigned(p.splits), stream, p);
+    return launch_after(fn, dim3(unsigned(grid)), kThreadsL, smem, unsigned(p.splits), stream, p);
 }
 
 }  // namespace cm
