@@ -91,6 +91,28 @@ __device__ __forceinline__ void put8(T *row, int c, int h, const V8 &v) {
     }
 }
 
+// Eight neighbouring elements as they were loaded: of bf16 half the registers of the
+// numbers, so that more warps fit on an SM.
+template <typename T, bool VEC>
+struct Raw8 {
+    V8 v;
+    __device__ __forceinline__ void load(const T *row, int c, int h) { v = get8<VEC>(row, c, h); }
+    __device__ __forceinline__ V8 get() const { return v; }
+};
+template <>
+struct Raw8<bf16, true> {
+    uint4 w;
+    __device__ __forceinline__ void load(const bf16 *row, int c, int h) {
+        if (c + 8 <= h) {
+            w = *reinterpret_cast<const uint4 *>(row + c);
+            return;
+        }
+        const V8 v = load_row8(row, c, h);
+        w = make_uint4(pack(v.p[0]), pack(v.p[1]), pack(v.p[2]), pack(v.p[3]));
+    }
+    __device__ __forceinline__ V8 get() const { return {{unpack(w.x), unpack(w.y), unpack(w.z), unpack(w.w)}}; }
+};
+
 // ---- lookup -------------------------------------------------------------------------
 struct LookupParams {
     Ids ids;
@@ -105,10 +127,11 @@ constexpr int kLookThreads = 256, kLookBatch = 4;
 
 // `width` (a power of two up to 256) neighbouring threads share a row, each with
 // four of its vectors under way before its first store; rows of more than 1024
-// vectors take several CTAs.  No division: counted through all rows' vectors, 16384
-// tokens of 8192 elements took 101 us instead of 70.
+// vectors take several CTAs.  Bound by memory: 16384 tokens of 8192 elements take 62 us.
+// (Counted through all rows' vectors, with a division each, 101; with half the CTAs an
+// SM 78.)
 template <typename W, typename Y, bool VEC>
-__global__ void __launch_bounds__(kLookThreads) cm_embedding_kernel(const LookupParams p) {
+__global__ void __launch_bounds__(kLookThreads, !VEC || sizeof(W) == 4 ? 4 : sizeof(Y) == 4 ? 6 : 8) cm_embedding_kernel(const LookupParams p) {
     let_next_start();
     wait_for_previous();
     const int lane = int(threadIdx.x) & (p.width - 1), rows = kLookThreads / p.width;
@@ -118,15 +141,13 @@ __global__ void __launch_bounds__(kLookThreads) cm_embedding_kernel(const Lookup
     const uint32_t row = row_of(p.ids, t);
     const W *from = static_cast<const W *>(p.w) + int64_t(row == kNoRow ? 0 : row) * p.ldw;
     Y *to = static_cast<Y *>(p.y) + t * p.ldy;
-    V8 v[kLookBatch];
-#pragma unroll
-    for (int k = 0; k < kLookBatch; ++k) {
-        v[k] = fill(0.0f);
-        if (row != kNoRow && c0 + k * step < p.h) v[k] = get8<VEC>(from, c0 + k * step, p.h);
-    }
+    Raw8<W, VEC> v[kLookBatch];
 #pragma unroll
     for (int k = 0; k < kLookBatch; ++k)
-        if (c0 + k * step < p.h) put8<VEC>(to, c0 + k * step, p.h, scaled(v[k], p.scale));
+        if (row != kNoRow && c0 + k * step < p.h) v[k].load(from, c0 + k * step, p.h);
+#pragma unroll
+    for (int k = 0; k < kLookBatch; ++k)
+        if (c0 + k * step < p.h) put8<VEC>(to, c0 + k * step, p.h, row != kNoRow ? scaled(v[k].get(), p.scale) : fill(0.0f));
 }
 
 // ---- tokens sorted by row -----------------------------------------------------------
@@ -281,28 +302,6 @@ __global__ void __launch_bounds__(256) cm_embedding_zero_kernel(const SumParams 
     for (int i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(row)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int c = whole * kPer + lane; c < p.h; c += 32) from_f(row + c, 0.0f);
 }
-
-// Eight neighbouring elements as they were loaded: of bf16 half the registers of the
-// numbers, so that more warps fit on an SM.
-template <typename T, bool VEC>
-struct Raw8 {
-    V8 v;
-    __device__ __forceinline__ void load(const T *row, int c, int h) { v = get8<VEC>(row, c, h); }
-    __device__ __forceinline__ V8 get() const { return v; }
-};
-template <>
-struct Raw8<bf16, true> {
-    uint4 w;
-    __device__ __forceinline__ void load(const bf16 *row, int c, int h) {
-        if (c + 8 <= h) {
-            w = *reinterpret_cast<const uint4 *>(row + c);
-            return;
-        }
-        const V8 v = load_row8(row, c, h);
-        w = make_uint4(pack(v.p[0]), pack(v.p[1]), pack(v.p[2]), pack(v.p[3]));
-    }
-    __device__ __forceinline__ V8 get() const { return {{unpack(w.x), unpack(w.y), unpack(w.z), unpack(w.w)}}; }
-};
 
 // A warp for each aligned piece of 16 sorted tokens and 256 columns; ADD: dw is added to.
 // Four rows, and as many old ones of dw, are under way at a time.

@@ -51,13 +51,12 @@ __global__ void __launch_bounds__(kRowsThreads) cm_head_rows_kernel(const HeadRo
     float top = 0.0f;
 #pragma unroll 4
     for (int64_t r = threadIdx.x; r < p.rows; r += kRowsThreads) {
-        if (target_of(p, r) < 0) continue;
+        const int64_t t = target_of(p, r);
+        const float a = p.dloss ? p.dloss[r] : 0.0f, b = p.dlse ? p.dlse[r] : 0.0f;   // read whether it counts or not
+        if (t < 0) continue;
         ++all;
         before += r < r0;
-        if (p.dloss) {
-            const float a = p.dloss[r];
-            top = larger(larger(top, a), p.dlse ? a + p.dlse[r] : a);
-        }
+        top = larger(larger(top, a), a + b);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {

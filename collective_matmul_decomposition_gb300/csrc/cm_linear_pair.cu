@@ -360,6 +360,9 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
     // With an fp32 y those are bf16 beside 4-byte chunks: read directly.
     // The gate's gradients read both z and write one gradient over each.
     constexpr bool kGate = MODE == kLinGateGrad;
+    // They pass through L2 once: they are not to push the operands out of it.
+    [[maybe_unused]] uint64_t once = 0;
+    if constexpr (kGate) once = policy_evict_first();
     const bool in0 = kGate || (!F32 && (e.res || e.accumulate)), in1 = kGate || (!F32 && e.dact);
     const uint32_t in_bytes = uint32_t(in0 ? kEpiBuf : 0) + uint32_t(in1 ? kEpiBuf : 0);
     // the second buffer holds the pre-activation if there is one; else chunks
@@ -393,8 +396,13 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
                 bulk_wait_read<0>();
             if (in_bytes) {
                 mbar_expect_tx(ibar, in_bytes);
-                if (in0) tma_load_3d(buf0, &p.tmIn0, ibar, cbase + ch * kChunk, row0, 0);
-                if (in1) tma_load_3d(buf1, &p.tmIn1, ibar, cbase + ch * kChunk, row0, 0);
+                if constexpr (kGate) {
+                    tma_load_3d_hint(buf0, &p.tmIn0, ibar, cbase + ch * kChunk, row0, 0, once);
+                    tma_load_3d_hint(buf1, &p.tmIn1, ibar, cbase + ch * kChunk, row0, 0, once);
+                } else {
+                    if (in0) tma_load_3d(buf0, &p.tmIn0, ibar, cbase + ch * kChunk, row0, 0);
+                    if (in1) tma_load_3d(buf1, &p.tmIn1, ibar, cbase + ch * kChunk, row0, 0);
+                }
             }
         };
         if (nch > 0 && in_bytes) {
@@ -526,11 +534,16 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
             __syncwarp();
             if (lane == 0) {
                 if (c0 < whole) {
-                    if (F32 && e.accumulate)
+                    if constexpr (kGate)
+                        tma_store_3d_hint(&p.tmY, buf0, c0, row0, 0, once);
+                    else if (F32 && e.accumulate)
                         tma_reduce_add_3d(&p.tmY, buf0, c0, row0, 0);
                     else
                         tma_store_3d(&p.tmY, buf0, c0, row0, 0);
-                    if (!F32 && e.z) tma_store_3d(&p.tmZ, buf1, c0, row0, 0);
+                    if constexpr (kGate)
+                        tma_store_3d_hint(&p.tmZ, buf1, c0, row0, 0, once);
+                    else if (!F32 && e.z)
+                        tma_store_3d(&p.tmZ, buf1, c0, row0, 0);
                 }
                 bulk_commit();
             }
