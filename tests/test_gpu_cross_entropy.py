@@ -295,3 +295,29 @@ def test_graph_and_streams(M):
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (loss, lse, dx, dw)))
         assert masked != "all" or not any(bool(v.any()) for v in got)
+
+
+def test_weights_behind_4_gb():
+    """Weights whose last rows start beyond 2^32 bytes and 2^31 elements, and a gradient as large."""
+    M, K, n = 3, 4096, 600_000
+    x, _ = matrix(M, K, seed=90)
+    w = torch.zeros(n, K, dtype=BF, device=DEV)
+    t = torch.tensor([n - 1, 524_288, 5], device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(91)
+    w[t] = (torch.randn(M, K, generator=g, device=DEV) * 0.1).to(BF)   # all other logits are zero
+    loss, lse = torch.empty(M, device=DEV), torch.empty(M, device=DEV)
+    ws, _ = space(max(cm.linear_cross_entropy_workspace_size(M, K, n), cm.linear_cross_entropy_backward_workspace_size(M, K, n)))
+    cm.cm_linear_cross_entropy(x, w, t, loss, lse, ws)
+    z = x.double() @ w[t].double().t()
+    b = product_bound(x.double(), w[t].double().t())
+    want = torch.logsumexp(torch.cat([z, torch.zeros(M, 1, device=DEV, dtype=torch.float64) + float(torch.tensor(n - M).double().log())], 1), 1)
+    bound = lse_error(z, b, want, n)
+    assert bool(((lse.double() - want).abs() <= bound).all())
+    assert bool(((loss.double() - (want - z.diagonal())).abs() <= bound + b.diagonal()).all())
+    dw = torch.empty(n, K, dtype=BF, device=DEV)
+    cm.cm_linear_cross_entropy_backward(x, w, t, lse, torch.ones(M, device=DEV), ws, dw=dw)
+    for row in (0, 5, 524_287, 524_288, n - 2, n - 1):
+        p = torch.exp((x.double() @ w[row].double()) - lse.double()) - (t == row).double()
+        exact = p @ x.double()
+        size = p.abs() @ x.double().abs()
+        assert bool(((dw[row].double() - exact).abs() <= (2.0 ** -8 + 2.0 ** -18) * size + half_ulp(exact, BF)).all()), row
