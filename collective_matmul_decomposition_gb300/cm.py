@@ -627,7 +627,8 @@ def cm_linear_cross_entropy(x, w, targets, loss, lse, ws, picked=None, first: in
     lib = _library()
     M, K, dev = _extents("x", x)
     layout = LAYOUTS[w_layout]
-    n = w.shape[layout != CM_W_NK]
+    columns = _columns("w", w)
+    n = w.shape[0] if layout == CM_W_NK else columns
     xp, ldx = _matrix("x", x, (M, K), dev, _b16)
     wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
     tp, bits = _index_vector("targets", targets, M, dev)
@@ -650,7 +651,8 @@ def cm_linear_cross_entropy_backward(x, w, targets, lse, dloss, ws, dx=None, dw=
     lib = _library()
     M, K, dev = _extents("x", x)
     layout = LAYOUTS[w_layout]
-    n = w.shape[layout != CM_W_NK]
+    columns = _columns("w", w)
+    n = w.shape[0] if layout == CM_W_NK else columns
     xp, ldx = _matrix("x", x, (M, K), dev, _b16)
     wp, ldw = _matrix("w", w, (n, K) if layout == CM_W_NK else (K, n), dev, _b16)
     dxp, lddx = _matrix("dx", dx, (M, K), dev) if dx is not None else (None, 0)
@@ -818,6 +820,7 @@ def cm_embedding_backward(dy, ids, dw, ws, scale: float = 1.0, first: int = 0, a
     in ws); with accumulate, rows of dw without a token are left as they are, else they become zeros."""
     lib = _library()
     tokens, h, dev = _extents("dy", dy)
+    _columns("dw", dw)
     n = dw.shape[0]
     ip, bits = _index_vector("ids", ids, tokens, dev)
     dyp, lddy = _matrix("dy", dy, (tokens, h), dev)

@@ -140,7 +140,7 @@ struct LinearPairMore : LinearPairParams {
 };
 
 // layout: bit 0 = B MN-major, bit 1 = A MN-major; the gated modes take 0 and 1, and
-// kLinGated tiles of 256 columns, half of them of each operand; the head's modes have
+// kLinGated, half of whose columns are of each operand, unsplit tiles of 256; the head's modes have
 // 0 and 1, tiles of 256 columns and no splits; kLinCounted has no splits.  splits: 1 (persistent, on
 // `clusters` pairs), or 2 or 4 pairs a cluster that share a tile's K slices,
 // one cluster a tile.  clusters[i]: clusters of 2^i pairs that run together.

@@ -159,20 +159,23 @@ struct Choice {
 //   rows 2048, K 12288, cols 4608:  129 / 161 / -     rows 1024, K 8192, cols 1024:  40.1 / 23.1 / 16.8
 // and between strips (one tile of rows / more, shorter ones):
 //   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  22.8 / 29.0 (three)
-// A gated product is estimated as one of the columns of both its operands; its
-// pair tiles have 256 of them (`wide`).
-Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn, bool wide = false) {
+// A gated product is estimated as one of the columns of both its operands.
+// Pair tiles of 128 columns: any, only where K is split (gated: an unsplit tile's
+// epilogue needs 64 columns a warp of either operand), or none.
+enum class Narrow { any, split, none };
+Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn, Narrow narrow = Narrow::any) {
     Choice best;
     double least = 1e30;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t slices = up(k, kBK);
     const double from_hbm = double(cols) * double(k) * 2.0 / 8.5e6;
     // pair tiles waste what they have beyond `rows`: not worth a look below 33
-    for (int bn = 256; bn >= (wide ? 256 : 128) && rows > 32; bn /= 2) {
+    for (int bn = 256; bn >= (narrow == Narrow::none ? 256 : 128) && rows > 32; bn /= 2) {
         const int64_t tiles = up(rows, 256) * up(cols, bn);
         for (int i = 0; i < 3; ++i) {
             const int splits = 1 << i;
             if (i > 0 && (tiles > d.clusters[i] || slices < 2 * splits)) break;
+            if (i == 0 && bn == 128 && narrow == Narrow::split) continue;
             const double wave = std::max(double(up(slices, splits)) * (bn == 256 ? 0.32 : 0.21), bn == 256 ? 2.9 : 2.0);
             const double run = double(up(tiles, d.clusters[i])) * wave;
             const double t = 3.8 + (i == 0 ? 0.0 : bn == 256 ? 2.6 : 1.6) + std::max(run, from_hbm) +
@@ -305,14 +308,18 @@ cm_status product_strip(const Device &d, const Choice &c, const Kind &kind, cons
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
                   const LinearEpilogue &e, cudaStream_t stream, const Kind &kind = {}) {
     const bool gated = kind.mode == kLinGated;
-    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated);
+    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated ? Narrow::split : Narrow::any);
     return c.pair ? product_pair(d, c, kind, a, b, rows, cols, k, e, stream) : product_strip(d, c, kind, a, b, rows, cols, k, e, stream);
 }
 
-// Logits, whose columns are as many as the vocabulary's: strips where choose() takes
-// them, else whole pair tiles.
+// Logits, whose columns are as many as the vocabulary's: for up to 256 rows strips where
+// choose() takes them, else whole pair tiles.  Several row tiles of strips have too long an
+// epilogue here: the loss of 300 rows, 4096 x 32768, took 114 us in strips, 400 rows take
+// 97 in pair tiles; 200 rows 67 us, 64 rows (131072 columns) 225 in strips.
 Choice choose_logits(const Device &d, int64_t rows, int64_t cols, int64_t k) {
-    Choice c = choose(d, rows, cols, k, false, true);
+    Choice c;
+    c.pair = true;
+    if (rows <= 256) c = choose(d, rows, cols, k, false, Narrow::none);
     if (c.pair) c.splits = 1;
     return c;
 }

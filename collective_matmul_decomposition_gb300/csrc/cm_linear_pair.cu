@@ -1248,7 +1248,7 @@ using PairKernel = void (*)(PairParams<MODE>);
 // not have is NULL.
 template <int MODE, int LAYOUT>
 PairKernel<MODE> pair_kernel_of(int bn, int splits) {
-    constexpr bool kSplits = !kIsCounted<MODE>, kNarrow = MODE == kLinPlain || MODE == kLinGateGrad || MODE == kLinCounted;
+    constexpr bool kSplits = !kIsCounted<MODE>, kNarrow = MODE != kLinGated && MODE != kLinStats && MODE != kLinSoftGrad;
     if (bn == 256 && splits == 1) return cm_linear_pair_kernel<LAYOUT, 256, MODE>;
     if constexpr (kNarrow)
         if (bn == 128 && splits == 1) return cm_linear_pair_kernel<LAYOUT, 128, MODE>;
@@ -1256,7 +1256,7 @@ PairKernel<MODE> pair_kernel_of(int bn, int splits) {
         if (bn == 256 && splits == 2) return cm_linear_split_kernel<LAYOUT, 256, 2, MODE>;
         if (bn == 256 && splits == 4) return cm_linear_split_kernel<LAYOUT, 256, 4, MODE>;
     }
-    if constexpr (kSplits && kNarrow) {
+    if constexpr (kSplits) {
         if (bn == 128 && splits == 2) return cm_linear_split_kernel<LAYOUT, 128, 2, MODE>;
         if (bn == 128 && splits == 4) return cm_linear_split_kernel<LAYOUT, 128, 4, MODE>;
     }
