@@ -541,7 +541,8 @@ def cm_linear_dgrad(dy, w, dx, preact=None, act: str = "none", residual=None, w_
 
 def _matrices(names, ts, shape, device, dtype):
     """Two matrices of one shape and row stride: (pointers, row stride)."""
-    (p0, ld0), (p1, ld1) = (_matrix(name, t, shape, device, dtype) for name, t in zip(names, ts))
+    p0, ld0 = _matrix(names[0], ts[0], shape, device, dtype)
+    p1, ld1 = _matrix(names[1], ts[1], shape, device, dtype)
     if ld0 != ld1:
         raise ValueError(f"{names[0]} and {names[1]} must have one row stride, not {ld0} and {ld1}")
     return p0, p1, ld0
@@ -554,7 +555,7 @@ def cm_linear_gated(x, w_gate, w_up, y, act: str = "silu", bias_gate=None, bias_
     M, K, dev = _extents("x", x)
     n = _columns("y", y)
     layout = LAYOUTS[w_layout]
-    if (bias_gate is None) != (bias_up is None) or (z_gate is None) != (z_up is None):
+    if (bias_gate is None) is not (bias_up is None) or (z_gate is None) is not (z_up is None):
         raise ValueError("biases and pre-activations are given for both projections or for neither")
     if bias_gate is not None and bias_gate.dtype is not bias_up.dtype:
         raise TypeError("bias_gate and bias_up must have one dtype")
