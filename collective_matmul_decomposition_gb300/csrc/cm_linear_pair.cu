@@ -374,6 +374,7 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
     constexpr int kPiece = F32 ? 4 : 8;
     const int rest = int(p.cols % kPiece);
     const int64_t whole = p.cols - rest;
+    [[maybe_unused]] const float scale = MODE == kLinCounted && e.scale ? *e.scale : 1.0f;
     int acc = flow.acc;
     uint32_t acc_phase = flow.acc_phase, in_phase = flow.in_phase;
     bool pending = false;   // inputs asked for and not yet waited for
@@ -444,8 +445,7 @@ __device__ __forceinline__ void finish_tiles(const LinearPairParams &p, const LS
                 float f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                if (MODE == kLinCounted && e.scale) {
-                    const float scale = *e.scale;
+                if constexpr (MODE == kLinCounted) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] *= scale;
                 }

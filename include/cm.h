@@ -707,8 +707,8 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
  *  (dx_dtype) and dw (dw_dtype) may each be NULL; with `accumulate` dw is added to.
  *  Rows without a target give zeros and count nowhere; their lse, dloss and dlse
  *  are not used.  The logits are computed again, some columns at a time, and dz is
- *  rounded to bf16 for the products (relative to the largest of the finite
- *  |dloss|, |dloss + dlse|); sums are fp32.
+ *  rounded to bf16 for the products, relative to the largest of the finite
+ *  |dloss|, |dloss + dlse| (what is below 2^-126 of it is lost); sums are fp32.
  *  ws: cm_linear_cross_entropy_backward_workspace_size(M, K, n) bytes, as above.
  */
 size_t cm_linear_cross_entropy_backward_workspace_size(int64_t M, int64_t K, int64_t n);
@@ -720,9 +720,9 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
                                            cm_stream_t stream);
 
 /*
- * cm_linear_choose -- how the calls above compute a product of `rows` x `cols`
- * elements with k terms each on the current device; asks for no launch and
- * no memory.  The forward call's product is M x n with k = K, the data
+ * cm_linear_choose -- how cm_linear and its gradients compute a product of `rows`
+ * x `cols` elements with k terms each on the current device; asks for no launch
+ * and no memory.  The forward call's product is M x n with k = K, the data
  * gradient's M x K with k = n.  The weight gradient's (`transposed` not 0) has
  * the weight's extents as it is stored, n x K or K x n, with k = M.
  *  Errors: CM_ERR_INVALID_ARG (NULL), CM_ERR_SHAPE (an extent that is not

@@ -321,3 +321,24 @@ def test_weights_behind_4_gb():
         exact = p @ x.double()
         size = p.abs() @ x.double().abs()
         assert bool(((dw[row].double() - exact).abs() <= (2.0 ** -8 + 2.0 ** -18) * size + half_ulp(exact, BF)).all()), row
+
+
+@pytest.mark.parametrize("M", [5, 800])
+def test_factors_of_zero_and_of_all_sizes(M):
+    """No gradient where both factors are zero; factors from 1e-30 to 1e30 each keep their row's accuracy."""
+    K, n = 72, 500
+    x, w, t, vocab, _ = make(M, K, n, 0, 0, "none", "nk", seed=95)
+    wide, buf = matrix(M, K, pad=24, seed=96)   # rows further apart than they are long
+    ws, _ = space(max(cm.linear_cross_entropy_workspace_size(M, K, n), cm.linear_cross_entropy_backward_workspace_size(M, K, n)))
+    loss, lse = torch.empty(M, device=DEV), torch.empty(M, device=DEV)
+    cm.cm_linear_cross_entropy(wide, w, t, loss, lse, ws)
+    dx, dw = torch.empty(M, K, device=DEV), torch.empty(n, K, device=DEV)
+    cm.cm_linear_cross_entropy_backward(wide, w, t, lse, torch.zeros(M, device=DEV), ws, dx=dx, dw=dw)
+    assert not bool(dx.any()) and not bool(dw.any())
+    dloss = 10.0 ** torch.linspace(-30, 30, M, device=DEV)
+    cm.cm_linear_cross_entropy_backward(wide, w, t, lse, dloss, ws, dx=dx, dw=dw)
+    (want, bound), (want_w, bound_w) = gradient(wide, w, t, lse, dloss, None, 0, "nk", torch.ones(M, dtype=torch.bool, device=DEV))
+    # relative to the largest factor the smallest ones' rows fall below fp32's least number times it, 2^-126 1e30
+    tiny = 2.0 ** -100 * 1e30
+    assert bool(((dx.double() - want).abs() <= (bound + half_ulp(want, F32)) * (1 + 2.0 ** -7) + tiny).all())
+    assert bool(((dw.double() - want_w).abs() <= (bound_w + half_ulp(want_w, F32)) * (1 + 2.0 ** -7) + tiny).all())

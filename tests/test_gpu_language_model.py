@@ -96,3 +96,30 @@ def test_trains_and_serves(example):
     want = torch.nn.functional.cross_entropy(logits.double(), targets[:40], reduction="none", ignore_index=-100)
     # the same numbers by other tiles: sums in another order may put a stored value on the neighbouring bf16
     assert bool(((loss[:40].double() - want)[on].abs() <= 2.0 ** -5 * (1 + want[on].abs())).all())
+
+
+def test_two_streams_at_once(example):
+    """Two models' steps under way together, each on a stream and in a workspace of its own: the bits of one after the
+    other."""
+    args = (256, 520, 2, 3000, 700)
+    ids, targets = example.data(3000, 700, 11)
+    dloss = torch.full((700,), 1.0 / 613, device="cuda")
+    models = [example.LanguageModel(*args, seed=s) for s in (12, 13)]
+    want = []
+    for m in models:
+        m.forward(ids, targets)
+        m.backward(ids, targets, dloss)
+        want.append((m.loss.clone(), {k: v.clone() for k, v in m.grad.items()}))
+        m.loss.zero_()
+        for v in m.grad.values():
+            v.zero_()
+    streams = [torch.cuda.Stream() for _ in models]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for m, s in zip(models, streams):
+            with torch.cuda.stream(s):
+                m.forward(ids, targets)
+                m.backward(ids, targets, dloss)
+    torch.cuda.synchronize()
+    for m, (loss, grad) in zip(models, want):
+        assert torch.equal(m.loss, loss) and all(torch.equal(m.grad[k], grad[k]) for k in grad)
