@@ -398,7 +398,11 @@ LossGradSpace loss_grad_space(Carve &c, int64_t M, int64_t K, int64_t n) {
 }
 
 cm_status check_head(const void *x, int64_t ldx, const void *w, int64_t ldw, cm_wlayout wlayout, const void *targets,
-                     int target_bits, int64_t first, int64_t vocab, int64_t K, int64_t n) {
+                     int target_bits, int64_t first, int64_t vocab, int64_t M, int64_t K, int64_t n) {
+    // tiles are counted in 31 bits (of 128 columns, where a product takes those): found out
+    // before the first launch of several
+    const int64_t m = (M + 127) / 128, k = (K + 127) / 128, v = (n + 127) / 128;
+    if (m * v > 0x7fffffff || m * k > 0x7fffffff || k * v > 0x7fffffff) return CM_ERR_SHAPE;
     if (!targets || first < 0 || first > kMaxExtent || vocab < first + n || vocab > 2 * kMaxExtent) return CM_ERR_INVALID_ARG;
     const cm_status st = check_matrix(x, ldx, K);
     if (st != CM_OK) return st;
@@ -609,7 +613,7 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
     if ((wlayout != CM_W_KN && wlayout != CM_W_NK) || (target_bits != 32 && target_bits != 64)) return CM_ERR_INVALID_ARG;
     CM_TRY(check_extents(M, K, n));
     if (M == 0) return CM_OK;
-    CM_TRY(check_head(x, ldx, w, ldw, wlayout, targets, target_bits, first, vocab, K, n));
+    CM_TRY(check_head(x, ldx, w, ldw, wlayout, targets, target_bits, first, vocab, M, K, n));
     if (!ws || ws_bytes < cm_linear_cross_entropy_workspace_size(M, K, n)) return CM_ERR_WORKSPACE;
     if (!aligned16(ws) || misaligned(loss, CM_F32) || misaligned(lse, CM_F32) || misaligned(picked, CM_F32)) return CM_ERR_ALIGNMENT;
     Device d;
@@ -683,7 +687,7 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
         return CM_OK;
     }
     if (!lse || !dloss) return CM_ERR_INVALID_ARG;
-    CM_TRY(check_head(x, ldx, w, ldw, wlayout, targets, target_bits, first, vocab, K, n));
+    CM_TRY(check_head(x, ldx, w, ldw, wlayout, targets, target_bits, first, vocab, M, K, n));
     if (dx) CM_TRY(check_matrix(dx, lddx, K));
     if (!ws || ws_bytes < cm_linear_cross_entropy_backward_workspace_size(M, K, n)) return CM_ERR_WORKSPACE;
     if (!aligned16(ws) || misaligned(lse, CM_F32) || misaligned(dloss, CM_F32) || misaligned(dlse, CM_F32)) return CM_ERR_ALIGNMENT;

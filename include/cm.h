@@ -686,7 +686,8 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
  *  there.  Where a target lies outside of the slice, picked is 0: over ranks that
  *  hold a slice each, log sum_ranks exp(lse) less the sum of picked is the loss of
  *  the whole.  A target of `vocab` or more has a NaN loss.  Products, maxima and
- *  sums are fp32.  first at most 2^30, vocab at least first + n and at most 2^31.
+ *  sums are fp32.  first at most 2^30, vocab at least first + n and at most 2^31;
+ *  M n, M K and K n below 2^45 (CM_ERR_SHAPE beyond).
  *  ws: cm_linear_cross_entropy_workspace_size(M, K, n) bytes, 16-byte aligned; no
  *  initialisation; calls that share it must be ordered on the GPU.  Results do not
  *  depend on timing.  Errors as cm_linear, and CM_ERR_WORKSPACE.

@@ -38,7 +38,8 @@ def test_both(lib, call):
     for kw in (dict(x=None), dict(w=None), dict(t=None), dict(layout=2), dict(bits=8), dict(first=-1), dict(vocab=31),
                dict(first=1), dict(first=(1 << 30) + 1, vocab=1 << 31), dict(vocab=(1 << 31) + 1)):
         assert call(lib, **kw) == cm.CM_ERR_INVALID_ARG, kw
-    for kw in (dict(M=-1), dict(K=0), dict(n=0), dict(M=(1 << 30) + 1), dict(ldx=56), dict(ldw=8), dict(layout=cm.CM_W_KN, ldw=24)):
+    for kw in (dict(M=-1), dict(K=0), dict(n=0), dict(M=(1 << 30) + 1), dict(ldx=56), dict(ldw=8), dict(layout=cm.CM_W_KN, ldw=24),
+               dict(M=1 << 30, n=1 << 17, vocab=1 << 17, ws_bytes=1 << 60)):   # more tiles than are counted
         assert call(lib, **kw) == cm.CM_ERR_SHAPE, kw
     for kw in (dict(x=A + 2), dict(w=A + 8), dict(ldx=65), dict(ldw=68), dict(t=A + 2), dict(t=A + 4, bits=64), dict(lse=A + 2),
                dict(ws=A + 8)):
