@@ -58,6 +58,10 @@ struct LinearHead {
     int64_t stride;          // slots there may be
     int64_t first;           // column of the slice that the product's first one is
 };
+// The tensor cores cut a sum off at each step of 16 terms, by which long sums fall
+// short: by 5e-6 of a logit of 4096 terms.  The loss's logits are therefore summed in
+// parts of this many slices of 64 terms, whose fp32 results are added with rounding.
+constexpr int kStatSlices = 16;
 constexpr int32_t kNotHere = -1, kNoToken = -2;   // of another slice; beyond the vocabulary
 
 // A product of the slots' rows: how many there are is known on the device only.

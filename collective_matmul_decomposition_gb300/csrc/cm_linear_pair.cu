@@ -253,15 +253,27 @@ __device__ __forceinline__ void multiply_tiles(const LinearPairParams &p, const 
     uint32_t phase = flow.phase, acc_phase = flow.acc_phase;
     bool ok = flow.ok;
     const uint16_t both = uint16_t(3u << w.leader);   // the pair's CTAs
+    constexpr bool kParts = MODE == kLinStats;        // an accumulator for each kStatSlices slices
     for (int t = w.first; t < tiles_of<MODE>(p, w) && ok; t += w.step) {
         if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) {
             ok = false;
             break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + uint32_t(acc * BN);
+        uint32_t d = tmem + uint32_t(acc * BN);
         bool ready = mbar_test_wait(s.full + stage, phase);   // looked at ahead, so that its latency overlaps the issue
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
+            if (kParts && kb > w.kb0 && (kb - w.kb0) % kStatSlices == 0) {
+                mma_commit_pair_mc(&s.tfull[acc], both);
+                acc ^= 1;
+                acc_phase ^= acc == 0 ? 1u : 0u;
+                if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                d = tmem + uint32_t(acc * BN);
+            }
             if (!ready && !mbar_try_wait(s.full + stage, phase) && !wait_p(p, s, s.full + stage, phase, kLinSiteFull, t)) {
                 ok = false;
                 break;
@@ -271,7 +283,8 @@ __device__ __forceinline__ void multiply_tiles(const LinearPairParams &p, const 
             const uint64_t bd = bd0 + uint64_t((uint32_t(stage) * kB) >> 4);
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-                mma_bf16_pair(d, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), kIdesc, kb > w.kb0 || k > 0 ? 1u : 0u);
+                mma_bf16_pair(d, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), kIdesc,
+                              (kParts ? (kb - w.kb0) % kStatSlices > 0 : kb > w.kb0) || k > 0 ? 1u : 0u);
             mma_commit_pair_mc(s.empty + stage, both);
             if (++stage == kStages) {
                 stage = 0;
@@ -666,14 +679,101 @@ __device__ void finish_gated(const LinearPairMore &p, const LSmem &s, uint32_t t
 }
 
 // The statistics of a softmax over the columns, without the logits: a thread owns one
-// row and half of the tile's columns, and goes through them 32 at a time with the
-// running maximum m and sum s of exp2(v log2(e) - m), all in fp32:
-//   m' = max(m, max v);  s' = s exp2(m - m') + sum exp2(v - m').
-// What is not a column counts as -infinity.  A NaN stays one through the sum.
+// row and half of the tile's columns, adds up their parts (kStatSlices) in registers
+// while the products go on, and reduces them to the largest m and the sum of exp2(v
+// log2(e) - m), all in fp32.  What is not a column counts as -infinity.  A NaN stays one
+// through the sum.
 // It leaves 8 bytes for 128 logits and costs the products little: 8192 x 4096 x 131072
-// takes 4.8 ms, 1830 TFLOP/s, and the tensor pipe is 88 % busy with 32 slices a tile.  With
-// one slice it is bound by the special-function units: 8192 x 64 x 131072 takes 383 us.
+// takes 4.8 ms, 1830 TFLOP/s.  Losses are off by 2.5e-7 of their value; with one
+// accumulator a tile it was 8.6e-7 for 4096 terms and 1.5e-6 for 7040, in the same time.
 __device__ void finish_stats(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
+    constexpr int BN = 256, kCols = BN / 2, kBlocks = kCols / 16;
+    const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
+    const int quad = ew & 3, half = ew >> 2;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    const int parts = (w.kb1 - w.kb0 + kStatSlices - 1) / kStatSlices;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = w.first; t < w.tiles && ok; t += w.step) {
+        int mt, nt;
+        tile_at(p, w.mtiles, t, mt, nt);
+        const int row0 = mt * kTile + rank * kHalf + quad * 32;
+        const int64_t c0 = int64_t(nt) * BN + half * kCols;
+        const bool live = row0 < w.rows && c0 < p.cols;   // the same in the whole warp
+        float f[kBlocks][16];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[b][i] = 0.0f;
+#pragma unroll 1
+        for (int part = 0; part < parts; ++part) {
+            ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (live) {
+                const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    uint32_t v[16];
+                    tmem_ld16(taddr + uint32_t(16 * b), v);
+                    tmem_wait_ld_regs(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[b][i] += __uint_as_float(v[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
+            acc ^= 1;
+            acc_phase ^= acc == 0 ? 1u : 0u;
+        }
+        if (!ok) break;
+        const int row = row0 + lane;
+        if (row >= w.rows) continue;
+        if (!live) {   // no column is here
+            p.head.stat[(int64_t(nt) * 2 + half) * p.head.stride + row] = make_float2(-INFINITY, 0.0f);
+            continue;
+        }
+        // the target's place among these columns, if it is there
+        const int64_t target = p.head.target[row], left = target - p.head.first - c0;
+        if (target >= 0 && left >= 0 && left < kCols && c0 + left < p.cols) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (int(left) == 16 * b + i) p.head.picked[row] = f[b][i];
+        }
+        if (c0 + kCols > p.cols) {
+            const int n = int(p.cols - c0);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[b][i] = 16 * b + i < n ? f[b][i] : -INFINITY;
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top[i & 3] = fmaxf(top[i & 3], f[b][i]);
+        const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * lin::kLog2e;
+        const float base = m == -INFINITY ? 0.0f : m;   // no number: exp2(-inf - 0) is 0
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i & 3] += lin::exp2_fast(fmaf(f[b][i], lin::kLog2e, -base));
+        p.head.stat[(int64_t(nt) * 2 + half) * p.head.stride + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    }
+    __syncwarp();
+}
+
+// The same for tiles of one part, whose epilogue sets the pace: through the columns 32 at
+// a time with the running maximum m and sum s,
+//   m' = max(m, max v);  s' = s exp2(m - m') + sum exp2(v - m'),
+// which needs half the registers and no copy of the columns.  65536 x 512 x 4096 takes
+// 235 us, with the columns in registers 308; 8192 x 64 x 131072 374 and 407.
+__device__ void finish_stats_few(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = BN / 2;
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
     const int quad = ew & 3, half = ew >> 2;
@@ -913,7 +1013,10 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
         if constexpr (MODE == kLinGated)
             finish_gated(p, s, tmem, rank);
         else if constexpr (MODE == kLinStats)
-            finish_stats(p, s, w, tmem, rank);
+            if (w.kb1 - w.kb0 > kStatSlices)
+                finish_stats(p, s, w, tmem, rank);
+            else
+                finish_stats_few(p, s, w, tmem, rank);
         else if constexpr (MODE == kLinSoftGrad)
             finish_softgrad(p, s, w, tmem, rank);
         else if (MODE != kLinGateGrad && p.e.y_f32)

@@ -265,6 +265,19 @@ __device__ __forceinline__ void finish_stats(const LinearHead &h, int count, con
     }
 }
 
+// The further accumulators' sums added to the first one's, as bits of fp32; those that
+// have no slice are left out.
+__device__ __forceinline__ void add_parts(uint32_t taddr, uint32_t acc_cols, int slices, int parts, uint32_t (&v)[32]) {
+    const int per_part = (slices + parts - 1) / parts;
+    for (int k = 1; k * per_part < slices; ++k) {
+        uint32_t u[32];
+        tmem_ld32(taddr + uint32_t(k) * acc_cols, u);
+        tmem_wait_ld_regs(u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+    }
+}
+
 template <int MODE>
 using StripParams = std::conditional_t<MODE == kLinPlain || MODE == kLinGateGrad, LinearStripParams, LinearStripMore>;
 
@@ -284,7 +297,14 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     s.abort = reinterpret_cast<volatile int *>(slots + 1);
 
     const int warp = int(threadIdx.x) >> 5;
-    const uint32_t tmem_cols = p.tok <= 32 ? 32u : p.tok <= 64 ? 64u : p.tok <= 128 ? 128u : 256u;
+    const uint32_t acc_cols = p.tok <= 32 ? 32u : p.tok <= 64 ? 64u : p.tok <= 128 ? 128u : 256u;
+    // the loss's logits are summed in parts, an accumulator each (kStatSlices), as far as
+    // half of the SM's tensor memory goes
+    constexpr bool kStats = MODE == kLinStats;
+    [[maybe_unused]] uint32_t acc_parts = 1;
+    if constexpr (kStats)
+        while (acc_parts * acc_cols < 256u && int(acc_parts) * p.splits * kStatSlices < p.kblocks) acc_parts *= 2;
+    const uint32_t tmem_cols = acc_parts * acc_cols;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s.full[i], 1);
@@ -381,6 +401,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             const uint64_t ad0 = desc_sw128(smem_u32(s.ring), kALbo, 1024);
             const uint64_t bd0 = desc_sw128(smem_u32(s.ring) + kStripA, kBLbo, 1024);
             bool ready = mbar_test_wait(&s.full[0], 0);   // looked at ahead, so that its latency overlaps the issue
+            [[maybe_unused]] const int per_part = (kb1 - kb0 + int(acc_parts) - 1) / int(acc_parts);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!ready && !mbar_try_wait(&s.full[stage], phase) && !wait_l(p, s, &s.full[stage], phase, kLinSiteFull)) {
                     ok = false;
@@ -389,9 +410,17 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 tc_fence_after();
                 const uint64_t off = (uint32_t(stage) * stage_bytes) >> 4;
                 const uint64_t ad = ad0 + off, bd = bd0 + off;
+                if constexpr (kStats) {
+                    const int part = (kb - kb0) / per_part;
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
-                    mma_bf16(tmem, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc, kb > kb0 || k ? 1u : 0u);
+                    for (int k = 0; k < kBK / 16; ++k)
+                        mma_bf16(tmem + uint32_t(part) * acc_cols, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc,
+                                 kb > kb0 + part * per_part || k ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k)
+                        mma_bf16(tmem, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc, kb > kb0 || k ? 1u : 0u);
+                }
                 mma_commit(&s.empty[stage]);
                 if (++stage == p.stages) {
                     stage = 0;
@@ -418,7 +447,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const int64_t col = int64_t(col0) + threadIdx.x;
     const uint32_t taddr = tmem + (uint32_t(warp * 32) << 16);
     const float bias = !kGated && col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
-    constexpr bool kStats = MODE == kLinStats;
     [[maybe_unused]] int count = 0;
     if constexpr (kStats || MODE == kLinSoftGrad) count = *p.count;
     if ((kGated || kStats) && p.splits == 1) {
@@ -433,6 +461,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 uint32_t v[32];
                 tmem_ld32(taddr + uint32_t(b + t0), v);
                 tmem_wait_ld();
+                if constexpr (kStats) add_parts(taddr + uint32_t(b + t0), acc_cols, kb1 - kb0, int(acc_parts), v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (t0 + i < end) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
@@ -474,6 +503,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             uint32_t v[32];
             tmem_ld32(taddr + uint32_t(t0), v);
             tmem_wait_ld();
+            if constexpr (kStats) add_parts(taddr + uint32_t(t0), acc_cols, kb1 - kb0, int(acc_parts), v);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (t0 + i < nrows) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
