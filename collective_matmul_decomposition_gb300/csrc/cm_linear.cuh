@@ -60,7 +60,8 @@ struct LinearHead {
 };
 // The tensor cores cut a sum off at each step of 16 terms, by which long sums fall
 // short: by 5e-6 of a logit of 4096 terms.  The loss's logits are therefore summed in
-// parts of this many slices of 64 terms, whose fp32 results are added with rounding.
+// parts of this many slices of 64 terms, whose fp32 results are added with rounding,
+// and in the same parts again for their gradient exp(z - lse): lse holds what z does.
 constexpr int kStatSlices = 16;
 constexpr int32_t kNotHere = -1, kNoToken = -2;   // of another slice; beyond the vocabulary
 

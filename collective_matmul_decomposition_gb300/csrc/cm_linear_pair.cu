@@ -253,7 +253,7 @@ __device__ __forceinline__ void multiply_tiles(const LinearPairParams &p, const 
     uint32_t phase = flow.phase, acc_phase = flow.acc_phase;
     bool ok = flow.ok;
     const uint16_t both = uint16_t(3u << w.leader);   // the pair's CTAs
-    constexpr bool kParts = MODE == kLinStats;        // an accumulator for each kStatSlices slices
+    constexpr bool kParts = MODE == kLinStats || MODE == kLinSoftGrad;   // an accumulator for each kStatSlices slices
     for (int t = w.first; t < tiles_of<MODE>(p, w) && ok; t += w.step) {
         if (!wait_p(p, s, &s.tempty[acc], acc_phase ^ 1u, kLinSiteTmem, t)) {
             ok = false;
@@ -678,11 +678,44 @@ __device__ void finish_gated(const LinearPairMore &p, const LSmem &s, uint32_t t
     __syncwarp();
 }
 
-// The statistics of a softmax over the columns, without the logits: a thread owns one
-// row and half of the tile's columns, adds up their parts (kStatSlices) in registers
-// while the products go on, and reduces them to the largest m and the sum of exp2(v
-// log2(e) - m), all in fp32.  What is not a column counts as -infinity.  A NaN stays one
-// through the sum.
+// A tile's logits, whose parts (kStatSlices) are added up in registers while the products
+// go on: a thread owns one row and half of the tile's columns.  An accumulator is given
+// back as soon as it is read.  False after an expired wait.
+__device__ __forceinline__ bool add_up_parts(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t taddr0, uint32_t tempty_leader,
+                                             bool live, int t, int &acc, uint32_t &acc_phase, float (&f)[8][16]) {
+    const int parts = (w.kb1 - w.kb0 + kStatSlices - 1) / kStatSlices;
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[b][i] = 0.0f;
+#pragma unroll 1
+    for (int part = 0; part < parts; ++part) {
+        const bool ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+        if (live) {
+            const uint32_t taddr = taddr0 + uint32_t(acc * kTile);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                uint32_t v[16];
+                tmem_ld16(taddr + uint32_t(16 * b), v);
+                tmem_wait_ld_regs(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[b][i] += __uint_as_float(v[i]);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
+        acc ^= 1;
+        acc_phase ^= acc == 0 ? 1u : 0u;
+    }
+    return true;
+}
+
+// The statistics of a softmax over the columns, without the logits: a thread reduces
+// those of its row to the largest m and the sum of exp2(v log2(e) - m), all in fp32.
+// What is not a column counts as -infinity.  A NaN stays one through the sum.
 // It leaves 8 bytes for 128 logits and costs the products little: 8192 x 4096 x 131072
 // takes 4.8 ms, 1830 TFLOP/s.  Losses are off by 2.5e-7 of their value; with one
 // accumulator a tile it was 8.6e-7 for 4096 terms and 1.5e-6 for 7040, in the same time.
@@ -691,45 +724,16 @@ __device__ void finish_stats(const LinearPairMore &p, const LSmem &s, const Shar
     const int ew = int(threadIdx.x) / 32 - 4, lane = int(threadIdx.x) & 31;
     const int quad = ew & 3, half = ew >> 2;
     const uint32_t tempty_leader = mapa_shared(smem_u32(&s.tempty[0]), 0);
-    const int parts = (w.kb1 - w.kb0 + kStatSlices - 1) / kStatSlices;
     int acc = 0;
     uint32_t acc_phase = 0;
-    bool ok = true;
-    for (int t = w.first; t < w.tiles && ok; t += w.step) {
+    for (int t = w.first; t < w.tiles; t += w.step) {
         int mt, nt;
         tile_at(p, w.mtiles, t, mt, nt);
         const int row0 = mt * kTile + rank * kHalf + quad * 32;
         const int64_t c0 = int64_t(nt) * BN + half * kCols;
         const bool live = row0 < w.rows && c0 < p.cols;   // the same in the whole warp
         float f[kBlocks][16];
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[b][i] = 0.0f;
-#pragma unroll 1
-        for (int part = 0; part < parts; ++part) {
-            ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            if (live) {
-                const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    uint32_t v[16];
-                    tmem_ld16(taddr + uint32_t(16 * b), v);
-                    tmem_wait_ld_regs(v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) f[b][i] += __uint_as_float(v[i]);
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * uint32_t(acc));
-            acc ^= 1;
-            acc_phase ^= acc == 0 ? 1u : 0u;
-        }
-        if (!ok) break;
+        if (!add_up_parts(p, s, w, tmem + (uint32_t(quad * 32) << 16) + uint32_t(half * kCols), tempty_leader, live, t, acc, acc_phase, f)) break;
         const int row = row0 + lane;
         if (row >= w.rows) continue;
         if (!live) {   // no column is here
@@ -844,7 +848,11 @@ __device__ void finish_stats_few(const LinearPairMore &p, const LSmem &s, const 
 // Rows behind the last slot are zeros up to the tile's end.  bf16 because two products
 // read it; grad and hit are relative to the largest factor, so that what is rounded is a
 // probability, not its product with a common factor (see cm_head_rows_kernel).
-// 2048 x 2048 x 32768 takes 149 us, the tensor pipe 81 % busy.
+// PARTS: tiles of more than one part, whose logits then are the forward pass's, and
+// near lse off by no more than lse is: the difference in the target's column is taken
+// in fp32, and of a row that is sure of its target little is left.
+// 2048 x 2048 x 32768 in two parts takes 147 to 149 us, as in one accumulator (146 to 149).
+template <bool PARTS>
 __device__ void finish_softgrad(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = BN / 2, kChunk = 64;
     const LinearEpilogue &e = p.e;
@@ -867,44 +875,67 @@ __device__ void finish_softgrad(const LinearPairMore &p, const LSmem &s, const S
         const float hit = slot ? p.head.hit[row] : 0.0f;
         const int64_t target = slot ? p.head.target[row] : kNotHere, left = target - p.head.first - cbase;
         const int at = target >= 0 && left >= 0 && left < kCols ? int(left) : -1;
+        const bool live = row0 < p.rows && cbase < p.cols;   // the same in the whole warp
+        const uint32_t taddr0 = tmem + (uint32_t(quad * 32) << 16) + uint32_t(half * kCols);
+        // 16 columns from c + 16 q on, as they lie in the buffer's rows
+        auto finish16 = [&](int c, int q, const auto &v) {
+            float g[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = slot ? lin::exp2_fast(fmaf(v(i), lin::kLog2e, -lse2)) * grad : 0.0f;
+            const int here = at - c - 16 * q;
+            if (__any_sync(0xffffffffu, at >= 0 && here >= 0 && here < 16)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] -= at >= 0 && here == i ? hit : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) *piece(buf, lane, q * 2 + j) = pack8(g + 8 * j);
+        };
+        auto open_chunk = [&]() {
+            if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has been read out
+            __syncwarp();
+        };
+        auto close_chunk = [&](int c) {
+            const int c0 = cbase + c;
+            if (rest && c0 + kChunk > whole && row < p.rows)
+                store_tail(buf, e.y, e.ldy, row, whole, int(whole - c0), rest, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (c0 < whole) tma_store_3d(&p.tmY, buf, c0, row0, 0);
+                bulk_commit();
+            }
+            buf = buf == bufs ? bufs + kEpiBuf : bufs;
+        };
+        if constexpr (PARTS) {
+            float f[kCols / 16][16];
+            if (!add_up_parts(p, s, w, taddr0, tempty_leader, live, t, acc, acc_phase, f)) break;
+#pragma unroll
+            for (int c = 0; c < kCols; c += kChunk) {
+                if (!live || cbase + c >= p.cols) continue;
+                open_chunk();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) finish16(c, q, [&](int i) { return f[c / 16 + q][i]; });
+                close_chunk(c);
+            }
+            continue;
+        }
         bool ok = wait_p(p, s, &s.tfull[acc], acc_phase, kLinSiteAcc, t);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN + half * kCols);
-        if (row0 < p.rows) {
+        const uint32_t taddr = taddr0 + uint32_t(acc * BN);
 #pragma unroll 1
-            for (int c = 0; c < kCols && cbase + c < p.cols; c += kChunk) {
-                if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has been read out
-                __syncwarp();
-                const int c0 = cbase + c;
+        for (int c = 0; live && c < kCols && cbase + c < p.cols; c += kChunk) {
+            open_chunk();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
-                    tmem_ld32(taddr + uint32_t(c + 32 * h), v);
-                    tmem_wait_ld_regs(v);
-                    float f[32];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                tmem_ld32(taddr + uint32_t(c + 32 * h), v);
+                tmem_wait_ld_regs(v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        f[i] = slot ? lin::exp2_fast(fmaf(__uint_as_float(v[i]), lin::kLog2e, -lse2)) * grad : 0.0f;
-                    const int here = at - c - 32 * h;
-                    if (__any_sync(0xffffffffu, at >= 0 && here >= 0 && here < 32)) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] -= at >= 0 && here == i ? hit : 0.0f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) *piece(buf, lane, h * 4 + j) = pack8(f + 8 * j);
-                }
-                if (rest && c0 + kChunk > whole && row < p.rows)
-                    store_tail(buf, e.y, e.ldy, row, whole, int(whole - c0), rest, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (c0 < whole) tma_store_3d(&p.tmY, buf, c0, row0, 0);
-                    bulk_commit();
-                }
-                buf = buf == bufs ? bufs + kEpiBuf : bufs;
+                for (int q = 0; q < 2; ++q) finish16(c, 2 * h + q, [&](int i) { return __uint_as_float(v[16 * q + i]); });
             }
+            close_chunk(c);
         }
         tc_fence_before();
         __syncwarp();
@@ -1018,7 +1049,10 @@ __global__ void __launch_bounds__(kLThreads, 1) cm_linear_pair_kernel(const __gr
             else
                 finish_stats_few(p, s, w, tmem, rank);
         else if constexpr (MODE == kLinSoftGrad)
-            finish_softgrad(p, s, w, tmem, rank);
+            if (w.kb1 - w.kb0 > kStatSlices)
+                finish_softgrad<true>(p, s, w, tmem, rank);
+            else
+                finish_softgrad<false>(p, s, w, tmem, rank);
         else if (MODE != kLinGateGrad && p.e.y_f32)
             finish_tiles<true, BN, MODE == kLinGateGrad ? kLinPlain : MODE>(p, s, w, tmem, rank, flow);
         else

@@ -299,11 +299,11 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
 
     const int warp = int(threadIdx.x) >> 5;
     const uint32_t acc_cols = p.tok <= 32 ? 32u : p.tok <= 64 ? 64u : p.tok <= 128 ? 128u : 256u;
-    // the loss's logits are summed in parts, an accumulator each (kStatSlices), as far as
+    // the loss's logits, forward and backward, are summed in parts, an accumulator each (kStatSlices), as far as
     // half of the SM's tensor memory goes
-    constexpr bool kStats = MODE == kLinStats;
+    constexpr bool kStats = MODE == kLinStats, kParts = kStats || MODE == kLinSoftGrad;
     [[maybe_unused]] uint32_t acc_parts = 1;
-    if constexpr (kStats)
+    if constexpr (kParts)
         while (acc_parts * acc_cols < 256u && int(acc_parts) * p.splits * kStatSlices < p.kblocks) acc_parts *= 2;
     const uint32_t tmem_cols = acc_parts * acc_cols;
     if (threadIdx.x == 0) {
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 tc_fence_after();
                 const uint64_t off = (uint32_t(stage) * stage_bytes) >> 4;
                 const uint64_t ad = ad0 + off, bd = bd0 + off;
-                if constexpr (kStats) {
+                if constexpr (kParts) {
                     const int part = (kb - kb0) / per_part;
 #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k)
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
     const uint32_t taddr = tmem + (uint32_t(warp * 32) << 16);
     const float bias = !kGated && col < p.cols ? lin::load_bias(p.e, col) : 0.0f;
     [[maybe_unused]] int count = 0;
-    if constexpr (kStats || MODE == kLinSoftGrad) count = *p.count;
+    if constexpr (kParts) count = *p.count;
     if ((kGated || kStats) && p.splits == 1) {
         // gate and up columns, or those of a row's sum, lie in different threads' lanes:
         // they meet in the ring, whose loads have all been multiplied, 128 tokens at a time
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 uint32_t v[32];
                 tmem_ld32(taddr + uint32_t(b + t0), v);
                 tmem_wait_ld();
-                if constexpr (kStats) add_parts(taddr + uint32_t(b + t0), acc_cols, kb1 - kb0, int(acc_parts), v);
+                if constexpr (kParts) add_parts(taddr + uint32_t(b + t0), acc_cols, kb1 - kb0, int(acc_parts), v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (t0 + i < end) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             uint32_t v[32];
             tmem_ld32(taddr + uint32_t(t0), v);
             tmem_wait_ld();
+            if constexpr (kParts) add_parts(taddr + uint32_t(t0), acc_cols, kb1 - kb0, int(acc_parts), v);
             if (good && col < p.cols) {
 #pragma unroll
                 for (int b = 0; b < 32; b += kBatch)
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             uint32_t v[32];
             tmem_ld32(taddr + uint32_t(t0), v);
             tmem_wait_ld();
-            if constexpr (kStats) add_parts(taddr + uint32_t(t0), acc_cols, kb1 - kb0, int(acc_parts), v);
+            if constexpr (kParts) add_parts(taddr + uint32_t(t0), acc_cols, kb1 - kb0, int(acc_parts), v);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (t0 + i < nrows) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
