@@ -116,6 +116,7 @@ struct LinearStripMore : LinearStripParams {
 constexpr int kStripAlone = 216 * 1024, kStripShared = 108 * 1024;   // ring bytes of a CTA alone on its SM, of one of two
 // clusters[i]: clusters of i CTAs (2 to kStripMostSplits) that run together, one CTA an SM.
 constexpr int kStripMostSplits = 8;
+constexpr int kStripRoundRows = 128;   // tiles of up to so many rows have two accumulators: parts of a sum in any number
 cudaError_t prepare_linear_strip(int sms, int *clusters);
 cudaError_t launch_linear_strip(const LinearStripMore &p, int layout, LinearMode mode, cudaStream_t stream);
 int linear_strip_stages(int tok, int ring_bytes);

@@ -161,7 +161,8 @@ struct Choice {
 //   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  22.8 / 29.0 (three)
 // A gated product is estimated as one of the columns of both its operands.
 // Pair tiles of 128 columns: any, only where K is split (gated: an unsplit tile's
-// epilogue needs 64 columns a warp of either operand), or none.
+// epilogue needs 64 columns a warp of either operand), or none (the loss's logits, whose
+// strips of more than kStripRoundRows rows have one accumulator, for one part of the sum).
 enum class Narrow { any, split, none };
 Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn, Narrow narrow = Narrow::any) {
     Choice best;
@@ -190,7 +191,7 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
     }
     for (int64_t parts = 1; parts <= 4 && rows <= 384; ++parts) {
         const int64_t unit = row_mn ? 64 : 16, tok = up(up(rows, parts), unit) * unit;
-        if (tok > 256) continue;
+        if (tok > 256 || (narrow == Narrow::none && tok > kStripRoundRows && slices > kStatSlices)) continue;
         const int64_t tiles = up(rows, tok) * up(cols, 128);
         const double from_l2 = double(tiles) * double(128 + tok) * double(k) * 2.0 / 22e6;
         // unsplit, or split as far as all tiles' clusters run at once, two CTAs

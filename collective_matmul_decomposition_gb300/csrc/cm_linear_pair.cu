@@ -717,7 +717,7 @@ __device__ __forceinline__ bool add_up_parts(const LinearPairMore &p, const LSme
 // those of its row to the largest m and the sum of exp2(v log2(e) - m), all in fp32.
 // What is not a column counts as -infinity.  A NaN stays one through the sum.
 // It leaves 8 bytes for 128 logits and costs the products little: 8192 x 4096 x 131072
-// takes 4.8 ms, 1830 TFLOP/s.  Losses are off by 2.5e-7 of their value; with one
+// takes 4.8 ms, 1830 TFLOP/s.  lse is off by 2.5e-7 of its value; with one
 // accumulator a tile it was 8.6e-7 for 4096 terms and 1.5e-6 for 7040, in the same time.
 __device__ void finish_stats(const LinearPairMore &p, const LSmem &s, const Share &w, uint32_t tmem, int rank) {
     constexpr int BN = 256, kCols = BN / 2, kBlocks = kCols / 16;

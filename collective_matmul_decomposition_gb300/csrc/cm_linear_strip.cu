@@ -266,17 +266,116 @@ __device__ __forceinline__ void finish_stats(const LinearHead &h, int count, con
     }
 }
 
-// The further accumulators' sums added to the first one's, as bits of fp32; those that
-// have no slice are left out.
-__device__ __forceinline__ void add_parts(uint32_t taddr, uint32_t acc_cols, int slices, int parts, uint32_t (&v)[32]) {
-    const int per_part = (slices + parts - 1) / parts;
-    for (int k = 1; k * per_part < slices; ++k) {
+// The sums of accumulators 1 .. used - 1 added to the first one's, as bits of fp32.
+__device__ __forceinline__ void add_parts(uint32_t taddr, uint32_t acc_cols, int used, uint32_t (&v)[32]) {
+    for (int k = 1; k < used; ++k) {
         uint32_t u[32];
         tmem_ld32(taddr + uint32_t(k) * acc_cols, u);
         tmem_wait_ld_regs(u);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
     }
+}
+
+// The products of the loss's logits, in parts of at most kStatSlices slices, an accumulator
+// each.  Where there are more parts than accumulators they are multiplied in rounds:
+// behind each round the accumulators' sum goes to the first one, and the others take the
+// next parts.  The ring is filled again meanwhile, and an SM's other CTA goes on.
+// 64 rows, 8192 x 32768 (three rounds): the loss takes 124 us; 128 rows (seven) 130, as with one.
+// Leaves how many accumulators hold a part or a sum in `used`; false after an expired wait,
+// with the loader's place in the ring for what it has to wait for.
+template <bool A_MN>
+__device__ __forceinline__ bool multiply_parts(const LinearStripMore &p, const StripSmem &s, uint32_t tmem, uint32_t acc_cols, int accs,
+                                               int col0, int row0, int nrows, int kb0, int kb1, int &used, int &stage, int &issued,
+                                               uint32_t &phase) {
+    const int warp = int(threadIdx.x) >> 5;
+    const uint32_t stage_bytes = uint32_t(kStripA + p.tok * kBK * 2), taddr = tmem + (uint32_t(warp * 32) << 16);
+    const int per_part = min(kStatSlices, (kb1 - kb0 + accs - 1) / accs);
+    bool good = true;
+    int next = kb0;   // the first slice that is not on its way yet
+    for (int first = kb0, round = 0;; ++round) {
+        const int kept = round ? 1 : 0, last = min(kb1, first + per_part * (accs - kept)), until = min(kb1, last + p.stages);
+        used = kept + (last - first + per_part - 1) / per_part;
+        if (warp == 0) {
+            if (elect_one()) {
+                for (int kb = next; kb < until; ++kb) {
+                    if (!mbar_try_wait(&s.empty[stage], phase ^ 1u) && !wait_l(p, s, &s.empty[stage], phase ^ 1u, kLinSiteEmpty))
+                        break;
+                    uint8_t *sa = s.ring + uint32_t(stage) * stage_bytes, *sb = sa + kStripA;
+                    mbar_expect_tx(&s.full[stage], stage_bytes);
+                    if (A_MN) {
+                        for (int j = 0; j < kTileCols / 64; ++j)
+                            tma_load_3d(sa + j * (64 * kBK * 2), &p.tmA, &s.full[stage], col0 + 64 * j, kb * kBK, 0);
+                    } else {
+                        tma_load_3d(sa, &p.tmA, &s.full[stage], kb * kBK, col0, 0);
+                    }
+                    tma_load_3d(sb, &p.tmB, &s.full[stage], kb * kBK, row0, 0);
+                    ++issued;
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (elect_one()) {
+                const uint32_t idesc = idesc_bf16(kTileCols, p.tok, false, A_MN);
+                constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kAStep = A_MN ? (16 * 128) >> 4 : 32 >> 4;
+                const uint64_t ad0 = desc_sw128(smem_u32(s.ring), kALbo, 1024);
+                const uint64_t bd0 = desc_sw128(smem_u32(s.ring) + kStripA, 16, 1024);
+                bool ok = true, ready = mbar_test_wait(&s.full[stage], phase);
+                uint32_t d = tmem + uint32_t(kept) * acc_cols;
+                for (int kb = first, left = per_part; kb < last; ++kb) {
+                    if (!ready && !mbar_try_wait(&s.full[stage], phase) && !wait_l(p, s, &s.full[stage], phase, kLinSiteFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t off = (uint32_t(stage) * stage_bytes) >> 4;
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k)
+                        mma_bf16(d, ad0 + off + uint64_t(kAStep * k), bd0 + off + uint64_t(2 * k), idesc, left < per_part || k ? 1u : 0u);
+                    mma_commit(&s.empty[stage]);
+                    if (--left == 0) {
+                        left = per_part;
+                        d += acc_cols;
+                    }
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    ready = kb + 1 < last && mbar_test_wait(&s.full[stage], phase);
+                }
+                if (ok) mma_commit(s.acc);
+            }
+            __syncwarp();
+        }
+        good = wait_l(p, s, s.acc, uint32_t(round & 1), kLinSiteAcc);
+        if (last == kb1) break;
+        good = __syncthreads_and(good) != 0;   // all threads go on to the next round, or none does
+        if (!good) break;
+        tc_fence_after();
+        for (int t0 = 0; t0 < nrows; t0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(taddr + uint32_t(t0), v);
+            tmem_wait_ld_regs(v);
+            add_parts(taddr + uint32_t(t0), acc_cols, used, v);
+            tmem_st32(taddr + uint32_t(t0), v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        next = until;
+        first = last;
+    }
+    if (warp == 1 && elect_one()) {   // every MMA is done before the tensor memory is freed
+        mma_commit(s.drain);
+        drain_l(p, s.drain, 0);
+    }
+    __syncwarp();
+    return good;
 }
 
 template <int MODE>
@@ -299,8 +398,8 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
 
     const int warp = int(threadIdx.x) >> 5;
     const uint32_t acc_cols = p.tok <= 32 ? 32u : p.tok <= 64 ? 64u : p.tok <= 128 ? 128u : 256u;
-    // the loss's logits, forward and backward, are summed in parts, an accumulator each (kStatSlices), as far as
-    // half of the SM's tensor memory goes
+    // the loss's logits, forward and backward, are summed in parts, an accumulator each, as far as
+    // half of the SM's tensor memory goes (multiply_parts)
     constexpr bool kStats = MODE == kLinStats, kParts = kStats || MODE == kLinSoftGrad;
     [[maybe_unused]] uint32_t acc_parts = 1;
     if constexpr (kParts)
@@ -358,7 +457,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
 
     int stage = 0, issued = 0;   // of the thread that loads, and of the one that multiplies
     uint32_t phase = 0;
-    if (warp == 0) {
+    if (!kParts && warp == 0) {
         if (elect_one()) {
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_try_wait(&s.empty[stage], phase ^ 1u) && !wait_l(p, s, &s.empty[stage], phase ^ 1u, kLinSiteEmpty))
@@ -393,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (!kParts && warp == 1) {
         if (elect_one()) {
             const uint32_t idesc = idesc_bf16(kTileCols, p.tok, B_MN, A_MN);
             constexpr uint32_t kALbo = A_MN ? 64 * kBK * 2 : 16, kBLbo = B_MN ? 64 * kBK * 2 : 16;
@@ -402,7 +501,6 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             const uint64_t ad0 = desc_sw128(smem_u32(s.ring), kALbo, 1024);
             const uint64_t bd0 = desc_sw128(smem_u32(s.ring) + kStripA, kBLbo, 1024);
             bool ready = mbar_test_wait(&s.full[0], 0);   // looked at ahead, so that its latency overlaps the issue
-            [[maybe_unused]] const int per_part = (kb1 - kb0 + int(acc_parts) - 1) / int(acc_parts);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!ready && !mbar_try_wait(&s.full[stage], phase) && !wait_l(p, s, &s.full[stage], phase, kLinSiteFull)) {
                     ok = false;
@@ -411,17 +509,9 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 tc_fence_after();
                 const uint64_t off = (uint32_t(stage) * stage_bytes) >> 4;
                 const uint64_t ad = ad0 + off, bd = bd0 + off;
-                if constexpr (kParts) {
-                    const int part = (kb - kb0) / per_part;
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        mma_bf16(tmem + uint32_t(part) * acc_cols, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc,
-                                 kb > kb0 + part * per_part || k ? 1u : 0u);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        mma_bf16(tmem, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc, kb > kb0 || k ? 1u : 0u);
-                }
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_bf16(tmem, ad + uint64_t(kAStep * k), bd + uint64_t(kBStep * k), idesc, kb > kb0 || k ? 1u : 0u);
                 mma_commit(&s.empty[stage]);
                 if (++stage == p.stages) {
                     stage = 0;
@@ -435,7 +525,13 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
         }
         __syncwarp();
     }
-    const bool good = wait_l(p, s, s.acc, 0, kLinSiteAcc);
+    bool good;
+    [[maybe_unused]] int used = 1;
+    if constexpr (kParts)
+        good = multiply_parts<A_MN>(p, s, tmem, acc_cols, int(acc_parts), col0, row0, int(min(int64_t(p.tok), p.rows - row0)), kb0, kb1,
+                                    used, stage, issued, phase);
+    else
+        good = wait_l(p, s, s.acc, 0, kLinSiteAcc);
     // The accumulator is complete once every load has landed.  If it was given up,
     // the loading thread waits for what it issued: no load may still write this
     // shared memory at exit.
@@ -462,7 +558,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
                 uint32_t v[32];
                 tmem_ld32(taddr + uint32_t(b + t0), v);
                 tmem_wait_ld();
-                if constexpr (kParts) add_parts(taddr + uint32_t(b + t0), acc_cols, kb1 - kb0, int(acc_parts), v);
+                if constexpr (kParts) add_parts(taddr + uint32_t(b + t0), acc_cols, used, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (t0 + i < end) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
@@ -480,7 +576,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             uint32_t v[32];
             tmem_ld32(taddr + uint32_t(t0), v);
             tmem_wait_ld();
-            if constexpr (kParts) add_parts(taddr + uint32_t(t0), acc_cols, kb1 - kb0, int(acc_parts), v);
+            if constexpr (kParts) add_parts(taddr + uint32_t(t0), acc_cols, used, v);
             if (good && col < p.cols) {
 #pragma unroll
                 for (int b = 0; b < 32; b += kBatch)
@@ -505,7 +601,7 @@ __global__ void __launch_bounds__(kThreadsL) cm_linear_strip_kernel(const __grid
             uint32_t v[32];
             tmem_ld32(taddr + uint32_t(t0), v);
             tmem_wait_ld();
-            if constexpr (kParts) add_parts(taddr + uint32_t(t0), acc_cols, kb1 - kb0, int(acc_parts), v);
+            if constexpr (kParts) add_parts(taddr + uint32_t(t0), acc_cols, used, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (t0 + i < nrows) part[(t0 + i) * kTileCols + int(threadIdx.x)] = __uint_as_float(v[i]);
@@ -607,6 +703,9 @@ cudaError_t launch_linear_strip(const LinearStripMore &p, int layout, LinearMode
     const int64_t tile_cols = mode == kLinGated ? kTileCols / 2 : kTileCols;
     const int64_t grid = (p.cols + tile_cols - 1) / tile_cols * p.row_tiles * p.splits;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    // rounds of parts need a second accumulator
+    if ((mode == kLinStats || mode == kLinSoftGrad) && p.tok > kStripRoundRows && (p.kblocks + p.splits - 1) / p.splits > kStatSlices)
+        return cudaErrorInvalidValue;
     const size_t smem = size_t(p.ring_bytes) + 1024;
     if (const StripKernel fn = strip_kernel(layout, mode))
         return launch_after(fn, dim3(unsigned(grid)), kThreadsL, smem, unsigned(p.splits), stream, static_cast<const LinearStripParams &>(p));

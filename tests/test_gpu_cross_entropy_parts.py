@@ -22,10 +22,11 @@ from test_gpu_linear import DEV, status_ok
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 
-# rows, terms, columns: strips with and without splits, pair tiles whose last columns are 1 to 128
+# rows, terms, columns: strips of 16 to 128 rows with and without splits, pair tiles whose last columns are 1 to 128
 CASES = [
-    (1, 4096, 515), (16, 16384, 1000), (40, 8192, 1500), (64, 4096, 30000), (100, 8192, 1111), (200, 8192, 3841),
-    (256, 4096, 515), (300, 1025, 257), (300, 4096, 385), (520, 3137, 1281), (700, 8192, 2050), (1100, 2100, 3001),
+    (1, 4096, 515), (3, 12288, 40000), (16, 16384, 1000), (33, 8192, 30001), (40, 8192, 1500), (64, 4096, 30000), (100, 8192, 1111),
+    (112, 8192, 32768), (128, 4100, 20000), (144, 12288, 20001), (200, 8192, 3841), (256, 4096, 515), (300, 1025, 257),
+    (300, 4096, 385), (520, 3137, 1281), (700, 8192, 2050), (1100, 2100, 3001),
 ]
 
 
