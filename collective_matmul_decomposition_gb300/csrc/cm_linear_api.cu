@@ -160,23 +160,24 @@ struct Choice {
 // and between strips (one tile of rows / more, shorter ones):
 //   rows 64, K 4096, cols 2048:  10.6 / 9.1 (two)     rows 33, K 2048, cols 28672:  22.8 / 29.0 (three)
 // A gated product is estimated as one of the columns of both its operands.
-// Pair tiles of 128 columns: any, only where K is split (gated: an unsplit tile's
-// epilogue needs 64 columns a warp of either operand), or none (the loss's logits, whose
-// strips of more than kStripRoundRows rows have one accumulator, for one part of the sum).
-enum class Narrow { any, split, none };
-Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn, Narrow narrow = Narrow::any) {
+// What a product's kernels have: all of the above; of the gated ones no unsplit pair
+// tiles of 128 columns (their epilogue needs 64 columns a warp of either operand); of the
+// loss's logits unsplit pair tiles of 256 columns, and strips (choose_logits); of the
+// counted ones unsplit pair tiles.
+enum class Has { all, gated, logits, counted };
+Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_mn, Has has = Has::all) {
     Choice best;
     double least = 1e30;
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t slices = up(k, kBK);
     const double from_hbm = double(cols) * double(k) * 2.0 / 8.5e6;
     // pair tiles waste what they have beyond `rows`: not worth a look below 33
-    for (int bn = 256; bn >= (narrow == Narrow::none ? 256 : 128) && rows > 32; bn /= 2) {
+    for (int bn = 256; bn >= (has == Has::logits ? 256 : 128) && (rows > 32 || has == Has::counted); bn /= 2) {
         const int64_t tiles = up(rows, 256) * up(cols, bn);
         for (int i = 0; i < 3; ++i) {
             const int splits = 1 << i;
-            if (i > 0 && (tiles > d.clusters[i] || slices < 2 * splits)) break;
-            if (i == 0 && bn == 128 && narrow == Narrow::split) continue;
+            if (i > 0 && (has == Has::logits || has == Has::counted || tiles > d.clusters[i] || slices < 2 * splits)) break;
+            if (i == 0 && bn == 128 && has == Has::gated) continue;
             const double wave = std::max(double(up(slices, splits)) * (bn == 256 ? 0.32 : 0.21), bn == 256 ? 2.9 : 2.0);
             const double run = double(up(tiles, d.clusters[i])) * wave;
             const double t = 3.8 + (i == 0 ? 0.0 : bn == 256 ? 2.6 : 1.6) + std::max(run, from_hbm) +
@@ -189,9 +190,9 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
             }
         }
     }
-    for (int64_t parts = 1; parts <= 4 && rows <= 384; ++parts) {
+    for (int64_t parts = 1; parts <= 4 && rows <= 384 && has != Has::counted; ++parts) {
         const int64_t unit = row_mn ? 64 : 16, tok = up(up(rows, parts), unit) * unit;
-        if (tok > 256 || (narrow == Narrow::none && tok > kStripRoundRows && slices > kStatSlices)) continue;
+        if (tok > 256) continue;
         const int64_t tiles = up(rows, tok) * up(cols, 128);
         const double from_l2 = double(tiles) * double(128 + tok) * double(k) * 2.0 / 22e6;
         // unsplit, or split as far as all tiles' clusters run at once, two CTAs
@@ -206,7 +207,11 @@ Choice choose(const Device &d, int64_t rows, int64_t cols, int64_t k, bool row_m
             const double run = 0.125 * double(up(slices, splits)) * double(up(tiles * splits, d.sms));
             const double longest = std::max({from_hbm, from_l2, run});
             const double second = std::max(std::min(from_hbm, from_l2), std::min(std::max(from_hbm, from_l2), run));
-            const double t = (splits > 1 ? 3.7 + 0.063 * double(tok) : 3.4 + 0.04 * double(tok)) + longest + 0.5 * second;
+            double t = (splits > 1 ? 3.7 + 0.063 * double(tok) : 3.4 + 0.04 * double(tok)) + longest + 0.5 * second;
+            if (has == Has::logits && rows > 32) {   // see choose_logits
+                if (splits == 1) continue;
+                t *= 1.6;
+            }
             if (t >= least) continue;
             least = t;
             best.pair = false;
@@ -314,20 +319,25 @@ cm_status product_strip(const Device &d, const Choice &c, const Kind &kind, cons
 cm_status product(const Device &d, const Operand &a, const Operand &b, int64_t rows, int64_t cols, int64_t k,
                   const LinearEpilogue &e, cudaStream_t stream, const Kind &kind = {}) {
     const bool gated = kind.mode == kLinGated;
-    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated ? Narrow::split : Narrow::any);
+    const Choice c = choose(d, rows, gated ? 2 * cols : cols, k, b.mn_major, gated ? Has::gated : Has::all);
     return c.pair ? product_pair(d, c, kind, a, b, rows, cols, k, e, stream) : product_strip(d, c, kind, a, b, rows, cols, k, e, stream);
 }
 
-// Logits, whose columns are as many as the vocabulary's: for up to 256 rows strips where
-// choose() takes them, else whole pair tiles.  Several row tiles of strips have too long an
-// epilogue here: the loss of 300 rows, 4096 x 32768, took 114 us in strips, 400 rows take
-// 97 in pair tiles; 200 rows 67 us, 64 rows (131072 columns) 225 in strips.
+// Logits: unsplit strips up to 32 rows; above that strips that are split, over a slice of a
+// few thousand columns, where choose() gives them less than pair tiles.  They take 1.6 times
+// the estimate, which knows of no softmax.  Loss, and its dx alone, by strips / pair tiles,
+// us in a graph with cold caches:
+//   unsplit: 1 row, 4096 x 131072:   177 / 320, 329 / 394     16 rows, 4096 x 131072: 185 / 194, 339 / 351
+//            33 rows, 4096 x 32768:  74 / 74, 119 / 122       100 rows, 4096 x 32768: 82 / 75, 136 / 133
+//            48 rows, 1024 x 131072: 87 / 74, 154 / 139       80 rows, 512 x 131072:  78 / 47, 127 / 93
+//            64 rows, 8192 x 131072: 366 / 362, 673 / 678
+//   split:   64 rows, 4096 x 4000:   30 / 36, 43 / 56         200 rows, 4096 x 4000:  41 / 36, 58 / 56
+//            160 rows, 8192 x 4000:  52 / 56, 75 / 90         256 rows, 8192 x 4000:  61 / 56, 83 / 91
+// Above 256 rows pair tiles always: 300 rows, 8192 x 4000: 67 / 59, 101 / 89.
 Choice choose_logits(const Device &d, int64_t rows, int64_t cols, int64_t k) {
     Choice c;
     c.pair = true;
-    if (rows <= 256) c = choose(d, rows, cols, k, false, Narrow::none);
-    if (c.pair) c.splits = 1;
-    return c;
+    return rows <= 256 ? choose(d, rows, cols, k, false, Has::logits) : c;
 }
 
 // ---- the loss over a vocabulary -----------------------------------------------------
@@ -700,9 +710,7 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
     // a chunk's logits and the two products behind them; tiles that are split, and strips, take all rows.
     // dw's are not split: its extents are the weights', and its epilogue scales
     const Choice cp = choose_logits(d, M, s.columns, K), cx = choose(d, M, K, s.columns, false);
-    Choice cw = choose(d, nk ? s.columns : K, nk ? K : s.columns, M, true);
-    if (!cw.pair) cw = Choice{true, 128};
-    cw.splits = 1;
+    const Choice cw = choose(d, nk ? s.columns : K, nk ? K : s.columns, M, true, Has::counted);
     const bool counted = cp.pair && (!dx || (cx.pair && cx.splits == 1));
     HeadRows r = {};
     r.targets = targets;
