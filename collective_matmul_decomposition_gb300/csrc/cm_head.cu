@@ -17,7 +17,7 @@ namespace {
 
 using namespace vec;
 
-constexpr int kRowsThreads = 256, kRowsMost = 64;
+constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32, kRowsMost = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int64_t target_of(const HeadRows &p, int64_t row) {
@@ -31,101 +31,146 @@ __device__ __forceinline__ float larger(float a, float b) {
     return b <= 3.0e38f ? fmaxf(a, b) : a;
 }
 
-// A CTA places 4 to 64 rows (`per`: 1003 rows of 4101 elements in 64s 86 us, on 16
-// SMs, now 15).  It counts all rows' targets itself, which costs a pass over them from L2
-// (rows^2 / per of them in all, little beside the products' rows K n), and saves a
-// launch and a scan across CTAs.
+// Counts of a CTA's threads, summed; the same in all of them.
+struct Counted {
+    int before, all;
+    float top;
+};
+__device__ __forceinline__ Counted over_cta(Counted c) {
+    __shared__ Counted warps[kRowsWarps];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        c.before += __shfl_xor_sync(0xffffffffu, c.before, o);
+        c.all += __shfl_xor_sync(0xffffffffu, c.all, o);
+        c.top = fmaxf(c.top, __shfl_xor_sync(0xffffffffu, c.top, o));
+    }
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = c;
+    __syncthreads();
+    c = {0, 0, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kRowsWarps; ++i) c = {c.before + warps[i].before, c.all + warps[i].all, fmaxf(c.top, warps[i].top)};
+    return c;
+}
+
+// The rows r0 .. r1 - 1 that have a target: those in front of row `split`, all, and the
+// largest of their factors.
+__device__ __forceinline__ Counted count_rows(const HeadRows &p, int64_t r0, int64_t r1, int64_t split) {
+    Counted c = {0, 0, 0.0f};
+#pragma unroll 4
+    for (int64_t r = r0 + threadIdx.x; r < r1; r += kRowsThreads) {
+        const int64_t t = target_of(p, r);
+        const float a = p.dloss ? p.dloss[r] : 0.0f, b = p.dlse ? p.dlse[r] : 0.0f;   // read whether it counts or not
+        if (t < 0) continue;
+        ++c.all;
+        c.before += r < split;
+        c.top = larger(larger(c.top, a), a + b);
+    }
+    return over_cta(c);
+}
+
+// Many rows: a CTA counts a group of `per` of them.
+__global__ void __launch_bounds__(kRowsThreads) cm_head_count_kernel(const HeadRows p, int64_t per) {
+    let_next_start();
+    wait_for_previous();
+    const int64_t r0 = int64_t(blockIdx.x) * per;
+    const Counted c = count_rows(p, r0, min(p.rows, r0 + per), r0);
+    if (threadIdx.x == 0) p.groups[blockIdx.x] = {c.all, c.top};
+}
+
+// A CTA places a group of `per` rows, `step` (4 to 64) at a time; up to kHeadRowsOnce rows
+// in one step (1003 rows of 4101 elements in 64s 86 us, on 16 SMs, in 4s 15).  Then
+// it counts all rows' targets itself, which costs a pass over them from L2, and saves a
+// launch and a scan across CTAs; beyond that the passes would cost more (rows^2 / per
+// targets in all: 2^20 rows of 8 elements over 8 columns took 7.2 ms, now 0.55), and it adds up the
+// groups' counts instead.
 //
 // The gradients' factors are kept relative to the largest of them (scale), by which the
 // results are multiplied at the end in fp32: the bf16 gradient of a logit then does not
 // carry the rounding of a common factor such as 1 / rows.
-__global__ void __launch_bounds__(kRowsThreads) cm_head_rows_kernel(const HeadRows p, int per) {
-    __shared__ int counts[2][kRowsThreads / 32];
-    __shared__ float tops[kRowsThreads / 32];
+template <bool GROUPS>
+__global__ void __launch_bounds__(kRowsThreads, 4) cm_head_rows_kernel(const HeadRows p, int64_t per, int step) {
     __shared__ int slots[kRowsMost];
     let_next_start();
     wait_for_previous();
-    const int64_t r0 = int64_t(blockIdx.x) * per, r1 = min(p.rows, r0 + per);
+    const int64_t g0 = int64_t(blockIdx.x) * per, g1 = min(p.rows, g0 + per);
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-    int before = 0, all = 0;
-    float top = 0.0f;
-#pragma unroll 4
-    for (int64_t r = threadIdx.x; r < p.rows; r += kRowsThreads) {
-        const int64_t t = target_of(p, r);
-        const float a = p.dloss ? p.dloss[r] : 0.0f, b = p.dlse ? p.dlse[r] : 0.0f;   // read whether it counts or not
-        if (t < 0) continue;
-        ++all;
-        before += r < r0;
-        top = larger(larger(top, a), a + b);
+    Counted counted = {0, 0, 0.0f};
+    if constexpr (!GROUPS) {
+        counted = count_rows(p, 0, p.rows, g0);
+    } else {
+        for (int i = int(threadIdx.x); i < int(gridDim.x); i += kRowsThreads) {
+            const HeadGroup g = p.groups[i];
+            counted = {counted.before + (i < int(blockIdx.x) ? g.count : 0), counted.all + g.count, fmaxf(counted.top, g.top)};
+        }
+        counted = over_cta(counted);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    if (lane == 0) counts[0][warp] = before, counts[1][warp] = all, tops[warp] = top;
-    __syncthreads();
-    before = all = 0, top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRowsThreads / 32; ++i) before += counts[0][i], all += counts[1][i], top = fmaxf(top, tops[i]);
-    const float scale = top > 0.0f ? top : 1.0f;
+    const int all = counted.all;
+    int before = counted.before;   // of warp 0: rows with a target in front of the step
+    const float scale = counted.top > 0.0f ? counted.top : 1.0f;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *p.count = all;
         if (p.scale) *p.scale = scale;
     }
-    if (warp == 0) {   // the CTA's rows, in order
-        for (int i = 0; i < per; i += 32) {
-            const int64_t r = r0 + i + lane;
-            const int64_t t = r < r1 ? target_of(p, r) : -1;
-            const uint32_t live = __ballot_sync(0xffffffffu, t >= 0);
-            const int slot = t >= 0 ? before + __popc(live & ((1u << lane) - 1)) : -1;
-            before += __popc(live);
-            if (r >= r1) continue;
-            slots[i + lane] = slot;
-            if (p.slot_of) p.slot_of[r] = slot;
-            if (slot < 0) {
-                if (p.loss) p.loss[r] = 0.0f;
-                if (p.lse_out) p.lse_out[r] = 0.0f;
-                if (p.picked_out) p.picked_out[r] = 0.0f;
-                continue;
-            }
-            p.target[slot] = t >= p.vocab ? kNoToken : t >= p.first && t - p.first < p.n ? int32_t(t - p.first) : kNotHere;
-            if (p.row_of) p.row_of[slot] = int32_t(r);
-            if (p.picked) p.picked[slot] = 0.0f;
-            if (p.dloss) {
-                // a target beyond the vocabulary: NaN, as its loss
-                const float a = t >= p.vocab ? __int_as_float(0x7fffffff) : p.dloss[r];
-                p.hit[slot] = a / scale;
-                p.grad[slot] = (p.dlse ? a + p.dlse[r] : a) / scale;
-                p.lse2[slot] = p.lse[r] * kLog2e;
-            }
-        }
-    }
-    if (all == p.rows && !p.always) return;   // the products read x itself
-    __syncthreads();
     const int K = int(p.K), nv = (K + 7) / 8;
     const bf16 *x = static_cast<const bf16 *>(p.x);
     bf16 *xs = static_cast<bf16 *>(p.xs);
-    const int total = int(r1 - r0) * nv;
-    for (int at = int(threadIdx.x); at < total; at += 4 * kRowsThreads) {   // four loads before the first store
-        V8 f[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int j = at + k * kRowsThreads, i = j / nv;
-            if (j < total && slots[i] >= 0) f[k] = load_row8(x + (r0 + i) * p.ldx, (j - i * nv) * 8, K);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int j = at + k * kRowsThreads, i = j / nv;
-            if (j < total && slots[i] >= 0) store_row8(xs + int64_t(slots[i]) * p.ldxs, (j - i * nv) * 8, K, f[k]);
-        }
-    }
     // zeros behind the last slot: where a product's contraction reads on to its slice's end
     const int64_t end = p.always ? p.rows : min(p.rows, int64_t(max(all, 1) + 63) / 64 * 64);
-    const V8 zero = fill(0.0f);
-    for (int64_t s = max(r0, int64_t(all)) + warp; s < min(r1, end); s += kRowsThreads / 32)
-        for (int v = lane; v < nv; v += 32) store_row8(xs + s * p.ldxs, v * 8, K, zero);
+    for (int64_t r0 = g0; r0 < g1; r0 += step) {
+        const int64_t r1 = GROUPS ? min(g1, r0 + step) : g1;
+        if (warp == 0) {   // the step's rows, in order
+            for (int i = 0; i < step; i += 32) {
+                const int64_t r = r0 + i + lane;
+                const int64_t t = r < r1 ? target_of(p, r) : -1;
+                const uint32_t live = __ballot_sync(0xffffffffu, t >= 0);
+                const int slot = t >= 0 ? before + __popc(live & ((1u << lane) - 1)) : -1;
+                before += __popc(live);
+                if (r >= r1) continue;
+                slots[i + lane] = slot;
+                if (p.slot_of) p.slot_of[r] = slot;
+                if (slot < 0) {
+                    if (p.loss) p.loss[r] = 0.0f;
+                    if (p.lse_out) p.lse_out[r] = 0.0f;
+                    if (p.picked_out) p.picked_out[r] = 0.0f;
+                    continue;
+                }
+                p.target[slot] = t >= p.vocab ? kNoToken : t >= p.first && t - p.first < p.n ? int32_t(t - p.first) : kNotHere;
+                if (p.row_of) p.row_of[slot] = int32_t(r);
+                if (p.picked) p.picked[slot] = 0.0f;
+                if (p.dloss) {
+                    // a target beyond the vocabulary: NaN, as its loss
+                    const float a = t >= p.vocab ? __int_as_float(0x7fffffff) : p.dloss[r];
+                    p.hit[slot] = a / scale;
+                    p.grad[slot] = (p.dlse ? a + p.dlse[r] : a) / scale;
+                    p.lse2[slot] = p.lse[r] * kLog2e;
+                }
+            }
+        }
+        if (all == p.rows && !p.always) {   // the products read x itself
+            if (GROUPS) continue;
+            return;
+        }
+        __syncthreads();
+        const int total = int(r1 - r0) * nv;
+        for (int at = int(threadIdx.x); at < total; at += 4 * kRowsThreads) {   // four loads before the first store
+            V8 f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = at + k * kRowsThreads, i = j / nv;
+                if (j < total && slots[i] >= 0) f[k] = load_row8(x + (r0 + i) * p.ldx, (j - i * nv) * 8, K);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = at + k * kRowsThreads, i = j / nv;
+                if (j < total && slots[i] >= 0) store_row8(xs + int64_t(slots[i]) * p.ldxs, (j - i * nv) * 8, K, f[k]);
+            }
+        }
+        const V8 zero = fill(0.0f);
+        for (int64_t s = max(r0, int64_t(all)) + warp; s < min(r1, end); s += kRowsWarps)
+            for (int v = lane; v < nv; v += 32) store_row8(xs + s * p.ldxs, v * 8, K, zero);
+        if constexpr (!GROUPS) return;
+        __syncthreads();   // the slots have been read
+    }
 }
 
 // {m, s}: m the largest in powers of two, s the sum of 2^(. - m).
@@ -208,8 +253,14 @@ __global__ void __launch_bounds__(256) cm_head_scatter_kernel(const HeadScatter 
 }  // namespace
 
 cudaError_t launch_head_rows(const HeadRows &p, cudaStream_t stream) {
-    const int per = int(std::max<int64_t>(4, std::min<int64_t>(kRowsMost, p.rows / 512 / 4 * 4)));
-    return launch_after(cm_head_rows_kernel, dim3(unsigned((p.rows + per - 1) / per)), kRowsThreads, 0, 1, stream, p, per);
+    const int step = int(std::max<int64_t>(4, std::min<int64_t>(kRowsMost, p.rows / 512 / 4 * 4)));
+    int64_t per = step;
+    if (p.rows > kHeadRowsOnce) {   // whole steps a group
+        per = (p.rows + kHeadGroups * step - 1) / (kHeadGroups * step) * step;
+        const cudaError_t e = launch_after(cm_head_count_kernel, dim3(unsigned((p.rows + per - 1) / per)), kRowsThreads, 0, 1, stream, p, per);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(p.rows > kHeadRowsOnce ? cm_head_rows_kernel<true> : cm_head_rows_kernel<false>, dim3(unsigned((p.rows + per - 1) / per)), kRowsThreads, 0, 1, stream, p, per, step);
 }
 cudaError_t launch_head_join(const HeadJoin &p, cudaStream_t stream) {
     return launch_after(cm_head_join_kernel, dim3(unsigned((p.stride + kJoinSlots - 1) / kJoinSlots)), 32 * kJoinWarps, 0, 1, stream, p);

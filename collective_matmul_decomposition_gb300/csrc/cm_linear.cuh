@@ -164,7 +164,14 @@ int64_t colsum_chunks(int64_t rows, int64_t cols);
 cudaError_t launch_colsum(const void *x, int64_t ldx, int64_t rows, int64_t cols, float *partial, void *out,
                           bool out_f32, bool accumulate, cudaStream_t stream);
 
-// Rows that have a target, gathered (cm_head.cu).  Slot j is the j-th of them.
+// Rows that have a target, gathered (cm_head.cu).  Slot j is the j-th of them.  More than
+// kHeadRowsOnce rows are counted in up to kHeadGroups groups by a launch of their own.
+constexpr int64_t kHeadRowsOnce = 32768;
+constexpr int kHeadGroups = 1024;
+struct HeadGroup {
+    int32_t count;   // rows with a target
+    float top;       // the largest finite |dloss|, |dloss + dlse| of them
+};
 struct HeadRows {
     const void *targets;
     int target_bits;
@@ -183,6 +190,7 @@ struct HeadRows {
     float *loss, *lse_out, *picked_out;   // by row, zeros for rows without a target (forward); may be NULL
     const float *lse, *dloss, *dlse;      // by row (backward); dlse may be NULL
     float *lse2, *grad, *hit, *scale;     // by slot, and one (backward)
+    HeadGroup *groups;                    // kHeadGroups where rows > kHeadRowsOnce
 };
 cudaError_t launch_head_rows(const HeadRows &p, cudaStream_t stream);
 

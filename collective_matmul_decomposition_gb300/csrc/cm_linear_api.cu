@@ -357,8 +357,12 @@ struct Carve {
 // Whole 128-byte lines: the rows of a box that a product loads then do not straddle them.
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 
+// The groups that many rows are counted in.
+HeadGroup *head_groups(Carve &c, int64_t M) { return M > kHeadRowsOnce ? c.take<HeadGroup>(kHeadGroups) : nullptr; }
+
 struct LossSpace {
     int32_t *count, *row_of, *target;
+    HeadGroup *groups;
     float *picked;
     uint16_t *xs;
     float2 *stat;
@@ -371,6 +375,7 @@ LossSpace loss_space(Carve &c, int64_t M, int64_t K, int64_t n) {
     s.picked = c.take<float>(size_t(M));
     s.xs = c.take<uint16_t>(size_t(M) * size_t(up64(K)));
     s.stat = c.take<float2>(size_t((n + 255) / 256 * 2) * size_t(M));
+    s.groups = head_groups(c, M);
     return s;
 }
 
@@ -386,6 +391,7 @@ int64_t loss_grad_columns(int64_t M, int64_t n) {
 
 struct LossGradSpace {
     int32_t *count, *slot_of, *target;
+    HeadGroup *groups;
     float *scale, *lse2, *grad, *hit, *sum;
     uint16_t *xs, *p;
     int64_t columns, ldp, lds;
@@ -405,6 +411,7 @@ LossGradSpace loss_grad_space(Carve &c, int64_t M, int64_t K, int64_t n) {
     s.xs = c.take<uint16_t>(size_t(M) * size_t(s.lds));
     s.p = c.take<uint16_t>(size_t(M) * size_t(s.ldp));
     s.sum = c.take<float>(size_t(M) * size_t(s.lds));
+    s.groups = head_groups(c, M);
     return s;
 }
 
@@ -650,6 +657,7 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
     r.loss = loss;
     r.lse_out = lse;
     r.picked_out = picked;
+    r.groups = s.groups;
     const Choice c = choose_logits(d, M, n, K);
     r.always = !c.pair;
     if (launch_head_rows(r, stream) != cudaSuccess) return CM_ERR_CUDA;
@@ -735,6 +743,7 @@ cm_status cm_linear_cross_entropy_backward(const void *x, int64_t ldx, const voi
     r.grad = s.grad;
     r.hit = s.hit;
     r.scale = s.scale;
+    r.groups = s.groups;
     if (launch_head_rows(r, stream) != cudaSuccess) return CM_ERR_CUDA;
     const Operand rows = {s.xs, s.lds, false}, rows_t = {s.xs, s.lds, true}, all = {x, ldx, false}, all_t = {x, ldx, true};
     for (int64_t c0 = 0; c0 < n; c0 += s.columns) {
