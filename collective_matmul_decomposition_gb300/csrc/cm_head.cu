@@ -28,7 +28,7 @@ __device__ __forceinline__ int64_t target_of(const HeadRows &p, int64_t row) {
 // The largest of the magnitudes that are finite.
 __device__ __forceinline__ float larger(float a, float b) {
     b = fabsf(b);
-    return b <= 3.0e38f ? fmaxf(a, b) : a;
+    return b < INFINITY ? fmaxf(a, b) : a;
 }
 
 // Counts of a CTA's threads, summed; the same in all of them.

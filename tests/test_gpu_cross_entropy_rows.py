@@ -71,3 +71,30 @@ def test_time_grows_with_the_rows():
             end.synchronize()
             best[-1] = min(best[-1], begin.elapsed_time(end))
     assert best[1] <= 32 * best[0], best
+
+
+@pytest.mark.parametrize("M", [1, 5, 700])
+def test_the_largest_factors(M):
+    """Factors up to fp32's largest number are finite: the logits' gradients are kept relative to them too, and neither they
+    nor results that fp32 holds overflow.  Infinite ones make their own row's dx infinite or NaN and no other's."""
+    K, n = 72, 1000
+    x, w, t, vocab, _ = make(M, K, n, 0, 0, "none", "nk", seed=M)
+    x, w = x * 2.0 ** -7, w * 2.0 ** -7
+    top = torch.finfo(F32).max
+    dloss = torch.linspace(0.8, 1.0, M, device=DEV) * top if M > 1 else torch.full((1,), top, device=DEV)
+    lse = torch.logsumexp(logits(x, w, "nk")[2], 1).float()
+    dx, dw = torch.empty(M, K, device=DEV), torch.empty(n, K, device=DEV)
+    ws, _ = space(cm.linear_cross_entropy_backward_workspace_size(M, K, n))
+    cm.cm_linear_cross_entropy_backward(x, w, t, lse, dloss, ws, dx=dx, dw=dw)
+    status_ok()
+    for (want, bound), got in zip(gradient(x, w, t, lse, dloss, None, 0, "nk", torch.ones(M, dtype=torch.bool, device=DEV)), (dx, dw)):
+        assert float(want.abs().max()) < top
+        assert bool(((got.double() - want).abs() <= (bound + half_ulp(want, F32) + 2.0 ** -22 * want.abs()) * (1 + 2.0 ** -7)).all())
+    if M > 1:
+        dloss = torch.ones(M, device=DEV)
+        cm.cm_linear_cross_entropy_backward(x, w, t, lse, dloss, ws, dx=dx)
+        good = dx.clone()
+        dloss[1] = math.inf
+        cm.cm_linear_cross_entropy_backward(x, w, t, lse, dloss, ws, dx=dx)
+        assert not bool(dx[1].isfinite().any())
+        assert torch.equal(torch.cat([dx[:1], dx[2:]]), torch.cat([good[:1], good[2:]]))
