@@ -15,7 +15,9 @@ namespace {
 
 __device__ LinearStatus g_linear_status;
 
-constexpr uint64_t kLinearTimeoutNs = 1000000000ull;
+// The longest wait is for a tile's products: a second, and a microsecond a slice (they take
+// 0.28: dw of the loss of 2^28 rows has 2^22 slices a tile, 1.2 s).
+uint64_t linear_timeout_ns(int kblocks) { return 1000000000ull + 1000ull * uint64_t(kblocks); }
 constexpr int64_t kMaxExtent = int64_t(1) << 30;
 
 struct NvtxRange {
@@ -256,7 +258,7 @@ cm_status pair_params(LinearPairMore &p, const Device &d, const Choice &c, const
     if (a.mn_major && b.mn_major && e.y_f32 && p.kblocks <= 16)
         p.band = std::min(p.band, (d.clusters[0] + p.ntiles - 1) / p.ntiles);
     p.status = d.status;
-    p.timeout_ns = kLinearTimeoutNs;
+    p.timeout_ns = linear_timeout_ns(p.kblocks);
     if (!map_operand(&p.tmA, b, rows, k, 128) || !map_operand(&p.tmB, a, cols, k, c.bn / 2) ||
         (kind.a2 && !map_operand(&p.tmB2, *kind.a2, cols, k, c.bn / 2)) ||
         (e.y && !map_written(&p.tmY, e.y, rows, cols, e.ldy, e.y_f32 != 0)))
@@ -307,7 +309,7 @@ cm_status product_strip(const Device &d, const Choice &c, const Kind &kind, cons
     p.head = kind.head;
     p.count = kind.live.count;
     p.status = d.status;
-    p.timeout_ns = kLinearTimeoutNs;
+    p.timeout_ns = linear_timeout_ns(p.kblocks);
     if (!map_operand(&p.tmA, a, cols, k, gated ? 64 : 128) || (gated && !map_operand(&p.tmA2, *kind.a2, cols, k, 64)) ||
         !map_operand(&p.tmB, b, rows, k, c.tok))
         return CM_ERR_CUDA;

@@ -29,3 +29,14 @@ def test_an_aborting_pair_waits_for_loads_that_no_barrier_counts():
     close = close[:close.index("\n}\n")]
     synced, settled = close.find("cluster_sync();"), close.find("settle(")
     assert 0 <= synced < settled, "leaves without waiting"
+
+
+def test_waits_last_as_long_as_a_tile_of_many_slices():
+    """A tile's products are waited for by its epilogue: 0.28 us a slice of 64 terms on the largest tiles, which for 2^30
+    terms is more than the second that a small call's waits are bounded by."""
+    text = source("cm_linear_api.cu")
+    limit = re.search(r"uint64_t linear_timeout_ns\(int kblocks\) \{ return (\d+)ull \+ (\d+)ull \* uint64_t\(kblocks\); \}", text)
+    assert limit and int(limit.group(1)) >= 10 ** 9
+    for kblocks in (1, 1 << 12, 1 << 22, 1 << 24):
+        assert int(limit.group(1)) + int(limit.group(2)) * kblocks > 1.5 * 281 * kblocks
+    assert re.findall(r"timeout_ns = (.*?);", text) == ["linear_timeout_ns(p.kblocks)"] * 2
