@@ -648,6 +648,7 @@ def linear_cross_entropy_backward_workspace_size(M: int, K: int, n: int) -> int:
 def cm_linear_cross_entropy_backward(x, w, targets, lse, dloss, ws, dx=None, dw=None, dlse=None, first: int = 0, vocab=None,
                                      accumulate: bool = False, w_layout: str = "nk", stream=None):
     """The gradients of sum(dloss * loss + dlse * lse): dx [M][K], and dw (+)= in the weight's layout (both optional).
+    Products of the logits' gradients rounded to bf16, whatever dx's and dw's dtype.
     lse [M] as the forward call wrote it, or joined over all slices; ws: linear_cross_entropy_backward_workspace_size."""
     lib = _library()
     M, K, dev = _extents("x", x)

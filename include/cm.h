@@ -686,7 +686,9 @@ cm_status cm_linear_wgrad(const void *x, int64_t ldx, const void *dy, int64_t ld
  *  there.  Where a target lies outside of the slice, picked is 0: over ranks that
  *  hold a slice each, log sum_ranks exp(lse) less the sum of picked is the loss of
  *  the whole.  A target of `vocab` or more has a NaN loss.  Products, maxima and
- *  sums are fp32.  first at most 2^30, vocab at least first + n and at most 2^31;
+ *  sums are fp32; a logit's terms are summed in parts of at most 1024, whose sums
+ *  are added with rounding.  loss is a difference: its error is relative to lse and
+ *  picked, not to itself.  first at most 2^30, vocab at least first + n and at most 2^31;
  *  M n, M K and K n below 2^45 (CM_ERR_SHAPE beyond).
  *  ws: cm_linear_cross_entropy_workspace_size(M, K, n) bytes, 16-byte aligned; no
  *  initialisation; calls that share it must be ordered on the GPU.  Results do not
@@ -702,14 +704,18 @@ cm_status cm_linear_cross_entropy(const void *x, int64_t ldx, const void *w, int
  * cm_linear_cross_entropy_backward -- the gradients of sum(dloss loss + dlse lse):
  *   dz = exp(z - lse) (dloss + dlse), less dloss in the target's column;
  *   dx = dz W;  dw (+)= dz^T x, laid out as the weight is.
+ *  dz is taken in fp32 from logits summed as in the forward call, and rounded to
+ *  bf16 for the two products: dx and dw carry that rounding (2^-8 of each dz at
+ *  most) in fp32 too.
  *  Arguments as in the forward call; lse [M] fp32 as that wrote it, or the log
  *  sum over all slices (dx is then this slice's share: the slices' dx add up, and
  *  each dw is whole).  dloss [M] fp32, dlse [M] fp32 or NULL (zeros).  dx [M][K]
  *  (dx_dtype) and dw (dw_dtype) may each be NULL; with `accumulate` dw is added to.
  *  Rows without a target give zeros and count nowhere; their lse, dloss and dlse
- *  are not used.  The logits are computed again, some columns at a time, and dz is
- *  rounded to bf16 for the products, relative to the largest of the finite
- *  |dloss|, |dloss + dlse| (what is below 2^-126 of it is lost); sums are fp32.
+ *  are not used.  A target of `vocab` or more makes its row of dx NaN, and all of
+ *  dw.  The logits are computed again, some columns at a time; dz is kept relative
+ *  to the largest of the finite |dloss|, |dloss + dlse| (what is below 2^-126 of it
+ *  is lost); sums are fp32.
  *  ws: cm_linear_cross_entropy_backward_workspace_size(M, K, n) bytes, as above.
  */
 size_t cm_linear_cross_entropy_backward_workspace_size(int64_t M, int64_t K, int64_t n);
