@@ -103,8 +103,8 @@ def test_gradient_of_sure_rows(M, K, n, layout, masked):
 
 
 def test_fewer_rows_do_not_take_longer():
-    """80 rows over a wide vocabulary and 257, which whole tiles of 256 rows compute: the tile is chosen among those that
-    run.  (Measured 48 and 64 us; 79 for 80 rows in tiles that are not.)"""
+    """80 rows over a wide vocabulary, and 257, which whole tiles of 256 rows compute.  (Measured 48 us in such tiles, 79 in
+    strips; 300 rows 64.)"""
     K, n = 512, 131072
     w = torch.randn(n, K, device=DEV).to(BF)
     graphs = []
